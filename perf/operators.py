@@ -1,0 +1,412 @@
+"""Cases of the serving operators that stand next to the sparse product in a decoder layer.
+
+A decoder layer of a served model is a few skinny matrix products (this library's main
+subject) around an attention over a cache of past keys and values.  The operators here are
+
+* ``quant``  -- the product of 1..64 token vectors with a weight matrix of 4-bit codes and
+  one scale (and optionally one zero point) per row and group of columns;
+* ``write``  -- new keys and values written into a paged cache, held in 8 bits (e4m3) with
+  one power-of-two scale per token and head;
+* ``read``   -- tokens of such a cache read back, in the model's type;
+* ``attend`` -- attention of each sequence's new tokens over its pages, whatever the number
+  of new tokens: one (decoding), some (a chunk of a prompt), none.
+
+Shapes are those of this library's benchmark (OPT-30B, -66B, -175B: 56, 72 and 96 heads of
+128 channels; matrices 28672 x 7168, 12288 x 49152, 1024 x 1024) or generic ones.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+#: Types of activations and of a 16-bit cache.
+TYPES = {"f16": torch.float16, "bf16": torch.bfloat16}
+#: Largest finite value of the 8-bit type.
+E4M3_MAX = 448.0
+
+
+def listed():
+    return [
+        # the smallest layer for one token: nothing but the latency of a call
+        dict(op="quant", name="quant 1024x1024, 1 token", M=1024, K=1024, N=1, group=128, zeros=False, type="f16"),
+        # OPT-30B MLP1 for a small batch of decoding sequences
+        dict(op="quant", name="quant 28672x7168, 16 tokens", M=28672, K=7168, N=16, group=128, zeros=False, type="f16"),
+        # OPT-175B MLP2 for a full batch, with zero points: the most bytes
+        dict(op="quant", name="quant 12288x49152, 64 tokens", M=12288, K=49152, N=64, group=128, zeros=True, type="f16"),
+        # sizes that are multiples of nothing, short groups, the other type
+        dict(op="quant", name="quant 5003x4099, 5 tokens", M=5003, K=4099, N=5, group=32, zeros=True, type="bf16"),
+        # one decoding step of 64 sequences: 64 tokens, each to a page of its own
+        dict(op="write", name="write 64 tokens, 96 heads", T=64, heads=96, dim=128, page=16, skip=False, type="f16"),
+        # a long prompt's keys and values, padding tokens among them
+        dict(op="write", name="write 4095 tokens, 56 heads", T=4095, heads=56, dim=128, page=64, skip=True, type="bf16"),
+        # a sequence's cache read back whole, as when it moves or is recomputed from
+        dict(op="read", name="read 4096 tokens, 56 heads", T=4096, heads=56, dim=128, page=16, skip=False, type="f16"),
+        # a short prefix, heads of 80 channels
+        dict(op="read", name="read 333 tokens, 8 heads of 80", T=333, heads=8, dim=80, page=32, skip=True, type="bf16"),
+        # one sequence that decodes: latency, and one short axis to split
+        dict(op="attend", name="attend 1 token over 1000", S=1, q=1, q_low=1, len=1000, len_low=1000, heads=32, kv=8,
+             dim=128, page=16, cache="f16", type="f16", window=0),
+        # a batch of 64 ragged sequences that decode, heads not shared, 8-bit cache
+        dict(op="attend", name="attend 64 x 1 token over 2048", S=64, q=1, q_low=1, len=2048, len_low=100, heads=96, kv=96,
+             dim=128, page=16, cache="e4m3", type="f16", window=0),
+        # a chunk of a long prompt over what came before it: matrix products
+        dict(op="attend", name="attend 2048 tokens over 16384", S=1, q=2048, q_low=2048, len=16384, len_low=16384, heads=32,
+             kv=8, dim=128, page=64, cache="bf16", type="bf16", window=0),
+        # prompts' chunks of all lengths and decoding sequences in one call, a sliding window
+        dict(op="attend", name="attend 16 x 0-300 tokens over 5000", S=16, q=300, q_low=0, len=5000, len_low=0, heads=16,
+             kv=4, dim=64, page=16, cache="e4m3", type="f16", window=1024),
+    ]
+
+
+def _between(rng, low, high):
+    """A whole number of [low, high], spread over its logarithm."""
+    return min(high, max(low, int(round(math.exp(rng.uniform(math.log(low), math.log(high)))))))
+
+
+def draw(rng):
+    op = rng.choice(["quant", "quant", "write", "read", "attend", "attend"])
+    kind = rng.choice(["f16", "bf16"])
+    if op == "quant":
+        M, K = _between(rng, 64, 49152), _between(rng, 64, 49152)
+        return dict(op=op, M=M, K=K, N=_between(rng, 1, 64), group=rng.choice([32, 64, 128]), zeros=rng.random() < 0.5,
+                    type=kind) if M * K <= 12288 * 49152 else dict(op=op, M=M // 4, K=K, N=_between(rng, 1, 64), group=128,
+                                                                  zeros=True, type=kind)
+    dim = rng.choice([64, 80, 128, 128])
+    page = rng.choice([16, 32, 64, 128])
+    if op in ("write", "read"):
+        heads = _between(rng, 1, 96)
+        T = _between(rng, 1, min(16384, 4095 * 56 // heads))
+        return dict(op=op, T=T, heads=heads, dim=dim, page=page, skip=rng.random() < 0.5, type=kind)
+    kv, share = rng.choice([1, 2, 4, 8, 8, 12]), rng.choice([1, 2, 4, 8])
+    cache = rng.choice([kind, "e4m3"])
+    window = rng.choice([0, 0, 0, 300])
+    if rng.random() < 0.5:  # decoding
+        S = _between(rng, 1, 64)
+        length = _between(rng, 16, min(32768, 131072 // S))
+        return dict(op=op, S=S, q=1, q_low=1, len=length, len_low=_between(rng, 1, length), heads=kv * share, kv=kv, dim=dim,
+                    page=page, cache=cache, type=kind, window=window)
+    S = _between(rng, 1, 8)  # chunks
+    length = _between(rng, 64, 16384 // S)
+    q = _between(rng, 2, min(length, 1024))
+    return dict(op=op, S=S, q=q, q_low=rng.randint(0, q), len=length, len_low=rng.randint(q, length), heads=min(32, kv * share),
+                kv=min(32, kv * share) // share, dim=dim, page=page, cache=cache, type=kind, window=window)
+
+
+# ------------------------------------------------------------------ inputs
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _normal(shape, g, type=torch.float32):
+    return torch.randn(shape, generator=g, device="cuda", dtype=torch.float32).to(type)
+
+
+def _lengths(c):
+    """Host lists: each sequence's new tokens and its length with them, the same for every seed."""
+    r = random.Random(c["S"])
+    new = [r.randint(c["q_low"], c["q"]) for _ in range(c["S"])]
+    length = [max(n, r.randint(c["len_low"], c["len"])) for n in new]
+    new[0], length[0] = c["q"], max(c["q"], c["len"])
+    return new, length
+
+
+def _pages(c, g, pages, cache, heads):
+    """A pool of `pages` pages as earlier steps left it: normal keys and values."""
+    shape = (pages, heads, c["page"], c["dim"])
+    if cache != "e4m3":
+        return dict(k=torch.randn(shape, generator=g, device="cuda", dtype=torch.float16).to(TYPES[cache]),
+                    v=torch.randn(shape, generator=g, device="cuda", dtype=torch.float16).to(TYPES[cache]), ks=None, vs=None)
+    out = {}
+    for n in ("k", "v"):
+        # codes of normal values of many sizes: a token's scale says where its largest value lies
+        out[n] = (torch.randn(shape, generator=g, device="cuda", dtype=torch.float16) * 80).clamp_(-E4M3_MAX, E4M3_MAX) \
+            .to(torch.float8_e4m3fn)
+        out[n + "s"] = torch.exp2(torch.randint(-8, -5, shape[:3], generator=g, device="cuda").float())
+    return out
+
+
+def _shuffled(count, g):
+    return torch.randperm(count, generator=g, device="cuda").to(torch.int32)
+
+
+def _slots(c, pages, g):
+    """T slots on whole pages in any order (as an allocator hands them out); some of no token."""
+    T, page = c["T"], c["page"]
+    order = _shuffled(pages, g)[:(T + page - 1) // page].long()
+    t = torch.arange(T, device="cuda")
+    slots = (order[t // page] * page + t % page).to(torch.int32)
+    if c["skip"]:
+        slots = torch.where((torch.rand(T, generator=g, device="cuda") < 0.1) & (t > 0), torch.full_like(slots, -1), slots)
+    return slots
+
+
+def prepare(case, seed):
+    c, g = case, _gen(seed)
+    if c["op"] == "quant":
+        M, K, N = c["M"], c["K"], c["N"]
+        kind, groups = TYPES[c["type"]], (K + c["group"] - 1) // c["group"]
+        s = dict(c, codes=torch.randint(0, 256, (M, (K + 1) // 2), generator=g, device="cuda", dtype=torch.uint8),
+                 scales=torch.exp(_normal((M, groups), g) * 0.3 - 5).to(kind), x=_normal((N, K), g),
+                 y=torch.empty((N, M), device="cuda", dtype=kind))
+        s["x"][:, ::97] *= 8  # a few channels are much larger than the others
+        s["x"] = s["x"].to(kind)
+        s["zero"] = torch.randint(4, 12, (M, groups), generator=g, device="cuda", dtype=torch.uint8) if c["zeros"] else None
+        if own:
+            import unstructured_sparse_skinny_amd as L
+            s["handle"] = L.lscd_quant_encode(s["codes"], s["scales"], K, s["zero"], c["group"])
+        return s
+    if c["op"] in ("write", "read"):
+        pages = (c["T"] + c["page"] - 1) // c["page"] + 3
+        if c["op"] == "write":  # into a pool in use; a decoding batch writes one token to a page
+            pages = max(pages, c["T"] + 3 if c["T"] <= 64 else 0)
+        s = dict(c, **_pages(c, g, pages, "e4m3", c["heads"]), slots=_slots(c, pages, g))
+        kind, shape = TYPES[c["type"]], (c["T"], c["heads"], c["dim"])
+        if c["op"] == "write":
+            if c["T"] <= 64:
+                at = _shuffled(pages, g)[:c["T"]]
+                s["slots"] = torch.where(s["slots"] < 0, s["slots"], at * c["page"] + at % c["page"])
+            # keys and values are slices of one product's output, as they are in a decoder layer
+            qkv = _normal((c["T"], 3, c["heads"], c["dim"]), g)
+            qkv *= torch.exp(_normal((c["T"], 3, 1, 1), g))
+            qkv = qkv.to(kind)
+            s["new_k"], s["new_v"] = qkv[:, 1], qkv[:, 2]
+        else:
+            s["out_k"], s["out_v"] = (torch.empty(shape, device="cuda", dtype=kind) for _ in range(2))
+        if own:
+            import unstructured_sparse_skinny_amd as L
+            s["cache_"] = L.Cache(s["k"], s["v"], s["ks"], s["vs"])
+        return s
+    new, length = _lengths(c)
+    page, wide = c["page"], (max(length) + c["page"] - 1) // c["page"]
+    need = [(n + page - 1) // page for n in length]
+    pages = sum(need) + 1
+    s = dict(c, **_pages(c, g, pages, c["cache"], c["kv"]), q_most=max(new), T=sum(new))
+    order, at, table = _shuffled(pages, g), 0, torch.zeros((c["S"], wide), device="cuda", dtype=torch.int32)
+    for i, n in enumerate(need):
+        table[i, :n] = order[at:at + n]
+        at += n
+    s["table"] = table
+    start = [0]
+    for n in new:
+        start.append(start[-1] + n)
+    s["start"] = torch.tensor(start, device="cuda", dtype=torch.int32)
+    s["length"] = torch.tensor(length, device="cuda", dtype=torch.int32)
+    kind = TYPES[c["type"]]
+    s["query"] = (_normal((max(1, s["T"]), c["heads"], c["dim"]), g) * 1.5).to(kind)[:s["T"]]
+    s["out"] = torch.empty_like(s["query"])
+    if own:
+        import unstructured_sparse_skinny_amd as L
+        s["cache_"] = L.Cache(s["k"], s["v"], s["ks"], s["vs"])
+        s["handle"] = L.lscd_attention_create(c["heads"], c["kv"], c["dim"])
+    return s
+
+
+# ------------------------------------------------------------------ one pass
+
+
+def run(state):
+    s = state
+    if own:
+        import unstructured_sparse_skinny_amd as L
+        if s["op"] == "quant":
+            L.lscd_quant_linear(s["handle"], s["x"], s["y"])
+            return s["y"]
+        if s["op"] == "write":
+            L.lscd_cache_write(s["cache_"], s["new_k"], s["new_v"], s["slots"])
+            return [s["k"], s["v"], s["ks"], s["vs"]]
+        if s["op"] == "read":
+            L.lscd_cache_read(s["cache_"], s["slots"], s["out_k"], s["out_v"])
+            return [s["out_k"], s["out_v"]]
+        L.lscd_attention(s["handle"], s["cache_"], s["query"], s["start"], s["length"], s["table"], s["out"],
+                         window=s["window"])
+        return s["out"]
+    if s["op"] == "quant":
+        return _plain_quant(s)
+    if s["op"] == "write":
+        _plain_write(s["new_k"], s["slots"], s["k"], s["ks"])
+        _plain_write(s["new_v"], s["slots"], s["v"], s["vs"])
+        return [s["k"], s["v"], s["ks"], s["vs"]]
+    if s["op"] == "read":
+        kind = TYPES[s["type"]]
+        return [_plain_read(s["k"], s["ks"], s["slots"], kind), _plain_read(s["v"], s["vs"], s["slots"], kind)]
+    return _plain_attend(s)
+
+
+def _plain_quant(s):
+    """y[n][m] = sum over k of x[n][k] * (code[m][k] - zero[m][k / group]) * scale[m][k / group]."""
+    K, group = s["K"], s["group"]
+    codes = torch.stack([s["codes"] & 15, s["codes"] >> 4], dim=2).flatten(1)[:, :K].float()
+    zero = 8.0 if s["zero"] is None else s["zero"].float().repeat_interleave(group, 1)[:, :K]
+    w = (codes - zero) * s["scales"].float().repeat_interleave(group, 1)[:, :K]
+    return (s["x"].float() @ w.t()).to(TYPES[s["type"]])
+
+
+def _plain_write(new, slots, pages, scales):
+    """Each token and head: scale = the least power of two with max |x| / scale <= 448 (1 where all
+    are zero), code = x / scale rounded to the nearest e4m3 value, ties to even."""
+    x = new.float()
+    most = x.abs().amax(dim=2)
+    fraction, exponent = torch.frexp(most / E4M3_MAX)
+    scale = torch.ldexp(torch.ones_like(most), exponent - (fraction == 0.5).int())
+    scale = torch.where(most > 0, scale, torch.ones_like(scale))
+    code = (x / scale[:, :, None]).to(torch.float8_e4m3fn)
+    # a token of no slot writes what is there already: the first slot's own values stay
+    page = pages.shape[2]
+    keep = slots >= 0
+    at = torch.where(keep, slots, slots.max()).long()
+    here = torch.argmax(slots)
+    code = torch.where(keep[:, None, None], code.view(torch.uint8), code.view(torch.uint8)[here])
+    scale = torch.where(keep[:, None], scale, scale[here])
+    pages.view(torch.uint8)[at // page, :, at % page] = code
+    scales[at // page, :, at % page] = scale
+
+
+def _plain_read(pages, scales, slots, kind):
+    """Code times scale in the model's type; zeros where there is no slot."""
+    page, at = pages.shape[2], slots.clamp(min=0).long()
+    # (indexing is by bytes: it has no 8-bit float form)
+    code = pages.view(torch.uint8)[at // page, :, at % page].view(torch.float8_e4m3fn).float()
+    x = code * scales[at // page, :, at % page][:, :, None]
+    return torch.where((slots >= 0)[:, None, None], x, torch.zeros_like(x)).to(kind)
+
+
+def _plain_cached(pages, scales, table):
+    """The tokens of each sequence's pages in order, in 32 bits: [sequence][head][token][channel]."""
+    S, wide = table.shape
+    kind, t = pages.dtype, table.long()
+    x = (pages.view(torch.uint8)[t].view(kind) if scales is not None else pages[t]).float()
+    if scales is not None:
+        x = x * scales[t][..., None]
+    return x.permute(0, 2, 1, 3, 4).reshape(S, pages.shape[1], wide * pages.shape[2], pages.shape[3])
+
+
+def _plain_attend(s):
+    """Token i of a sequence's n new ones stands at position p = length - n + i and sees the positions j with
+    j <= p and, with a window, j > p - window; softmax of q.k / sqrt(dim) over them; zeros where there is none."""
+    S, most, T = s["S"], s["q_most"], s["T"]
+    heads, kv, dim = s["heads"], s["kv"], s["dim"]
+    if T == 0:
+        return s["query"].clone()
+    start, length = s["start"].long(), s["length"].long()
+    new = start[1:] - start[:-1]
+    i = torch.arange(most, device="cuda")
+    q = s["query"][(start[:-1, None] + i).clamp(max=T - 1)].float()  # [S][most][heads][dim]
+    q = q.reshape(S, most, kv, heads // kv, dim).permute(0, 2, 3, 1, 4).reshape(S, kv, heads // kv * most, dim)
+    k = _plain_cached(s["k"], s["ks"], s["table"])
+    score = torch.matmul(q, k.transpose(2, 3)).mul_(1.0 / math.sqrt(dim))
+    del k
+    score = score.reshape(S, kv, heads // kv, most, -1)
+    p, j = (length - new)[:, None, None] + i[:, None], torch.arange(score.shape[-1], device="cuda")
+    sees = (j <= p) & (j < length[:, None, None])
+    if s["window"]:
+        sees &= j > p - s["window"]
+    score.masked_fill_(~sees[:, None, None], -math.inf)
+    most_ = score.amax(dim=-1, keepdim=True).clamp_(min=-3e38)
+    score = score.sub_(most_).exp_()
+    total = score.sum(dim=-1, keepdim=True)
+    v = _plain_cached(s["v"], s["vs"], s["table"])
+    o = torch.matmul(score.reshape(S, kv, heads // kv * most, -1), v).reshape(S, kv, heads // kv, most, dim)
+    o = torch.where(total > 0, o / total, torch.zeros_like(o)).permute(0, 3, 1, 2, 4).reshape(S, most, heads, dim)
+    t = torch.arange(T, device="cuda")
+    at = torch.searchsorted(start[1:].contiguous(), t, right=True)
+    return o[at, t - start[at]].to(TYPES[s["type"]])
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+
+
+def _positions(new, length, window):
+    """(positions that some token of the sequence sees, pairs of a token and a position that it sees)"""
+    first = length - new
+    pairs = sum(min(first + i + 1, window or length) for i in range(new))
+    seen = (length if not window else min(length, window + new - 1)) if new else 0
+    return seen, pairs
+
+
+def work(case):
+    c = case
+    if c["op"] == "quant":
+        M, K, N = c["M"], c["K"], c["N"]
+        groups = (K + c["group"] - 1) // c["group"]
+        return {"bytes": M * K / 2 + M * groups * (2.5 if c["zeros"] else 2) + 2 * N * (M + K), "flops": 2 * M * N * K}
+    if c["op"] in ("write", "read"):
+        # a token's 16-bit values on one side, codes and a scale on the other; the slots
+        return {"bytes": c["T"] * (2 * c["heads"] * (3 * c["dim"] + 4) + 4), "flops": 4 * c["T"] * c["heads"] * c["dim"]}
+    new, length = _lengths(c)
+    parts = [_positions(a, b, c["window"]) for a, b in zip(new, length)]
+    token = 2 * c["kv"] * (c["dim"] + 4 if c["cache"] == "e4m3" else 2 * c["dim"])
+    return {"bytes": sum(p[0] for p in parts) * token + 4 * sum(new) * c["heads"] * c["dim"],
+            "flops": 4 * sum(p[1] for p in parts) * c["heads"] * c["dim"]}
+
+
+# ------------------------------------------------------------------ the definitions in 64 bits
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False
+    try:
+        s = prepare(case, seed)
+    finally:
+        own = was
+    if s["op"] == "quant":
+        y = torch.zeros((s["N"], s["M"]), device="cuda", dtype=torch.float64)
+        x = s["x"].double()
+        for g in range(s["scales"].shape[1]):  # group by group: sums of whole numbers of codes, then the scale
+            k = torch.arange(g * s["group"], min(s["K"], (g + 1) * s["group"]), device="cuda")
+            code = (s["codes"][:, k // 2] >> (4 * (k % 2)).to(torch.uint8)) & 15
+            zero = s["zero"][:, g].double() if s["zero"] is not None else torch.full((s["M"],), 8.0, device="cuda").double()
+            y += (x[:, k] @ (code.double() - zero[:, None]).t()) * s["scales"][:, g].double()
+        return y
+    if s["op"] == "write":
+        out = []
+        for new, pages, scales in ((s["new_k"], s["k"], s["ks"]), (s["new_v"], s["v"], s["vs"])):
+            codes, scales, page = pages.double(), scales.double(), pages.shape[2]
+            t = (s["slots"] >= 0).nonzero()[:, 0]
+            x = new[t].double()
+            most = x.abs().amax(dim=2)
+            power = torch.ceil(torch.log2(most / E4M3_MAX))
+            power = torch.where(most / torch.exp2(power - 1) <= E4M3_MAX, power - 1, power)
+            scale = torch.where(most > 0, torch.exp2(power), torch.ones_like(most))
+            x = x / scale[..., None]
+            # e4m3 values step by 2^-3 of the leading power of two, which is at least 2^-6
+            step = torch.exp2(torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -6))) - 3)
+            at = s["slots"][t].long()
+            codes[at // page, :, at % page] = torch.round(x / step) * step
+            scales[at // page, :, at % page] = scale
+            out.append((codes, scales))
+        return [out[0][0], out[1][0], out[0][1], out[1][1]]
+    if s["op"] == "read":
+        out = []
+        for pages, scales in ((s["k"], s["ks"]), (s["v"], s["vs"])):
+            x = torch.zeros((s["T"], s["heads"], s["dim"]), device="cuda", dtype=torch.float64)
+            full = pages.double() * scales.double()[..., None]
+            t = (s["slots"] >= 0).nonzero()[:, 0]
+            at = s["slots"][t].long()
+            x[t] = full[at // pages.shape[2], :, at % pages.shape[2]]
+            out.append(x)
+        return out
+    out = torch.zeros((s["T"], s["heads"], s["dim"]), device="cuda", dtype=torch.float64)
+    start, length, share, page = s["start"].tolist(), s["length"].tolist(), s["heads"] // s["kv"], s["page"]
+    for i in range(s["S"]):
+        a, b, n = start[i], start[i + 1], length[i]
+        if a == b or n == 0:
+            continue
+        pos = torch.arange(n, device="cuda")
+        at = s["table"][i].long()[pos // page]
+        for h in range(s["kv"]):
+            k, v = s["k"][:, h].view(torch.uint8), s["v"][:, h].view(torch.uint8)
+            k, v = (x.reshape(x.shape[0], page, -1)[at, pos % page].view(s["k"].dtype).double() for x in (k, v))
+            if s["ks"] is not None:
+                k = k * s["ks"][at, h, pos % page].double()[:, None]
+                v = v * s["vs"][at, h, pos % page].double()[:, None]
+            for f in range(h * share, (h + 1) * share):
+                z = s["query"][a:b, f].double() @ k.t() / math.sqrt(s["dim"])
+                p = n - (b - a) + torch.arange(b - a, device="cuda")[:, None]
+                hidden = (pos > p) | ((pos <= p - s["window"]) if s["window"] else (pos < 0))
+                out[a:b, f] = torch.softmax(z.masked_fill(hidden, -math.inf), dim=1) @ v
+    return out
