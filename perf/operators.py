@@ -30,21 +30,21 @@ E4M3_MAX = 448.0
 def listed():
     return [
         # the smallest layer for one token: nothing but the latency of a call
-        dict(op="quant", name="quant 1024x1024, 1 token", M=1024, K=1024, N=1, group=128, zeros=False, type="f16"),
+        dict(op="quant", name="quant 1024x1024 x 1 token", M=1024, K=1024, N=1, group=128, zeros=False, type="f16"),
         # OPT-30B MLP1 for a small batch of decoding sequences
-        dict(op="quant", name="quant 28672x7168, 16 tokens", M=28672, K=7168, N=16, group=128, zeros=False, type="f16"),
+        dict(op="quant", name="quant 28672x7168 x 16 tokens", M=28672, K=7168, N=16, group=128, zeros=False, type="f16"),
         # OPT-175B MLP2 for a full batch, with zero points: the most bytes
-        dict(op="quant", name="quant 12288x49152, 64 tokens", M=12288, K=49152, N=64, group=128, zeros=True, type="f16"),
+        dict(op="quant", name="quant 12288x49152 x 64 tokens", M=12288, K=49152, N=64, group=128, zeros=True, type="f16"),
         # sizes that are multiples of nothing, short groups, the other type
-        dict(op="quant", name="quant 5003x4099, 5 tokens", M=5003, K=4099, N=5, group=32, zeros=True, type="bf16"),
+        dict(op="quant", name="quant 5003x4099 x 5 tokens", M=5003, K=4099, N=5, group=32, zeros=True, type="bf16"),
         # one decoding step of 64 sequences: 64 tokens, each to a page of its own
-        dict(op="write", name="write 64 tokens, 96 heads", T=64, heads=96, dim=128, page=16, skip=False, type="f16"),
+        dict(op="write", name="write 64 tokens x 96 heads", T=64, heads=96, dim=128, page=16, skip=False, type="f16"),
         # a long prompt's keys and values, padding tokens among them
-        dict(op="write", name="write 4095 tokens, 56 heads", T=4095, heads=56, dim=128, page=64, skip=True, type="bf16"),
+        dict(op="write", name="write 4095 tokens x 56 heads", T=4095, heads=56, dim=128, page=64, skip=True, type="bf16"),
         # a sequence's cache read back whole, as when it moves or is recomputed from
-        dict(op="read", name="read 4096 tokens, 56 heads", T=4096, heads=56, dim=128, page=16, skip=False, type="f16"),
+        dict(op="read", name="read 4096 tokens x 56 heads", T=4096, heads=56, dim=128, page=16, skip=False, type="f16"),
         # a short prefix, heads of 80 channels
-        dict(op="read", name="read 333 tokens, 8 heads of 80", T=333, heads=8, dim=80, page=32, skip=True, type="bf16"),
+        dict(op="read", name="read 333 tokens x 8 heads of 80", T=333, heads=8, dim=80, page=32, skip=True, type="bf16"),
         # one sequence that decodes: latency, and one short axis to split
         dict(op="attend", name="attend 1 token over 1000", S=1, q=1, q_low=1, len=1000, len_low=1000, heads=32, kv=8,
              dim=128, page=16, cache="f16", type="f16", window=0),
