@@ -381,6 +381,104 @@ lscd_status_t lscd_destroy(lscd_handle_t h);
 /* lscd_status_string -- static text for a status code. */
 const char* lscd_status_string(lscd_status_t s);
 
+/* ====================================================================================
+ * Serving operators: what stands next to the skinny products in a decoder layer.
+ * Types of activations, weights' scales and cached values.
+ * ==================================================================================== */
+typedef enum {
+    LSCD_F16 = 0,
+    LSCD_BF16 = 1,
+    LSCD_E4M3 = 2  /* 8-bit floating point, 4 significant bits, largest value 448, no infinities */
+} lscd_type_t;
+
+/*
+ * Paged cache of keys and values, in device memory of the caller.
+ *   k, v  [num_pages][heads][page_size][head_dim] values of `type`, 16-byte aligned.
+ *   k_scale, v_scale  LSCD_E4M3 only (NULL otherwise): [num_pages][heads][page_size] floats,
+ *         16-byte aligned; a value is its code times its token's and head's scale.  Scales are
+ *         positive powers of two (what lscd_cache_write writes; readers use the exponent only).
+ *   page_size  a power of two, 16..1024.   head_dim  a multiple of 16, 16..256.
+ *   heads  1..65535.  num_pages * page_size <= 2^31 - 1 (slots are 32-bit numbers; element
+ *         offsets are 64-bit throughout).
+ * Slot s is row s % page_size of page s / page_size.  The struct is read during the call only.
+ */
+typedef struct {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t num_pages;
+    int32_t heads, page_size, head_dim;
+    int32_t type;  /* lscd_type_t */
+} lscd_cache_t;
+
+/*
+ * lscd_cache_write -- put T tokens' keys and values into slots of the cache, on `stream`.
+ *   k, v   device, T rows of heads * head_dim values of `type` (LSCD_F16 or LSCD_BF16), 16-byte
+ *          aligned; k_stride, v_stride elements (a multiple of 8) from one token to the next, so
+ *          that slices of a fused product's output can be passed.
+ *   slots  device, T slot numbers.  A token whose number is negative or past the cache is not
+ *          written (padding).  Two tokens in one slot leave either's values, head by head.
+ *   E4M3:  per token and head, scale = 2^e with the least e >= -126 such that max |x| <= 448 * 2^e
+ *          over the finite values (1 where all are zero), code = x / 2^e rounded to the nearest
+ *          e4m3 value, ties to even: the only rounding.  Infinities and NaN are stored as NaN.
+ *   16 bits: copied; `type` has to be the cache's (NOT_SUPPORTED otherwise).
+ * T = 0 is a no-op.  Asynchronous, no allocation.
+ */
+lscd_status_t lscd_cache_write(const lscd_cache_t* cache, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const int32_t* slots, int64_t T, int32_t type, void* stream);
+
+/*
+ * lscd_cache_read -- the values in T slots as rows of `type`: the reverse of lscd_cache_write
+ * (code times scale, exact unless it leaves the type's normal range).  A slot number that is
+ * negative or past the cache gives zeros.  Same argument rules; any slot may be read any number of
+ * times.
+ */
+lscd_status_t lscd_cache_read(const lscd_cache_t* cache, const int32_t* slots, int64_t T, void* k, int64_t k_stride,
+                              void* v, int64_t v_stride, int32_t type, void* stream);
+
+/*
+ * Attention of new tokens over a paged cache: one call serves a batch of sequences, each with any
+ * number of new tokens -- none, one (decoding) or a chunk of a prompt.
+ *
+ * lscd_attention_create -- a handle for q_heads query heads over kv_heads key heads (q_heads a
+ *   multiple of kv_heads, q_heads <= 65535: query head h reads key head h / (q_heads / kv_heads))
+ *   of head_dim channels, on the current device.  It owns the workspace for work that is split
+ *   over workgroups, of a size that depends on the GPU and head_dim only; layers can share it as
+ *   long as its calls do not overlap (one stream at a time).  Synchronous.
+ */
+typedef struct lscd_attention_s* lscd_attention_t;
+lscd_status_t lscd_attention_create(int32_t q_heads, int32_t kv_heads, int32_t head_dim, lscd_attention_t* out);
+lscd_status_t lscd_attention_destroy(lscd_attention_t h);
+
+/*
+ * lscd_attention -- on `stream`, for every sequence s and its new tokens start[s] .. start[s+1]-1:
+ *   o = softmax(scale * q . k) v over the cached positions that the token sees.  The sequence has
+ *   length[s] positions in the cache, its new tokens (written before) the last of them: token i of
+ *   n stands at p = length[s] - n + i.  It sees the positions j < length[s] with j <= p (causal) and
+ *   j > p - window (window > 0).  A token that sees none gets zeros.  What is not seen has no
+ *   effect, whatever it holds.
+ *   q, o    device, T rows of q_heads * head_dim values of `type`, 16-byte aligned; q_stride,
+ *           o_stride elements (a multiple of 8) from one token to the next.  o may not overlap q.
+ *   start   device, sequences + 1 ascending numbers, from 0 to T.
+ *   length  device, one number for each sequence.
+ *   table   device; page j of sequence s is table[s * table_stride + j], table_pages of them.
+ *   cache   of the handle's heads and head_dim; of `type` or LSCD_E4M3.
+ * Lengths stay on the device: the call neither waits nor copies, and can be captured into a graph
+ * and replayed with other lengths.  Array contents outside these rules are clamped (tokens to T,
+ * lengths to the table, pages to the pool), so that no call reads or writes out of bounds.
+ * Scores, softmax and sums are fp32; the softmax weights are rounded once to `type` for the second
+ * product.  Results do not depend on timing (partial sums are added in a fixed order) but their
+ * last bits may depend on the other sequences in the call, which move the points where work is split.
+ * INVALID_VALUE: null pointers, misalignment, negative sizes, a scale that is not finite, wrong
+ * device.  NOT_SUPPORTED: T * (q_heads / kv_heads) or table_pages * page_size above 2^30, types
+ * that do not fit together.
+ */
+lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, const void* q, int64_t q_stride,
+                             const int32_t* start, const int32_t* length, const int32_t* table, int64_t table_stride,
+                             int32_t table_pages, int32_t sequences, int64_t T, float scale, int32_t causal,
+                             int32_t window, void* o, int64_t o_stride, int32_t type, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,7 +38,14 @@ EXPORTS = ("lscd_pack_size", "lscd_pack", "lscd_default_tile_m", "lscd_encode", 
            "lscd_import", "lscd_export",
            "lscd_get_info", "lscd_spmm", "lscd_debug_decode", "lscd_attach_dense", "lscd_linear",
            "lscd_linear_path", "lscd_set_linear_crossover", "lscd_linear_model", "lscd_tune_dense", "lscd_destroy",
-           "lscd_status_string", "lscd_stream_read", "lscd_spmm_noalloc", "lscd_linear_times")
+           "lscd_status_string", "lscd_stream_read", "lscd_spmm_noalloc", "lscd_linear_times",
+           "lscd_cache_write", "lscd_cache_read",
+           "lscd_attention_create", "lscd_attention", "lscd_attention_destroy")
+
+LSCD_F16 = 0
+LSCD_BF16 = 1
+LSCD_E4M3 = 2
+_TYPES = {torch.float16: LSCD_F16, torch.bfloat16: LSCD_BF16, torch.float8_e4m3fn: LSCD_E4M3}
 
 
 class lscd_info_t(ctypes.Structure):
@@ -50,6 +57,12 @@ class lscd_info_t(ctypes.Structure):
                 ("splits", ctypes.c_int32 * 3), ("variant", ctypes.c_int32 * 3),
                 ("splits_wide", ctypes.c_int32 * 3), ("reg_vectors_wide", ctypes.c_int32),
                 ("format", ctypes.c_int32)]
+
+
+class lscd_cache_t(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
 
 
 class LSCDError(RuntimeError):
@@ -92,6 +105,11 @@ def _load():
         "lscd_stream_read": [VP, I64, I32, VP, VP],
         "lscd_linear_times": [VP, I32, P(ctypes.c_double), P(ctypes.c_double), P(I32)],
         "lscd_spmm_noalloc": [VP, VP, VP, I32, VP],
+        "lscd_cache_write": [VP, VP, I64, VP, I64, VP, I64, I32, VP],
+        "lscd_cache_read": [VP, VP, I64, VP, I64, VP, I64, I32, VP],
+        "lscd_attention_create": [I32, I32, I32, P(VP)],
+        "lscd_attention_destroy": [VP],
+        "lscd_attention": [VP, VP, VP, I64, VP, VP, VP, I64, I32, I32, I64, ctypes.c_float, I32, I32, VP, I64, I32, VP],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -383,4 +401,121 @@ def lscd_stream_read(src, nbytes: int, blocks_per_cu: int, sink, stream=None):
 
 
 def lscd_destroy(h: Handle):
+    h.close()
+
+
+# ---------------------------------------------------------------- serving operators
+
+
+class Cache:
+    """A paged cache over the caller's tensors (lscd_cache_t): k, v [pages][heads][page_size][head_dim] in
+    float16, bfloat16 or float8_e4m3fn; the last with k_scale, v_scale float32 [pages][heads][page_size]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        scaled = k.dtype == torch.float8_e4m3fn
+        if k.dtype not in _TYPES or v.dtype != k.dtype or k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must be tensors of one type and shape [pages][heads][page_size][head_dim]")
+        if scaled != (k_scale is not None) or scaled != (v_scale is not None):
+            raise ValueError("k_scale and v_scale go with float8_e4m3fn keys and values")
+        for t in (k_scale, v_scale) if scaled else ():
+            if t.dtype != torch.float32 or tuple(t.shape) != tuple(k.shape[:3]):
+                raise ValueError("scales must be float32 [pages][heads][page_size]")
+        self.tensors = (k, v, k_scale, v_scale)
+        for t in self.tensors:
+            if t is not None and not (t.is_cuda and t.is_contiguous() and t.device == k.device):
+                raise ValueError("the cache's tensors must be contiguous and on one CUDA device")
+        pages, self.heads, page_size, self.head_dim = k.shape
+        self.dtype, self.device = k.dtype, k.device
+        self.struct = lscd_cache_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if scaled else None,
+                                   v_scale.data_ptr() if scaled else None, pages, self.heads, page_size, self.head_dim,
+                                   _TYPES[k.dtype])
+        self.ptr = ctypes.addressof(self.struct)
+
+
+def _rows(t, name, heads, dim, device):
+    """(pointer, elements from row to row) of a [T][heads][dim] tensor whose rows are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens][{heads}][{dim}] on the cache's device")
+    if stride[2] != 1 or (stride[1] != dim and heads != 1):
+        raise ValueError(f"the heads of one token of {name} must be contiguous")
+    return t.data_ptr(), (stride[0] if shape[0] > 1 else heads * dim)
+
+
+def _ints(t, name, device, dim=1):
+    if t.dtype != torch.int32 or t.dim() != dim or t.device != device or (t.numel() and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be an int32 tensor of {dim} dimension(s) on the cache's device, last one contiguous")
+    return t.data_ptr()
+
+
+def _same_type(a, b, name):
+    if a.dtype != b.dtype or a.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name} must both be float16 or both be bfloat16")
+    return _TYPES[a.dtype]
+
+
+def lscd_cache_write(cache: Cache, k, v, slots, stream=None):
+    """Write the tokens' keys and values (k, v [T][heads][head_dim]) into slots (int32 [T]; negative: none)."""
+    pk, sk = _rows(k, "k", cache.heads, cache.head_dim, cache.device)
+    pv, sv = _rows(v, "v", cache.heads, cache.head_dim, cache.device)
+    T = slots.shape[0]
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("k, v and slots must have one number of tokens")
+    _check(_lib.lscd_cache_write(cache.ptr, pk, sk, pv, sv, _ints(slots, "slots", cache.device), T,
+                                 _same_type(k, v, "k and v"), _stream(stream)), "lscd_cache_write")
+
+
+def lscd_cache_read(cache: Cache, slots, k, v, stream=None):
+    """Read the slots' keys and values back into k, v [T][heads][head_dim] (zeros where a slot is negative)."""
+    pk, sk = _rows(k, "k", cache.heads, cache.head_dim, cache.device)
+    pv, sv = _rows(v, "v", cache.heads, cache.head_dim, cache.device)
+    T = slots.shape[0]
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("k, v and slots must have one number of tokens")
+    _check(_lib.lscd_cache_read(cache.ptr, _ints(slots, "slots", cache.device), T, pk, sk, pv, sv,
+                                _same_type(k, v, "k and v"), _stream(stream)), "lscd_cache_read")
+    return k, v
+
+
+class Attention:
+    """Owner of an lscd_attention_t; freed by lscd_attention_destroy (or when collected)."""
+
+    def __init__(self, ptr: int, q_heads: int, kv_heads: int, head_dim: int):
+        self.ptr, self.q_heads, self.kv_heads, self.head_dim = ptr, q_heads, kv_heads, head_dim
+
+    def __del__(self):
+        self.close()
+
+    def close(self):
+        if getattr(self, "ptr", None) and _lib is not None:
+            _lib.lscd_attention_destroy(self.ptr)
+            self.ptr = None
+
+
+def lscd_attention_create(q_heads: int, kv_heads: int, head_dim: int) -> Attention:
+    h = ctypes.c_void_p()
+    _check(_lib.lscd_attention_create(q_heads, kv_heads, head_dim, ctypes.byref(h)), "lscd_attention_create")
+    return Attention(h.value, q_heads, kv_heads, head_dim)
+
+
+def lscd_attention(h: Attention, cache: Cache, q, start, length, table, out, scale=None, causal=True, window=0,
+                   stream=None):
+    """Attention of the new tokens q [T][q_heads][head_dim] of a batch of sequences over their cached positions:
+    sequence s has the tokens start[s] .. start[s + 1] - 1 (int32) as the last of its length[s] positions, which lie
+    in the pages table[s] (int32 [sequences][pages]).  scale defaults to head_dim ** -0.5."""
+    pq, sq = _rows(q, "q", h.q_heads, h.head_dim, cache.device)
+    po, so = _rows(out, "out", h.q_heads, h.head_dim, cache.device)
+    S, T = length.shape[0], q.shape[0]
+    if start.shape[0] != S + 1 or table.shape[0] != S or out.shape[0] != T:
+        raise ValueError("start must have one entry more than length, table as many rows, out as many tokens as q")
+    dev = cache.device
+    pt = _ints(table, "table", dev, 2)
+    _check(_lib.lscd_attention(h.ptr, cache.ptr, pq, sq, _ints(start, "start", dev), _ints(length, "length", dev), pt,
+                               table.stride(0) if S > 1 else table.shape[1], table.shape[1], S, T,
+                               h.head_dim ** -0.5 if scale is None else scale, causal, window, po, so,
+                               _same_type(q, out, "q and out"), _stream(stream)), "lscd_attention")
+    return out
+
+
+def lscd_attention_destroy(h: Attention):
     h.close()

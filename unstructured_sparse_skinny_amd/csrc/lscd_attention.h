@@ -1,0 +1,175 @@
+// Attention of new tokens over a paged cache: what its two kernels share.
+//
+// For query row r (token i of a sequence's n new ones, one of the heads that share a key head):
+//   o_r = sum_j exp(s_rj - m_r) v_j / sum_j exp(s_rj - m_r),  s_rj = scale * q_r . k_j,
+// over the positions j that the row sees: j <= length - n + i (causal) or j < length, and
+// j > that - window.  One pass over the keys and values with a running maximum m and running sums;
+// scores are kept in units of log2, so that exp is one v_exp_f32.  A row that sees nothing is zero.
+//
+// Both kernels compute S^T = K Q^T and O^T = V^T P^T on the matrix cores.  In that orientation a
+// lane holds scores of one query row only, so maximum, sum and rescaling are (nearly) lane-local,
+// and the scores of a lane are, after rounding to 16 bits, already the B operand of the second
+// product: its k index may run over the tokens in any order as long as V^T uses the same one.
+// The maximum is moved only when some score exceeds it by 8 (a factor 256, far inside 16-bit
+// range for P and fp32 for the sums): most tiles then skip the exchange and the rescaling.
+// Sums, maxima and the output accumulate in fp32; P is rounded once to the model's 16-bit type,
+// whose relative step is that of the values it multiplies.
+//
+// Work is split over all sequences, key heads, row tiles and cached positions at once: the units
+// (one row tile x one stretch of positions) are numbered in that order and cut into equal ranges,
+// one per workgroup, wherever the cuts fall; an item (row tile) cut by a range's end leaves partial
+// results, and the last workgroup to arrive adds them in ascending order, so that results do not
+// depend on who arrives when.  Ragged batches, one long sequence and many short ones all balance,
+// and one launch does it.  Lengths are read on the device: no host copy, no plan.
+#pragma once
+
+#include "lscd_serve.h"
+#include "lscd_serve_device.h"
+
+namespace lscd {
+namespace {
+
+constexpr float kNoScore = -1e30f;  // maximum before any score: finite, so that differences stay defined
+constexpr float kLazy = 8.f;
+
+// The rows and positions of one sequence.
+struct Seq {
+    int first;      // its first row in q
+    int n, len;     // new tokens; cached positions, new ones among them
+    int rows;       // n * share
+};
+
+// Reads are clamped to what the arguments allow, whatever the arrays hold.
+__device__ __forceinline__ Seq read_seq(const AttnArgs& a, int s) {
+    Seq q;
+    const int64_t b0 = min(max((int64_t)a.start[s], (int64_t)0), a.T);
+    const int64_t b1 = min(max((int64_t)a.start[s + 1], b0), a.T);
+    q.first = (int)b0;
+    q.n = (int)(b1 - b0);
+    q.len = min(max((int64_t)a.length[s], (int64_t)0), (int64_t)a.table_pages << a.page_log2);
+    q.rows = q.n * a.share;
+    return q;
+}
+
+// Positions [low, high) that some row of tile `t` (ROWS rows) sees.
+template <int ROWS>
+__device__ __forceinline__ void tile_range(const AttnArgs& a, const Seq& q, int t, int* low, int* high) {
+    const int i0 = t * ROWS / a.share, i1 = (min(q.rows, (t + 1) * ROWS) - 1) / a.share;
+    const int p0 = q.len - q.n + i0, p1 = q.len - q.n + i1;
+    *high = a.causal ? min(max(p1 + 1, 0), q.len) : q.len;
+    *low = a.window ? min(max(p0 - a.window + 1, 0), *high) : 0;
+}
+template <int ROWS, int TOKENS>
+__device__ __forceinline__ int tile_units(const AttnArgs& a, const Seq& q, int t) {
+    int low, high;
+    tile_range<ROWS>(a, q, t, &low, &high);
+    return max(1, (high + TOKENS - 1) / TOKENS - low / TOKENS);
+}
+// Units of one key head of the sequence; 0 if it belongs to the other kernel.
+template <int ROWS, int TOKENS, bool FEW>
+__device__ __forceinline__ int head_units(const AttnArgs& a, const Seq& q) {
+    if (q.rows == 0 || (q.rows <= a.few_limit) != FEW) return 0;
+    int u = 0;
+    for (int t = 0; t * ROWS < q.rows; ++t) u += tile_units<ROWS, TOKENS>(a, q, t);
+    return u;
+}
+
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// Where a range of units begins: sequence, key head, row tile, unit inside the tile.
+struct Place {
+    int seq, head, tile, unit;
+    int per_head;
+};
+
+// Total units, and the sequence that holds unit `u` with the units before it; every wavefront
+// works it out for itself (64 sequences at a time).
+template <int ROWS, int TOKENS, bool FEW>
+__device__ __forceinline__ int64_t total_units(const AttnArgs& a, int lane) {
+    int64_t total = 0;
+    for (int s0 = 0; s0 < a.sequences; s0 += 64) {
+        int64_t mine = 0;
+        if (s0 + lane < a.sequences)
+            mine = (int64_t)head_units<ROWS, TOKENS, FEW>(a, read_seq(a, s0 + lane)) * a.c.heads;
+        for (int d = 1; d < 64; d <<= 1) mine += __shfl_xor(mine, d, 64);
+        total += mine;
+    }
+    return uniform(total);
+}
+template <int ROWS, int TOKENS, bool FEW>
+__device__ __forceinline__ Place find_unit(const AttnArgs& a, int64_t u, int lane) {
+    Place p = {};
+    int64_t before = 0;
+    for (int s0 = 0; s0 < a.sequences; s0 += 64) {
+        int per = 0;
+        if (s0 + lane < a.sequences) per = head_units<ROWS, TOKENS, FEW>(a, read_seq(a, s0 + lane));
+        int64_t sum = (int64_t)per * a.c.heads;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int64_t up = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += up;
+        }
+        const uint64_t past = __ballot(before + sum > u);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            p.seq = s0 + l;
+            p.per_head = __builtin_amdgcn_readlane(per, l);
+            const int64_t start = before + __shfl(sum, l, 64) - (int64_t)p.per_head * a.c.heads;
+            const int rest = (int)(u - start);
+            p.head = rest / p.per_head;
+            p.unit = rest % p.per_head;
+            break;
+        }
+        before += __shfl(sum, 63, 64);
+    }
+    p.seq = __builtin_amdgcn_readfirstlane(p.seq);
+    p.head = __builtin_amdgcn_readfirstlane(p.head);
+    p.unit = __builtin_amdgcn_readfirstlane(p.unit);
+    p.per_head = __builtin_amdgcn_readfirstlane(p.per_head);
+    const Seq q = read_seq(a, p.seq);
+    for (p.tile = 0; (p.tile + 1) * ROWS < q.rows; ++p.tile) {
+        const int n = tile_units<ROWS, TOKENS>(a, q, p.tile);
+        if (p.unit < n) break;
+        p.unit -= n;
+    }
+    return p;
+}
+
+// The cut of U units into G ranges whose sizes differ by at most one.
+struct Cut {
+    int64_t base, extra;
+    __device__ __forceinline__ Cut(int64_t U, int G) : base(U / G), extra(U % G) {}
+    __device__ __forceinline__ int64_t begin(int w) const { return w * base + (w < extra ? w : extra); }
+    __device__ __forceinline__ int owner(int64_t u) const {
+        const int64_t big = extra * (base + 1);
+        return (int)(u < big ? u / (base + 1) : extra + (u - big) / base);
+    }
+};
+
+// The page that holds position t (clamped to the pool: an entry outside it is read as page 0).
+__device__ __forceinline__ int64_t page_of(const AttnArgs& a, int seq, int t) {
+    const int i = min(t >> a.page_log2, a.table_pages - 1);
+    const int64_t p = a.table[seq * a.table_stride + i];
+    return p >= 0 && p < a.c.num_pages ? p : 0;
+}
+
+// A partial result is complete in memory before its arrival is counted; the last to arrive sees
+// all of them.  Returns whether this workgroup is the last of `expected`, and clears the count.
+__device__ __forceinline__ bool arrive_last(uint32_t* count, uint32_t expected, uint32_t* shared) {
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        *shared = before + 1 == expected;
+        if (before + 1 == expected) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    const bool last = *shared != 0;
+    if (last) __threadfence();
+    return last;
+}
+
+}  // namespace
+}  // namespace lscd

@@ -1,0 +1,400 @@
+// Attention over a paged cache for few query rows (decoding): up to 16 rows (tokens x heads that
+// share a key head) per item, memory-bound: every key and value is read once, straight into
+// registers.
+//
+// A workgroup is four wavefronts; each takes 32 of a unit's 128 positions with a running maximum
+// and sums of its own, joined through LDS where an item ends.  Per 32 positions a wavefront needs
+// no LDS at all: the key rows are the A operand as they lie in memory (16 bytes of 64 channels per
+// lane), and the values become the A operand V^T by an in-register transposition: lane l loads the
+// same 8 channels of 8 tokens, and one v_perm_b32 per pair of values puts two tokens into one word
+// (half an instruction per value; an LDS transposition would cost a write and a read).  The loads
+// of the next unit's keys are issued when the scores are done with this one's, the next values
+// when the second product is, so that 8 to 16 KB per wavefront are always in flight.
+
+#include "lscd_attention.h"
+
+namespace lscd {
+namespace {
+
+constexpr int kFewWaves = 4;
+
+// DP: channels padded to 64, 128 or 256.
+template <typename T, bool E4M3, int DP>
+struct Few {
+    static constexpr int kSteps = DP / 32;  // MFMA steps over the channels of q . k
+    static constexpr int VW = DP / 16;      // channels per lane of a value row
+    static constexpr int kKeyRegs = E4M3 ? DP / 16 : DP / 8;        // words of one 16-token key tile per lane
+    static constexpr int kValWords = E4M3 ? VW / 4 : VW / 2;        // words of one value row per lane
+    uint32_t kr[2][kKeyRegs];
+    uint32_t vr[8][kValWords];
+    float ks[2], vs[8];
+
+    // 32 positions from t0 on; `high`: the first position that nobody sees.
+    __device__ __forceinline__ void load_keys(const AttnArgs& a, int seq, int head, int t0, int high, int lane) {
+        const int D = a.c.head_dim;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = t0 + 16 * h, row = (t & (a.c.page_size - 1)) + (lane & 15);
+            const int64_t tile = page_of(a, seq, t) * a.c.heads + head;
+            const bool on = t + (lane & 15) < high;
+            if (E4M3) {
+                const auto rs = buffer_of((const uint8_t*)a.c.k + tile * a.c.page_size * D, a.c.page_size * D);
+#pragma unroll
+                for (int u = 0; u < DP / 64; ++u) {
+                    const int d = 64 * u + 16 * (lane >> 4);
+                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? row * D + d : kNoRow, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
+                }
+                const auto ss = buffer_of(a.c.k_scale + tile * a.c.page_size, a.c.page_size * 4);
+                ks[h] = as_float(__builtin_amdgcn_raw_buffer_load_b32(ss, on ? row * 4 : kNoRow, 0, 0));
+            } else {
+                const auto rs = buffer_of((const uint16_t*)a.c.k + tile * a.c.page_size * D, a.c.page_size * D * 2);
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    const int d = 32 * s + 8 * (lane >> 4);
+                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? (row * D + d) * 2 : kNoRow, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kr[h][4 * s + i] = x[i];
+                }
+            }
+        }
+    }
+
+    // Value rows of lane group g: positions 4g .. 4g+3 of each of the two 16-position halves.
+    __device__ __forceinline__ void load_values(const AttnArgs& a, int seq, int head, int t0, int low, int high, int lane) {
+        const int D = a.c.head_dim, g = lane >> 4, d = VW * (lane & 15);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int t = t0 + 16 * h, r0 = (t & (a.c.page_size - 1)) + 4 * g;
+            const int64_t tile = page_of(a, seq, t) * a.c.heads + head;
+            if (E4M3) {
+                const auto rs = buffer_of((const uint8_t*)a.c.v + tile * a.c.page_size * D, a.c.page_size * D);
+                const auto ss = buffer_of(a.c.v_scale + tile * a.c.page_size, a.c.page_size * 4);
+                const u32x4v sc = __builtin_amdgcn_raw_buffer_load_b128(ss, r0 * 4, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int p = t + 4 * g + j;
+                    const bool on = p < high && p >= low;
+                    vs[4 * h + j] = on ? as_float(sc[j]) : 1.f;
+#pragma unroll
+                    for (int w = 0; w < kValWords; w += 2) {  // 8 channels at a time (4 where a row has 64)
+                        const int off = on && d + 4 * w < D ? (r0 + j) * D + d + 4 * w : kNoRow;
+                        if constexpr (kValWords == 1) {
+                            vr[4 * h + j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
+                        } else {
+                            const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
+                            vr[4 * h + j][w] = x[0];
+                            vr[4 * h + j][w + 1] = x[1];
+                        }
+                    }
+                }
+            } else {
+                const auto rs = buffer_of((const uint16_t*)a.c.v + tile * a.c.page_size * D, a.c.page_size * D * 2);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int p = t + 4 * g + j;
+                    const bool on = p < high && p >= low;
+                    if constexpr (kValWords == 2) {
+                        const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, on && d < D ? ((r0 + j) * D + d) * 2 : kNoRow, 0, 0);
+                        vr[4 * h + j][0] = x[0];
+                        vr[4 * h + j][1] = x[1];
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < kValWords; w += 4) {
+                            const int off = on && d + 2 * w < D ? ((r0 + j) * D + d + 2 * w) * 2 : kNoRow;
+                            const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) vr[4 * h + j][w + i] = x[i];
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // The A operand of key half h, step s, in 16 bits.
+    __device__ __forceinline__ u32x4v key_operand(int h, int s) const {
+        u32x4v x;
+        if (E4M3) {  // two words of codes per step: channels 16 g + 8 (s % 2) of the 64 of step s / 2
+            const uint32_t lo = kr[h][4 * (s / 2) + 2 * (s % 2)], hi = kr[h][4 * (s / 2) + 2 * (s % 2) + 1];
+            x[0] = T::template from_e4m3<false>(lo, ks[h]);
+            x[1] = T::template from_e4m3<true>(lo, ks[h]);
+            x[2] = T::template from_e4m3<false>(hi, ks[h]);
+            x[3] = T::template from_e4m3<true>(hi, ks[h]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = kr[h][4 * s + i];
+        }
+        return x;
+    }
+    // The channel that step s, lane group g begins with (the q operand uses the same order).
+    __device__ static __forceinline__ int step_channel(int s, int g) {
+        return E4M3 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+    }
+    // Word of channels 2w, 2w+1 of value row j in 16 bits.
+    __device__ __forceinline__ uint32_t value_word(int j, int w) const {
+        if (E4M3) return w % 2 ? T::template from_e4m3<true>(vr[j][w / 2], vs[j]) : T::template from_e4m3<false>(vr[j][w / 2], vs[j]);
+        return vr[j][w];
+    }
+};
+
+template <typename T, bool E4M3, int DP>
+__global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs a) {
+    using F = Few<T, E4M3, DP>;
+    constexpr int VW = F::VW;
+    __shared__ float sh_o[kFewWaves][kFewRows][DP];
+    __shared__ float sh_m[kFewWaves][kFewRows], sh_l[kFewWaves][kFewRows];
+    __shared__ uint32_t sh_last;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int G = gridDim.x, me = blockIdx.x;
+    const int64_t U = total_units<kFewRows, kFewTokens, true>(a, lane);
+    if (U == 0) return;
+    const Cut cut(U, G);
+    int64_t u = cut.begin(me);
+    const int64_t end = cut.begin(me + 1);
+    if (u >= end) return;
+    Place p = find_unit<kFewRows, kFewTokens, true>(a, u, lane);
+    Seq q = read_seq(a, p.seq);
+    const int D = a.c.head_dim;
+
+    while (u < end) {
+        // One item, or the part of it that lies in this range: row tile p.tile, units [p.unit, last).
+        int low, high;
+        tile_range<kFewRows>(a, q, p.tile, &low, &high);
+        const int units = max(1, (high + kFewTokens - 1) / kFewTokens - low / kFewTokens);
+        const int64_t item = u - p.unit;  // the item's first unit
+        const int last = (int)min((int64_t)units, p.unit + (end - u));
+        const int t_base = low / kFewTokens * kFewTokens;
+
+        // Query rows: the B operand, and what each row sees.
+        const int row = p.tile * kFewRows + (lane & 15);
+        const bool live = row < q.rows;
+        const int token = row / a.share;
+        const int qh = p.head * a.share + row % a.share;
+        const uint16_t* qp = (const uint16_t*)a.q + (int64_t)(q.first + (live ? token : 0)) * a.q_stride + (int64_t)qh * D;
+        u32x4v qr[F::kSteps];
+#pragma unroll
+        for (int s = 0; s < F::kSteps; ++s) {
+            const int d = F::step_channel(s, lane >> 4);
+            qr[s] = u32x4v{0u, 0u, 0u, 0u};
+            if (live && d < D) qr[s] = *(const u32x4v*)(qp + d);
+        }
+        const int pos = q.len - q.n + token;
+        const int see_high = live ? (a.causal ? min(pos + 1, q.len) : q.len) : 0;
+        const int see_low = a.window ? pos - a.window + 1 : 0;
+        // every row sees positions [all_low, all_high): no masks there
+        const int tok0 = p.tile * kFewRows / a.share, tok1 = (min(q.rows, (p.tile + 1) * kFewRows) - 1) / a.share;
+        const int all_high = a.causal ? min(q.len - q.n + tok0 + 1, q.len) : q.len;
+        const int all_low = a.window ? q.len - q.n + tok1 - a.window + 1 : 0;
+
+        float m = kNoScore, l = 0.f;
+        f32x4v o[VW];
+#pragma unroll
+        for (int i = 0; i < VW; ++i) o[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
+
+        F f;
+        int t0 = t_base + p.unit * kFewTokens + 32 * wave;
+        f.load_keys(a, p.seq, p.head, t0, high, lane);
+        f.load_values(a, p.seq, p.head, t0, low, high, lane);
+        for (int k = p.unit; k < last; ++k, t0 += kFewTokens) {
+            f32x4v s[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s[h] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(f.key_operand(h, st), qr[st], s[h]);
+            }
+            if (k + 1 < last) f.load_keys(a, p.seq, p.head, t0 + kFewTokens, high, lane);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = s[i / 4][i % 4] * a.scale_log2;
+            const bool masked = t0 < all_low || t0 + 32 > all_high;
+            if (masked) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int t = t0 + 16 * (i / 4) + 4 * (lane >> 4) + i % 4;
+                    if (t >= see_high || t < see_low) x[i] = -__builtin_inff();
+                }
+            }
+            float most = x[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) most = fmaxf(most, x[i]);
+            if (__any(most > m + kLazy)) {
+                const float to = fmaxf(m, max_quarters(most));
+                const float by = exp2_fast(m - to);
+                m = to;
+                l *= by;
+#pragma unroll
+                for (int i = 0; i < VW; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) o[i][r] *= by;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = exp2_fast(x[i] - m);
+                l += x[i];
+            }
+            u32x4v pb;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) pb[i] = T::pack(x[2 * i], x[2 * i + 1]);
+            bool odd = false;  // an infinity or NaN that some row must not see
+#pragma unroll
+            for (int w = 0; w < VW / 2; ++w) {
+                uint32_t v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = f.value_word(j, w);
+                if (masked)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) odd |= T::odd(v[j]);
+                u32x4v a0, a1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a0[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x05040100u);
+                    a1[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07060302u);
+                }
+                if (!(masked && __any(odd))) {
+                    o[2 * w] = T::mfma16(a0, pb, o[2 * w]);
+                    o[2 * w + 1] = T::mfma16(a1, pb, o[2 * w + 1]);
+                } else {
+                    // 0 * infinity would be NaN in rows that do not see the token: what is finite as
+                    // ever, the rest one token at a time and added only where it is seen
+                    u32x4v f0, f1;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f0[i] = T::finite(a0[i]);
+                        f1[i] = T::finite(a1[i]);
+                        a0[i] ^= f0[i];
+                        a1[i] ^= f1[i];
+                    }
+                    o[2 * w] = T::mfma16(f0, pb, o[2 * w]);
+                    o[2 * w + 1] = T::mfma16(f1, pb, o[2 * w + 1]);
+                    for (int j = 0; j < 32; ++j) {
+                        const int t = t0 + 16 * ((j & 7) / 4) + 4 * (j >> 3) + (j & 3);
+                        const bool mine = (lane >> 4) == (j >> 3);
+                        u32x4v b0, b1;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t keep = mine && (j & 7) / 2 == i ? ((j & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+                            b0[i] = a0[i] & keep;
+                            b1[i] = a1[i] & keep;
+                        }
+                        const f32x4v z = {0.f, 0.f, 0.f, 0.f};
+                        const f32x4v y0 = T::mfma16(b0, pb, z), y1 = T::mfma16(b1, pb, z);
+                        if (t < see_high && t >= see_low) {
+                            o[2 * w] += y0;
+                            o[2 * w + 1] += y1;
+                        }
+                    }
+                }
+            }
+            if (k + 1 < last) f.load_values(a, p.seq, p.head, t0 + kFewTokens, low, high, lane);
+        }
+        l = sum_quarters(l);
+
+        // Join the four wavefronts.
+        __syncthreads();
+        if (lane < 16) {
+            sh_m[wave][lane] = m;
+            sh_l[wave][lane] = l;
+        }
+        if (live) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < VW; i += 4) {
+                    f32x4v x = {o[i][r], o[i + 1][r], o[i + 2][r], o[i + 3][r]};
+                    *(f32x4v*)&sh_o[wave][lane & 15][VW * (4 * (lane >> 4) + r) + i] = x;
+                }
+        }
+        __syncthreads();
+        const int rows = min(kFewRows, q.rows - p.tile * kFewRows);
+        const bool whole = p.unit == 0 && last == units;
+        const int owner = whole ? me : cut.owner(item), behind = whole ? me : cut.owner(item + units - 1);
+        constexpr int kFloats = kFewRows * (DP + 2);
+        float* mine = a.part + (int64_t)(2 * me + (p.unit == 0 ? 1 : 0)) * kFloats;
+        for (int i = threadIdx.x; i < rows * DP; i += 64 * kFewWaves) {
+            const int r = i / DP, d = i % DP;
+            float M = sh_m[0][r];
+#pragma unroll
+            for (int w = 1; w < kFewWaves; ++w) M = fmaxf(M, sh_m[w][r]);
+            float L = 0.f, O = 0.f;
+#pragma unroll
+            for (int w = 0; w < kFewWaves; ++w) {
+                const float by = exp2_fast(sh_m[w][r] - M);
+                L += by * sh_l[w][r];
+                O += by * sh_o[w][r][d];
+            }
+            if (whole) {
+                const int rw = p.tile * kFewRows + r;
+                if (d < D)
+                    ((uint16_t*)a.o)[(int64_t)(q.first + rw / a.share) * a.o_stride + (int64_t)(p.head * a.share + rw % a.share) * D + d] =
+                        (uint16_t)T::pack(L != 0.f ? O / L : 0.f, 0.f);
+            } else {
+                mine[2 * kFewRows + i] = O;
+                if (d == 0) {
+                    mine[r] = M;
+                    mine[kFewRows + r] = L;
+                }
+            }
+        }
+        if (!whole && arrive_last(a.count + owner, (uint32_t)(behind - owner + 1), &sh_last)) {
+            for (int i = threadIdx.x; i < rows * DP; i += 64 * kFewWaves) {
+                const int r = i / DP, d = i % DP;
+                const float* x = a.part + (int64_t)(2 * owner + 1) * kFloats;
+                float M = x[r], L = x[kFewRows + r], O = x[2 * kFewRows + i];
+                for (int w = owner + 1; w <= behind; ++w) {
+                    const float* y = a.part + (int64_t)(2 * w) * kFloats;
+                    const float to = fmaxf(M, y[r]), b0 = exp2_fast(M - to), b1 = exp2_fast(y[r] - to);
+                    M = to;
+                    L = L * b0 + y[kFewRows + r] * b1;
+                    O = O * b0 + y[2 * kFewRows + i] * b1;
+                }
+                const int rw = p.tile * kFewRows + r;
+                if (d < D)
+                    ((uint16_t*)a.o)[(int64_t)(q.first + rw / a.share) * a.o_stride + (int64_t)(p.head * a.share + rw % a.share) * D + d] =
+                        (uint16_t)T::pack(L != 0.f ? O / L : 0.f, 0.f);
+            }
+        }
+
+        // The next item.
+        u += last - p.unit;
+        if (u >= end) break;
+        p.unit = 0;
+        if ((++p.tile) * kFewRows >= q.rows) {
+            p.tile = 0;
+            if (++p.head == a.c.heads) {
+                p.head = 0;
+                do {
+                    ++p.seq;
+                    q = read_seq(a, p.seq);
+                } while (q.rows == 0 || q.rows > a.few_limit);
+            }
+        }
+    }
+}
+
+template <typename T, bool E4M3>
+hipError_t few_dim(const AttnArgs& a, int grid, hipStream_t s) {
+    const int D = a.c.head_dim;
+    if (D <= 64)
+        attention_few_kernel<T, E4M3, 64><<<grid, 64 * kFewWaves, 0, s>>>(a);
+    else if (D <= 128)
+        attention_few_kernel<T, E4M3, 128><<<grid, 64 * kFewWaves, 0, s>>>(a);
+    else
+        attention_few_kernel<T, E4M3, 256><<<grid, 64 * kFewWaves, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int attention_few_grid(int cus) { return 2 * cus; }
+int64_t attention_few_floats(int dim) { return kFewRows * ((dim <= 64 ? 64 : dim <= 128 ? 128 : 256) + 2); }
+
+hipError_t launch_attention_few(const AttnArgs& a, int type, int grid, hipStream_t s) {
+    const bool e = a.c.type == LSCD_E4M3;
+    if (type == LSCD_F16) return e ? few_dim<F16, true>(a, grid, s) : few_dim<F16, false>(a, grid, s);
+    return e ? few_dim<BF16, true>(a, grid, s) : few_dim<BF16, false>(a, grid, s);
+}
+
+}  // namespace lscd

@@ -1,0 +1,360 @@
+// Attention over a paged cache for many query rows (a chunk of a prompt): 128 rows (tokens x heads
+// that share a key head) per item, bound by the matrix cores and the exponentials between the two
+// products.
+//
+// A workgroup is four wavefronts of 32 rows each; they share tiles of 64 keys and values in LDS,
+// double-buffered with one barrier per tile: the next tile's loads are issued before the current
+// one is computed and written to the other buffer after it (codes of an 8-bit cache become 16-bit
+// values on the way; scales are powers of two, so that rounds nothing).  Keys are read back row by
+// row (128-bit reads), values as V^T by the transposing LDS read (ds_read_b64_tr_b16): 16 lanes read
+// a 4 x 16 block and get its columns, which is the A operand in the token order that P has.
+// 16-byte chunks are XOR-swizzled by the row so that the lanes of one read spread over the banks.
+
+#include "lscd_attention.h"
+
+namespace lscd {
+namespace {
+
+constexpr int kManyWaves = kManyRows / 32;
+constexpr int kManyThreads = 64 * kManyWaves;
+
+typedef __attribute__((address_space(3))) s16x4v lds_s16x4;
+
+template <typename T, bool E4M3, int DP>
+struct Many {
+    static constexpr int kSteps = DP / 16;    // MFMA steps over the channels of q . k
+    static constexpr int kBlocks = DP / 32;   // 32-channel blocks of the output
+    static constexpr int kRow = DP * 2;       // bytes of an LDS row
+    static constexpr int kTile = kManyTokens * kRow;
+    // 16-byte loads: lanes per row (a power of two that covers DP), rows per pass, passes
+    static constexpr int kPer = DP <= 64 ? (E4M3 ? 4 : 8) : DP <= 128 ? (E4M3 ? 8 : 16) : (E4M3 ? 16 : 32);
+    static constexpr int kPassRows = kManyThreads / kPer;
+    static constexpr int kPasses = kManyTokens / kPassRows;
+    static_assert(64 / kPer <= 16, "a wavefront's rows of one pass lie in one page");
+
+    __device__ static __forceinline__ int key_at(int row, int chunk) {
+        constexpr int mask = DP == 96 ? 3 : (DP == 64 ? 7 : 15);
+        return row * kRow + ((chunk ^ (row & mask)) << 4);
+    }
+    __device__ static __forceinline__ int val_swizzle(int row) {
+        return DP == 96 ? 0 : (DP == 64 ? ((row >> 1) & 1) << 2 : (row & 3) << 2);
+    }
+    __device__ static __forceinline__ int val_at(int row, int chunk) { return row * kRow + ((chunk ^ val_swizzle(row)) << 4); }
+
+    u32x4v k[kPasses], v[kPasses];
+    float ks[kPasses], vs[kPasses];
+    int64_t page[kPasses];  // of the next tile to load
+
+    __device__ __forceinline__ static int row_of(int pass, int tid) { return pass * kPassRows + tid / kPer; }
+
+    __device__ __forceinline__ void look_up(const AttnArgs& a, int seq, int t0, int wave) {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) page[i] = page_of(a, seq, t0 + i * kPassRows + wave * (64 / kPer));
+    }
+    // Loads the tile whose pages look_up() found; rows from `high` on are zero.
+    __device__ __forceinline__ void load(const AttnArgs& a, int head, int t0, int low, int high, int tid) {
+        const int D = a.c.head_dim, width = E4M3 ? 1 : 2, d = (tid % kPer) * (E4M3 ? 16 : 8);
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int t = t0 + row_of(i, tid), row = t & (a.c.page_size - 1);
+            const int64_t tile = page[i] * a.c.heads + head;
+            const auto kb = buffer_of((const uint8_t*)a.c.k + tile * a.c.page_size * D * width, a.c.page_size * D * width);
+            const auto vb = buffer_of((const uint8_t*)a.c.v + tile * a.c.page_size * D * width, a.c.page_size * D * width);
+            const bool on = t < high && t >= low;
+            const int at = on && d < D ? (row * D + d) * width : kNoRow;
+            k[i] = __builtin_amdgcn_raw_buffer_load_b128(kb, at, 0, 0);
+            v[i] = __builtin_amdgcn_raw_buffer_load_b128(vb, at, 0, 0);
+            if (E4M3) {
+                const auto ksb = buffer_of(a.c.k_scale + tile * a.c.page_size, a.c.page_size * 4);
+                const auto vsb = buffer_of(a.c.v_scale + tile * a.c.page_size, a.c.page_size * 4);
+                ks[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(ksb, on ? row * 4 : kNoRow, 0, 0));
+                vs[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(vsb, on ? row * 4 : kNoRow, 0, 0));
+            }
+        }
+    }
+    __device__ __forceinline__ void store(unsigned char* kb, unsigned char* vb, int tid) const {
+        const int c = tid % kPer;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int row = row_of(i, tid);
+            if (E4M3) {
+                if (DP == 96 && c >= DP / 16) continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    u32x4v x, y;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        x[2 * w] = T::template from_e4m3<false>(k[i][2 * h + w], ks[i]);
+                        x[2 * w + 1] = T::template from_e4m3<true>(k[i][2 * h + w], ks[i]);
+                        y[2 * w] = T::template from_e4m3<false>(v[i][2 * h + w], vs[i]);
+                        y[2 * w + 1] = T::template from_e4m3<true>(v[i][2 * h + w], vs[i]);
+                    }
+                    *(u32x4v*)(kb + key_at(row, 2 * c + h)) = x;
+                    *(u32x4v*)(vb + val_at(row, 2 * c + h)) = y;
+                }
+            } else {
+                if (DP == 96 && c >= DP / 8) continue;
+                *(u32x4v*)(kb + key_at(row, c)) = k[i];
+                *(u32x4v*)(vb + val_at(row, c)) = v[i];
+            }
+        }
+    }
+};
+
+template <typename T, bool E4M3, int DP>
+__global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_many_kernel(AttnArgs a) {
+    using F = Many<T, E4M3, DP>;
+    __shared__ __attribute__((aligned(16))) unsigned char sh[2][2][F::kTile];
+    __shared__ uint32_t sh_last;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int half = lane >> 5;
+    const int G = gridDim.x;
+    // consecutive ranges on one XCD (workgroups go to the 8 XCDs in turn): they share keys in its L2
+    const int me = (G & 7) == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+    const int64_t U = total_units<kManyRows, kManyTokens, false>(a, lane);
+    if (U == 0) return;
+    const Cut cut(U, G);
+    int64_t u = cut.begin(me);
+    const int64_t end = cut.begin(me + 1);
+    if (u >= end) return;
+    Place p = find_unit<kManyRows, kManyTokens, false>(a, u, lane);
+    Seq q = read_seq(a, p.seq);
+    const int D = a.c.head_dim;
+
+    // LDS offsets of this lane: key chunks by step, value columns by block
+    const int key_row = lane & 31;
+    const int vtok = 4 * half + ((lane & 15) >> 2);
+    const int vchunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1), vhalf = (lane & 1) * 8;
+
+    while (u < end) {
+        int low, high;
+        tile_range<kManyRows>(a, q, p.tile, &low, &high);
+        const int units = max(1, (high + kManyTokens - 1) / kManyTokens - low / kManyTokens);
+        const int64_t item = u - p.unit;
+        const int last = (int)min((int64_t)units, p.unit + (end - u));
+        const int t_base = low / kManyTokens * kManyTokens;
+
+        const int row0 = p.tile * kManyRows + 32 * wave, row = row0 + (lane & 31);
+        const bool live = row < q.rows;
+        const int token = row / a.share;
+        const int qh = p.head * a.share + row % a.share;
+        const uint16_t* qp = (const uint16_t*)a.q + (int64_t)(q.first + (live ? token : 0)) * a.q_stride + (int64_t)qh * D;
+        u32x4v qr[F::kSteps];
+#pragma unroll
+        for (int s = 0; s < F::kSteps; ++s) {
+            const int d = 16 * s + 8 * half;
+            qr[s] = u32x4v{0u, 0u, 0u, 0u};
+            if (live && d < D) qr[s] = *(const u32x4v*)(qp + d);
+        }
+        const int pos = q.len - q.n + token;
+        const int see_high = live ? (a.causal ? min(pos + 1, q.len) : q.len) : 0;
+        const int see_low = a.window ? pos - a.window + 1 : 0;
+        // this wavefront's rows: what some row sees, and what every row sees
+        const int tok0 = row0 / a.share, tok1 = (min(q.rows, row0 + 32) - 1) / a.share;
+        const int some_high = row0 < q.rows ? (a.causal ? min(q.len - q.n + tok1 + 1, q.len) : q.len) : 0;
+        const int some_low = a.window ? q.len - q.n + tok0 - a.window + 1 : 0;
+        const int all_high = a.causal ? min(q.len - q.n + tok0 + 1, q.len) : q.len;
+        const int all_low = a.window ? q.len - q.n + tok1 - a.window + 1 : 0;
+
+        float m = kNoScore, l = 0.f;
+        f32x16v o[F::kBlocks];
+#pragma unroll
+        for (int b = 0; b < F::kBlocks; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
+
+        F f;
+        int t0 = t_base + p.unit * kManyTokens;
+        f.look_up(a, p.seq, t0, wave);
+        f.load(a, p.head, t0, low, high, tid);
+        f.look_up(a, p.seq, t0 + kManyTokens, wave);
+        __syncthreads();  // the previous item's reads of the buffers are done
+        f.store(sh[0][0], sh[0][1], tid);
+        __syncthreads();
+        for (int k = p.unit; k < last; ++k, t0 += kManyTokens) {
+            const int buf = (k - p.unit) & 1;
+            if (k + 1 < last) {
+                f.load(a, p.head, t0 + kManyTokens, low, high, tid);
+                f.look_up(a, p.seq, t0 + 2 * kManyTokens, wave);
+            }
+            if (t0 < some_high && t0 + kManyTokens > some_low) {
+                const unsigned char* kb = sh[buf][0];
+                unsigned char* vb = sh[buf][1];
+                f32x16v s[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
+#pragma unroll
+                    for (int st = 0; st < F::kSteps; ++st)
+                        s[h] = T::mfma32(*(const u32x4v*)(kb + F::key_at(key_row, 2 * st + half) + h * 32 * F::kRow), qr[st], s[h]);
+                }
+                const bool masked = t0 < all_low || t0 + kManyTokens > all_high;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) s[h][i] *= a.scale_log2;
+                if (masked) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int t = t0 + 32 * h + 8 * (i / 4) + 4 * half + i % 4;
+                            if (t >= see_high || t < see_low) s[h][i] = -__builtin_inff();
+                        }
+                }
+                float most = s[0][0];
+#pragma unroll
+                for (int i = 1; i < 32; ++i) most = fmaxf(most, s[i / 16][i % 16]);
+                if (__any(most > m + kLazy)) {
+                    const float to = fmaxf(m, max_halves(most));
+                    const float by = exp2_fast(m - to);
+                    m = to;
+                    l *= by;
+#pragma unroll
+                    for (int b = 0; b < F::kBlocks; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[b][i] *= by;
+                }
+                u32x4v pb[4];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float x = exp2_fast(s[i / 8][(2 * i) % 16] - m), y = exp2_fast(s[i / 8][(2 * i) % 16 + 1] - m);
+                    l += x + y;
+                    pb[i / 4][i % 4] = T::pack(x, y);
+                }
+#pragma unroll
+                for (int b = 0; b < F::kBlocks; ++b) {
+                    const int at = vtok * F::kRow + (((4 * b + vchunk) ^ F::val_swizzle(vtok)) << 4) + vhalf;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const auto x = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at + 16 * ks * F::kRow)));
+                        const auto y = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at + (16 * ks + 8) * F::kRow)));
+                        const u32x4v av = {x[0], x[1], y[0], y[1]};
+                        if (masked && __any(T::odd(av[0]) || T::odd(av[1]) || T::odd(av[2]) || T::odd(av[3]))) {
+                            // 0 * infinity would be NaN in rows that do not see the token: what is
+                            // finite as ever, the rest one token at a time, added only where it is seen
+                            u32x4v fin;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) fin[i] = T::finite(av[i]);
+                            o[b] = T::mfma32(fin, pb[ks], o[b]);
+                            for (int j = 0; j < 16; ++j) {
+                                const int t = t0 + 16 * ks + 8 * ((j & 7) >> 2) + 4 * (j >> 3) + (j & 3);
+                                u32x4v one;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    one[i] = half == (j >> 3) && (j & 7) / 2 == i ? (av[i] ^ fin[i]) & ((j & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
+                                f32x16v z;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) z[i] = 0.f;
+                                z = T::mfma32(one, pb[ks], z);
+                                if (t < see_high && t >= see_low)
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i) o[b][i] += z[i];
+                            }
+                        } else {
+                            o[b] = T::mfma32(av, pb[ks], o[b]);
+                        }
+                    }
+                }
+            }
+            if (k + 1 < last) f.store(sh[buf ^ 1][0], sh[buf ^ 1][1], tid);
+            __syncthreads();
+        }
+        l = sum_halves(l);
+
+        const bool whole = p.unit == 0 && last == units;
+        constexpr int64_t kFloats = (int64_t)kManyRows * (DP + 2);
+        bool write = whole;
+        if (!whole) {
+            const int owner = cut.owner(item), behind = cut.owner(item + units - 1);
+            float* mine = a.part + (int64_t)(2 * me + (p.unit == 0 ? 1 : 0)) * kFloats;
+            if (half == 0) {
+                mine[32 * wave + lane] = m;
+                mine[kManyRows + 32 * wave + lane] = l;
+            }
+#pragma unroll
+            for (int b = 0; b < F::kBlocks; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    f32x4v x = {o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
+                    *(f32x4v*)(mine + 2 * kManyRows + ((((wave * F::kBlocks + b) * 4) + i / 4) * 64 + lane) * 4) = x;
+                }
+            write = arrive_last(a.count + owner, (uint32_t)(behind - owner + 1), &sh_last);
+            if (write) {
+                for (int w = owner; w <= behind; ++w) {
+                    const float* y = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
+                    const float my = y[32 * wave + (lane & 31)], ly = y[kManyRows + 32 * wave + (lane & 31)];
+                    const float to = w == owner ? my : fmaxf(m, my);
+                    const float b0 = w == owner ? 0.f : exp2_fast(m - to), b1 = exp2_fast(my - to);
+                    m = to;
+                    l = (w == owner ? 0.f : l * b0) + ly * b1;
+#pragma unroll
+                    for (int b = 0; b < F::kBlocks; ++b)
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const f32x4v x = *(const f32x4v*)(y + 2 * kManyRows + ((((wave * F::kBlocks + b) * 4) + i / 4) * 64 + lane) * 4);
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) o[b][i + r] = (w == owner ? 0.f : o[b][i + r] * b0) + x[r] * b1;
+                        }
+                }
+            }
+        }
+        if (write && live) {
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            uint16_t* op = (uint16_t*)a.o + (int64_t)(q.first + token) * a.o_stride + (int64_t)qh * D;
+#pragma unroll
+            for (int b = 0; b < F::kBlocks; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const int d = 32 * b + 8 * (i / 4) + 4 * half;
+                    u32x2v x = {T::pack(o[b][i] * inv, o[b][i + 1] * inv), T::pack(o[b][i + 2] * inv, o[b][i + 3] * inv)};
+                    if (l == 0.f) x = u32x2v{0u, 0u};
+                    if (d < D) *(u32x2v*)(op + d) = x;
+                }
+        }
+
+        u += last - p.unit;
+        if (u >= end) break;
+        p.unit = 0;
+        if ((++p.tile) * kManyRows >= q.rows) {
+            p.tile = 0;
+            if (++p.head == a.c.heads) {
+                p.head = 0;
+                do {
+                    ++p.seq;
+                    q = read_seq(a, p.seq);
+                } while (q.rows <= a.few_limit);
+            }
+        }
+    }
+}
+
+template <typename T, bool E4M3>
+hipError_t many_dim(const AttnArgs& a, int grid, hipStream_t s) {
+    const int D = a.c.head_dim;
+    if (D <= 64)
+        attention_many_kernel<T, E4M3, 64><<<grid, kManyThreads, 0, s>>>(a);
+    else if (D <= 96)
+        attention_many_kernel<T, E4M3, 96><<<grid, kManyThreads, 0, s>>>(a);
+    else if (D <= 128)
+        attention_many_kernel<T, E4M3, 128><<<grid, kManyThreads, 0, s>>>(a);
+    else
+        attention_many_kernel<T, E4M3, 256><<<grid, kManyThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int attention_many_grid(int cus) { return 2 * cus; }
+int64_t attention_many_floats(int dim) {
+    return (int64_t)kManyRows * ((dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : 256) + 2);
+}
+
+hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStream_t s) {
+    const bool e = a.c.type == LSCD_E4M3;
+    if (type == LSCD_F16) return e ? many_dim<F16, true>(a, grid, s) : many_dim<F16, false>(a, grid, s);
+    return e ? many_dim<BF16, true>(a, grid, s) : many_dim<BF16, false>(a, grid, s);
+}
+
+}  // namespace lscd

@@ -1,0 +1,194 @@
+// C-ABI layer of the serving operators: argument checks, handles and launches.  Entry points are
+// declared and documented in include/lscd.h.
+
+#include <math.h>
+
+#include <algorithm>
+#include <new>
+
+#include "lscd_serve.h"
+
+namespace {
+
+lscd_status_t status_of(hipError_t e) {
+    if (e == hipSuccess) return LSCD_SUCCESS;
+    return e == hipErrorOutOfMemory ? LSCD_ERROR_OUT_OF_MEMORY : LSCD_ERROR_HIP;
+}
+bool aligned(const void* p, uintptr_t n) { return p && ((uintptr_t)p & (n - 1)) == 0; }
+
+lscd_status_t check_cache(const lscd_cache_t* c) {
+    if (!c || !aligned(c->k, 16) || !aligned(c->v, 16) || c->num_pages < 1 || c->heads < 1 || c->page_size < 1 ||
+        c->head_dim < 1)
+        return LSCD_ERROR_INVALID_VALUE;
+    if (c->type != LSCD_F16 && c->type != LSCD_BF16 && c->type != LSCD_E4M3) return LSCD_ERROR_INVALID_VALUE;
+    const bool scaled = c->type == LSCD_E4M3;
+    if (scaled ? !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16) : c->k_scale || c->v_scale)
+        return LSCD_ERROR_INVALID_VALUE;
+    if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) || c->head_dim % 16 ||
+        c->head_dim > lscd::kAttnMaxDim || c->heads > 65535 || c->num_pages > 0x7FFFFFFF / c->page_size)
+        return LSCD_ERROR_NOT_SUPPORTED;
+    return LSCD_SUCCESS;
+}
+
+// Rows of `width` values, `stride` apart.
+bool bad_rows(const void* p, int64_t stride, int64_t width) {
+    return !aligned(p, 16) || stride < width || stride % 8 || stride > ((int64_t)1 << 40);
+}
+
+lscd_status_t check_move(const lscd_cache_t* c, const void* k, int64_t ks, const void* v, int64_t vs, const int32_t* slots,
+                         int64_t T, int32_t type) {
+    lscd_status_t st = check_cache(c);
+    if (st != LSCD_SUCCESS) return st;
+    if (T < 0 || (type != LSCD_F16 && type != LSCD_BF16)) return LSCD_ERROR_INVALID_VALUE;
+    if (c->type != LSCD_E4M3 && c->type != type) return LSCD_ERROR_NOT_SUPPORTED;
+    if (T == 0) return LSCD_SUCCESS;
+    const int64_t width = (int64_t)c->heads * c->head_dim;
+    if (bad_rows(k, ks, width) || bad_rows(v, vs, width) || !aligned(slots, 4)) return LSCD_ERROR_INVALID_VALUE;
+    if (T > ((int64_t)1 << 30)) return LSCD_ERROR_NOT_SUPPORTED;
+    return LSCD_SUCCESS;
+}
+
+void free_attention(lscd_attention_s* h) {
+    if (!h) return;
+    if (h->part) (void)hipFree(h->part);
+    if (h->count) (void)hipFree(h->count);
+    delete h;
+}
+
+}  // namespace
+
+extern "C" {
+
+lscd_status_t lscd_cache_write(const lscd_cache_t* cache, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, const int32_t* slots, int64_t T, int32_t type, void* stream) {
+    lscd_status_t st = check_move(cache, k, k_stride, v, v_stride, slots, T, type);
+    if (st != LSCD_SUCCESS || T == 0) return st;
+    lscd::CacheMoveArgs a = {};
+    a.c = *cache;
+    a.in[0] = k;
+    a.in[1] = v;
+    a.stride[0] = k_stride;
+    a.stride[1] = v_stride;
+    a.slots = slots;
+    a.T = T;
+    return status_of(lscd::launch_cache_write(a, type, (hipStream_t)stream));
+}
+
+lscd_status_t lscd_cache_read(const lscd_cache_t* cache, const int32_t* slots, int64_t T, void* k, int64_t k_stride,
+                              void* v, int64_t v_stride, int32_t type, void* stream) {
+    lscd_status_t st = check_move(cache, k, k_stride, v, v_stride, slots, T, type);
+    if (st != LSCD_SUCCESS || T == 0) return st;
+    lscd::CacheMoveArgs a = {};
+    a.c = *cache;
+    a.out[0] = k;
+    a.out[1] = v;
+    a.stride[0] = k_stride;
+    a.stride[1] = v_stride;
+    a.slots = slots;
+    a.T = T;
+    return status_of(lscd::launch_cache_read(a, type, (hipStream_t)stream));
+}
+
+lscd_status_t lscd_attention_create(int32_t q_heads, int32_t kv_heads, int32_t head_dim, lscd_attention_t* out) {
+    if (!out) return LSCD_ERROR_INVALID_VALUE;
+    *out = nullptr;
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads || head_dim < 1) return LSCD_ERROR_INVALID_VALUE;
+    if (q_heads > 65535 || head_dim % 16 || head_dim > lscd::kAttnMaxDim) return LSCD_ERROR_NOT_SUPPORTED;
+    lscd_attention_s* h = new (std::nothrow) lscd_attention_s();
+    if (!h) return LSCD_ERROR_OUT_OF_MEMORY;
+    h->q_heads = q_heads;
+    h->kv_heads = kv_heads;
+    h->head_dim = head_dim;
+    int cus = 0;
+    hipError_t e = hipGetDevice(&h->device);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, h->device);
+    if (e != hipSuccess || cus <= 0) {
+        free_attention(h);
+        return LSCD_ERROR_HIP;
+    }
+    h->cus = cus;
+    const int few = lscd::attention_few_grid(cus), many = lscd::attention_many_grid(cus), most = std::max(few, many);
+    const int64_t floats = std::max(2 * few * lscd::attention_few_floats(head_dim),
+                                    2 * many * lscd::attention_many_floats(head_dim));
+    if ((e = hipMalloc((void**)&h->part, (size_t)floats * 4)) != hipSuccess ||
+        (e = hipMalloc((void**)&h->count, (size_t)most * 4)) != hipSuccess ||
+        (e = hipMemset(h->count, 0, (size_t)most * 4)) != hipSuccess || (e = hipDeviceSynchronize()) != hipSuccess) {
+        free_attention(h);
+        return status_of(e);
+    }
+    *out = h;
+    return LSCD_SUCCESS;
+}
+
+lscd_status_t lscd_attention_destroy(lscd_attention_t h) {
+    free_attention(h);
+    return LSCD_SUCCESS;
+}
+
+lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, const void* q, int64_t q_stride,
+                             const int32_t* start, const int32_t* length, const int32_t* table, int64_t table_stride,
+                             int32_t table_pages, int32_t sequences, int64_t T, float scale, int32_t causal,
+                             int32_t window, void* o, int64_t o_stride, int32_t type, void* stream) {
+    if (!h) return LSCD_ERROR_INVALID_VALUE;
+    lscd_status_t st = check_cache(cache);
+    if (st != LSCD_SUCCESS) return st;
+    if (cache->heads != h->kv_heads || cache->head_dim != h->head_dim) return LSCD_ERROR_INVALID_VALUE;
+    if ((type != LSCD_F16 && type != LSCD_BF16) || T < 0 || sequences < 0 || table_pages < 0 || window < 0 ||
+        !isfinite(scale))
+        return LSCD_ERROR_INVALID_VALUE;
+    if (cache->type != LSCD_E4M3 && cache->type != type) return LSCD_ERROR_NOT_SUPPORTED;
+    if (T == 0 || sequences == 0) return LSCD_SUCCESS;
+    const int64_t width = (int64_t)h->q_heads * h->head_dim;
+    if (bad_rows(q, q_stride, width) || bad_rows(o, o_stride, width) || !aligned(start, 4) || !aligned(length, 4) ||
+        !aligned(table, 4) || table_pages < 1 || table_stride < table_pages)
+        return LSCD_ERROR_INVALID_VALUE;
+    const int64_t share = h->q_heads / h->kv_heads, span = (int64_t)table_pages * cache->page_size;
+    if (T > ((int64_t)1 << 30) / share || span > ((int64_t)1 << 30)) return LSCD_ERROR_NOT_SUPPORTED;
+    int device = 0;
+    if (hipGetDevice(&device) != hipSuccess) return LSCD_ERROR_HIP;
+    if (device != h->device) return LSCD_ERROR_INVALID_VALUE;
+    lscd::AttnArgs a = {};
+    a.c = *cache;
+    a.q = q;
+    a.o = o;
+    a.q_stride = q_stride;
+    a.o_stride = o_stride;
+    a.table_stride = table_stride;
+    a.start = start;
+    a.length = length;
+    a.table = table;
+    a.table_pages = table_pages;
+    a.sequences = sequences;
+    a.q_heads = h->q_heads;
+    a.share = (int32_t)share;
+    a.causal = causal != 0;
+    a.window = (int32_t)std::min<int64_t>(window, (int64_t)1 << 30);
+    a.T = T;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.page_log2 = __builtin_ctz((unsigned)cache->page_size);
+    a.part = h->part;
+    a.count = h->count;
+    // Sequences of up to 16 query rows are the few-row kernel's, longer ones the other's.  Where no
+    // sequence can be longer (or each has one new token, as far as the counts tell), the few-row
+    // kernel takes all of them, whatever the device arrays hold.
+    const bool both = T * share > lscd::kFewRows && T > sequences;
+    a.few_limit = both ? lscd::kFewRows : 0x7FFFFFFF;
+    auto grid = [&](int most, int rows, int tokens) {
+        const int64_t tiles = T * share / rows + sequences;
+        const int64_t units = (span + tokens - 1) / tokens * h->kv_heads;
+        return (int)std::min<int64_t>(most, tiles > most ? most : tiles * std::min<int64_t>(units, most));
+    };
+    if (sequences > 1 || !both) {
+        hipError_t e = lscd::launch_attention_few(
+            a, type, grid(lscd::attention_few_grid(h->cus), lscd::kFewRows, lscd::kFewTokens), (hipStream_t)stream);
+        if (e != hipSuccess) return status_of(e);
+    }
+    if (both) {
+        hipError_t e = lscd::launch_attention_many(
+            a, type, grid(lscd::attention_many_grid(h->cus), lscd::kManyRows, lscd::kManyTokens), (hipStream_t)stream);
+        if (e != hipSuccess) return status_of(e);
+    }
+    return LSCD_SUCCESS;
+}
+
+}  // extern "C"
