@@ -392,6 +392,42 @@ typedef enum {
 } lscd_type_t;
 
 /*
+ * Product of token vectors with a matrix of 4-bit codes and group scales.
+ *   weight (m, k) = (code - zero) * scale, code and zero 0..15, one zero and scale per row and group
+ *   of `group` consecutive columns (the last group of a row may be shorter).
+ *
+ * lscd_quant_encode -- a handle for such an M x K matrix on the current device; the codes are laid
+ *   out for the product by a kernel on `stream`, and the call returns when that is done.
+ *   codes   device, M rows of row_bytes bytes (at least (K + 1) / 2): column k in byte k / 2, the low
+ *           half for even k.
+ *   scales  device, [M][ceil(K / group)] values of `type` (LSCD_F16 or LSCD_BF16), the type of the
+ *           products' x and y too.
+ *   zeros   device, [M][ceil(K / group)] bytes 0..15 (the low four bits count), or NULL: 8 throughout.
+ *   group   32, 64 or a multiple of 128 (NOT_SUPPORTED otherwise).  M, K 1..2^30.
+ *   The handle owns its copy (M * K / 2 bytes, rows rounded up to 16 and columns to 128, and the
+ *   scales) and a workspace for products split along K; the arrays are not needed afterwards.
+ *
+ * lscd_quant_linear -- y[n][m] = sum over k of x[n][k] * weight(m, k) for N tokens, on `stream`.
+ *   x, y   device, N rows of K and M values of the handle's type, ldx >= K and ldy >= M elements apart;
+ *          any 2-byte alignment (16-byte aligned x rows load faster).
+ *   N      0 is a no-op; 1..LSCD_MAX_N, in launches of up to 64 tokens that read the codes once each.
+ * Sums are fp32, the scale is applied to each group's sum, y is rounded once (nearest-even).  float16:
+ * (code - zero) x is exact; bfloat16: an infinity in x gives NaN.  Sums over a split K are added in a
+ * fixed order: bit-reproducible.  Asynchronous, no allocation, graph-capturable; one handle must not
+ * run on two streams at once (it owns one workspace).
+ *
+ * lscd_quant_decode -- the weights as the handle holds them, rounded to its type: device, M x K,
+ *   row-major.  Asynchronous on `stream`.
+ */
+typedef struct lscd_quant_s* lscd_quant_t;
+lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void* scales, const void* zeros, int64_t M,
+                                int64_t K, int32_t group, int32_t type, void* stream, lscd_quant_t* out);
+lscd_status_t lscd_quant_linear(lscd_quant_t h, const void* x, int64_t ldx, void* y, int64_t ldy, int32_t N,
+                                void* stream);
+lscd_status_t lscd_quant_decode(lscd_quant_t h, void* w, void* stream);
+lscd_status_t lscd_quant_destroy(lscd_quant_t h);
+
+/*
  * Paged cache of keys and values, in device memory of the caller.
  *   k, v  [num_pages][heads][page_size][head_dim] values of `type`, 16-byte aligned.
  *   k_scale, v_scale  LSCD_E4M3 only (NULL otherwise): [num_pages][heads][page_size] floats,

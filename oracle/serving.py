@@ -69,3 +69,14 @@ def attention(q, k, v, scale, causal=True, window=0):
             a[i, h] = w @ np.abs(v[seen, g])
             big[i, h] = (np.abs(scale * k[seen, g]) @ np.abs(q[i, h])).max()
     return o, a, big
+
+
+def quant_weights(codes, scales, zeros, K, group):
+    """(codes - zeros [M][K] whole numbers, scales [M][K]) of a packed matrix, column by column."""
+    M = codes.shape[0]
+    c, s = np.empty((M, K)), np.empty((M, K))
+    for k in range(K):
+        z = 8 if zeros is None else zeros[:, k // group].astype(np.int64) & 15
+        c[:, k] = ((codes[:, k // 2].astype(np.int64) >> (4 * (k % 2))) & 15) - z
+        s[:, k] = scales[:, k // group]
+    return c, s

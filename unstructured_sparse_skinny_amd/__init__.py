@@ -39,6 +39,7 @@ EXPORTS = ("lscd_pack_size", "lscd_pack", "lscd_default_tile_m", "lscd_encode", 
            "lscd_get_info", "lscd_spmm", "lscd_debug_decode", "lscd_attach_dense", "lscd_linear",
            "lscd_linear_path", "lscd_set_linear_crossover", "lscd_linear_model", "lscd_tune_dense", "lscd_destroy",
            "lscd_status_string", "lscd_stream_read", "lscd_spmm_noalloc", "lscd_linear_times",
+           "lscd_quant_encode", "lscd_quant_linear", "lscd_quant_decode", "lscd_quant_destroy",
            "lscd_cache_write", "lscd_cache_read",
            "lscd_attention_create", "lscd_attention", "lscd_attention_destroy")
 
@@ -105,6 +106,10 @@ def _load():
         "lscd_stream_read": [VP, I64, I32, VP, VP],
         "lscd_linear_times": [VP, I32, P(ctypes.c_double), P(ctypes.c_double), P(I32)],
         "lscd_spmm_noalloc": [VP, VP, VP, I32, VP],
+        "lscd_quant_encode": [VP, I64, VP, VP, I64, I64, I32, I32, VP, P(VP)],
+        "lscd_quant_linear": [VP, VP, I64, VP, I64, I32, VP],
+        "lscd_quant_decode": [VP, VP, VP],
+        "lscd_quant_destroy": [VP],
         "lscd_cache_write": [VP, VP, I64, VP, I64, VP, I64, I32, VP],
         "lscd_cache_read": [VP, VP, I64, VP, I64, VP, I64, I32, VP],
         "lscd_attention_create": [I32, I32, I32, P(VP)],
@@ -405,6 +410,73 @@ def lscd_destroy(h: Handle):
 
 
 # ---------------------------------------------------------------- serving operators
+
+
+class Quant:
+    """Owner of an lscd_quant_t (an M x K matrix of 4-bit codes); freed by lscd_quant_destroy (or when collected)."""
+
+    def __init__(self, ptr: int, M: int, K: int, group: int, dtype, device):
+        self.ptr, self.M, self.K, self.group, self.dtype, self.device = ptr, M, K, group, dtype, device
+
+    def __del__(self):
+        self.close()
+
+    def close(self):
+        if getattr(self, "ptr", None) and _lib is not None:
+            _lib.lscd_quant_destroy(self.ptr)
+            self.ptr = None
+
+
+def lscd_quant_encode(codes, scales, K: int, zeros=None, group: int = 128, stream=None) -> Quant:
+    """Lay out a matrix of 4-bit codes: codes uint8 [M][(K + 1) // 2] (low half: even column), scales [M][ceil(K / group)]
+    float16 or bfloat16 (the type of the products), zeros uint8 of the scales' shape or None (8)."""
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_cuda or codes.stride(1) != 1:
+        raise ValueError("codes must be a uint8 CUDA tensor of rows")
+    M, groups = codes.shape[0], -(-K // group) if group > 0 else 0
+    if scales.dtype not in (torch.float16, torch.bfloat16) or codes.shape[1] != (K + 1) // 2:
+        raise ValueError("codes must have (K + 1) // 2 bytes a row, scales be float16 or bfloat16")
+    for t, name in ((scales, "scales"), (zeros, "zeros")):
+        if t is not None and (tuple(t.shape) != (M, groups) or not t.is_contiguous() or t.device != codes.device):
+            raise ValueError(f"{name} must be contiguous, [{M}][{groups}], on the codes' device")
+    if zeros is not None and zeros.dtype != torch.uint8:
+        raise ValueError("zeros must be uint8")
+    h = ctypes.c_void_p()
+    _check(_lib.lscd_quant_encode(codes.data_ptr(), codes.stride(0), scales.data_ptr(),
+                                  None if zeros is None else zeros.data_ptr(), M, K, group, _TYPES[scales.dtype],
+                                  _stream(stream), ctypes.byref(h)), "lscd_quant_encode")
+    return Quant(h.value, M, K, group, scales.dtype, codes.device)
+
+
+def _matrix(t, name, rows, cols, h):
+    """(pointer, elements from row to row) of a [rows][cols] tensor of h's type whose rows are contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype != h.dtype or t.device != h.device:
+        raise ValueError(f"{name} must be a {h.dtype} CUDA tensor [{rows}][{cols}] on the handle's device")
+    if stride[1] != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), (stride[0] if rows > 1 else cols)
+
+
+def lscd_quant_linear(h: Quant, B, C, stream=None):
+    """C[N][M] = B[N][K] . W^T for the matrix of 4-bit codes W, enqueued on `stream`."""
+    N = B.shape[0]
+    pb, lb = _matrix(B, "B", N, h.K, h)
+    pc, lc = _matrix(C, "C", N, h.M, h)
+    _check(_lib.lscd_quant_linear(h.ptr, pb, lb, pc, lc, N, _stream(stream)), "lscd_quant_linear")
+    return C
+
+
+def lscd_quant_decode(h: Quant, W, stream=None):
+    """Write the weights the handle holds into W [M][K], rounded to its type."""
+    p, ld = _matrix(W, "W", h.M, h.K, h)
+    if ld != h.K:
+        raise ValueError("W must be contiguous")
+    _check(_lib.lscd_quant_decode(h.ptr, p, _stream(stream)), "lscd_quant_decode")
+    return W
+
+
+def lscd_quant_destroy(h: Quant):
+    h.close()
 
 
 class Cache:

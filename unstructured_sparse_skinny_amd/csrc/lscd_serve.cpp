@@ -55,9 +55,142 @@ void free_attention(lscd_attention_s* h) {
     delete h;
 }
 
+void free_quant(lscd_quant_s* h) {
+    if (!h) return;
+    if (h->codes) (void)hipFree(h->codes);
+    if (h->scales) (void)hipFree(h->scales);
+    if (h->zeros) (void)hipFree(h->zeros);
+    if (h->part) (void)hipFree(h->part);
+    if (h->count) (void)hipFree(h->count);
+    delete h;
+}
+
+// Ranges of K that workgroups split a product into: enough workgroups for every CU.
+int quant_splits(const lscd_quant_s* h) {
+    const int groups = (h->tiles + 1) / 2;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * (int64_t)h->cus / groups, h->units / lscd::kQuantWaves, 16}));
+}
+
+lscd_status_t check_quant(const lscd_quant_s* h) {
+    int device = 0;
+    if (hipGetDevice(&device) != hipSuccess) return LSCD_ERROR_HIP;
+    return device == h->device ? LSCD_SUCCESS : LSCD_ERROR_INVALID_VALUE;
+}
+
+lscd::QuantArgs quant_args(const lscd_quant_s* h) {
+    lscd::QuantArgs a = {};
+    a.codes = h->codes;
+    a.scales = h->scales;
+    a.zeros = h->zeros;
+    a.part = h->part;
+    a.count = h->count;
+    a.M = (int32_t)h->M;
+    a.K = (int32_t)h->K;
+    a.tiles = h->tiles;
+    a.units = h->units;
+    return a;
+}
+
 }  // namespace
 
 extern "C" {
+
+lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void* scales, const void* zeros, int64_t M,
+                                int64_t K, int32_t group, int32_t type, void* stream, lscd_quant_t* out) {
+    if (!out) return LSCD_ERROR_INVALID_VALUE;
+    *out = nullptr;
+    if (!codes || !aligned(scales, 2) || M < 1 || K < 1 || group < 1 || row_bytes < (K + 1) / 2 ||
+        (type != LSCD_F16 && type != LSCD_BF16))
+        return LSCD_ERROR_INVALID_VALUE;
+    if (M > ((int64_t)1 << 30) || K > ((int64_t)1 << 30)) return LSCD_ERROR_INVALID_VALUE;
+    if (group < 32 || (group < 128 ? group != 32 && group != 64 : group % 128)) return LSCD_ERROR_NOT_SUPPORTED;
+    lscd_quant_s* h = new (std::nothrow) lscd_quant_s();
+    if (!h) return LSCD_ERROR_OUT_OF_MEMORY;
+    int cus = 0;
+    hipError_t e = hipGetDevice(&h->device);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, h->device);
+    if (e != hipSuccess || cus <= 0) {
+        free_quant(h);
+        return LSCD_ERROR_HIP;
+    }
+    h->cus = cus;
+    h->M = M;
+    h->K = K;
+    h->group = group;
+    h->type = type;
+    h->per_unit = group >= 128 ? 1 : 128 / group;
+    h->tiles = (int32_t)((M + lscd::kQuantRows - 1) / lscd::kQuantRows);
+    h->units = (int32_t)((K + lscd::kQuantUnit - 1) / lscd::kQuantUnit);
+    const int64_t blocks = (int64_t)h->tiles * ((h->units + 3) / 4);
+    if (blocks >= ((int64_t)1 << 31)) {
+        free_quant(h);
+        return LSCD_ERROR_NOT_SUPPORTED;
+    }
+    const int splits = quant_splits(h);
+    h->part_floats = splits > 1 ? splits * M * lscd::kQuantMaxTokens : 0;
+    lscd::QuantEncodeArgs a = {};
+    if ((e = hipMalloc((void**)&h->codes, (size_t)h->tiles * h->units * 1024)) == hipSuccess &&
+        (e = hipMalloc((void**)&h->scales, (size_t)blocks * 16 * 8 * h->per_unit)) == hipSuccess &&
+        (!zeros || (e = hipMalloc((void**)&h->zeros, (size_t)blocks * 16 * (h->per_unit == 4 ? 8 : 4))) == hipSuccess) &&
+        (!h->part_floats || (e = hipMalloc((void**)&h->part, (size_t)h->part_floats * 4)) == hipSuccess)) {
+        a.q = (const uint8_t*)codes;
+        a.scales = (const uint16_t*)scales;
+        a.zeros = (const uint8_t*)zeros;
+        a.codes = h->codes;
+        a.scales_out = h->scales;
+        a.zeros_out = h->zeros;
+        a.M = M;
+        a.K = K;
+        a.row_bytes = row_bytes;
+        a.groups = (K + group - 1) / group;
+        a.group = group;
+        a.per_unit = h->per_unit;
+        a.tiles = h->tiles;
+        a.units = h->units;
+        e = lscd::launch_quant_encode(a, (hipStream_t)stream);
+        if (e == hipSuccess) e = hipStreamSynchronize((hipStream_t)stream);
+    }
+    if (e != hipSuccess) {
+        free_quant(h);
+        return status_of(e);
+    }
+    *out = h;
+    return LSCD_SUCCESS;
+}
+
+lscd_status_t lscd_quant_linear(lscd_quant_t h, const void* x, int64_t ldx, void* y, int64_t ldy, int32_t N,
+                                void* stream) {
+    if (!h || N < 0) return LSCD_ERROR_INVALID_VALUE;
+    if (N == 0) return LSCD_SUCCESS;
+    if (!aligned(x, 2) || !aligned(y, 2) || ldx < h->K || ldy < h->M) return LSCD_ERROR_INVALID_VALUE;
+    if (N > LSCD_MAX_N) return LSCD_ERROR_NOT_SUPPORTED;
+    lscd_status_t st = check_quant(h);
+    if (st != LSCD_SUCCESS) return st;
+    lscd::QuantArgs a = quant_args(h);
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.splits = quant_splits(h);
+    for (int32_t n = 0; n < N; n += lscd::kQuantMaxTokens) {
+        a.x = (const uint16_t*)x + n * ldx;
+        a.y = (uint16_t*)y + n * ldy;
+        a.N = std::min(N - n, lscd::kQuantMaxTokens);
+        hipError_t e = lscd::launch_quant(a, h->type, h->per_unit, (hipStream_t)stream);
+        if (e != hipSuccess) return status_of(e);
+    }
+    return LSCD_SUCCESS;
+}
+
+lscd_status_t lscd_quant_decode(lscd_quant_t h, void* w, void* stream) {
+    if (!h || !aligned(w, 2)) return LSCD_ERROR_INVALID_VALUE;
+    lscd_status_t st = check_quant(h);
+    if (st != LSCD_SUCCESS) return st;
+    return status_of(lscd::launch_quant_decode(quant_args(h), h->type, h->per_unit, (uint16_t*)w, (hipStream_t)stream));
+}
+
+lscd_status_t lscd_quant_destroy(lscd_quant_t h) {
+    free_quant(h);
+    return LSCD_SUCCESS;
+}
 
 lscd_status_t lscd_cache_write(const lscd_cache_t* cache, const void* k, int64_t k_stride, const void* v,
                                int64_t v_stride, const int32_t* slots, int64_t T, int32_t type, void* stream) {

@@ -54,7 +54,67 @@ int64_t attention_many_floats(int dim);
 hipError_t launch_attention_few(const AttnArgs& a, int type, int grid, hipStream_t s);
 hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStream_t s);
 
+// ---------------------------------------------------------------- quantised product
+// Device layout of the codes: row tiles of 16 rows, units of 128 columns, [row tile][unit][64 lanes]
+// [4 words].  Lane l of a unit has row l % 16; word s its 8 codes of columns 32 s + 8 (l / 16) + 0..7,
+// placed so that pairs come out of a word with one shift and one mask (quant_word).  Scales and zero
+// points: [row tile][unit / 4][16 rows][4 units][groups per unit], 16-bit scales and 4-bit zeros.
+// Rows past M and columns past K hold zero points (weights of zero).
+constexpr int kQuantUnit = 128;
+constexpr int kQuantRows = 16;
+constexpr int kQuantMaxTokens = 64;  // tokens of one launch
+constexpr int kQuantWaves = 8;
+
+// Position of bit `bit` (0..3) of code j (0..7) in its word: pair p = j / 2 of codes (low and high
+// half) sits at bits 6-9 of each half for p = 0, 4 above for p = 1, 4 below for p = 2, and 8 above,
+// wrapping around the word, for p = 3.
+__host__ __device__ inline int quant_bit(int j, int bit) {
+    const int p = j / 2, at = 6 + 16 * (j & 1) + bit + (p == 1 ? 4 : p == 2 ? -4 : p == 3 ? 8 : 0);
+    return at & 31;
+}
+
+struct QuantArgs {
+    const uint32_t* codes;
+    const uint16_t* scales;
+    const uint32_t* zeros;   // one word per (row, 4 units): 4 * groups nibbles in 32- or 64-bit records
+    const uint16_t* x;
+    uint16_t* y;
+    float* part;
+    uint32_t* count;
+    int64_t ldx, ldy;
+    int32_t M, K, N;
+    int32_t tiles, units, splits;
+};
+struct QuantEncodeArgs {
+    const uint8_t* q;        // [M][row_bytes]
+    const uint16_t* scales;  // [M][groups]
+    const uint8_t* zeros;    // [M][groups] or null
+    uint32_t* codes;
+    uint16_t* scales_out;
+    uint32_t* zeros_out;
+    int64_t M, K, row_bytes, groups;
+    int32_t group, per_unit; // columns of a group, groups of a unit (1, 2 or 4)
+    int32_t tiles, units;
+};
+hipError_t launch_quant_encode(const QuantEncodeArgs& a, hipStream_t s);
+hipError_t launch_quant_decode(const QuantArgs& a, int type, int per_unit, uint16_t* w, hipStream_t s);
+hipError_t launch_quant(const QuantArgs& a, int type, int per_unit, hipStream_t s);
+
 }  // namespace lscd
+
+struct lscd_quant_s {
+    int device = 0;
+    int cus = 256;
+    int64_t M = 0, K = 0;
+    int32_t group = 0, type = 0, per_unit = 1;
+    int32_t tiles = 0, units = 0;
+    uint32_t* codes = nullptr;
+    uint16_t* scales = nullptr;
+    uint32_t* zeros = nullptr;
+    float* part = nullptr;
+    uint32_t* count = nullptr;
+    int64_t part_floats = 0;
+};
 
 struct lscd_attention_s {
     int device = 0;
