@@ -39,14 +39,20 @@ struct Seq {
     int rows;       // n * share
 };
 
+// Starts, lengths and tables do not change while a kernel runs: read as constants, so that uniform
+// reads are scalar loads, which do not queue behind the loads of keys and values.
+typedef __attribute__((address_space(4))) const int32_t const_i32;
+
 // Reads are clamped to what the arguments allow, whatever the arrays hold.
 __device__ __forceinline__ Seq read_seq(const AttnArgs& a, int s) {
     Seq q;
-    const int64_t b0 = min(max((int64_t)a.start[s], (int64_t)0), a.T);
-    const int64_t b1 = min(max((int64_t)a.start[s + 1], b0), a.T);
+    const const_i32* start = (const const_i32*)(uintptr_t)a.start;
+    const const_i32* length = (const const_i32*)(uintptr_t)a.length;
+    const int64_t b0 = min(max((int64_t)start[s], (int64_t)0), a.T);
+    const int64_t b1 = min(max((int64_t)start[s + 1], b0), a.T);
     q.first = (int)b0;
     q.n = (int)(b1 - b0);
-    q.len = min(max((int64_t)a.length[s], (int64_t)0), (int64_t)a.table_pages << a.page_log2);
+    q.len = min(max((int64_t)length[s], (int64_t)0), (int64_t)a.table_pages << a.page_log2);
     q.rows = q.n * a.share;
     return q;
 }
@@ -148,27 +154,68 @@ struct Cut {
     }
 };
 
-// The page that holds position t (clamped to the pool: an entry outside it is read as page 0).
-__device__ __forceinline__ int64_t page_of(const AttnArgs& a, int seq, int t) {
+// The table's entry for position t (the last one behind the table), and the page it names (an entry
+// outside the pool is read as page 0).
+__device__ __forceinline__ int entry_of(const AttnArgs& a, int seq, int t) {
     const int i = min(t >> a.page_log2, a.table_pages - 1);
-    const int64_t p = a.table[seq * a.table_stride + i];
-    return p >= 0 && p < a.c.num_pages ? p : 0;
+    return ((const const_i32*)(uintptr_t)a.table)[seq * a.table_stride + i];
+}
+__device__ __forceinline__ uint32_t page_of(const AttnArgs& a, int entry) {
+    return (uint32_t)entry < (uint32_t)a.c.num_pages ? (uint32_t)entry : 0u;
 }
 
-// A partial result is complete in memory before its arrival is counted; the last to arrive sees
-// all of them.  Returns whether this workgroup is the last of `expected`, and clears the count.
+// One key head's part of the cache: its block of page 0, and the bytes from a page's to the next's.
+struct HeadBase {
+    const uint8_t *k, *v;
+    const float *ks, *vs;
+    uint64_t page, page_scales;
+    int block, block_scales;  // bytes of one page's block
+    __device__ __forceinline__ HeadBase(const AttnArgs& a, int head, int width) {
+        block = a.c.page_size * a.c.head_dim * width;
+        block_scales = a.c.page_size * 4;
+        page = (uint64_t)a.c.heads * block;
+        page_scales = (uint64_t)a.c.heads * block_scales;
+        k = (const uint8_t*)a.c.k + (uint64_t)head * block;
+        v = (const uint8_t*)a.c.v + (uint64_t)head * block;
+        ks = a.c.k_scale + (uint64_t)head * a.c.page_size;
+        vs = a.c.v_scale + (uint64_t)head * a.c.page_size;
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t keys(uint32_t p) const { return buffer_of(k + p * page, block); }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t values(uint32_t p) const { return buffer_of(v + p * page, block); }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t key_scales(uint32_t p) const {
+        return buffer_of((const uint8_t*)ks + p * page_scales, block_scales);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t value_scales(uint32_t p) const {
+        return buffer_of((const uint8_t*)vs + p * page_scales, block_scales);
+    }
+};
+
+// Partial results travel between workgroups, maybe on different XCDs, by relaxed agent-scope accesses:
+// the stores go through to memory and the loads come from there, whatever the L2 caches hold.  (A
+// release fence would write back and an acquire fence invalidate a whole L2 instead; under full load a
+// fence per cut took longer than the rest: 584 us against 310 us for 64 ragged sequences of 96 heads.)
+__device__ __forceinline__ void put2(float* p, float x, float y) {
+    const uint64_t w = (uint64_t)__builtin_bit_cast(uint32_t, y) << 32 | __builtin_bit_cast(uint32_t, x);
+    __hip_atomic_store((uint64_t*)p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void get2(const float* p, float* x, float* y) {
+    const uint64_t w = __hip_atomic_load((uint64_t*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *x = as_float((uint32_t)w);
+    *y = as_float((uint32_t)(w >> 32));
+}
+// Counts this workgroup's arrival after its put2 stores have completed (the wait below: a store that
+// goes through is counted off when it has reached memory).  Returns whether it is the last of
+// `expected`, and clears the count for the next call.
 __device__ __forceinline__ bool arrive_last(uint32_t* count, uint32_t expected, uint32_t* shared) {
-    __threadfence();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     if (threadIdx.x == 0) {
-        const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         *shared = before + 1 == expected;
         if (before + 1 == expected) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
-    const bool last = *shared != 0;
-    if (last) __threadfence();
-    return last;
+    return *shared != 0;
 }
 
 }  // namespace

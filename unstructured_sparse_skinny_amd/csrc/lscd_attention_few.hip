@@ -27,18 +27,20 @@ struct Few {
     static constexpr int kValWords = E4M3 ? VW / 4 : VW / 2;        // words of one value row per lane
     uint32_t kr[2][kKeyRegs];
     uint32_t vr[8][kValWords];
-    float ks[2], vs[8];
+    uint32_t ks[2], vs[8];  // scales as loaded (e4m3)
 
-    // 32 positions from t0 on; `high`: the first position that nobody sees.
-    __device__ __forceinline__ void load_keys(const AttnArgs& a, int seq, int head, int t0, int high, int lane) {
+    // 32 positions from t0 on, in the pages of the table entries e; positions from `high` on are zero
+    // (lanes without a position read outside the descriptor, which costs no traffic).
+    __device__ __forceinline__ void load_keys(const AttnArgs& a, const HeadBase& hb, const int (&e)[2], int t0, int high,
+                                              int lane) {
         const int D = a.c.head_dim;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int t = t0 + 16 * h, row = (t & (a.c.page_size - 1)) + (lane & 15);
-            const int64_t tile = page_of(a, seq, t) * a.c.heads + head;
+            const uint32_t p = page_of(a, e[h]);
             const bool on = t + (lane & 15) < high;
+            const auto rs = hb.keys(p);
             if (E4M3) {
-                const auto rs = buffer_of((const uint8_t*)a.c.k + tile * a.c.page_size * D, a.c.page_size * D);
 #pragma unroll
                 for (int u = 0; u < DP / 64; ++u) {
                     const int d = 64 * u + 16 * (lane >> 4);
@@ -46,10 +48,8 @@ struct Few {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
                 }
-                const auto ss = buffer_of(a.c.k_scale + tile * a.c.page_size, a.c.page_size * 4);
-                ks[h] = as_float(__builtin_amdgcn_raw_buffer_load_b32(ss, on ? row * 4 : kNoRow, 0, 0));
+                ks[h] = __builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0);
             } else {
-                const auto rs = buffer_of((const uint16_t*)a.c.k + tile * a.c.page_size * D, a.c.page_size * D * 2);
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
                     const int d = 32 * s + 8 * (lane >> 4);
@@ -62,54 +62,52 @@ struct Few {
     }
 
     // Value rows of lane group g: positions 4g .. 4g+3 of each of the two 16-position halves.
-    __device__ __forceinline__ void load_values(const AttnArgs& a, int seq, int head, int t0, int low, int high, int lane) {
+    // Positions outside [low, high) are zero (their scales are left out by value_scale).
+    __device__ __forceinline__ void load_values(const AttnArgs& a, const HeadBase& hb, const int (&e)[2], int t0, int low,
+                                                int high, int lane) {
+        constexpr int W = E4M3 ? 1 : 2;
         const int D = a.c.head_dim, g = lane >> 4, d = VW * (lane & 15);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int t = t0 + 16 * h, r0 = (t & (a.c.page_size - 1)) + 4 * g;
-            const int64_t tile = page_of(a, seq, t) * a.c.heads + head;
+            const uint32_t p = page_of(a, e[h]);
+            const auto rs = hb.values(p);
             if (E4M3) {
-                const auto rs = buffer_of((const uint8_t*)a.c.v + tile * a.c.page_size * D, a.c.page_size * D);
-                const auto ss = buffer_of(a.c.v_scale + tile * a.c.page_size, a.c.page_size * 4);
-                const u32x4v sc = __builtin_amdgcn_raw_buffer_load_b128(ss, r0 * 4, 0, 0);
+                const u32x4v sc = __builtin_amdgcn_raw_buffer_load_b128(hb.value_scales(p), r0 * 4, 0, 0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int p = t + 4 * g + j;
-                    const bool on = p < high && p >= low;
-                    vs[4 * h + j] = on ? as_float(sc[j]) : 1.f;
+                for (int j = 0; j < 4; ++j) vs[4 * h + j] = sc[j];
+            }
 #pragma unroll
-                    for (int w = 0; w < kValWords; w += 2) {  // 8 channels at a time (4 where a row has 64)
-                        const int off = on && d + 4 * w < D ? (r0 + j) * D + d + 4 * w : kNoRow;
-                        if constexpr (kValWords == 1) {
-                            vr[4 * h + j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
-                        } else {
-                            const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
-                            vr[4 * h + j][w] = x[0];
-                            vr[4 * h + j][w + 1] = x[1];
-                        }
-                    }
-                }
-            } else {
-                const auto rs = buffer_of((const uint16_t*)a.c.v + tile * a.c.page_size * D, a.c.page_size * D * 2);
+            for (int j = 0; j < 4; ++j) {
+                const int pos = t + 4 * g + j;
+                const bool on = pos < high && pos >= low;
+                constexpr int kPer = kValWords < 4 ? kValWords : 4;  // words of one load
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int p = t + 4 * g + j;
-                    const bool on = p < high && p >= low;
-                    if constexpr (kValWords == 2) {
-                        const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, on && d < D ? ((r0 + j) * D + d) * 2 : kNoRow, 0, 0);
-                        vr[4 * h + j][0] = x[0];
-                        vr[4 * h + j][1] = x[1];
+                for (int w = 0; w < kValWords; w += kPer) {
+                    const int at = d + w * 4 / W;
+                    const int off = on && at < D ? ((r0 + j) * D + at) * W : kNoRow;
+                    if constexpr (kPer == 1) {
+                        vr[4 * h + j][w] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
+                    } else if constexpr (kPer == 2) {
+                        const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
+                        vr[4 * h + j][w] = x[0];
+                        vr[4 * h + j][w + 1] = x[1];
                     } else {
+                        const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
 #pragma unroll
-                        for (int w = 0; w < kValWords; w += 4) {
-                            const int off = on && d + 2 * w < D ? ((r0 + j) * D + d + 2 * w) * 2 : kNoRow;
-                            const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) vr[4 * h + j][w + i] = x[i];
-                        }
+                        for (int i = 0; i < 4; ++i) vr[4 * h + j][w + i] = x[i];
                     }
                 }
             }
+        }
+    }
+    // A position that was not loaded has zeros for codes, but any scale: 1 instead.
+    __device__ __forceinline__ void mask_scales(int t0, int low, int high, int lane) {
+        if (!E4M3) return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int pos = t0 + 16 * (j / 4) + 4 * (lane >> 4) + j % 4;
+            if (pos >= high || pos < low) vs[j] = 0x3F800000u;
         }
     }
 
@@ -118,10 +116,10 @@ struct Few {
         u32x4v x;
         if (E4M3) {  // two words of codes per step: channels 16 g + 8 (s % 2) of the 64 of step s / 2
             const uint32_t lo = kr[h][4 * (s / 2) + 2 * (s % 2)], hi = kr[h][4 * (s / 2) + 2 * (s % 2) + 1];
-            x[0] = T::template from_e4m3<false>(lo, ks[h]);
-            x[1] = T::template from_e4m3<true>(lo, ks[h]);
-            x[2] = T::template from_e4m3<false>(hi, ks[h]);
-            x[3] = T::template from_e4m3<true>(hi, ks[h]);
+            x[0] = T::template from_e4m3<false>(lo, as_float(ks[h]));
+            x[1] = T::template from_e4m3<true>(lo, as_float(ks[h]));
+            x[2] = T::template from_e4m3<false>(hi, as_float(ks[h]));
+            x[3] = T::template from_e4m3<true>(hi, as_float(ks[h]));
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = kr[h][4 * s + i];
@@ -134,8 +132,25 @@ struct Few {
     }
     // Word of channels 2w, 2w+1 of value row j in 16 bits.
     __device__ __forceinline__ uint32_t value_word(int j, int w) const {
-        if (E4M3) return w % 2 ? T::template from_e4m3<true>(vr[j][w / 2], vs[j]) : T::template from_e4m3<false>(vr[j][w / 2], vs[j]);
+        if (E4M3) return w % 2 ? T::template from_e4m3<true>(vr[j][w / 2], as_float(vs[j])) : T::template from_e4m3<false>(vr[j][w / 2], as_float(vs[j]));
         return vr[j][w];
+    }
+    // The A operands of channels 2w and 2w + 1 of every lane: tokens in pairs.
+    __device__ __forceinline__ void value_operands(int w, u32x4v& v0, u32x4v& v1) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t x = value_word(2 * i, w), y = value_word(2 * i + 1, w);
+            v0[i] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+            v1[i] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+        }
+    }
+    __device__ __forceinline__ bool any_odd() const {
+        bool odd = false;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int w = 0; w < VW / 2; ++w) odd |= T::odd(value_word(j, w));
+        return odd;
     }
 };
 
@@ -194,10 +209,24 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         for (int i = 0; i < VW; ++i) o[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
 
         F f;
+        const HeadBase hb(a, p.head, E4M3 ? 1 : 2);
         int t0 = t_base + p.unit * kFewTokens + 32 * wave;
-        f.load_keys(a, p.seq, p.head, t0, high, lane);
-        f.load_values(a, p.seq, p.head, t0, low, high, lane);
+        int here[2] = {entry_of(a, p.seq, t0), entry_of(a, p.seq, t0 + 16)};
+        // keys before values, here as in the loop: the wait for the older loads then leaves the younger
+        // ones in flight
+        f.load_keys(a, hb, here, t0, high, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        f.load_values(a, hb, here, t0, low, high, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        int next[2] = {entry_of(a, p.seq, t0 + kFewTokens), entry_of(a, p.seq, t0 + kFewTokens + 16)};
         for (int k = p.unit; k < last; ++k, t0 += kFewTokens) {
+            here[0] = next[0];
+            here[1] = next[1];
+            next[0] = entry_of(a, p.seq, t0 + 2 * kFewTokens);
+            next[1] = entry_of(a, p.seq, t0 + 2 * kFewTokens + 16);
+            // (the last unit loads nothing, with the same instructions: no branch between loads, whose
+            // number in flight the waits count)
+            const int next_high = k + 1 < last ? high : 0;
             f32x4v s[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -205,7 +234,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
 #pragma unroll
                 for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(f.key_operand(h, st), qr[st], s[h]);
             }
-            if (k + 1 < last) f.load_keys(a, p.seq, p.head, t0 + kFewTokens, high, lane);
+            f.load_keys(a, hb, here, t0 + kFewTokens, next_high, lane);
             float x[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[i] = s[i / 4][i % 4] * a.scale_log2;
@@ -238,37 +267,36 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             u32x4v pb;
 #pragma unroll
             for (int i = 0; i < 4; ++i) pb[i] = T::pack(x[2 * i], x[2 * i + 1]);
-            bool odd = false;  // an infinity or NaN that some row must not see
+            bool odd = false;  // an infinity or NaN that some row may not see
+            if (masked) {
+                f.mask_scales(t0, low, high, lane);
+                odd = __any(f.any_odd());
+            }
+            if (!odd) {
 #pragma unroll
-            for (int w = 0; w < VW / 2; ++w) {
-                uint32_t v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = f.value_word(j, w);
-                if (masked)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) odd |= T::odd(v[j]);
-                u32x4v a0, a1;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a0[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x05040100u);
-                    a1[i] = __builtin_amdgcn_perm(v[2 * i + 1], v[2 * i], 0x07060302u);
+                for (int w = 0; w < VW / 2; ++w) {
+                    u32x4v v0, v1;
+                    f.value_operands(w, v0, v1);
+                    o[2 * w] = T::mfma16(v0, pb, o[2 * w]);
+                    o[2 * w + 1] = T::mfma16(v1, pb, o[2 * w + 1]);
                 }
-                if (!(masked && __any(odd))) {
-                    o[2 * w] = T::mfma16(a0, pb, o[2 * w]);
-                    o[2 * w + 1] = T::mfma16(a1, pb, o[2 * w + 1]);
-                } else {
-                    // 0 * infinity would be NaN in rows that do not see the token: what is finite as
-                    // ever, the rest one token at a time and added only where it is seen
-                    u32x4v f0, f1;
+            } else {
+                // 0 * infinity would be NaN in rows that do not see the token: what is finite as
+                // ever, the rest one token at a time and added only where it is seen
+#pragma unroll
+                for (int w = 0; w < VW / 2; ++w) {
+                    u32x4v v0, v1, f0, f1;
+                    f.value_operands(w, v0, v1);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        f0[i] = T::finite(a0[i]);
-                        f1[i] = T::finite(a1[i]);
-                        a0[i] ^= f0[i];
-                        a1[i] ^= f1[i];
+                        f0[i] = T::finite(v0[i]);
+                        f1[i] = T::finite(v1[i]);
+                        v0[i] ^= f0[i];
+                        v1[i] ^= f1[i];
                     }
                     o[2 * w] = T::mfma16(f0, pb, o[2 * w]);
                     o[2 * w + 1] = T::mfma16(f1, pb, o[2 * w + 1]);
+#pragma unroll 1
                     for (int j = 0; j < 32; ++j) {
                         const int t = t0 + 16 * ((j & 7) / 4) + 4 * (j >> 3) + (j & 3);
                         const bool mine = (lane >> 4) == (j >> 3);
@@ -276,8 +304,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t keep = mine && (j & 7) / 2 == i ? ((j & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-                            b0[i] = a0[i] & keep;
-                            b1[i] = a1[i] & keep;
+                            b0[i] = v0[i] & keep;
+                            b1[i] = v1[i] & keep;
                         }
                         const f32x4v z = {0.f, 0.f, 0.f, 0.f};
                         const f32x4v y0 = T::mfma16(b0, pb, z), y1 = T::mfma16(b1, pb, z);
@@ -288,7 +316,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                     }
                 }
             }
-            if (k + 1 < last) f.load_values(a, p.seq, p.head, t0 + kFewTokens, low, high, lane);
+            f.load_values(a, hb, here, t0 + kFewTokens, low, next_high, lane);
         }
         l = sum_quarters(l);
 
@@ -311,49 +339,51 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         const int rows = min(kFewRows, q.rows - p.tile * kFewRows);
         const bool whole = p.unit == 0 && last == units;
         const int owner = whole ? me : cut.owner(item), behind = whole ? me : cut.owner(item + units - 1);
-        constexpr int kFloats = kFewRows * (DP + 2);
+        constexpr int kFloats = kFewRows * (DP + 2);  // a pair (maximum, sum) per row, then the rows
         float* mine = a.part + (int64_t)(2 * me + (p.unit == 0 ? 1 : 0)) * kFloats;
-        for (int i = threadIdx.x; i < rows * DP; i += 64 * kFewWaves) {
-            const int r = i / DP, d = i % DP;
+        auto write = [&](int r, int d, float L, float x, float y) {  // channels d, d + 1 of row r
+            const int rw = p.tile * kFewRows + r;
+            const float inv = L != 0.f ? 1.f / L : 0.f;
+            uint16_t* op = (uint16_t*)a.o + (int64_t)(q.first + rw / a.share) * a.o_stride +
+                           (int64_t)(p.head * a.share + rw % a.share) * D + d;
+            if (d < D) *(uint32_t*)op = L != 0.f ? T::pack(x * inv, y * inv) : 0u;
+        };
+        for (int i = threadIdx.x; i < rows * (DP / 2); i += 64 * kFewWaves) {
+            const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
             float M = sh_m[0][r];
 #pragma unroll
             for (int w = 1; w < kFewWaves; ++w) M = fmaxf(M, sh_m[w][r]);
-            float L = 0.f, O = 0.f;
+            float L = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
             for (int w = 0; w < kFewWaves; ++w) {
                 const float by = exp2_fast(sh_m[w][r] - M);
                 L += by * sh_l[w][r];
-                O += by * sh_o[w][r][d];
+                x += by * sh_o[w][r][d];
+                y += by * sh_o[w][r][d + 1];
             }
             if (whole) {
-                const int rw = p.tile * kFewRows + r;
-                if (d < D)
-                    ((uint16_t*)a.o)[(int64_t)(q.first + rw / a.share) * a.o_stride + (int64_t)(p.head * a.share + rw % a.share) * D + d] =
-                        (uint16_t)T::pack(L != 0.f ? O / L : 0.f, 0.f);
+                write(r, d, L, x, y);
             } else {
-                mine[2 * kFewRows + i] = O;
-                if (d == 0) {
-                    mine[r] = M;
-                    mine[kFewRows + r] = L;
-                }
+                put2(mine + 2 * kFewRows + r * DP + d, x, y);
+                if (d == 0) put2(mine + 2 * r, M, L);
             }
         }
         if (!whole && arrive_last(a.count + owner, (uint32_t)(behind - owner + 1), &sh_last)) {
-            for (int i = threadIdx.x; i < rows * DP; i += 64 * kFewWaves) {
-                const int r = i / DP, d = i % DP;
-                const float* x = a.part + (int64_t)(2 * owner + 1) * kFloats;
-                float M = x[r], L = x[kFewRows + r], O = x[2 * kFewRows + i];
-                for (int w = owner + 1; w <= behind; ++w) {
-                    const float* y = a.part + (int64_t)(2 * w) * kFloats;
-                    const float to = fmaxf(M, y[r]), b0 = exp2_fast(M - to), b1 = exp2_fast(y[r] - to);
+            for (int i = threadIdx.x; i < rows * (DP / 2); i += 64 * kFewWaves) {
+                const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
+                float M = kNoScore, L = 0.f, x = 0.f, y = 0.f;
+                for (int w = owner; w <= behind; ++w) {
+                    const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
+                    float m1, l1, x1, y1;
+                    get2(part + 2 * r, &m1, &l1);
+                    get2(part + 2 * kFewRows + r * DP + d, &x1, &y1);
+                    const float to = fmaxf(M, m1), b0 = exp2_fast(M - to), b1 = exp2_fast(m1 - to);
                     M = to;
-                    L = L * b0 + y[kFewRows + r] * b1;
-                    O = O * b0 + y[2 * kFewRows + i] * b1;
+                    L = L * b0 + l1 * b1;
+                    x = x * b0 + x1 * b1;
+                    y = y * b0 + y1 * b1;
                 }
-                const int rw = p.tile * kFewRows + r;
-                if (d < D)
-                    ((uint16_t*)a.o)[(int64_t)(q.first + rw / a.share) * a.o_stride + (int64_t)(p.head * a.share + rw % a.share) * D + d] =
-                        (uint16_t)T::pack(L != 0.f ? O / L : 0.f, 0.f);
+                write(r, d, L, x, y);
             }
         }
 

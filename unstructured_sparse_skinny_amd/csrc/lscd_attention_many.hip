@@ -43,32 +43,28 @@ struct Many {
 
     u32x4v k[kPasses], v[kPasses];
     float ks[kPasses], vs[kPasses];
-    int64_t page[kPasses];  // of the next tile to load
+    int entry[kPasses];  // table entries of the next tile to load
 
     __device__ __forceinline__ static int row_of(int pass, int tid) { return pass * kPassRows + tid / kPer; }
 
     __device__ __forceinline__ void look_up(const AttnArgs& a, int seq, int t0, int wave) {
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) page[i] = page_of(a, seq, t0 + i * kPassRows + wave * (64 / kPer));
+        for (int i = 0; i < kPasses; ++i) entry[i] = entry_of(a, seq, t0 + i * kPassRows + wave * (64 / kPer));
     }
-    // Loads the tile whose pages look_up() found; rows from `high` on are zero.
-    __device__ __forceinline__ void load(const AttnArgs& a, int head, int t0, int low, int high, int tid) {
+    // Loads the tile whose entries look_up() found; rows from `high` on are zero.
+    __device__ __forceinline__ void load(const AttnArgs& a, const HeadBase& hb, int t0, int low, int high, int tid) {
         const int D = a.c.head_dim, width = E4M3 ? 1 : 2, d = (tid % kPer) * (E4M3 ? 16 : 8);
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int t = t0 + row_of(i, tid), row = t & (a.c.page_size - 1);
-            const int64_t tile = page[i] * a.c.heads + head;
-            const auto kb = buffer_of((const uint8_t*)a.c.k + tile * a.c.page_size * D * width, a.c.page_size * D * width);
-            const auto vb = buffer_of((const uint8_t*)a.c.v + tile * a.c.page_size * D * width, a.c.page_size * D * width);
+            const uint32_t p = page_of(a, entry[i]);
             const bool on = t < high && t >= low;
             const int at = on && d < D ? (row * D + d) * width : kNoRow;
-            k[i] = __builtin_amdgcn_raw_buffer_load_b128(kb, at, 0, 0);
-            v[i] = __builtin_amdgcn_raw_buffer_load_b128(vb, at, 0, 0);
+            k[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.keys(p), at, 0, 0);
+            v[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.values(p), at, 0, 0);
             if (E4M3) {
-                const auto ksb = buffer_of(a.c.k_scale + tile * a.c.page_size, a.c.page_size * 4);
-                const auto vsb = buffer_of(a.c.v_scale + tile * a.c.page_size, a.c.page_size * 4);
-                ks[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(ksb, on ? row * 4 : kNoRow, 0, 0));
-                vs[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(vsb, on ? row * 4 : kNoRow, 0, 0));
+                ks[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0));
+                vs[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(hb.value_scales(p), on ? row * 4 : kNoRow, 0, 0));
             }
         }
     }
@@ -164,9 +160,10 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
             for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
 
         F f;
+        const HeadBase hb(a, p.head, E4M3 ? 1 : 2);
         int t0 = t_base + p.unit * kManyTokens;
         f.look_up(a, p.seq, t0, wave);
-        f.load(a, p.head, t0, low, high, tid);
+        f.load(a, hb, t0, low, high, tid);
         f.look_up(a, p.seq, t0 + kManyTokens, wave);
         __syncthreads();  // the previous item's reads of the buffers are done
         f.store(sh[0][0], sh[0][1], tid);
@@ -174,7 +171,7 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
         for (int k = p.unit; k < last; ++k, t0 += kManyTokens) {
             const int buf = (k - p.unit) & 1;
             if (k + 1 < last) {
-                f.load(a, p.head, t0 + kManyTokens, low, high, tid);
+                f.load(a, hb, t0 + kManyTokens, low, high, tid);
                 f.look_up(a, p.seq, t0 + 2 * kManyTokens, wave);
             }
             if (t0 < some_high && t0 + kManyTokens > some_low) {
@@ -269,33 +266,36 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
         if (!whole) {
             const int owner = cut.owner(item), behind = cut.owner(item + units - 1);
             float* mine = a.part + (int64_t)(2 * me + (p.unit == 0 ? 1 : 0)) * kFloats;
-            if (half == 0) {
-                mine[32 * wave + lane] = m;
-                mine[kManyRows + 32 * wave + lane] = l;
-            }
+            // a pair (maximum, sum) per row, then each lane's values as it holds them
+            auto at = [&](int b, int i) { return 2 * kManyRows + (((wave * F::kBlocks + b) * 8 + i / 2) * 64 + lane) * 2; };
+            if (half == 0) put2(mine + 2 * (32 * wave + lane), m, l);
 #pragma unroll
             for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    f32x4v x = {o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
-                    *(f32x4v*)(mine + 2 * kManyRows + ((((wave * F::kBlocks + b) * 4) + i / 4) * 64 + lane) * 4) = x;
-                }
+                for (int i = 0; i < 16; i += 2) put2(mine + at(b, i), o[b][i], o[b][i + 1]);
             write = arrive_last(a.count + owner, (uint32_t)(behind - owner + 1), &sh_last);
             if (write) {
+                m = kNoScore;
+                l = 0.f;
+#pragma unroll
+                for (int b = 0; b < F::kBlocks; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
                 for (int w = owner; w <= behind; ++w) {
-                    const float* y = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
-                    const float my = y[32 * wave + (lane & 31)], ly = y[kManyRows + 32 * wave + (lane & 31)];
-                    const float to = w == owner ? my : fmaxf(m, my);
-                    const float b0 = w == owner ? 0.f : exp2_fast(m - to), b1 = exp2_fast(my - to);
+                    const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
+                    float m1, l1;
+                    get2(part + 2 * (32 * wave + (lane & 31)), &m1, &l1);
+                    const float to = fmaxf(m, m1), b0 = exp2_fast(m - to), b1 = exp2_fast(m1 - to);
                     m = to;
-                    l = (w == owner ? 0.f : l * b0) + ly * b1;
+                    l = l * b0 + l1 * b1;
 #pragma unroll
                     for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
-                        for (int i = 0; i < 16; i += 4) {
-                            const f32x4v x = *(const f32x4v*)(y + 2 * kManyRows + ((((wave * F::kBlocks + b) * 4) + i / 4) * 64 + lane) * 4);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) o[b][i + r] = (w == owner ? 0.f : o[b][i + r] * b0) + x[r] * b1;
+                        for (int i = 0; i < 16; i += 2) {
+                            float x, y;
+                            get2(part + at(b, i), &x, &y);
+                            o[b][i] = o[b][i] * b0 + x * b1;
+                            o[b][i + 1] = o[b][i + 1] * b0 + y * b1;
                         }
                 }
             }
