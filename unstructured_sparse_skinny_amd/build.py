@@ -35,6 +35,9 @@ DEVICE_SOURCES_BY_FORMAT = {
     "three-level": _COMMON_DEVICE + ["csrc/lscd_three_level.hip"],
 }
 DEVICE_SOURCES = sorted({f for v in DEVICE_SOURCES_BY_FORMAT.values() for f in v})
+# Sources compiled without the option that keeps MFMA results in ordinary registers: the compiler ends
+# on the 256-channel kernels of this one with it, and its 128-channel ones come out the same.
+DEFAULT_MFMA_REGISTERS = ("csrc/lscd_attention_many.hip",)
 ARCH = os.environ.get("LSCD_OFFLOAD_ARCH", "gfx950")
 
 
@@ -62,7 +65,11 @@ def build(verbose: bool = False, pkg_dir: str = HERE) -> str:
 
     def compile_one(src):
         obj = os.path.join(build_dir, os.path.basename(src) + ".o")
-        cmd = [hipcc, *_flags(), "-I", os.path.join(pkg_dir, "csrc"), "-c", os.path.join(pkg_dir, src),
+        flags = _flags()
+        if src in DEFAULT_MFMA_REGISTERS:
+            i = flags.index("-amdgpu-mfma-vgpr-form")
+            del flags[i - 1:i + 1]
+        cmd = [hipcc, *flags, "-I", os.path.join(pkg_dir, "csrc"), "-c", os.path.join(pkg_dir, src),
                "-o", obj]
         if src.endswith(".cpp"):
             cmd[1:1] = ["-x", "hip"]

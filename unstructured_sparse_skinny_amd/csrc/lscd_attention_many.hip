@@ -20,16 +20,20 @@ constexpr int kManyThreads = 64 * kManyWaves;
 
 typedef __attribute__((address_space(3))) s16x4v lds_s16x4;
 
+// Tokens of a tile: fewer for heads of more than 128 channels, whose registers would not hold more.
+constexpr int many_tokens(int dp) { return dp <= 128 ? kManyTokens : kManyTokens / 2; }
+
 template <typename T, bool E4M3, int DP>
 struct Many {
     static constexpr int kSteps = DP / 16;    // MFMA steps over the channels of q . k
     static constexpr int kBlocks = DP / 32;   // 32-channel blocks of the output
     static constexpr int kRow = DP * 2;       // bytes of an LDS row
-    static constexpr int kTile = kManyTokens * kRow;
+    static constexpr int kTokens = many_tokens(DP);
+    static constexpr int kTile = kTokens * kRow;
     // 16-byte loads: lanes per row (a power of two that covers DP), rows per pass, passes
     static constexpr int kPer = DP <= 64 ? (E4M3 ? 4 : 8) : DP <= 128 ? (E4M3 ? 8 : 16) : (E4M3 ? 16 : 32);
     static constexpr int kPassRows = kManyThreads / kPer;
-    static constexpr int kPasses = kManyTokens / kPassRows;
+    static constexpr int kPasses = kTokens / kPassRows;
     static_assert(64 / kPer <= 16, "a wavefront's rows of one pass lie in one page");
 
     __device__ static __forceinline__ int key_at(int row, int chunk) {
@@ -107,13 +111,13 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
     const int G = gridDim.x;
     // consecutive ranges on one XCD (workgroups go to the 8 XCDs in turn): they share keys in its L2
     const int me = (G & 7) == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
-    const int64_t U = total_units<kManyRows, kManyTokens, false>(a, lane);
+    const int64_t U = total_units<kManyRows, F::kTokens, false>(a, lane);
     if (U == 0) return;
     const Cut cut(U, G);
     int64_t u = cut.begin(me);
     const int64_t end = cut.begin(me + 1);
     if (u >= end) return;
-    Place p = find_unit<kManyRows, kManyTokens, false>(a, u, lane);
+    Place p = find_unit<kManyRows, F::kTokens, false>(a, u, lane);
     Seq q = read_seq(a, p.seq);
     const int D = a.c.head_dim;
 
@@ -125,10 +129,10 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
     while (u < end) {
         int low, high;
         tile_range<kManyRows>(a, q, p.tile, &low, &high);
-        const int units = max(1, (high + kManyTokens - 1) / kManyTokens - low / kManyTokens);
+        const int units = max(1, (high + F::kTokens - 1) / F::kTokens - low / F::kTokens);
         const int64_t item = u - p.unit;
         const int last = (int)min((int64_t)units, p.unit + (end - u));
-        const int t_base = low / kManyTokens * kManyTokens;
+        const int t_base = low / F::kTokens * F::kTokens;
 
         const int row0 = p.tile * kManyRows + 32 * wave, row = row0 + (lane & 31);
         const bool live = row < q.rows;
@@ -141,7 +145,9 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
             const int d = 16 * s + 8 * half;
             qr[s] = u32x4v{0u, 0u, 0u, 0u};
             if (live && d < D) qr[s] = *(const u32x4v*)(qp + d);
+            if (a.scale_log2 < 0.f) qr[s] ^= 0x80008000u;  // so that the scale below is positive
         }
+        const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);  // (hidden scores of -infinity stay that with a scale of 0)
         const int pos = q.len - q.n + token;
         const int see_high = live ? (a.causal ? min(pos + 1, q.len) : q.len) : 0;
         const int see_low = a.window ? pos - a.window + 1 : 0;
@@ -161,39 +167,36 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
 
         F f;
         const HeadBase hb(a, p.head, E4M3 ? 1 : 2);
-        int t0 = t_base + p.unit * kManyTokens;
+        int t0 = t_base + p.unit * F::kTokens;
         f.look_up(a, p.seq, t0, wave);
         f.load(a, hb, t0, low, high, tid);
-        f.look_up(a, p.seq, t0 + kManyTokens, wave);
+        f.look_up(a, p.seq, t0 + F::kTokens, wave);
         __syncthreads();  // the previous item's reads of the buffers are done
         f.store(sh[0][0], sh[0][1], tid);
         __syncthreads();
-        for (int k = p.unit; k < last; ++k, t0 += kManyTokens) {
+        for (int k = p.unit; k < last; ++k, t0 += F::kTokens) {
             const int buf = (k - p.unit) & 1;
             if (k + 1 < last) {
-                f.load(a, hb, t0 + kManyTokens, low, high, tid);
-                f.look_up(a, p.seq, t0 + 2 * kManyTokens, wave);
+                f.load(a, hb, t0 + F::kTokens, low, high, tid);
+                f.look_up(a, p.seq, t0 + 2 * F::kTokens, wave);
             }
-            if (t0 < some_high && t0 + kManyTokens > some_low) {
+            if (t0 < some_high && t0 + F::kTokens > some_low) {
                 const unsigned char* kb = sh[buf][0];
                 unsigned char* vb = sh[buf][1];
-                f32x16v s[2];
+                constexpr int kHalves = F::kTokens / 32;
+                f32x16v s[kHalves];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int h = 0; h < kHalves; ++h) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
 #pragma unroll
                     for (int st = 0; st < F::kSteps; ++st)
                         s[h] = T::mfma32(*(const u32x4v*)(kb + F::key_at(key_row, 2 * st + half) + h * 32 * F::kRow), qr[st], s[h]);
                 }
-                const bool masked = t0 < all_low || t0 + kManyTokens > all_high;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) s[h][i] *= a.scale_log2;
+                const bool masked = t0 < all_low || t0 + F::kTokens > all_high;
                 if (masked) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < kHalves; ++h)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const int t = t0 + 32 * h + 8 * (i / 4) + 4 * half + i % 4;
@@ -202,9 +205,10 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
                 }
                 float most = s[0][0];
 #pragma unroll
-                for (int i = 1; i < 32; ++i) most = fmaxf(most, s[i / 16][i % 16]);
-                if (__any(most > m + kLazy)) {
-                    const float to = fmaxf(m, max_halves(most));
+                for (int i = 1; i < 16 * kHalves - 1; i += 2) most = max3(most, s[i / 16][i % 16], s[(i + 1) / 16][(i + 1) % 16]);
+                most = max3(most, s[kHalves - 1][15], s[kHalves - 1][15]);
+                if (__any(most * scale > m + kLazy)) {
+                    const float to = fmaxf(m, max_halves(most) * scale);
                     const float by = exp2_fast(m - to);
                     m = to;
                     l *= by;
@@ -213,44 +217,60 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[b][i] *= by;
                 }
-                u32x4v pb[4];
+                u32x4v pb[F::kTokens / 16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float x = exp2_fast(s[i / 8][(2 * i) % 16] - m), y = exp2_fast(s[i / 8][(2 * i) % 16 + 1] - m);
-                    l += x + y;
-                    pb[i / 4][i % 4] = T::pack(x, y);
+                for (int i = 0; i < F::kTokens / 4; ++i) {
+                    const float x = exp2_fast(__builtin_fmaf(s[i / 8][(2 * i) % 16], scale, -m));
+                    const float y = exp2_fast(__builtin_fmaf(s[i / 8][(2 * i) % 16 + 1], scale, -m));
+                    const uint32_t w = T::pack(x, y);
+                    l = T::add_pair(w, l);
+                    pb[i / 4][i % 4] = w;
                 }
+                auto value = [&](int b, int ks) {  // A operand of channels 32 b .., tokens 16 ks ..
+                    const int at = vtok * F::kRow + (((4 * b + vchunk) ^ F::val_swizzle(vtok)) << 4) + vhalf + 16 * ks * F::kRow;
+                    const auto x = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at)));
+                    const auto y = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at + 8 * F::kRow)));
+                    return u32x4v{x[0], x[1], y[0], y[1]};
+                };
+                if (!masked) {
 #pragma unroll
-                for (int b = 0; b < F::kBlocks; ++b) {
-                    const int at = vtok * F::kRow + (((4 * b + vchunk) ^ F::val_swizzle(vtok)) << 4) + vhalf;
+                    for (int ks = 0; ks < F::kTokens / 16; ++ks)
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const auto x = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at + 16 * ks * F::kRow)));
-                        const auto y = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at + (16 * ks + 8) * F::kRow)));
-                        const u32x4v av = {x[0], x[1], y[0], y[1]};
-                        if (masked && __any(T::odd(av[0]) || T::odd(av[1]) || T::odd(av[2]) || T::odd(av[3]))) {
-                            // 0 * infinity would be NaN in rows that do not see the token: what is
-                            // finite as ever, the rest one token at a time, added only where it is seen
-                            u32x4v fin;
+                        for (int b = 0; b < F::kBlocks; ++b) o[b] = T::mfma32(value(b, ks), pb[ks], o[b]);
+                } else {
+                    // A row that does not see a token has weight 0 for it, but 0 * infinity is NaN: the
+                    // product takes what is finite, and infinities and NaN are added where they are seen
+                    // (any weight that is not zero leaves them as they are).
+                    bool odd = false;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) fin[i] = T::finite(av[i]);
-                            o[b] = T::mfma32(fin, pb[ks], o[b]);
-                            for (int j = 0; j < 16; ++j) {
-                                const int t = t0 + 16 * ks + 8 * ((j & 7) >> 2) + 4 * (j >> 3) + (j & 3);
-                                u32x4v one;
+                    for (int ks = 0; ks < F::kTokens / 16; ++ks)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    one[i] = half == (j >> 3) && (j & 7) / 2 == i ? (av[i] ^ fin[i]) & ((j & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
-                                f32x16v z;
+                        for (int b = 0; b < F::kBlocks; ++b) {
+                            u32x4v x = value(b, ks);
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) z[i] = 0.f;
-                                z = T::mfma32(one, pb[ks], z);
-                                if (t < see_high && t >= see_low)
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i) o[b][i] += z[i];
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t w = T::finite(x[i]);
+                                odd |= w != x[i];
+                                x[i] = w;
                             }
-                        } else {
-                            o[b] = T::mfma32(av, pb[ks], o[b]);
+                            o[b] = T::mfma32(x, pb[ks], o[b]);
+                        }
+                    if (__any(odd)) {
+#pragma unroll 1
+                        for (int t = 0; t < F::kTokens; ++t) {
+                            const bool seen = t0 + t < see_high && t0 + t >= see_low;
+#pragma unroll
+                            for (int b = 0; b < F::kBlocks; ++b)
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) {
+                                    const u32x2v x = *(const u32x2v*)(vb + F::val_at(t, 4 * b + i / 4) + 8 * half);
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j) {
+                                        const uint32_t w = seen ? x[j] ^ T::finite(x[j]) : 0u;
+                                        o[b][i + 2 * j] += T::low(w);
+                                        o[b][i + 2 * j + 1] += T::high(w);
+                                    }
+                                }
                         }
                     }
                 }

@@ -46,6 +46,11 @@ struct F16 {
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(half8v, a), __builtin_bit_cast(half8v, b), c, 0,
                                                       0, 0);
     }
+    // sum of the pair's values, and s
+    __device__ static __forceinline__ float add_pair(uint32_t w, float s) {
+        const half2v one = {(_Float16)1.f, (_Float16)1.f};
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, w), one, s, false);
+    }
     // whether either value of the pair is an infinity or NaN
     __device__ static __forceinline__ bool odd(uint32_t w) {
         return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
@@ -75,6 +80,10 @@ struct BF16 {
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8v, a), __builtin_bit_cast(bf8v, b), c, 0, 0,
                                                        0);
     }
+    __device__ static __forceinline__ float add_pair(uint32_t w, float s) {
+        const bf2v one = {(__bf16)1.f, (__bf16)1.f};
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2v, w), one, s, false);
+    }
     __device__ static __forceinline__ bool odd(uint32_t w) {
         return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
     }
@@ -85,6 +94,13 @@ struct BF16 {
 };
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32
+
+// Largest of three, without the quieting of NaN that fmaxf asks for.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
 
 // The values of the lanes l and l ^ 32 (l and l ^ 16): the swap exchanges halves (odd and even
 // quarters) of two registers.
