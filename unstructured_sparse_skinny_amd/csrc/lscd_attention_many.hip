@@ -1,8 +1,8 @@
-// Attention over a paged cache for many query rows (a chunk of a prompt): 128 rows (tokens x heads
+// Attention over a paged cache for many query rows (a chunk of a prompt): 256 rows (tokens x heads
 // that share a key head) per item, bound by the matrix cores and the exponentials between the two
 // products.
 //
-// A workgroup is four wavefronts of 32 rows each; they share tiles of 64 keys and values in LDS,
+// A workgroup is eight wavefronts of 32 rows each; they share tiles of 64 keys and values in LDS,
 // double-buffered with one barrier per tile: the next tile's loads are issued before the current
 // one is computed and written to the other buffer after it (codes of an 8-bit cache become 16-bit
 // values on the way; scales are powers of two, so that rounds nothing).  Keys are read back row by
@@ -20,6 +20,9 @@ constexpr int kManyThreads = 64 * kManyWaves;
 
 typedef __attribute__((address_space(3))) s16x4v lds_s16x4;
 
+// Kinds of instructions for the scheduler's group barriers.
+constexpr int kSchedVector = 0x2, kSchedMfma = 0x8, kSchedLdsRead = 0x100;
+
 // Tokens of a tile: fewer for heads of more than 128 channels, whose registers would not hold more.
 constexpr int many_tokens(int dp) { return dp <= 128 ? kManyTokens : kManyTokens / 2; }
 
@@ -33,7 +36,8 @@ struct Many {
     // 16-byte loads: lanes per row (a power of two that covers DP), rows per pass, passes
     static constexpr int kPer = DP <= 64 ? (E4M3 ? 4 : 8) : DP <= 128 ? (E4M3 ? 8 : 16) : (E4M3 ? 16 : 32);
     static constexpr int kPassRows = kManyThreads / kPer;
-    static constexpr int kPasses = kTokens / kPassRows;
+    static constexpr int kPasses = kTokens < kPassRows ? 1 : kTokens / kPassRows;
+    static constexpr bool kSpare = kTokens < kPassRows;  // some threads have no row
     static_assert(64 / kPer <= 16, "a wavefront's rows of one pass lie in one page");
 
     __device__ static __forceinline__ int key_at(int row, int chunk) {
@@ -62,7 +66,7 @@ struct Many {
         for (int i = 0; i < kPasses; ++i) {
             const int t = t0 + row_of(i, tid), row = t & (a.c.page_size - 1);
             const uint32_t p = page_of(a, entry[i]);
-            const bool on = t < high && t >= low;
+            const bool on = t < high && t >= low && (!kSpare || row_of(i, tid) < kTokens);
             const int at = on && d < D ? (row * D + d) * width : kNoRow;
             k[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.keys(p), at, 0, 0);
             v[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.values(p), at, 0, 0);
@@ -72,16 +76,21 @@ struct Many {
             }
         }
     }
-    __device__ __forceinline__ void store(unsigned char* kb, unsigned char* vb, int tid) const {
+    // Writes the loaded tile as 16-bit values.  `edge`: some row may not see some position; such a row's
+    // weight is 0, but 0 * infinity is NaN, so infinities and NaN among the values become zeros (the kernel
+    // adds them where they are seen, when the item is done).  Returns whether this lane had any.
+    __device__ __forceinline__ bool store(unsigned char* kb, unsigned char* vb, int tid, bool edge) {
         const int c = tid % kPer;
+        bool odd = false;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int row = row_of(i, tid);
-            if (E4M3) {
-                if (DP == 96 && c >= DP / 16) continue;
+            if (kSpare && row >= kTokens) continue;
+            if (DP == 96 && c >= DP / (E4M3 ? 16 : 8)) continue;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    u32x4v x, y;
+            for (int h = 0; h < (E4M3 ? 2 : 1); ++h) {
+                u32x4v x = k[i], y = v[i];
+                if (E4M3) {
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
                         x[2 * w] = T::template from_e4m3<false>(k[i][2 * h + w], ks[i]);
@@ -89,20 +98,26 @@ struct Many {
                         y[2 * w] = T::template from_e4m3<false>(v[i][2 * h + w], vs[i]);
                         y[2 * w + 1] = T::template from_e4m3<true>(v[i][2 * h + w], vs[i]);
                     }
-                    *(u32x4v*)(kb + key_at(row, 2 * c + h)) = x;
-                    *(u32x4v*)(vb + val_at(row, 2 * c + h)) = y;
                 }
-            } else {
-                if (DP == 96 && c >= DP / 8) continue;
-                *(u32x4v*)(kb + key_at(row, c)) = k[i];
-                *(u32x4v*)(vb + val_at(row, c)) = v[i];
+                if (edge) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t f = T::finite(y[w]);
+                        odd |= f != y[w];
+                        y[w] = f;
+                    }
+                }
+                const int chunk = E4M3 ? 2 * c + h : c;
+                *(u32x4v*)(kb + key_at(row, chunk)) = x;
+                *(u32x4v*)(vb + val_at(row, chunk)) = y;
             }
         }
+        return odd;
     }
 };
 
 template <typename T, bool E4M3, int DP>
-__global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_many_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArgs a) {
     using F = Many<T, E4M3, DP>;
     __shared__ __attribute__((aligned(16))) unsigned char sh[2][2][F::kTile];
     __shared__ uint32_t sh_last;
@@ -158,6 +173,11 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
         const int all_high = a.causal ? min(q.len - q.n + tok0 + 1, q.len) : q.len;
         const int all_low = a.window ? q.len - q.n + tok1 - a.window + 1 : 0;
 
+        // the same for all rows of the item
+        const int end0 = p.tile * kManyRows / a.share, end1 = (min(q.rows, (p.tile + 1) * kManyRows) - 1) / a.share;
+        const int tile_all_high = a.causal ? min(q.len - q.n + end0 + 1, q.len) : q.len;
+        const int tile_all_low = a.window ? q.len - q.n + end1 - a.window + 1 : 0;
+
         float m = kNoScore, l = 0.f;
         f32x16v o[F::kBlocks];
 #pragma unroll
@@ -171,8 +191,15 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
         f.look_up(a, p.seq, t0, wave);
         f.load(a, hb, t0, low, high, tid);
         f.look_up(a, p.seq, t0 + F::kTokens, wave);
+        int any_odd = 0;  // an edge tile had infinities or NaN among its values
+        auto is_edge = [&](int t) { return t < tile_all_low || t + F::kTokens > tile_all_high; };
+        auto put = [&](int buf, int t) {
+            const bool edge = is_edge(t);
+            const bool odd = f.store(sh[buf][0], sh[buf][1], tid, edge);
+            if (edge) any_odd |= __syncthreads_or(odd);
+        };
         __syncthreads();  // the previous item's reads of the buffers are done
-        f.store(sh[0][0], sh[0][1], tid);
+        put(0, t0);
         __syncthreads();
         for (int k = p.unit; k < last; ++k, t0 += F::kTokens) {
             const int buf = (k - p.unit) & 1;
@@ -193,6 +220,14 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
                     for (int st = 0; st < F::kSteps; ++st)
                         s[h] = T::mfma32(*(const u32x4v*)(kb + F::key_at(key_row, 2 * st + half) + h * 32 * F::kRow), qr[st], s[h]);
                 }
+                // keep four reads ahead of the products
+                __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 4, 0);
+#pragma unroll
+                for (int i = 0; i < kHalves * F::kSteps - 4; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 4, 0);
                 const bool masked = t0 < all_low || t0 + F::kTokens > all_high;
                 if (masked) {
 #pragma unroll
@@ -217,68 +252,83 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[b][i] *= by;
                 }
-                u32x4v pb[F::kTokens / 16];
+                // weights of the 16 tokens of step ks, as the B operand
+                auto weights = [&](int ks) {
+                    u32x4v w;
 #pragma unroll
-                for (int i = 0; i < F::kTokens / 4; ++i) {
-                    const float x = exp2_fast(__builtin_fmaf(s[i / 8][(2 * i) % 16], scale, -m));
-                    const float y = exp2_fast(__builtin_fmaf(s[i / 8][(2 * i) % 16 + 1], scale, -m));
-                    const uint32_t w = T::pack(x, y);
-                    l = T::add_pair(w, l);
-                    pb[i / 4][i % 4] = w;
-                }
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = exp2_fast(__builtin_fmaf(s[ks / 2][8 * (ks % 2) + 2 * i], scale, -m));
+                        const float y = exp2_fast(__builtin_fmaf(s[ks / 2][8 * (ks % 2) + 2 * i + 1], scale, -m));
+                        w[i] = T::pack(x, y);
+                        l = T::add_pair(w[i], l);
+                    }
+                    return w;
+                };
                 auto value = [&](int b, int ks) {  // A operand of channels 32 b .., tokens 16 ks ..
                     const int at = vtok * F::kRow + (((4 * b + vchunk) ^ F::val_swizzle(vtok)) << 4) + vhalf + 16 * ks * F::kRow;
                     const auto x = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at)));
                     const auto y = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at + 8 * F::kRow)));
                     return u32x4v{x[0], x[1], y[0], y[1]};
                 };
-                if (!masked) {
+                u32x4v pb = weights(0);
 #pragma unroll
-                    for (int ks = 0; ks < F::kTokens / 16; ++ks)
+                for (int ks = 0; ks < F::kTokens / 16; ++ks) {
+                    const u32x4v pk = pb;
+                    if (ks + 1 < F::kTokens / 16) pb = weights(ks + 1);
 #pragma unroll
-                        for (int b = 0; b < F::kBlocks; ++b) o[b] = T::mfma32(value(b, ks), pb[ks], o[b]);
-                } else {
-                    // A row that does not see a token has weight 0 for it, but 0 * infinity is NaN: the
-                    // product takes what is finite, and infinities and NaN are added where they are seen
-                    // (any weight that is not zero leaves them as they are).
-                    bool odd = false;
-#pragma unroll
-                    for (int ks = 0; ks < F::kTokens / 16; ++ks)
-#pragma unroll
-                        for (int b = 0; b < F::kBlocks; ++b) {
-                            u32x4v x = value(b, ks);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t w = T::finite(x[i]);
-                                odd |= w != x[i];
-                                x[i] = w;
-                            }
-                            o[b] = T::mfma32(x, pb[ks], o[b]);
-                        }
-                    if (__any(odd)) {
-#pragma unroll 1
-                        for (int t = 0; t < F::kTokens; ++t) {
-                            const bool seen = t0 + t < see_high && t0 + t >= see_low;
-#pragma unroll
-                            for (int b = 0; b < F::kBlocks; ++b)
-#pragma unroll
-                                for (int i = 0; i < 16; i += 4) {
-                                    const u32x2v x = *(const u32x2v*)(vb + F::val_at(t, 4 * b + i / 4) + 8 * half);
-#pragma unroll
-                                    for (int j = 0; j < 2; ++j) {
-                                        const uint32_t w = seen ? x[j] ^ T::finite(x[j]) : 0u;
-                                        o[b][i + 2 * j] += T::low(w);
-                                        o[b][i + 2 * j + 1] += T::high(w);
-                                    }
-                                }
-                        }
-                    }
+                    for (int b = 0; b < F::kBlocks; ++b) o[b] = T::mfma32(value(b, ks), pk, o[b]);
                 }
+                // reads ahead of the products, the next step's exponentials between them
+                __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 4, 0);
+#pragma unroll
+                for (int i = 0; i < F::kBlocks * F::kTokens / 16 - 2; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 2, 0);
+                    __builtin_amdgcn_sched_group_barrier(kSchedVector, 24 / F::kBlocks, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 2, 0);
             }
-            if (k + 1 < last) f.store(sh[buf ^ 1][0], sh[buf ^ 1][1], tid);
+            if (k + 1 < last) put(buf ^ 1, t0 + F::kTokens);
             __syncthreads();
         }
         l = sum_halves(l);
+        // What follows runs once per item: addresses are worked out here, not kept in registers through
+        // the loop above (the compiler would move them out of all loops).
+        const int lane_e = opaque(lane), half_e = lane_e >> 5;
+        if (any_odd) {
+            // The infinities and NaN of edge tiles, which store() left out, for the rows that see them (a
+            // weight that is not zero leaves them as they are).  Rare: straight from the cache.
+#pragma unroll 1
+            for (int t = t_base + p.unit * F::kTokens; t < t_base + last * F::kTokens; ++t) {
+                if (!is_edge(t / F::kTokens * F::kTokens)) continue;
+                const uint32_t pg = page_of(a, entry_of(a, p.seq, t));
+                const int at = t & (a.c.page_size - 1);
+                const bool seen = t < see_high && t >= see_low;
+                float vscale = 1.f;
+                if (E4M3)
+                    vscale = as_float(__builtin_amdgcn_raw_buffer_load_b32(hb.value_scales(pg), seen ? at * 4 : kNoRow, 0, 0));
+#pragma unroll
+                for (int b = 0; b < F::kBlocks; ++b)
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const int d = 32 * b + 8 * (i / 4) + 4 * half_e;
+                        const int off = seen && d < D ? (at * D + d) * (E4M3 ? 1 : 2) : kNoRow;
+                        u32x2v x;
+                        if (E4M3) {
+                            const uint32_t c = __builtin_amdgcn_raw_buffer_load_b32(hb.values(pg), off, 0, 0);
+                            x = u32x2v{T::template from_e4m3<false>(c, vscale), T::template from_e4m3<true>(c, vscale)};
+                        } else {
+                            x = __builtin_amdgcn_raw_buffer_load_b64(hb.values(pg), off, 0, 0);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t xw = x[j], w = seen ? xw ^ T::finite(xw) : 0u;
+                            o[b][i + 2 * j] += T::low(w);
+                            o[b][i + 2 * j + 1] += T::high(w);
+                        }
+                    }
+            }
+        }
 
         const bool whole = p.unit == 0 && last == units;
         constexpr int64_t kFloats = (int64_t)kManyRows * (DP + 2);
@@ -287,8 +337,8 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
             const int owner = cut.owner(item), behind = cut.owner(item + units - 1);
             float* mine = a.part + (int64_t)(2 * me + (p.unit == 0 ? 1 : 0)) * kFloats;
             // a pair (maximum, sum) per row, then each lane's values as it holds them
-            auto at = [&](int b, int i) { return 2 * kManyRows + (((wave * F::kBlocks + b) * 8 + i / 2) * 64 + lane) * 2; };
-            if (half == 0) put2(mine + 2 * (32 * wave + lane), m, l);
+            auto at = [&](int b, int i) { return 2 * kManyRows + (((wave * F::kBlocks + b) * 8 + i / 2) * 64 + lane_e) * 2; };
+            if (half_e == 0) put2(mine + 2 * (32 * wave + lane_e), m, l);
 #pragma unroll
             for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
@@ -304,7 +354,7 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
                 for (int w = owner; w <= behind; ++w) {
                     const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
                     float m1, l1;
-                    get2(part + 2 * (32 * wave + (lane & 31)), &m1, &l1);
+                    get2(part + 2 * (32 * wave + (lane_e & 31)), &m1, &l1);
                     const float to = fmaxf(m, m1), b0 = exp2_fast(m - to), b1 = exp2_fast(m1 - to);
                     m = to;
                     l = l * b0 + l1 * b1;
@@ -322,12 +372,12 @@ __global__ __launch_bounds__(kManyThreads, DP <= 128 ? 2 : 1) void attention_man
         }
         if (write && live) {
             const float inv = l != 0.f ? 1.f / l : 0.f;
-            uint16_t* op = (uint16_t*)a.o + (int64_t)(q.first + token) * a.o_stride + (int64_t)qh * D;
+            uint16_t* op = (uint16_t*)a.o + (int64_t)(q.first + opaque(token)) * a.o_stride + (int64_t)opaque(qh) * D;
 #pragma unroll
             for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
-                    const int d = 32 * b + 8 * (i / 4) + 4 * half;
+                    const int d = 32 * b + 8 * (i / 4) + 4 * half_e;
                     u32x2v x = {T::pack(o[b][i] * inv, o[b][i + 1] * inv), T::pack(o[b][i + 2] * inv, o[b][i + 3] * inv)};
                     if (l == 0.f) x = u32x2v{0u, 0u};
                     if (d < D) *(u32x2v*)(op + d) = x;
@@ -366,7 +416,7 @@ hipError_t many_dim(const AttnArgs& a, int grid, hipStream_t s) {
 
 }  // namespace
 
-int attention_many_grid(int cus) { return 2 * cus; }
+int attention_many_grid(int cus) { return cus; }
 int64_t attention_many_floats(int dim) {
     return (int64_t)kManyRows * ((dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : 256) + 2);
 }

@@ -27,7 +27,7 @@ hipError_t launch_cache_read(const CacheMoveArgs& a, int type, hipStream_t s);
 constexpr int kAttnMaxDim = 256;
 constexpr int kFewRows = 16;      // query rows of the kernel for few rows: one MFMA tile
 constexpr int kFewTokens = 128;   // cached tokens of one of its work units (32 per wavefront)
-constexpr int kManyRows = 128;    // the kernel for many rows: 32 per wavefront
+constexpr int kManyRows = 256;    // the kernel for many rows: 32 per wavefront
 constexpr int kManyTokens = 64;
 
 struct AttnArgs {

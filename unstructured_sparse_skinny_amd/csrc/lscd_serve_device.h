@@ -95,6 +95,12 @@ struct BF16 {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32
 
+// x, in a way that the compiler does not see through.
+__device__ __forceinline__ int opaque(int x) {
+    asm("" : "+v"(x));
+    return x;
+}
+
 // Largest of three, without the quieting of NaN that fmaxf asks for.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
