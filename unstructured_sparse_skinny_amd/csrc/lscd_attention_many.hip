@@ -20,8 +20,8 @@ constexpr int kManyThreads = 64 * kManyWaves;
 
 typedef __attribute__((address_space(3))) s16x4v lds_s16x4;
 
-// Kinds of instructions for the scheduler's group barriers.
-constexpr int kSchedVector = 0x2, kSchedMfma = 0x8, kSchedLdsRead = 0x100;
+// Instructions that may cross the scheduling barriers below: vector and scalar arithmetic.
+constexpr int kSchedFree = 0x6;
 
 // Tokens of a tile: fewer for heads of more than 128 channels, whose registers would not hold more.
 constexpr int many_tokens(int dp) { return dp <= 128 ? kManyTokens : kManyTokens / 2; }
@@ -212,22 +212,25 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
                 unsigned char* vb = sh[buf][1];
                 constexpr int kHalves = F::kTokens / 32;
                 f32x16v s[kHalves];
+// reads run kAhead steps before the products that use them; the barriers keep that order
+                constexpr int kAhead = 4, kKeySteps = kHalves * F::kSteps;
+                auto key = [&](int i) {
+                    return *(const u32x4v*)(kb + F::key_at(key_row, 2 * (i % F::kSteps) + half) + i / F::kSteps * 32 * F::kRow);
+                };
+                u32x4v kr[kAhead];
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
+                for (int i = 0; i < kAhead; ++i) kr[i] = key(i);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) s[h][i] = 0.f;
+                for (int i = 0; i < kKeySteps; ++i) {
+                    const int h = i / F::kSteps;
+                    if (i % F::kSteps == 0)
 #pragma unroll
-                    for (int st = 0; st < F::kSteps; ++st)
-                        s[h] = T::mfma32(*(const u32x4v*)(kb + F::key_at(key_row, 2 * st + half) + h * 32 * F::kRow), qr[st], s[h]);
+                        for (int e = 0; e < 16; ++e) s[h][e] = 0.f;
+                    s[h] = T::mfma32(kr[i % kAhead], qr[i % F::kSteps], s[h]);
+                    if (i + kAhead < kKeySteps) kr[i % kAhead] = key(i + kAhead);
+                    __builtin_amdgcn_sched_barrier(kSchedFree);
                 }
-                // keep four reads ahead of the products
-                __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 4, 0);
-#pragma unroll
-                for (int i = 0; i < kHalves * F::kSteps - 4; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
-                }
-                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 4, 0);
                 const bool masked = t0 < all_low || t0 + F::kTokens > all_high;
                 if (masked) {
 #pragma unroll
@@ -270,23 +273,20 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
                     const auto y = __builtin_bit_cast(u32x2v, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(vb + at + 8 * F::kRow)));
                     return u32x4v{x[0], x[1], y[0], y[1]};
                 };
-                u32x4v pb = weights(0);
+                constexpr int kValSteps = F::kBlocks * F::kTokens / 16;
+                u32x4v vr[kAhead], pb[2];
 #pragma unroll
-                for (int ks = 0; ks < F::kTokens / 16; ++ks) {
-                    const u32x4v pk = pb;
-                    if (ks + 1 < F::kTokens / 16) pb = weights(ks + 1);
+                for (int i = 0; i < kAhead; ++i) vr[i] = value(i % F::kBlocks, i / F::kBlocks);
+                __builtin_amdgcn_sched_barrier(kSchedFree);
+                pb[0] = weights(0);
 #pragma unroll
-                    for (int b = 0; b < F::kBlocks; ++b) o[b] = T::mfma32(value(b, ks), pk, o[b]);
+                for (int i = 0; i < kValSteps; ++i) {
+                    const int ks = i / F::kBlocks, b = i % F::kBlocks;
+                    if (b == 0 && ks + 1 < F::kTokens / 16) pb[(ks + 1) & 1] = weights(ks + 1);  // between the products
+                    o[b] = T::mfma32(vr[i % kAhead], pb[ks & 1], o[b]);
+                    if (i + kAhead < kValSteps) vr[i % kAhead] = value((i + kAhead) % F::kBlocks, (i + kAhead) / F::kBlocks);
+                    __builtin_amdgcn_sched_barrier(kSchedFree);
                 }
-                // reads ahead of the products, the next step's exponentials between them
-                __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 4, 0);
-#pragma unroll
-                for (int i = 0; i < F::kBlocks * F::kTokens / 16 - 2; ++i) {
-                    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-                    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 2, 0);
-                    __builtin_amdgcn_sched_group_barrier(kSchedVector, 24 / F::kBlocks, 0);
-                }
-                __builtin_amdgcn_sched_group_barrier(kSchedMfma, 2, 0);
             }
             if (k + 1 < last) put(buf ^ 1, t0 + F::kTokens);
             __syncthreads();
