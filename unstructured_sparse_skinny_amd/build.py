@@ -22,7 +22,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 # The kernel families are separate translation units so that they compile in parallel.
 SOURCES = ["csrc/lscd_skinny64.hip", "csrc/lscd_skinny32.hip", "csrc/lscd_skinny16.hip", "csrc/lscd_three_level.hip",
            "csrc/lscd_bitmap.hip", "csrc/lscd_wide.hip", "csrc/lscd_kernels.hip", "csrc/lscd_encode_dev.hip",
-           "csrc/lscd_attention_many.hip", "csrc/lscd_quant.hip",
+           "csrc/lscd_attention_many.hip", "csrc/lscd_quant_bf16.hip", "csrc/lscd_quant_f16.hip",
+           "csrc/lscd_quant.hip",
            "csrc/lscd_attention_few.hip", "csrc/lscd_cache.hip", "csrc/lscd_serve.cpp",
            "csrc/lscd_api.cpp", "csrc/lscd_linear.cpp", "csrc/lscd_pack.cpp"]
 # Device sources of each format's product (their hash identifies the kernels behind a committed

@@ -42,22 +42,49 @@ __device__ __forceinline__ uint32_t take_off(uint32_t w, uint32_t less) {
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, w) + __builtin_bit_cast(half2v, less));
 }
 
-// 8 values of x from column k on, zeros from column K on.
-__device__ __forceinline__ u32x4v load_x(const uint16_t* x, int k, int K) {
+// -(16 + z) twice: 0xCC00 | z << 6 in float16.
+__device__ __forceinline__ uint32_t less_of(uint32_t z) { return (0xCC00u | z << 6) * 0x00010001u; }
+
+// 8 values of x from column k on: all of them, whatever the alignment; or up to column K, then zeros.
+__device__ __forceinline__ u32x4v load_x(const uint16_t* x) {
     struct __attribute__((packed, aligned(2))) Loose {
         uint32_t w[4];
     };
+    const Loose v = *(const Loose*)x;
+    return u32x4v{v.w[0], v.w[1], v.w[2], v.w[3]};
+}
+__device__ __forceinline__ u32x4v load_x_end(const uint16_t* x, int k, int K) {
     u32x4v r = {0u, 0u, 0u, 0u};
-    if (k + 8 <= K) {
-        const Loose v = *(const Loose*)(x + k);  // rows need not be aligned
-        r = u32x4v{v.w[0], v.w[1], v.w[2], v.w[3]};
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (k + i < K) r[i / 2] |= (uint32_t)x[k + i] << (16 * (i & 1));
-    }
+    for (int i = 0; i < 8; ++i)
+        if (k + i < K) r[i / 2] |= (uint32_t)x[i] << (16 * (i & 1));
     return r;
 }
+
+// Scales and zero points of a lane's row for one unit (kinds of quant_kind).
+template <typename T, int KIND>
+struct Aux {
+    static constexpr int kPer = KIND < 2 ? 1 : KIND;  // groups of a unit
+    static constexpr int kBytes = KIND == 0 ? 2 : 4 * KIND;
+    uint32_t w[kPer];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, int voff, int soff) {
+        if constexpr (KIND == 0) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b16(rs, voff, soff, 0);
+        } else if constexpr (KIND == 1) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, voff, soff, 0);
+        } else if constexpr (KIND == 2) {
+            const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, voff, soff, 0);
+            w[0] = x[0];
+            w[1] = x[1];
+        } else {
+            const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, voff, soff, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = x[i];
+        }
+    }
+    __device__ __forceinline__ float scale(int p) const { return T::low(w[p] & 0xFFFFu); }
+    __device__ __forceinline__ uint32_t zero(int p) const { return KIND == 0 ? 8u : w[p] >> 16; }
+};
 
 }  // namespace
 }  // namespace lscd

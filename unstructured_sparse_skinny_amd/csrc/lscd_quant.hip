@@ -1,232 +1,87 @@
-// Product of a few token vectors with a matrix of 4-bit codes and group scales (see lscd_quant.h for
-// the arithmetic): encoding into the device layout, decoding, and the product.
+// Matrices of 4-bit codes: encoding into the device layout, decoding, and how a product is split.
+
+#include <algorithm>
 
 #include "lscd_quant.h"
 
 namespace lscd {
 namespace {
 
-// ---------------------------------------------------------------- layout
 // One workgroup per row tile and 4 units: 256 threads = 4 units x 64 lanes, 4 words each.
 __global__ __launch_bounds__(256) void quant_encode_kernel(QuantEncodeArgs a) {
     const int blocks4 = (a.units + 3) / 4;
-    const int rt = blockIdx.x / blocks4, u4 = blockIdx.x % blocks4;
-    const int lane = threadIdx.x & 63, u = u4 * 4 + (threadIdx.x >> 6);
+    const int rt = blockIdx.x / blocks4, u = blockIdx.x % blocks4 * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
     const int64_t row = (int64_t)rt * kQuantRows + (lane & 15);
     auto zero_of = [&](int64_t r, int64_t g) { return r < a.M && g < a.groups && a.zeros ? a.zeros[r * a.groups + g] & 15u : 8u; };
-    if (u < a.units) {
-        u32x4v out;
+    if (u >= a.units) return;
+    u32x4v out;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            uint32_t w = 0;
+    for (int s = 0; s < 4; ++s) {
+        uint32_t w = 0;
+        const int64_t k0 = (int64_t)u * kQuantUnit + 32 * s + 8 * (lane >> 4);
+        const uint32_t z = zero_of(row, k0 / a.group);  // (groups are multiples of 32: one for the word)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int64_t k = (int64_t)u * kQuantUnit + 32 * s + 8 * (lane >> 4) + j;
-                uint32_t c = zero_of(row, k / a.group);
-                if (row < a.M && k < a.K) c = (a.q[row * a.row_bytes + k / 2] >> (4 * (k & 1))) & 15u;
+        for (int j = 0; j < 8; ++j) {
+            const int64_t k = k0 + j;
+            uint32_t c = z;
+            if (row < a.M && k < a.K) c = (a.q[row * a.row_bytes + k / 2] >> (4 * (k & 1))) & 15u;
 #pragma unroll
-                for (int b = 0; b < 4; ++b) w |= ((c >> b) & 1u) << quant_bit(j, b);
-            }
-            out[s] = w;
+            for (int b = 0; b < 4; ++b) w |= ((c >> b) & 1u) << quant_bit(j, b);
         }
-        *(u32x4v*)(a.codes + (((int64_t)rt * a.units + u) * 64 + lane) * 4) = out;
+        out[s] = w;
     }
-    if (threadIdx.x < kQuantRows) {
-        const int64_t r = (int64_t)rt * kQuantRows + threadIdx.x;
-        const int n = 4 * a.per_unit;
-        const int64_t rec = ((int64_t)rt * blocks4 + u4) * kQuantRows + threadIdx.x;
-        uint32_t z[2] = {0, 0};
-        for (int i = 0; i < n; ++i) {
-            const int64_t k = ((int64_t)u4 * 4 + i / a.per_unit) * kQuantUnit + (i % a.per_unit) * (kQuantUnit / a.per_unit);
-            const int64_t g = k / a.group;
-            a.scales_out[rec * n + i] = r < a.M && g < a.groups ? a.scales[r * a.groups + g] : (uint16_t)0;
-            z[i / 8] |= zero_of(r, g) << (4 * (i % 8));
-        }
-        if (a.zeros_out) {
-            const int words = a.per_unit == 4 ? 2 : 1;
-            for (int i = 0; i < words; ++i) a.zeros_out[rec * words + i] = z[i];
+    const int64_t unit = (int64_t)rt * a.units + u;
+    *(u32x4v*)(a.codes + (unit * 64 + lane) * 4) = out;
+    if (lane < kQuantRows) {
+        for (int p = 0; p < a.per_unit; ++p) {
+            const int64_t k = (int64_t)u * kQuantUnit + p * (kQuantUnit / a.per_unit), g = k / a.group;
+            const uint32_t s = row < a.M && g < a.groups ? a.scales[row * a.groups + g] : 0u;
+            const int64_t at = (unit * kQuantRows + lane) * a.per_unit + p;
+            if (a.short_aux)
+                ((uint16_t*)a.aux)[at] = (uint16_t)s;
+            else
+                ((uint32_t*)a.aux)[at] = s | zero_of(row, g) << 16;
         }
     }
 }
 
-// Scales and zero points of one lane's row for 4 units.
-template <int PER>
-struct Aux {
-    static constexpr int kWords = 2 * PER;  // words of 4 * PER scales
-    uint32_t s[kWords], z[PER == 4 ? 2 : 1];
-    __device__ __forceinline__ void load(const QuantArgs& a, int64_t rec) {
-        const uint32_t* p = (const uint32_t*)a.scales + rec * kWords;
-#pragma unroll
-        for (int i = 0; i < kWords; ++i) s[i] = p[i];
-        constexpr int n = PER == 4 ? 2 : 1;
-#pragma unroll
-        for (int i = 0; i < n; ++i) z[i] = a.zeros ? a.zeros[rec * n + i] : 0x88888888u;
-    }
-    // group i (0 .. 4 PER - 1); i is a constant after unrolling
-    template <typename T>
-    __device__ __forceinline__ float scale(int i) const {
-        return i & 1 ? T::high(s[i / 2]) : T::low(s[i / 2]);
-    }
-    __device__ __forceinline__ uint32_t zero(int i) const { return (z[i / 8] >> (4 * (i % 8))) & 15u; }
-};
-
-template <typename T, int PER>
+template <typename T, int KIND>
 __global__ __launch_bounds__(256) void quant_decode_kernel(QuantArgs a, uint16_t* w) {
-    const int rt = blockIdx.x / ((a.units + 3) / 4), u4 = blockIdx.x % ((a.units + 3) / 4);
-    const int lane = threadIdx.x & 63, u = u4 * 4 + (threadIdx.x >> 6);
+    using A = Aux<T, KIND>;
+    const int blocks4 = (a.units + 3) / 4;
+    const int rt = blockIdx.x / blocks4, u = blockIdx.x % blocks4 * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
     const int64_t row = (int64_t)rt * kQuantRows + (lane & 15);
     if (u >= a.units || row >= a.M) return;
-    Aux<PER> x;
-    x.load(a, ((int64_t)rt * ((a.units + 3) / 4) + u4) * kQuantRows + (lane & 15));
-    const uint32_t* c = a.codes + (((int64_t)rt * a.units + u) * 64 + lane) * 4;
+    const int64_t unit = (int64_t)rt * a.units + u;
+    const uint8_t* rec = (const uint8_t*)a.aux + (unit * kQuantRows + (lane & 15)) * A::kBytes;
+#pragma unroll
     for (int s = 0; s < 4; ++s) {
-        const u32x4v v = unpack_codes<T>(c[s]);
+        uint32_t x;
+        if (KIND == 0)
+            x = *(const uint16_t*)rec | 8u << 16;
+        else
+            x = ((const uint32_t*)rec)[s * A::kPer / 4];
+        const u32x4v v = unpack_codes<T>(a.codes[(unit * 64 + lane) * 4 + s]);
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int64_t k = (int64_t)u * kQuantUnit + 32 * s + 8 * (lane >> 4) + j;
-            if (k >= a.K) continue;
-            float f = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4 * PER; ++i)  // constant indices only
-                if (i == (u & 3) * PER + s * PER / 4) {
-                    const uint32_t p = v[j / 2];
-                    f = ((j & 1 ? T::high(p) : T::low(p)) - (16.f + (float)x.zero(i))) * x.template scale<T>(i);
-                }
-            w[row * a.K + k] = (uint16_t)T::pack(f, 0.f);
+            const uint32_t p = v[j / 2];
+            const float c = (j & 1 ? T::high(p) : T::low(p)) - (16.f + (float)(x >> 16));
+            if (k < a.K) w[row * a.K + k] = (uint16_t)T::pack(c * T::low(x & 0xFFFFu), 0.f);
         }
     }
 }
 
-// ---------------------------------------------------------------- product
-// One workgroup: RT row tiles, one of a.splits ranges of units, which its eight wavefronts split
-// further; their sums are joined through LDS.  NT: tiles of 16 tokens.
-template <typename T, int PER, int NT, int RT>
-__global__ __launch_bounds__(64 * kQuantWaves) void quant_kernel(QuantArgs a) {
-    __shared__ float sh[kQuantWaves][NT * 16][RT * 16 + 1];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
-    const int blocks4 = (a.units + 3) / 4;
-    const int rt0 = blockIdx.x * RT, parts = kQuantWaves * a.splits, part = blockIdx.y * kQuantWaves + wave;
-    const int u0 = (int)((int64_t)a.units * part / parts), u1 = (int)((int64_t)a.units * (part + 1) / parts);
-    f32x4v acc[RT][NT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4v{0.f, 0.f, 0.f, 0.f};
-    const f32x4v none = {0.f, 0.f, 0.f, 0.f};
-    const u32x4v ones = T::bf ? u32x4v{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u}
-                              : u32x4v{0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
-    for (int b = u0 / 4; b * 4 < u1; ++b) {
-        Aux<PER> aux[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-            aux[r].load(a, ((int64_t)min(rt0 + r, a.tiles - 1) * blocks4 + b) * kQuantRows + (lane & 15));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int u = 4 * b + i;
-            if (u < u0 || u >= u1) continue;
-            u32x4v c[RT], x[NT][4];
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-                c[r] = *(const u32x4v*)(a.codes + (((int64_t)min(rt0 + r, a.tiles - 1) * a.units + u) * 64 + lane) * 4);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int token = 16 * n + (lane & 15);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    x[n][s] = u32x4v{0u, 0u, 0u, 0u};
-                    if (token < a.N) x[n][s] = load_x(a.x + token * a.ldx, u * kQuantUnit + 32 * s + 8 * g, a.K);
-                }
-            }
-#pragma unroll
-            for (int p = 0; p < PER; ++p) {
-                f32x4v sx[NT];
-                if (T::bf) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        sx[n] = none;
-#pragma unroll
-                        for (int s = 4 / PER * p; s < 4 / PER * (p + 1); ++s) sx[n] = T::mfma16(x[n][s], ones, sx[n]);
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const uint32_t z = aux[r].zero(i * PER + p);
-                    const float scale = aux[r].template scale<T>(i * PER + p);
-                    // -(16 + z): 0xCC00 | z << 6 in float16
-                    const uint32_t less = (0xCC00u | z << 6) * 0x00010001u;
-                    f32x4v d[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) d[n] = none;
-#pragma unroll
-                    for (int s = 4 / PER * p; s < 4 / PER * (p + 1); ++s) {
-                        u32x4v w = unpack_codes<T>(c[r][s]);
-                        if (!T::bf)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) w[j] = take_off(w[j], less);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) d[n] = T::mfma16(x[n][s], w, d[n]);
-                    }
-                    const float off = 16.f + (float)z;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            acc[r][n][e] += scale * (T::bf ? d[n][e] - off * sx[n][e] : d[n][e]);
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sh[wave][16 * n + 4 * g + e][16 * r + (lane & 15)] = acc[r][n][e];
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.N * RT * 16; i += 64 * kQuantWaves) {
-        const int n = i / (RT * 16), m = i % (RT * 16);
-        const int64_t row = (int64_t)rt0 * 16 + m;
-        if (row >= a.M) continue;
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < kQuantWaves; ++w) v += sh[w][n][m];
-        if (a.splits == 1)
-            a.y[n * a.ldy + row] = (uint16_t)T::pack(v, 0.f);
-        else
-            a.part[((int64_t)blockIdx.y * a.N + n) * a.M + row] = v;
-    }
-}
-
-// Second pass of a split product: the partial sums in ascending order.
 template <typename T>
-__global__ __launch_bounds__(256) void quant_join_kernel(QuantArgs a) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = (int64_t)a.N * a.M;
-    if (i >= total) return;
-    float v = 0.f;
-    for (int s = 0; s < a.splits; ++s) v += a.part[s * total + i];
-    a.y[i / a.M * a.ldy + i % a.M] = (uint16_t)T::pack(v, 0.f);
-}
-
-template <typename T, int PER, int NT, int RT>
-hipError_t run(const QuantArgs& a, hipStream_t s) {
-    quant_kernel<T, PER, NT, RT><<<dim3((a.tiles + RT - 1) / RT, a.splits), 64 * kQuantWaves, 0, s>>>(a);
-    if (a.splits > 1) {
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        quant_join_kernel<T><<<(unsigned)(((int64_t)a.N * a.M + 255) / 256), 256, 0, s>>>(a);
-    }
+hipError_t decode_kind(const QuantArgs& a, int kind, uint16_t* w, hipStream_t s) {
+    const unsigned grid = (unsigned)(a.tiles * (int64_t)((a.units + 3) / 4));
+    if (kind == 0) quant_decode_kernel<T, 0><<<grid, 256, 0, s>>>(a, w);
+    else if (kind == 1) quant_decode_kernel<T, 1><<<grid, 256, 0, s>>>(a, w);
+    else if (kind == 2) quant_decode_kernel<T, 2><<<grid, 256, 0, s>>>(a, w);
+    else quant_decode_kernel<T, 4><<<grid, 256, 0, s>>>(a, w);
     return hipGetLastError();
-}
-template <typename T, int PER>
-hipError_t run_tokens(const QuantArgs& a, hipStream_t s) {
-    if (a.N <= 16) return run<T, PER, 1, 2>(a, s);
-    if (a.N <= 32) return run<T, PER, 2, 2>(a, s);
-    return run<T, PER, 4, 2>(a, s);
-}
-template <typename T>
-hipError_t run_groups(const QuantArgs& a, int per_unit, hipStream_t s) {
-    if (per_unit == 1) return run_tokens<T, 1>(a, s);
-    if (per_unit == 2) return run_tokens<T, 2>(a, s);
-    return run_tokens<T, 4>(a, s);
 }
 
 }  // namespace
@@ -236,22 +91,31 @@ hipError_t launch_quant_encode(const QuantEncodeArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-hipError_t launch_quant_decode(const QuantArgs& a, int type, int per_unit, uint16_t* w, hipStream_t s) {
-    const unsigned grid = (unsigned)(a.tiles * (int64_t)((a.units + 3) / 4));
-    if (type == LSCD_F16) {
-        if (per_unit == 1) quant_decode_kernel<F16, 1><<<grid, 256, 0, s>>>(a, w);
-        else if (per_unit == 2) quant_decode_kernel<F16, 2><<<grid, 256, 0, s>>>(a, w);
-        else quant_decode_kernel<F16, 4><<<grid, 256, 0, s>>>(a, w);
-    } else {
-        if (per_unit == 1) quant_decode_kernel<BF16, 1><<<grid, 256, 0, s>>>(a, w);
-        else if (per_unit == 2) quant_decode_kernel<BF16, 2><<<grid, 256, 0, s>>>(a, w);
-        else quant_decode_kernel<BF16, 4><<<grid, 256, 0, s>>>(a, w);
-    }
-    return hipGetLastError();
+hipError_t launch_quant_decode(const QuantArgs& a, int type, int kind, uint16_t* w, hipStream_t s) {
+    return type == LSCD_F16 ? decode_kind<F16>(a, kind, w, s) : decode_kind<BF16>(a, kind, w, s);
 }
 
-hipError_t launch_quant(const QuantArgs& a, int type, int per_unit, hipStream_t s) {
-    return type == LSCD_F16 ? run_groups<F16>(a, per_unit, s) : run_groups<BF16>(a, per_unit, s);
+// The busiest CU's work: its workgroups times (row tiles x units of each, and a fixed part for a
+// workgroup's start, its join and its results); splits along K add partial sums.
+QuantPlan plan_quant(int tiles, int units, int N, int cus) {
+    QuantPlan best = {N > 16, 1, 1};
+    double cost = 0;
+    static const int few[] = {1, 2, 3, 4, 6, 7}, many[] = {1, 2, 3, 4};
+    const int* rts = best.shared ? many : few;
+    const int n = best.shared ? 4 : 6, wr = best.shared ? 4 : 1, wk = kQuantWaves / wr;
+    for (int i = 0; i < n; ++i) {
+        const int64_t groups = (tiles + (int64_t)rts[i] * wr - 1) / (rts[i] * wr);
+        for (int s = 1; s <= 16 && (s == 1 || s * wk <= units); ++s) {
+            const double each = (double)rts[i] * ((units + s * wk - 1) / (s * wk)) + (best.shared ? 8.0 : 4.0);
+            const double c = (double)((groups * s + cus - 1) / cus) * each * (1.0 + (s > 1 ? 0.06 + 0.01 * s : 0.0));
+            if ((i == 0 && s == 1) || c < cost) {
+                cost = c;
+                best.rt = rts[i];
+                best.splits = s;
+            }
+        }
+    }
+    return best;
 }
 
 }  // namespace lscd

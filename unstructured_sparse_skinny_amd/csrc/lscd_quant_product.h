@@ -1,0 +1,331 @@
+// The product kernels of matrices of 4-bit codes (see lscd_quant.h for the arithmetic); compiled once
+// per 16-bit type.
+#pragma once
+
+#include "lscd_quant.h"
+
+namespace lscd {
+namespace {
+
+constexpr int kQuantThreads = 64 * kQuantWaves;
+
+template <typename T>
+__device__ __forceinline__ u32x4v ones_of() {
+    const uint32_t w = T::bf ? 0x3F803F80u : 0x3C003C00u;
+    return u32x4v{w, w, w, w};
+}
+
+// A workgroup's row tiles as one buffer: unit u of its tile r begins (r * units + u) KB into it.
+// (Offsets of lanes that are off lie outside it: no traffic, zeros.)
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const void* p, int64_t tile, int tiles, int64_t bytes) {
+    return buffer_of((const uint8_t*)p + tile * bytes, (int)(tiles * bytes));
+}
+
+// Up to 16 tokens.  One workgroup: RT row tiles and one of a.splits ranges of units, which its eight
+// wavefronts split further: each streams its own units of all RT tiles (one contiguous KB of codes
+// per tile and unit) with x straight from the caches, kAhead units in flight, and needs no barrier
+// until the sums are joined through LDS.  x costs 4 KB per unit of a wavefront for 16 tokens (less for
+// fewer: lanes past N repeat a token, the same lines), against RT KB of codes.
+template <typename T, int KIND, int RT>
+__global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a) {
+    using A = Aux<T, KIND>;
+    constexpr int kAhead = RT <= 2 ? 4 : (RT == 3 ? 3 : 2);
+    __shared__ float sh[kQuantWaves][16][RT * 16 + 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
+    const int rt0 = blockIdx.x * RT, parts = kQuantWaves * a.splits, part = blockIdx.y * kQuantWaves + wave;
+    const int u0 = (int)((int64_t)a.units * part / parts), u1 = (int)((int64_t)a.units * (part + 1) / parts);
+    const int have = min(RT, a.tiles - rt0);
+    const auto cb = tile_buffer(a.codes, rt0, have, (int64_t)a.units * 1024);
+    const auto ab = tile_buffer(a.aux, rt0, have, (int64_t)a.units * kQuantRows * A::kBytes);
+    const int token = min(lane & 15, a.N - 1);
+    const uint16_t* xp = a.x + token * a.ldx + 8 * g;
+    const bool loose = a.K % kQuantUnit != 0;  // the last unit is not full
+
+    f32x4v acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    u32x4v c[kAhead][RT], x[kAhead][4];
+    A aux[kAhead][RT];
+    auto load = [&](int i, int u) {
+        const bool on = u < u1;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const bool here = on && r < have;  // (the scalar offset is not part of the bounds check)
+            const int unit = here ? r * a.units + u : 0;
+            c[i][r] = __builtin_amdgcn_raw_buffer_load_b128(cb, here ? lane * 16 : kNoRow, unit * 1024, 2);
+            aux[i][r].load(ab, here ? (lane & 15) * A::kBytes : kNoRow, unit * (kQuantRows * A::kBytes));
+        }
+    };
+    auto load_tokens = [&](int i, int u) {
+        u = min(u, u1 - 1);
+        const uint16_t* p = xp + (int64_t)u * kQuantUnit;
+        if (!(loose && u == a.units - 1)) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) x[i][s] = load_x(p + 32 * s);
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) x[i][s] = load_x_end(p + 32 * s, u * kQuantUnit + 32 * s + 8 * g, a.K);
+        }
+    };
+    auto compute = [&](int i) {
+        const f32x4v none = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < A::kPer; ++p) {
+            constexpr int kSteps = 4 / A::kPer;
+            f32x4v sx = none;
+            if (T::bf)
+#pragma unroll
+                for (int s = kSteps * p; s < kSteps * (p + 1); ++s) sx = T::mfma16(x[i][s], ones_of<T>(), sx);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const uint32_t z = aux[i][r].zero(p), less = less_of(z);
+                f32x4v d = none;
+#pragma unroll
+                for (int s = kSteps * p; s < kSteps * (p + 1); ++s) {
+                    u32x4v w = unpack_codes<T>(c[i][r][s]);
+                    if (!T::bf)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = take_off(w[j], less);
+                    d = T::mfma16(x[i][s], w, d);
+                }
+                const float scale = aux[i][r].scale(p), off = 16.f + (float)z;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[r][e] += scale * (T::bf ? d[e] - off * sx[e] : d[e]);
+            }
+        }
+    };
+    if (u0 < u1) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            load(i, u0 + i);
+            load_tokens(i, u0 + i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        for (int u = u0; u < u1; u += kAhead) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                compute(i);  // (a unit past the end has codes, scales and so weights of zero)
+                load(i, u + i + kAhead);
+                load_tokens(i, u + i + kAhead);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sh[wave][4 * g + e][16 * r + (lane & 15)] = acc[r][e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.N * RT * 16; i += kQuantThreads) {
+        const int n = i / (RT * 16), m = i % (RT * 16);
+        const int64_t row = (int64_t)rt0 * 16 + m;
+        if (row >= a.M) continue;
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kQuantWaves; ++w) v += sh[w][n][m];
+        if (a.splits == 1)
+            a.y[n * a.ldy + row] = (uint16_t)T::pack(v, 0.f);
+        else
+            a.part[((int64_t)blockIdx.y * a.N + n) * a.M + row] = v;
+    }
+}
+
+// 17 to 64 tokens (NT tiles of 16).  One workgroup: four wavefronts by rows, RT row tiles each, times
+// two by units; the four share their units' x in LDS (double-buffered, one barrier per unit), so that
+// x comes from the L2 once per 4 RT KB of codes.  Rows of x are 256 bytes in LDS, 16-byte chunks
+// XOR-swizzled by the token.
+template <typename T, int KIND, int NT, int RT>
+__global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs a) {
+    using A = Aux<T, KIND>;
+    constexpr int kRowWaves = 4, kTokens = 16 * NT, kTile = kTokens * 256, kPer = kTokens * 16 / 256;
+    constexpr int kJoin = kRowWaves * 64 * RT * NT * 4 * 4;  // bytes of one half's sums
+    constexpr int kLds = 4 * kTile > kJoin ? 4 * kTile : kJoin;
+    __shared__ __attribute__((aligned(16))) unsigned char sh[kLds];
+    const int tid = threadIdx.x & 255, lane = threadIdx.x & 63, g = lane >> 4;
+    const int half = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);      // which units
+    const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) & 3);  // which rows
+    const int rt0 = (blockIdx.x * kRowWaves + wave) * RT;
+    const int parts = 2 * a.splits, part = blockIdx.y * 2 + half;
+    const int u0 = (int)((int64_t)a.units * part / parts), u1 = (int)((int64_t)a.units * (part + 1) / parts);
+    const int rounds = (a.units + parts - 1) / parts;  // the same for all: barriers
+    const int have = max(0, min(RT, a.tiles - rt0));
+    const int first = min(rt0, a.tiles - 1);
+    const auto cb = tile_buffer(a.codes, first, have, (int64_t)a.units * 1024);
+    const auto ab = tile_buffer(a.aux, first, have, (int64_t)a.units * kQuantRows * A::kBytes);
+    const bool loose = a.K % kQuantUnit != 0;
+    const uint16_t* xp[kPer];
+    int at[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int n = i * 16 + (tid >> 4), ch = tid & 15;
+        xp[i] = a.x + min(n, a.N - 1) * a.ldx + 8 * ch;
+        at[i] = n * 256 + ((ch ^ (n & 15)) << 4);
+    }
+    u32x4v c[2][RT], xs[kPer];
+    A aux[2][RT];
+    auto load = [&](int i, int u) {
+        const bool on = u < u1;
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const bool here = on && r < have;  // (the scalar offset is not part of the bounds check)
+            const int unit = here ? r * a.units + u : 0;
+            c[i][r] = __builtin_amdgcn_raw_buffer_load_b128(cb, here ? lane * 16 : kNoRow, unit * 1024, 2);
+            aux[i][r].load(ab, here ? (lane & 15) * A::kBytes : kNoRow, unit * (kQuantRows * A::kBytes));
+        }
+    };
+    auto load_tokens = [&](int u) {
+        u = max(u0, min(u, u1 - 1));
+        u = min(u, a.units - 1);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint16_t* p = xp[i] + (int64_t)u * kQuantUnit;
+            if (!(loose && u == a.units - 1))
+                xs[i] = load_x(p);
+            else
+                xs[i] = load_x_end(p, u * kQuantUnit + 8 * (tid & 15), a.K);
+        }
+    };
+    f32x4v acc[RT][NT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4v{0.f, 0.f, 0.f, 0.f};
+
+    load_tokens(u0);
+    load(0, u0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) *(u32x4v*)(sh + half * kTile + at[i]) = xs[i];
+    load_tokens(u0 + 1);
+    load(1, u0 + 1);
+    __syncthreads();
+    auto unit = [&](int i, int k) {
+        const unsigned char* xb = sh + (2 * i + half) * kTile;
+        const f32x4v none = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int p = 0; p < A::kPer; ++p) {
+            constexpr int kSteps = 4 / A::kPer;
+            u32x4v x[kSteps][NT];
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    x[s][n] = *(const u32x4v*)(xb + (16 * n + (lane & 15)) * 256 + (((4 * (kSteps * p + s) + g) ^ (lane & 15)) << 4));
+            f32x4v sx[NT];
+            if (T::bf)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    sx[n] = none;
+#pragma unroll
+                    for (int s = 0; s < kSteps; ++s) sx[n] = T::mfma16(x[s][n], ones_of<T>(), sx[n]);
+                }
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const uint32_t z = aux[i][r].zero(p), less = less_of(z);
+                f32x4v d[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) d[n] = none;
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    u32x4v w = unpack_codes<T>(c[i][r][kSteps * p + s]);
+                    if (!T::bf)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[j] = take_off(w[j], less);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) d[n] = T::mfma16(x[s][n], w, d[n]);
+                }
+                const float scale = aux[i][r].scale(p), off = 16.f + (float)z;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][n][e] += scale * (T::bf ? d[n][e] - off * sx[n][e] : d[n][e]);
+            }
+        }
+        // the next unit's x into the other buffer (its last reads were before the last barrier)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) *(u32x4v*)(sh + (2 * (i ^ 1) + half) * kTile + at[j]) = xs[j];
+        load_tokens(u0 + k + 2);
+        load(i, u0 + k + 2);
+        __syncthreads();
+    };
+    for (int k = 0; k < rounds; k += 2) {  // (units past the end have weights of zero)
+        unit(0, k);
+        if (k + 1 < rounds) unit(1, k + 1);
+    }
+    // join the two halves; wavefront `wave` of half 0 then holds the sums of its rows
+    float* js = (float*)sh + (wave * 64 + lane) * (RT * NT * 4);
+    if (half == 1)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) *(f32x4v*)(js + (r * NT + n) * 4) = acc[r][n];
+    __syncthreads();
+    if (half == 1) return;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int64_t row = (int64_t)(rt0 + r) * 16 + (lane & 15);
+        if (row >= a.M) continue;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const f32x4v v = acc[r][n] + *(const f32x4v*)(js + (r * NT + n) * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int t = 16 * n + 4 * g + e;
+                if (t >= a.N) continue;
+                if (a.splits == 1)
+                    a.y[t * a.ldy + row] = (uint16_t)T::pack(v[e], 0.f);
+                else
+                    a.part[((int64_t)blockIdx.y * a.N + t) * a.M + row] = v[e];
+            }
+        }
+    }
+}
+
+// Second pass of a split product: the partial sums in ascending order.
+template <typename T>
+__global__ __launch_bounds__(256) void quant_join_kernel(QuantArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, total = (int64_t)a.N * a.M;
+    if (i >= total) return;
+    float v = 0.f;
+    for (int s = 0; s < a.splits; ++s) v += a.part[s * total + i];
+    a.y[i / a.M * a.ldy + i % a.M] = (uint16_t)T::pack(v, 0.f);
+}
+
+template <typename T, int KIND, int NT>
+void run_many(const QuantArgs& a, int rt, hipStream_t s) {
+    const dim3 grid((unsigned)((a.tiles + 4 * rt - 1) / (4 * rt)), (unsigned)a.splits);
+    if (rt == 1) quant_many_kernel<T, KIND, NT, 1><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 2) quant_many_kernel<T, KIND, NT, 2><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 3) quant_many_kernel<T, KIND, NT, 3><<<grid, kQuantThreads, 0, s>>>(a);
+    else quant_many_kernel<T, KIND, NT, 4><<<grid, kQuantThreads, 0, s>>>(a);
+}
+template <typename T, int KIND>
+void run_few(const QuantArgs& a, int rt, hipStream_t s) {
+    const dim3 grid((unsigned)((a.tiles + rt - 1) / rt), (unsigned)a.splits);
+    if (rt == 1) quant_few_kernel<T, KIND, 1><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 2) quant_few_kernel<T, KIND, 2><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 3) quant_few_kernel<T, KIND, 3><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 4) quant_few_kernel<T, KIND, 4><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 6) quant_few_kernel<T, KIND, 6><<<grid, kQuantThreads, 0, s>>>(a);
+    else quant_few_kernel<T, KIND, 7><<<grid, kQuantThreads, 0, s>>>(a);
+}
+template <typename T, int KIND>
+void run_kind(const QuantArgs& a, const QuantPlan& p, hipStream_t s) {
+    if (!p.shared) run_few<T, KIND>(a, p.rt, s);
+    else if (a.N <= 32) run_many<T, KIND, 2>(a, p.rt, s);
+    else run_many<T, KIND, 4>(a, p.rt, s);
+}
+template <typename T>
+hipError_t run_product(const QuantArgs& a, int kind, const QuantPlan& p, hipStream_t s) {
+    if (kind == 0) run_kind<T, 0>(a, p, s);
+    else if (kind == 1) run_kind<T, 1>(a, p, s);
+    else if (kind == 2) run_kind<T, 2>(a, p, s);
+    else run_kind<T, 4>(a, p, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    quant_join_kernel<T><<<(unsigned)(((int64_t)a.N * a.M + 255) / 256), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace lscd

@@ -58,17 +58,10 @@ void free_attention(lscd_attention_s* h) {
 void free_quant(lscd_quant_s* h) {
     if (!h) return;
     if (h->codes) (void)hipFree(h->codes);
-    if (h->scales) (void)hipFree(h->scales);
-    if (h->zeros) (void)hipFree(h->zeros);
+    if (h->aux) (void)hipFree(h->aux);
     if (h->part) (void)hipFree(h->part);
     if (h->count) (void)hipFree(h->count);
     delete h;
-}
-
-// Ranges of K that workgroups split a product into: enough workgroups for every CU.
-int quant_splits(const lscd_quant_s* h) {
-    const int groups = (h->tiles + 1) / 2;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({2 * (int64_t)h->cus / groups, h->units / lscd::kQuantWaves, 16}));
 }
 
 lscd_status_t check_quant(const lscd_quant_s* h) {
@@ -80,8 +73,7 @@ lscd_status_t check_quant(const lscd_quant_s* h) {
 lscd::QuantArgs quant_args(const lscd_quant_s* h) {
     lscd::QuantArgs a = {};
     a.codes = h->codes;
-    a.scales = h->scales;
-    a.zeros = h->zeros;
+    a.aux = h->aux;
     a.part = h->part;
     a.count = h->count;
     a.M = (int32_t)h->M;
@@ -102,7 +94,7 @@ lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void
     if (!codes || !aligned(scales, 2) || M < 1 || K < 1 || group < 1 || row_bytes < (K + 1) / 2 ||
         (type != LSCD_F16 && type != LSCD_BF16))
         return LSCD_ERROR_INVALID_VALUE;
-    if (M > ((int64_t)1 << 30) || K > ((int64_t)1 << 30)) return LSCD_ERROR_INVALID_VALUE;
+    if (M > ((int64_t)1 << 30) || K > ((int64_t)1 << 24)) return LSCD_ERROR_NOT_SUPPORTED;
     if (group < 32 || (group < 128 ? group != 32 && group != 64 : group % 128)) return LSCD_ERROR_NOT_SUPPORTED;
     lscd_quant_s* h = new (std::nothrow) lscd_quant_s();
     if (!h) return LSCD_ERROR_OUT_OF_MEMORY;
@@ -126,19 +118,22 @@ lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void
         free_quant(h);
         return LSCD_ERROR_NOT_SUPPORTED;
     }
-    const int splits = quant_splits(h);
-    h->part_floats = splits > 1 ? splits * M * lscd::kQuantMaxTokens : 0;
+    h->kind = lscd::quant_kind(h->per_unit, zeros != nullptr);
+    for (int n : {16, 32, 64}) {
+        const lscd::QuantPlan p = lscd::plan_quant(h->tiles, h->units, n, cus);
+        if (p.splits > 1) h->part_floats = std::max(h->part_floats, (int64_t)p.splits * M * n);
+    }
     lscd::QuantEncodeArgs a = {};
-    if ((e = hipMalloc((void**)&h->codes, (size_t)h->tiles * h->units * 1024)) == hipSuccess &&
-        (e = hipMalloc((void**)&h->scales, (size_t)blocks * 16 * 8 * h->per_unit)) == hipSuccess &&
-        (!zeros || (e = hipMalloc((void**)&h->zeros, (size_t)blocks * 16 * (h->per_unit == 4 ? 8 : 4))) == hipSuccess) &&
+    const int64_t units = (int64_t)h->tiles * h->units;
+    if ((e = hipMalloc((void**)&h->codes, (size_t)units * 1024)) == hipSuccess &&
+        (e = hipMalloc((void**)&h->aux, (size_t)units * 16 * lscd::quant_aux_bytes(h->kind))) == hipSuccess &&
         (!h->part_floats || (e = hipMalloc((void**)&h->part, (size_t)h->part_floats * 4)) == hipSuccess)) {
         a.q = (const uint8_t*)codes;
         a.scales = (const uint16_t*)scales;
         a.zeros = (const uint8_t*)zeros;
         a.codes = h->codes;
-        a.scales_out = h->scales;
-        a.zeros_out = h->zeros;
+        a.aux = h->aux;
+        a.short_aux = h->kind == 0;
         a.M = M;
         a.K = K;
         a.row_bytes = row_bytes;
@@ -169,12 +164,14 @@ lscd_status_t lscd_quant_linear(lscd_quant_t h, const void* x, int64_t ldx, void
     lscd::QuantArgs a = quant_args(h);
     a.ldx = ldx;
     a.ldy = ldy;
-    a.splits = quant_splits(h);
     for (int32_t n = 0; n < N; n += lscd::kQuantMaxTokens) {
         a.x = (const uint16_t*)x + n * ldx;
         a.y = (uint16_t*)y + n * ldy;
         a.N = std::min(N - n, lscd::kQuantMaxTokens);
-        hipError_t e = lscd::launch_quant(a, h->type, h->per_unit, (hipStream_t)stream);
+        const lscd::QuantPlan p = lscd::plan_quant(h->tiles, h->units, a.N, h->cus);
+        a.splits = p.splits;
+        hipError_t e = h->type == LSCD_F16 ? lscd::launch_quant_f16(a, h->kind, p, (hipStream_t)stream)
+                                           : lscd::launch_quant_bf16(a, h->kind, p, (hipStream_t)stream);
         if (e != hipSuccess) return status_of(e);
     }
     return LSCD_SUCCESS;
@@ -184,7 +181,7 @@ lscd_status_t lscd_quant_decode(lscd_quant_t h, void* w, void* stream) {
     if (!h || !aligned(w, 2)) return LSCD_ERROR_INVALID_VALUE;
     lscd_status_t st = check_quant(h);
     if (st != LSCD_SUCCESS) return st;
-    return status_of(lscd::launch_quant_decode(quant_args(h), h->type, h->per_unit, (uint16_t*)w, (hipStream_t)stream));
+    return status_of(lscd::launch_quant_decode(quant_args(h), h->type, h->kind, (uint16_t*)w, (hipStream_t)stream));
 }
 
 lscd_status_t lscd_quant_destroy(lscd_quant_t h) {

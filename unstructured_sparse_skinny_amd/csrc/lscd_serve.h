@@ -57,9 +57,10 @@ hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStrea
 // ---------------------------------------------------------------- quantised product
 // Device layout of the codes: row tiles of 16 rows, units of 128 columns, [row tile][unit][64 lanes]
 // [4 words].  Lane l of a unit has row l % 16; word s its 8 codes of columns 32 s + 8 (l / 16) + 0..7,
-// placed so that pairs come out of a word with one shift and one mask (quant_word).  Scales and zero
-// points: [row tile][unit / 4][16 rows][4 units][groups per unit], 16-bit scales and 4-bit zeros.
-// Rows past M and columns past K hold zero points (weights of zero).
+// placed so that pairs come out of a word with one shift and one mask (quant_bit).  Scales and zero
+// points: [row tile][unit][16 rows] records, one entry per group of the unit: with groups of 128
+// columns and no zero points a 16-bit scale, else a word scale | zero << 16.  Rows past M and columns
+// past K hold zero points (weights of zero).
 constexpr int kQuantUnit = 128;
 constexpr int kQuantRows = 16;
 constexpr int kQuantMaxTokens = 64;  // tokens of one launch
@@ -73,10 +74,16 @@ __host__ __device__ inline int quant_bit(int j, int bit) {
     return at & 31;
 }
 
+// How one product runs: the kernel (0: up to 16 tokens, 1: more), row tiles per wavefront, and the
+// ranges of K that workgroups split it into.
+struct QuantPlan {
+    int shared, rt, splits;
+};
+QuantPlan plan_quant(int tiles, int units, int N, int cus);
+
 struct QuantArgs {
     const uint32_t* codes;
-    const uint16_t* scales;
-    const uint32_t* zeros;   // one word per (row, 4 units): 4 * groups nibbles in 32- or 64-bit records
+    const void* aux;         // scales and zero points
     const uint16_t* x;
     uint16_t* y;
     float* part;
@@ -90,15 +97,20 @@ struct QuantEncodeArgs {
     const uint16_t* scales;  // [M][groups]
     const uint8_t* zeros;    // [M][groups] or null
     uint32_t* codes;
-    uint16_t* scales_out;
-    uint32_t* zeros_out;
+    void* aux;
     int64_t M, K, row_bytes, groups;
     int32_t group, per_unit; // columns of a group, groups of a unit (1, 2 or 4)
+    int32_t short_aux;       // 16-bit records
     int32_t tiles, units;
 };
+// Kinds of records: one 16-bit scale, one word, two words, four words a unit and row.
+inline int quant_kind(int per_unit, bool zeros) { return per_unit == 1 ? (zeros ? 1 : 0) : per_unit; }
+inline int quant_aux_bytes(int kind) { return kind == 0 ? 2 : 4 * kind; }
 hipError_t launch_quant_encode(const QuantEncodeArgs& a, hipStream_t s);
-hipError_t launch_quant_decode(const QuantArgs& a, int type, int per_unit, uint16_t* w, hipStream_t s);
-hipError_t launch_quant(const QuantArgs& a, int type, int per_unit, hipStream_t s);
+hipError_t launch_quant_decode(const QuantArgs& a, int type, int kind, uint16_t* w, hipStream_t s);
+// (one source file per type)
+hipError_t launch_quant_f16(const QuantArgs& a, int kind, const QuantPlan& p, hipStream_t s);
+hipError_t launch_quant_bf16(const QuantArgs& a, int kind, const QuantPlan& p, hipStream_t s);
 
 }  // namespace lscd
 
@@ -109,8 +121,8 @@ struct lscd_quant_s {
     int32_t group = 0, type = 0, per_unit = 1;
     int32_t tiles = 0, units = 0;
     uint32_t* codes = nullptr;
-    uint16_t* scales = nullptr;
-    uint32_t* zeros = nullptr;
+    void* aux = nullptr;
+    int kind = 0;
     float* part = nullptr;
     uint32_t* count = nullptr;
     int64_t part_floats = 0;
