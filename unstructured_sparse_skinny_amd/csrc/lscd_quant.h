@@ -60,6 +60,17 @@ __device__ __forceinline__ u32x4v load_x_end(const uint16_t* x, int k, int K) {
         if (k + i < K) r[i / 2] |= (uint32_t)x[i] << (16 * (i & 1));
     return r;
 }
+// The same from the row's last 8 values `v`, loaded at column K - 8 where k > K - 8: s = k - (K - 8)
+// values further on, zeros behind them.
+__device__ __forceinline__ u32x4v shift_end(u32x4v v, int s) {
+    if (s >= 8) v = u32x4v{0u, 0u, 0u, 0u};
+    if (s > 0) {
+        if (s & 4) v = u32x4v{v[2], v[3], 0u, 0u};
+        if (s & 2) v = u32x4v{v[1], v[2], v[3], 0u};
+        if (s & 1) v = u32x4v{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+    }
+    return v;
+}
 
 // Scales and zero points of a lane's row for one unit (kinds of quant_kind).
 template <typename T, int KIND>

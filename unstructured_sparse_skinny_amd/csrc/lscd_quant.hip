@@ -102,7 +102,8 @@ QuantPlan plan_quant(int tiles, int units, int N, int cus) {
     double cost = 0;
     static const int few[] = {1, 2, 3, 4, 6, 7}, many[] = {1, 2, 3, 4};
     const int* rts = best.shared ? many : few;
-    const int n = best.shared ? 4 : 6, wr = best.shared ? 4 : 1, wk = kQuantWaves / wr;
+    const int n = N > 32 ? 3 : (best.shared ? 4 : 6),  // (four row tiles of 64 tokens do not fit the registers)
+              wr = best.shared ? 4 : 1, wk = kQuantWaves / wr;
     for (int i = 0; i < n; ++i) {
         const int64_t groups = (tiles + (int64_t)rts[i] * wr - 1) / (rts[i] * wr);
         for (int s = 1; s <= 16 && (s == 1 || s * wk <= units); ++s) {

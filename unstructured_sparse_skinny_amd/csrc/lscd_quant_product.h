@@ -39,15 +39,15 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
     const auto ab = tile_buffer(a.aux, rt0, have, (int64_t)a.units * kQuantRows * A::kBytes);
     const int token = min(lane & 15, a.N - 1);
     const uint16_t* xp = a.x + token * a.ldx + 8 * g;
-    const bool loose = a.K % kQuantUnit != 0;  // the last unit is not full
+    const int full = min(u1, a.K / kQuantUnit);  // the last unit of a row may not be full
 
     f32x4v acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r] = f32x4v{0.f, 0.f, 0.f, 0.f};
     u32x4v c[kAhead][RT], x[kAhead][4];
     A aux[kAhead][RT];
-    auto load = [&](int i, int u) {
-        const bool on = u < u1;
+    auto load = [&](int i, int u, int end) {
+        const bool on = u < end;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const bool here = on && r < have;  // (the scalar offset is not part of the bounds check)
@@ -57,15 +57,9 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
         }
     };
     auto load_tokens = [&](int i, int u) {
-        u = min(u, u1 - 1);
-        const uint16_t* p = xp + (int64_t)u * kQuantUnit;
-        if (!(loose && u == a.units - 1)) {
+        const uint16_t* p = xp + (int64_t)min(u, full - 1) * kQuantUnit;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) x[i][s] = load_x(p + 32 * s);
-        } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) x[i][s] = load_x_end(p + 32 * s, u * kQuantUnit + 32 * s + 8 * g, a.K);
-        }
+        for (int s = 0; s < 4; ++s) x[i][s] = load_x(p + 32 * s);
     };
     auto compute = [&](int i) {
         const f32x4v none = {0.f, 0.f, 0.f, 0.f};
@@ -94,22 +88,29 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
             }
         }
     };
-    if (u0 < u1) {
+    if (u0 < full) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            load(i, u0 + i);
+            load(i, u0 + i, full);
             load_tokens(i, u0 + i);
             __builtin_amdgcn_sched_barrier(0);
         }
-        for (int u = u0; u < u1; u += kAhead) {
+        for (int u = u0; u < full; u += kAhead) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
                 compute(i);  // (a unit past the end has codes, scales and so weights of zero)
-                load(i, u + i + kAhead);
+                load(i, u + i + kAhead, full);
                 load_tokens(i, u + i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+    }
+    if (u0 < u1 && full < u1) {
+        load(0, full, u1);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+            x[0][s] = load_x_end(xp + (int64_t)full * kQuantUnit + 32 * s, full * kQuantUnit + 32 * s + 8 * g, a.K);
+        compute(0);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -152,13 +153,13 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs 
     const int first = min(rt0, a.tiles - 1);
     const auto cb = tile_buffer(a.codes, first, have, (int64_t)a.units * 1024);
     const auto ab = tile_buffer(a.aux, first, have, (int64_t)a.units * kQuantRows * A::kBytes);
-    const bool loose = a.K % kQuantUnit != 0;
+    const int ch = tid & 15;
     const uint16_t* xp[kPer];
     int at[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int n = i * 16 + (tid >> 4), ch = tid & 15;
-        xp[i] = a.x + min(n, a.N - 1) * a.ldx + 8 * ch;
+        const int n = i * 16 + (tid >> 4);
+        xp[i] = a.x + min(n, a.N - 1) * a.ldx;
         at[i] = n * 256 + ((ch ^ (n & 15)) << 4);
     }
     u32x4v c[2][RT], xs[kPer];
@@ -173,17 +174,20 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs 
             aux[i][r].load(ab, here ? (lane & 15) * A::kBytes : kNoRow, unit * (kQuantRows * A::kBytes));
         }
     };
+    // (K is at least 8 here: a row's last 8 values stand in for chunks that reach past its end)
+    auto clamp = [&](int u) { return min(max(u0, min(u, u1 - 1)), a.units - 1); };
     auto load_tokens = [&](int u) {
-        u = max(u0, min(u, u1 - 1));
-        u = min(u, a.units - 1);
+        const int k = min(clamp(u) * kQuantUnit + 8 * ch, a.K - 8);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const uint16_t* p = xp[i] + (int64_t)u * kQuantUnit;
-            if (!(loose && u == a.units - 1))
-                xs[i] = load_x(p);
-            else
-                xs[i] = load_x_end(p, u * kQuantUnit + 8 * (tid & 15), a.K);
-        }
+        for (int i = 0; i < kPer; ++i) xs[i] = load_x(xp[i] + k);
+    };
+    auto store_tokens = [&](int i, int u) {
+        u = clamp(u);
+        if ((u + 1) * kQuantUnit > a.K)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) xs[j] = shift_end(xs[j], u * kQuantUnit + 8 * ch - (a.K - 8));
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) *(u32x4v*)(sh + (2 * i + half) * kTile + at[j]) = xs[j];
     };
     f32x4v acc[RT][NT];
 #pragma unroll
@@ -194,8 +198,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs 
     load_tokens(u0);
     load(0, u0);
     __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) *(u32x4v*)(sh + half * kTile + at[i]) = xs[i];
+    store_tokens(0, u0);
     load_tokens(u0 + 1);
     load(1, u0 + 1);
     __syncthreads();
@@ -239,11 +242,12 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs 
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[r][n][e] += scale * (T::bf ? d[n][e] - off * sx[n][e] : d[n][e]);
+                // (with several groups a unit, mixing all of them would not fit the registers)
+                if (A::kPer > 1) __builtin_amdgcn_sched_barrier(0);
             }
         }
         // the next unit's x into the other buffer (its last reads were before the last barrier)
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) *(u32x4v*)(sh + (2 * (i ^ 1) + half) * kTile + at[j]) = xs[j];
+        store_tokens(i ^ 1, u0 + k + 1);
         load_tokens(u0 + k + 2);
         load(i, u0 + k + 2);
         __syncthreads();
@@ -297,7 +301,7 @@ void run_many(const QuantArgs& a, int rt, hipStream_t s) {
     if (rt == 1) quant_many_kernel<T, KIND, NT, 1><<<grid, kQuantThreads, 0, s>>>(a);
     else if (rt == 2) quant_many_kernel<T, KIND, NT, 2><<<grid, kQuantThreads, 0, s>>>(a);
     else if (rt == 3) quant_many_kernel<T, KIND, NT, 3><<<grid, kQuantThreads, 0, s>>>(a);
-    else quant_many_kernel<T, KIND, NT, 4><<<grid, kQuantThreads, 0, s>>>(a);
+    else if constexpr (NT < 4) quant_many_kernel<T, KIND, NT, 4><<<grid, kQuantThreads, 0, s>>>(a);
 }
 template <typename T, int KIND>
 void run_few(const QuantArgs& a, int rt, hipStream_t s) {

@@ -164,10 +164,12 @@ lscd_status_t lscd_quant_linear(lscd_quant_t h, const void* x, int64_t ldx, void
     lscd::QuantArgs a = quant_args(h);
     a.ldx = ldx;
     a.ldy = ldy;
-    for (int32_t n = 0; n < N; n += lscd::kQuantMaxTokens) {
+    // (rows of fewer than 8 values: the kernel for up to 16 tokens, which has no 16-byte loads then)
+    const int32_t most = h->K < 8 ? 16 : lscd::kQuantMaxTokens;
+    for (int32_t n = 0; n < N; n += most) {
         a.x = (const uint16_t*)x + n * ldx;
         a.y = (uint16_t*)y + n * ldy;
-        a.N = std::min(N - n, lscd::kQuantMaxTokens);
+        a.N = std::min(N - n, most);
         const lscd::QuantPlan p = lscd::plan_quant(h->tiles, h->units, a.N, h->cus);
         a.splits = p.splits;
         hipError_t e = h->type == LSCD_F16 ? lscd::launch_quant_f16(a, h->kind, p, (hipStream_t)stream)
