@@ -80,11 +80,6 @@ __device__ __forceinline__ int head_units(const AttnArgs& a, const Seq& q) {
     return u;
 }
 
-__device__ __forceinline__ int64_t uniform(int64_t x) {
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
-    return (int64_t)((uint64_t)hi << 32 | lo);
-}
-
 // Where a range of units begins: sequence, key head, row tile, unit inside the tile.
 struct Place {
     int seq, head, tile, unit;

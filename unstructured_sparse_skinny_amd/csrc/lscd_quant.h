@@ -24,16 +24,16 @@ __device__ __forceinline__ u32x4v unpack_codes(uint32_t w) {
     u32x4v r;
     if (T::bf) {  // 16 + c = 0x4180 | c << 3
         const uint32_t mask = 0x00780078u, base = 0x41804180u;
-        r[0] = ((w >> 3) & mask) | base;
-        r[1] = ((w >> 7) & mask) | base;
-        r[2] = ((w << 1) & mask) | base;
-        r[3] = (__builtin_amdgcn_alignbit(w, w, 11) & mask) | base;
+        r[0] = and_or(w >> 3, mask, base);
+        r[1] = and_or(w >> 7, mask, base);
+        r[2] = and_or(w << 1, mask, base);
+        r[3] = and_or(__builtin_amdgcn_alignbit(w, w, 11), mask, base);
     } else {  // 16 + c = 0x4C00 | c << 6
         const uint32_t mask = 0x03C003C0u, base = 0x4C004C00u;
-        r[0] = (w & mask) | base;
-        r[1] = ((w >> 4) & mask) | base;
-        r[2] = ((w << 4) & mask) | base;
-        r[3] = (__builtin_amdgcn_alignbit(w, w, 8) & mask) | base;
+        r[0] = and_or(w, mask, base);
+        r[1] = and_or(w >> 4, mask, base);
+        r[2] = and_or(w << 4, mask, base);
+        r[3] = and_or(__builtin_amdgcn_alignbit(w, w, 8), mask, base);
     }
     return r;
 }
@@ -41,7 +41,6 @@ __device__ __forceinline__ u32x4v unpack_codes(uint32_t w) {
 __device__ __forceinline__ uint32_t take_off(uint32_t w, uint32_t less) {
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, w) + __builtin_bit_cast(half2v, less));
 }
-
 // -(16 + z) twice: 0xCC00 | z << 6 in float16.
 __device__ __forceinline__ uint32_t less_of(uint32_t z) { return (0xCC00u | z << 6) * 0x00010001u; }
 

@@ -18,7 +18,8 @@ __device__ __forceinline__ u32x4v ones_of() {
 // A workgroup's row tiles as one buffer: unit u of its tile r begins (r * units + u) KB into it.
 // (Offsets of lanes that are off lie outside it: no traffic, zeros.)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const void* p, int64_t tile, int tiles, int64_t bytes) {
-    return buffer_of((const uint8_t*)p + tile * bytes, (int)(tiles * bytes));
+    const int64_t at = uniform((int64_t)(uintptr_t)p + tile * bytes);
+    return buffer_of((const void*)(uintptr_t)at, __builtin_amdgcn_readfirstlane((int)(tiles * bytes)));
 }
 
 // Up to 16 tokens.  One workgroup: RT row tiles and one of a.splits ranges of units, which its eight

@@ -101,6 +101,19 @@ __device__ __forceinline__ int opaque(int x) {
     return x;
 }
 
+// x & mask | base in one instruction (mask and base as registers: two literals would make it two).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t base) {
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "s"(mask), "v"(base));
+    return r;
+}
+
+// A value that is the same in all lanes, as a scalar.
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+    return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
 // Largest of three, without the quieting of NaN that fmaxf asks for.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
