@@ -20,23 +20,18 @@ namespace {
 
 // The four words (8 values 16 + c) of one word of codes.
 template <typename T>
-__device__ __forceinline__ u32x4v unpack_codes(uint32_t w) {
-    u32x4v r;
-    if (T::bf) {  // 16 + c = 0x4180 | c << 3
-        const uint32_t mask = 0x00780078u, base = 0x41804180u;
-        r[0] = and_or(w >> 3, mask, base);
-        r[1] = and_or(w >> 7, mask, base);
-        r[2] = and_or(w << 1, mask, base);
-        r[3] = and_or(__builtin_amdgcn_alignbit(w, w, 11), mask, base);
-    } else {  // 16 + c = 0x4C00 | c << 6
-        const uint32_t mask = 0x03C003C0u, base = 0x4C004C00u;
-        r[0] = and_or(w, mask, base);
-        r[1] = and_or(w >> 4, mask, base);
-        r[2] = and_or(w << 4, mask, base);
-        r[3] = and_or(__builtin_amdgcn_alignbit(w, w, 8), mask, base);
+struct Unpack {
+    const uint32_t mask, base;  // bfloat16: 16 + c = 0x4180 | c << 3; float16: 0x4C00 | c << 6
+    __device__ __forceinline__ Unpack()
+        : mask(scalar_constant(T::bf ? 0x00780078u : 0x03C003C0u)), base(vector_constant(T::bf ? 0x41804180u : 0x4C004C00u)) {}
+    __device__ __forceinline__ u32x4v operator()(uint32_t w) const {
+        if (T::bf)
+            return u32x4v{(w >> 3 & mask) | base, (w >> 7 & mask) | base, (w << 1 & mask) | base,
+                          (__builtin_amdgcn_alignbit(w, w, 11) & mask) | base};
+        return u32x4v{(w & mask) | base, (w >> 4 & mask) | base, (w << 4 & mask) | base,
+                      (__builtin_amdgcn_alignbit(w, w, 8) & mask) | base};
     }
-    return r;
-}
+};
 // 16 + c - (16 + z) for two codes, in float16; `less` = -(16 + z) twice.
 __device__ __forceinline__ uint32_t take_off(uint32_t w, uint32_t less) {
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, w) + __builtin_bit_cast(half2v, less));

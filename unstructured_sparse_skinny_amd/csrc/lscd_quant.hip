@@ -63,7 +63,7 @@ __global__ __launch_bounds__(256) void quant_decode_kernel(QuantArgs a, uint16_t
             x = *(const uint16_t*)rec | 8u << 16;
         else
             x = ((const uint32_t*)rec)[s * A::kPer / 4];
-        const u32x4v v = unpack_codes<T>(a.codes[(unit * 64 + lane) * 4 + s]);
+        const u32x4v v = Unpack<T>()(a.codes[(unit * 64 + lane) * 4 + s]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int64_t k = (int64_t)u * kQuantUnit + 32 * s + 8 * (lane >> 4) + j;

@@ -15,6 +15,9 @@ __device__ __forceinline__ u32x4v ones_of() {
     return u32x4v{w, w, w, w};
 }
 
+// Instructions that may cross the scheduling barriers below: arithmetic and matrix products.
+constexpr int kFreeOrder = 0xE;
+
 // A workgroup's row tiles as one buffer: unit u of its tile r begins (r * units + u) KB into it.
 // (Offsets of lanes that are off lie outside it: no traffic, zeros.)
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const void* p, int64_t tile, int tiles, int64_t bytes) {
@@ -31,6 +34,7 @@ template <typename T, int KIND, int RT>
 __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a) {
     using A = Aux<T, KIND>;
     constexpr int kAhead = RT <= 2 ? 4 : (RT == 3 ? 3 : 2);
+    const Unpack<T> unpack;
     __shared__ float sh[kQuantWaves][16][RT * 16 + 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
     const int rt0 = blockIdx.x * RT, parts = kQuantWaves * a.splits, part = blockIdx.y * kQuantWaves + wave;
@@ -77,7 +81,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
                 f32x4v d = none;
 #pragma unroll
                 for (int s = kSteps * p; s < kSteps * (p + 1); ++s) {
-                    u32x4v w = unpack_codes<T>(c[i][r][s]);
+                    u32x4v w = unpack(c[i][r][s]);
                     if (!T::bf)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) w[j] = take_off(w[j], less);
@@ -99,7 +103,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
         for (int u = u0; u < full; u += kAhead) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                compute(i);  // (a unit past the end has codes, scales and so weights of zero)
+                if (u + i < full) compute(i);  // (no loads under the branch: the waits count them)
                 load(i, u + i + kAhead, full);
                 load_tokens(i, u + i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
@@ -142,6 +146,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs 
     constexpr int kRowWaves = 4, kTokens = 16 * NT, kTile = kTokens * 256, kPer = kTokens * 16 / 256;
     constexpr int kJoin = kRowWaves * 64 * RT * NT * 4 * 4;  // bytes of one half's sums
     constexpr int kLds = 4 * kTile > kJoin ? 4 * kTile : kJoin;
+    const Unpack<T> unpack;
     __shared__ __attribute__((aligned(16))) unsigned char sh[kLds];
     const int tid = threadIdx.x & 255, lane = threadIdx.x & 63, g = lane >> 4;
     const int half = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);      // which units
@@ -202,60 +207,65 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs 
     store_tokens(0, u0);
     load_tokens(u0 + 1);
     load(1, u0 + 1);
-    __syncthreads();
+    lds_barrier();
     auto unit = [&](int i, int k) {
         const unsigned char* xb = sh + (2 * i + half) * kTile;
         const f32x4v none = {0.f, 0.f, 0.f, 0.f};
+        constexpr int kSteps = 4 / A::kPer;  // steps of one group
+        // x of one step of 32 columns, read a step ahead: the reads of a workgroup take about half as long
+        // as its products, so they have to go on beside them
+        u32x4v x[2][NT];
+        auto read = [&](int s) {
 #pragma unroll
-        for (int p = 0; p < A::kPer; ++p) {
-            constexpr int kSteps = 4 / A::kPer;
-            u32x4v x[kSteps][NT];
+            for (int n = 0; n < NT; ++n)
+                x[s & 1][n] = *(const u32x4v*)(xb + (16 * n + (lane & 15)) * 256 + (((4 * s + g) ^ (lane & 15)) << 4));
+        };
+        f32x4v d[RT][NT], sx[NT];
+        if (u0 + k < u1) {
+        read(0);
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    x[s][n] = *(const u32x4v*)(xb + (16 * n + (lane & 15)) * 256 + (((4 * (kSteps * p + s) + g) ^ (lane & 15)) << 4));
-            f32x4v sx[NT];
+        for (int s = 0; s < 4; ++s) {
+            const int p = s / kSteps;
+            if (s < 3) read(s + 1);
+            __builtin_amdgcn_sched_barrier(kFreeOrder);
+            const bool first = s % kSteps == 0;
             if (T::bf)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    sx[n] = none;
-#pragma unroll
-                    for (int s = 0; s < kSteps; ++s) sx[n] = T::mfma16(x[s][n], ones_of<T>(), sx[n]);
-                }
+                for (int n = 0; n < NT; ++n) sx[n] = T::mfma16(x[s & 1][n], ones_of<T>(), first ? none : sx[n]);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-                const uint32_t z = aux[i][r].zero(p), less = less_of(z);
-                f32x4v d[NT];
+                u32x4v w = unpack(c[i][r][s]);
+                if (!T::bf) {
+                    const uint32_t less = less_of(aux[i][r].zero(p));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) d[n] = none;
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    u32x4v w = unpack_codes<T>(c[i][r][kSteps * p + s]);
-                    if (!T::bf)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) w[j] = take_off(w[j], less);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) d[n] = T::mfma16(x[s][n], w, d[n]);
+                    for (int j = 0; j < 4; ++j) w[j] = take_off(w[j], less);
                 }
-                const float scale = aux[i][r].scale(p), off = 16.f + (float)z;
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[r][n][e] += scale * (T::bf ? d[n][e] - off * sx[n][e] : d[n][e]);
-                // (with several groups a unit, mixing all of them would not fit the registers)
-                if (A::kPer > 1) __builtin_amdgcn_sched_barrier(0);
+                for (int n = 0; n < NT; ++n) d[r][n] = T::mfma16(x[s & 1][n], w, first ? none : d[r][n]);
             }
+            if (s % kSteps == kSteps - 1)
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const float scale = aux[i][r].scale(p), off = 16.f + (float)aux[i][r].zero(p);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[r][n][e] += scale * (T::bf ? d[r][n][e] - off * sx[n][e] : d[r][n][e]);
+                }
+        }
         }
         // the next unit's x into the other buffer (its last reads were before the last barrier)
         store_tokens(i ^ 1, u0 + k + 1);
         load_tokens(u0 + k + 2);
         load(i, u0 + k + 2);
-        __syncthreads();
+        lds_barrier();
     };
-    for (int k = 0; k < rounds; k += 2) {  // (units past the end have weights of zero)
+    // An even number of units (nothing is computed past the end), so that every wait can count on the
+    // other buffer's loads behind its own.
+    for (int k = 0; k < rounds; k += 2) {
         unit(0, k);
-        if (k + 1 < rounds) unit(1, k + 1);
+        unit(1, k + 1);
     }
     // join the two halves; wavefront `wave` of half 0 then holds the sums of its rows
     float* js = (float*)sh + (wave * 64 + lane) * (RT * NT * 4);

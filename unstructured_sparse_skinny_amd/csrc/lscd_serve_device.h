@@ -101,11 +101,15 @@ __device__ __forceinline__ int opaque(int x) {
     return x;
 }
 
-// x & mask | base in one instruction (mask and base as registers: two literals would make it two).
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t base) {
-    uint32_t r;
-    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "s"(mask), "v"(base));
-    return r;
+// Constants in registers that the compiler does not see through: x & mask | base is one v_and_or_b32
+// with them, two instructions with literals.
+__device__ __forceinline__ uint32_t scalar_constant(uint32_t x) {
+    asm("" : "+s"(x));
+    return x;
+}
+__device__ __forceinline__ uint32_t vector_constant(uint32_t x) {
+    asm("" : "+v"(x));
+    return x;
 }
 
 // A value that is the same in all lanes, as a scalar.
@@ -114,11 +118,17 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
     return (int64_t)((uint64_t)hi << 32 | lo);
 }
 
-// Largest of three, without the quieting of NaN that fmaxf asks for.
+// A barrier for data in LDS: waits for this wavefront's LDS accesses, not (as __syncthreads does) for
+// its loads from memory, which may stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Largest of three; NaN if one is (v_maximum3_f32, which asks for no quieting of its operands).
 __device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-    return r;
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // The values of the lanes l and l ^ 32 (l and l ^ 16): the swap exchanges halves (odd and even
