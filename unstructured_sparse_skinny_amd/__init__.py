@@ -411,6 +411,15 @@ def lscd_destroy(h: Handle):
 
 # ---------------------------------------------------------------- serving operators
 
+_current_raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream() builds an object: 3 us)
+
+
+def _stream_on(stream, device):
+    """The given stream's handle, or that of the device's current one."""
+    if stream is None:
+        return _current_raw_stream(device.index)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
 
 class Quant:
     """Owner of an lscd_quant_t (an M x K matrix of 4-bit codes); freed by lscd_quant_destroy (or when collected)."""
@@ -443,7 +452,7 @@ def lscd_quant_encode(codes, scales, K: int, zeros=None, group: int = 128, strea
     h = ctypes.c_void_p()
     _check(_lib.lscd_quant_encode(codes.data_ptr(), codes.stride(0), scales.data_ptr(),
                                   None if zeros is None else zeros.data_ptr(), M, K, group, _TYPES[scales.dtype],
-                                  _stream(stream), ctypes.byref(h)), "lscd_quant_encode")
+                                  _stream_on(stream, codes.device), ctypes.byref(h)), "lscd_quant_encode")
     return Quant(h.value, M, K, group, scales.dtype, codes.device)
 
 
@@ -462,7 +471,7 @@ def lscd_quant_linear(h: Quant, B, C, stream=None):
     N = B.shape[0]
     pb, lb = _matrix(B, "B", N, h.K, h)
     pc, lc = _matrix(C, "C", N, h.M, h)
-    _check(_lib.lscd_quant_linear(h.ptr, pb, lb, pc, lc, N, _stream(stream)), "lscd_quant_linear")
+    _check(_lib.lscd_quant_linear(h.ptr, pb, lb, pc, lc, N, _stream_on(stream, h.device)), "lscd_quant_linear")
     return C
 
 
@@ -471,7 +480,7 @@ def lscd_quant_decode(h: Quant, W, stream=None):
     p, ld = _matrix(W, "W", h.M, h.K, h)
     if ld != h.K:
         raise ValueError("W must be contiguous")
-    _check(_lib.lscd_quant_decode(h.ptr, p, _stream(stream)), "lscd_quant_decode")
+    _check(_lib.lscd_quant_decode(h.ptr, p, _stream_on(stream, h.device)), "lscd_quant_decode")
     return W
 
 
@@ -534,7 +543,7 @@ def lscd_cache_write(cache: Cache, k, v, slots, stream=None):
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("k, v and slots must have one number of tokens")
     _check(_lib.lscd_cache_write(cache.ptr, pk, sk, pv, sv, _ints(slots, "slots", cache.device), T,
-                                 _same_type(k, v, "k and v"), _stream(stream)), "lscd_cache_write")
+                                 _same_type(k, v, "k and v"), _stream_on(stream, cache.device)), "lscd_cache_write")
 
 
 def lscd_cache_read(cache: Cache, slots, k, v, stream=None):
@@ -545,7 +554,7 @@ def lscd_cache_read(cache: Cache, slots, k, v, stream=None):
     if k.shape[0] != T or v.shape[0] != T:
         raise ValueError("k, v and slots must have one number of tokens")
     _check(_lib.lscd_cache_read(cache.ptr, _ints(slots, "slots", cache.device), T, pk, sk, pv, sv,
-                                _same_type(k, v, "k and v"), _stream(stream)), "lscd_cache_read")
+                                _same_type(k, v, "k and v"), _stream_on(stream, cache.device)), "lscd_cache_read")
     return k, v
 
 
@@ -585,7 +594,7 @@ def lscd_attention(h: Attention, cache: Cache, q, start, length, table, out, sca
     _check(_lib.lscd_attention(h.ptr, cache.ptr, pq, sq, _ints(start, "start", dev), _ints(length, "length", dev), pt,
                                table.stride(0) if S > 1 else table.shape[1], table.shape[1], S, T,
                                h.head_dim ** -0.5 if scale is None else scale, causal, window, po, so,
-                               _same_type(q, out, "q and out"), _stream(stream)), "lscd_attention")
+                               _same_type(q, out, "q and out"), _stream_on(stream, dev)), "lscd_attention")
     return out
 
 
