@@ -507,8 +507,9 @@ lscd_status_t lscd_attention_destroy(lscd_attention_t h);
  * product.  Results do not depend on timing (partial sums are added in a fixed order) but their
  * last bits may depend on the other sequences in the call, which move the points where work is split.
  * INVALID_VALUE: null pointers, misalignment, negative sizes, a scale that is not finite, wrong
- * device.  NOT_SUPPORTED: T * (q_heads / kv_heads) or table_pages * page_size above 2^30, types
- * that do not fit together.
+ * device.  NOT_SUPPORTED: T * (q_heads / kv_heads) or table_pages * page_size above 2^30, more than
+ * 2^31 stretches of 32 positions over all key heads and tiles of 16 query rows if every sequence filled
+ * its table, types that do not fit together.
  */
 lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, const void* q, int64_t q_stride,
                              const int32_t* start, const int32_t* length, const int32_t* table, int64_t table_stride,

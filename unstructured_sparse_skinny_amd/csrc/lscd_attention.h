@@ -71,83 +71,107 @@ __device__ __forceinline__ int tile_units(const AttnArgs& a, const Seq& q, int t
     tile_range<ROWS>(a, q, t, &low, &high);
     return max(1, (high + TOKENS - 1) / TOKENS - low / TOKENS);
 }
-// Units of one key head of the sequence; 0 if it belongs to the other kernel.
+// The units are laid out on a line, sequence after sequence, key head after key head, row tile after
+// row tile; kStart slots before an item's units stand for what its start and end cost.  Slots of one
+// key head of the sequence; 0 if it belongs to the other kernel.
+constexpr int kStart = 1;
 template <int ROWS, int TOKENS, bool FEW>
-__device__ __forceinline__ int head_units(const AttnArgs& a, const Seq& q) {
+__device__ __forceinline__ int head_slots(const AttnArgs& a, const Seq& q) {
     if (q.rows == 0 || (q.rows <= a.few_limit) != FEW) return 0;
     int u = 0;
-    for (int t = 0; t * ROWS < q.rows; ++t) u += tile_units<ROWS, TOKENS>(a, q, t);
+    for (int t = 0; t * ROWS < q.rows; ++t) u += tile_units<ROWS, TOKENS>(a, q, t) + kStart;
     return u;
 }
 
-// Where a range of units begins: sequence, key head, row tile, unit inside the tile.
-struct Place {
-    int seq, head, tile, unit;
-    int per_head;
+// The cut of U slots into G ranges whose sizes differ by at most one.
+struct Cut {
+    int base, extra;
+    Cut() = default;
+    __device__ __forceinline__ Cut(int U, int G) : base(U / G), extra(U % G) {}
+    __device__ __forceinline__ int begin(int w) const { return w * base + (w < extra ? w : extra); }
+    __device__ __forceinline__ int owner(int u) const {
+        const int big = extra * (base + 1);
+        return u < big ? u / (base + 1) : extra + (u - big) / base;
+    }
 };
 
-// Total units, and the sequence that holds unit `u` with the units before it; every wavefront
-// works it out for itself (64 sequences at a time).
+// A workgroup's range of slots, and the item it begins in: sequence, key head, row tile, unit (or
+// -1, -2 .. in the slots before its units).
+struct Work {
+    Cut cut;
+    int u, end;
+    int seq, head, tile, unit;
+    Seq q;
+};
+// Works it out (every wavefront for itself, 64 sequences at a time).  False: there is nothing to do.
 template <int ROWS, int TOKENS, bool FEW>
-__device__ __forceinline__ int64_t total_units(const AttnArgs& a, int lane) {
-    int64_t total = 0;
-    for (int s0 = 0; s0 < a.sequences; s0 += 64) {
-        int64_t mine = 0;
-        if (s0 + lane < a.sequences)
-            mine = (int64_t)head_units<ROWS, TOKENS, FEW>(a, read_seq(a, s0 + lane)) * a.c.heads;
-        for (int d = 1; d < 64; d <<= 1) mine += __shfl_xor(mine, d, 64);
-        total += mine;
-    }
-    return uniform(total);
-}
-template <int ROWS, int TOKENS, bool FEW>
-__device__ __forceinline__ Place find_unit(const AttnArgs& a, int64_t u, int lane) {
-    Place p = {};
-    int64_t before = 0;
-    for (int s0 = 0; s0 < a.sequences; s0 += 64) {
-        int per = 0;
-        if (s0 + lane < a.sequences) per = head_units<ROWS, TOKENS, FEW>(a, read_seq(a, s0 + lane));
-        int64_t sum = (int64_t)per * a.c.heads;
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int lane, int me, int G, Work* w) {
+    auto slots_of = [&](int s, Seq* q) {
+        if (s >= a.sequences) return 0;
+        *q = read_seq(a, s);
+        return head_slots<ROWS, TOKENS, FEW>(a, *q);
+    };
+    auto scan = [&](int x) {  // inclusive sums over the lanes
         for (int d = 1; d < 64; d <<= 1) {
-            const int64_t up = __shfl_up(sum, d, 64);
-            if (lane >= d) sum += up;
+            const int up = __shfl_up(x, d, 64);
+            if (lane >= d) x += up;
         }
-        const uint64_t past = __ballot(before + sum > u);
+        return x;
+    };
+    Seq q = {};
+    int per = slots_of(lane, &q), sum = scan(per * a.c.heads);
+    int U = __builtin_amdgcn_readlane(sum, 63);
+    for (int s0 = 64; s0 < a.sequences; s0 += 64) {
+        Seq other = {};
+        U += __builtin_amdgcn_readlane(scan(slots_of(s0 + lane, &other) * a.c.heads), 63);
+    }
+    w->cut = Cut(U, G);
+    w->u = w->cut.begin(me);
+    w->end = w->cut.begin(me + 1);
+    if (w->u >= w->end) return false;
+    int before = 0, s0 = 0;
+    for (;;) {
+        const uint64_t past = __ballot(before + sum > w->u);
         if (past) {
             const int l = __builtin_ctzll(past);
-            p.seq = s0 + l;
-            p.per_head = __builtin_amdgcn_readlane(per, l);
-            const int64_t start = before + __shfl(sum, l, 64) - (int64_t)p.per_head * a.c.heads;
-            const int rest = (int)(u - start);
-            p.head = rest / p.per_head;
-            p.unit = rest % p.per_head;
+            const int ph = __builtin_amdgcn_readlane(per, l);
+            const int rest = w->u - (before + __builtin_amdgcn_readlane(sum, l) - ph * a.c.heads);
+            w->seq = s0 + l;
+            w->head = rest / ph;
+            w->unit = rest % ph;
+            w->q.first = __builtin_amdgcn_readlane(q.first, l);
+            w->q.n = __builtin_amdgcn_readlane(q.n, l);
+            w->q.len = __builtin_amdgcn_readlane(q.len, l);
+            w->q.rows = __builtin_amdgcn_readlane(q.rows, l);
             break;
         }
-        before += __shfl(sum, 63, 64);
+        before += __builtin_amdgcn_readlane(sum, 63);
+        s0 += 64;
+        q = Seq{};
+        per = slots_of(s0 + lane, &q);
+        sum = scan(per * a.c.heads);
     }
-    p.seq = __builtin_amdgcn_readfirstlane(p.seq);
-    p.head = __builtin_amdgcn_readfirstlane(p.head);
-    p.unit = __builtin_amdgcn_readfirstlane(p.unit);
-    p.per_head = __builtin_amdgcn_readfirstlane(p.per_head);
-    const Seq q = read_seq(a, p.seq);
-    for (p.tile = 0; (p.tile + 1) * ROWS < q.rows; ++p.tile) {
-        const int n = tile_units<ROWS, TOKENS>(a, q, p.tile);
-        if (p.unit < n) break;
-        p.unit -= n;
+    for (w->tile = 0; (w->tile + 1) * ROWS < w->q.rows; ++w->tile) {
+        const int n = tile_units<ROWS, TOKENS>(a, w->q, w->tile) + kStart;
+        if (w->unit < n) break;
+        w->unit -= n;
     }
-    return p;
+    w->unit -= kStart;
+    return true;
 }
 
-// The cut of U units into G ranges whose sizes differ by at most one.
-struct Cut {
-    int64_t base, extra;
-    __device__ __forceinline__ Cut(int64_t U, int G) : base(U / G), extra(U % G) {}
-    __device__ __forceinline__ int64_t begin(int w) const { return w * base + (w < extra ? w : extra); }
-    __device__ __forceinline__ int owner(int64_t u) const {
-        const int64_t big = extra * (base + 1);
-        return (int)(u < big ? u / (base + 1) : extra + (u - big) / base);
-    }
-};
+// The next item that belongs to this kernel; there has to be one.
+template <int ROWS, bool FEW>
+__device__ __forceinline__ void next_item(const AttnArgs& a, int* seq, int* head, int* tile, Seq* q) {
+    if ((++*tile) * ROWS < q->rows) return;
+    *tile = 0;
+    if (++*head < a.c.heads) return;
+    *head = 0;
+    do {
+        ++*seq;
+        *q = read_seq(a, *seq);
+    } while (q->rows == 0 || (q->rows <= a.few_limit) != FEW);
+}
 
 // The table's entry for position t (the last one behind the table), and the page it names (an entry
 // outside the pool is read as page 0).

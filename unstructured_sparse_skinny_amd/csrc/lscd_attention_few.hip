@@ -154,6 +154,18 @@ struct Few {
     }
 };
 
+// One item, a row tile: its rows, and the positions that they see.
+struct FewItem {
+    Seq q;
+    int seq, head, tile;
+    int low, high, units;  // positions [low, high) are seen by some row; units from low / kFewTokens on
+    __device__ __forceinline__ void measure(const AttnArgs& a) {
+        tile_range<kFewRows>(a, q, tile, &low, &high);
+        units = max(1, (high + kFewTokens - 1) / kFewTokens - low / kFewTokens);
+    }
+    __device__ __forceinline__ int first_position(int unit) const { return (low / kFewTokens + unit) * kFewTokens; }
+};
+
 template <typename T, bool E4M3, int DP>
 __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs a) {
     using F = Few<T, E4M3, DP>;
@@ -162,169 +174,63 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
     __shared__ float sh_m[kFewWaves][kFewRows], sh_l[kFewWaves][kFewRows];
     __shared__ uint32_t sh_last;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int G = gridDim.x, me = blockIdx.x;
-    const int64_t U = total_units<kFewRows, kFewTokens, true>(a, lane);
-    if (U == 0) return;
-    const Cut cut(U, G);
-    int64_t u = cut.begin(me);
-    const int64_t end = cut.begin(me + 1);
-    if (u >= end) return;
-    Place p = find_unit<kFewRows, kFewTokens, true>(a, u, lane);
-    Seq q = read_seq(a, p.seq);
-    const int D = a.c.head_dim;
+    const int me = blockIdx.x;
+    Work wk;
+    if (!find_work<kFewRows, kFewTokens, true>(a, lane, me, gridDim.x, &wk)) return;
+    const Cut cut = wk.cut;
+    const int end = wk.end, D = a.c.head_dim;
 
-    while (u < end) {
-        // One item, or the part of it that lies in this range: row tile p.tile, units [p.unit, last).
-        int low, high;
-        tile_range<kFewRows>(a, q, p.tile, &low, &high);
-        const int units = max(1, (high + kFewTokens - 1) / kFewTokens - low / kFewTokens);
-        const int64_t item = u - p.unit;  // the item's first unit
-        const int last = (int)min((int64_t)units, p.unit + (end - u));
-        const int t_base = low / kFewTokens * kFewTokens;
+    FewItem it = {wk.q, wk.seq, wk.head, wk.tile};
+    it.measure(a);
+    int item = wk.u - wk.unit;                 // the slot of the item's first unit
+    int first = max(wk.unit, 0), k = first;    // the first unit of it in this range; the present one
+    if (item + first >= end) return;
 
-        // Query rows: the B operand, and what each row sees.
-        const int row = p.tile * kFewRows + (lane & 15);
-        const bool live = row < q.rows;
-        const int token = row / a.share;
-        const int qh = p.head * a.share + row % a.share;
-        const uint16_t* qp = (const uint16_t*)a.q + (int64_t)(q.first + (live ? token : 0)) * a.q_stride + (int64_t)qh * D;
-        u32x4v qr[F::kSteps];
+    // What the lane's query row is and sees.
+    bool live;
+    int see_high, see_low, all_high, all_low;
+    u32x4v qr[F::kSteps];
+    auto load_queries = [&]() {
+        const int row = it.tile * kFewRows + (lane & 15);
+        live = row < it.q.rows;
+        const int token = row / a.share, qh = it.head * a.share + row % a.share;
+        const uint16_t* qp = (const uint16_t*)a.q + (int64_t)(it.q.first + (live ? token : 0)) * a.q_stride + (int64_t)qh * D;
 #pragma unroll
         for (int s = 0; s < F::kSteps; ++s) {
             const int d = F::step_channel(s, lane >> 4);
             qr[s] = u32x4v{0u, 0u, 0u, 0u};
             if (live && d < D) qr[s] = *(const u32x4v*)(qp + d);
         }
-        const int pos = q.len - q.n + token;
-        const int see_high = live ? (a.causal ? min(pos + 1, q.len) : q.len) : 0;
-        const int see_low = a.window ? pos - a.window + 1 : 0;
+        const int pos = it.q.len - it.q.n + token;
+        see_high = live ? (a.causal ? min(pos + 1, it.q.len) : it.q.len) : 0;
+        see_low = a.window ? pos - a.window + 1 : 0;
         // every row sees positions [all_low, all_high): no masks there
-        const int tok0 = p.tile * kFewRows / a.share, tok1 = (min(q.rows, (p.tile + 1) * kFewRows) - 1) / a.share;
-        const int all_high = a.causal ? min(q.len - q.n + tok0 + 1, q.len) : q.len;
-        const int all_low = a.window ? q.len - q.n + tok1 - a.window + 1 : 0;
+        const int tok0 = it.tile * kFewRows / a.share, tok1 = (min(it.q.rows, (it.tile + 1) * kFewRows) - 1) / a.share;
+        all_high = a.causal ? min(it.q.len - it.q.n + tok0 + 1, it.q.len) : it.q.len;
+        all_low = a.window ? it.q.len - it.q.n + tok1 - a.window + 1 : 0;
+    };
 
-        float m = kNoScore, l = 0.f;
-        f32x4v o[VW];
+    float m = kNoScore, l = 0.f;
+    f32x4v o[VW];
+    auto clear = [&]() {
+        m = kNoScore;
+        l = 0.f;
 #pragma unroll
         for (int i = 0; i < VW; ++i) o[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
+    };
 
-        F f;
-        const HeadBase hb(a, p.head, E4M3 ? 1 : 2);
-        int t0 = t_base + p.unit * kFewTokens + 32 * wave;
-        int here[2] = {entry_of(a, p.seq, t0), entry_of(a, p.seq, t0 + 16)};
-        // keys before values, here as in the loop: the wait for the older loads then leaves the younger
-        // ones in flight
-        f.load_keys(a, hb, here, t0, high, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        f.load_values(a, hb, here, t0, low, high, lane);
-        __builtin_amdgcn_sched_barrier(0);
-        int next[2] = {entry_of(a, p.seq, t0 + kFewTokens), entry_of(a, p.seq, t0 + kFewTokens + 16)};
-        for (int k = p.unit; k < last; ++k, t0 += kFewTokens) {
-            here[0] = next[0];
-            here[1] = next[1];
-            next[0] = entry_of(a, p.seq, t0 + 2 * kFewTokens);
-            next[1] = entry_of(a, p.seq, t0 + 2 * kFewTokens + 16);
-            // (the last unit loads nothing, with the same instructions: no branch between loads, whose
-            // number in flight the waits count)
-            const int next_high = k + 1 < last ? high : 0;
-            f32x4v s[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                s[h] = f32x4v{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(f.key_operand(h, st), qr[st], s[h]);
-            }
-            f.load_keys(a, hb, here, t0 + kFewTokens, next_high, lane);
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = s[i / 4][i % 4] * a.scale_log2;
-            const bool masked = t0 < all_low || t0 + 32 > all_high;
-            if (masked) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int t = t0 + 16 * (i / 4) + 4 * (lane >> 4) + i % 4;
-                    if (t >= see_high || t < see_low) x[i] = -__builtin_inff();
-                }
-            }
-            float most = x[0];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) most = fmaxf(most, x[i]);
-            if (__any(most > m + kLazy)) {
-                const float to = fmaxf(m, max_quarters(most));
-                const float by = exp2_fast(m - to);
-                m = to;
-                l *= by;
-#pragma unroll
-                for (int i = 0; i < VW; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) o[i][r] *= by;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = exp2_fast(x[i] - m);
-                l += x[i];
-            }
-            u32x4v pb;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pb[i] = T::pack(x[2 * i], x[2 * i + 1]);
-            bool odd = false;  // an infinity or NaN that some row may not see
-            if (masked) {
-                f.mask_scales(t0, low, high, lane);
-                odd = __any(f.any_odd());
-            }
-            if (!odd) {
-#pragma unroll
-                for (int w = 0; w < VW / 2; ++w) {
-                    u32x4v v0, v1;
-                    f.value_operands(w, v0, v1);
-                    o[2 * w] = T::mfma16(v0, pb, o[2 * w]);
-                    o[2 * w + 1] = T::mfma16(v1, pb, o[2 * w + 1]);
-                }
-            } else {
-                // 0 * infinity would be NaN in rows that do not see the token: what is finite as
-                // ever, the rest one token at a time and added only where it is seen
-#pragma unroll
-                for (int w = 0; w < VW / 2; ++w) {
-                    u32x4v v0, v1, f0, f1;
-                    f.value_operands(w, v0, v1);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        f0[i] = T::finite(v0[i]);
-                        f1[i] = T::finite(v1[i]);
-                        v0[i] ^= f0[i];
-                        v1[i] ^= f1[i];
-                    }
-                    o[2 * w] = T::mfma16(f0, pb, o[2 * w]);
-                    o[2 * w + 1] = T::mfma16(f1, pb, o[2 * w + 1]);
-#pragma unroll 1
-                    for (int j = 0; j < 32; ++j) {
-                        const int t = t0 + 16 * ((j & 7) / 4) + 4 * (j >> 3) + (j & 3);
-                        const bool mine = (lane >> 4) == (j >> 3);
-                        u32x4v b0, b1;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t keep = mine && (j & 7) / 2 == i ? ((j & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-                            b0[i] = v0[i] & keep;
-                            b1[i] = v1[i] & keep;
-                        }
-                        const f32x4v z = {0.f, 0.f, 0.f, 0.f};
-                        const f32x4v y0 = T::mfma16(b0, pb, z), y1 = T::mfma16(b1, pb, z);
-                        if (t < see_high && t >= see_low) {
-                            o[2 * w] += y0;
-                            o[2 * w + 1] += y1;
-                        }
-                    }
-                }
-            }
-            f.load_values(a, hb, here, t0 + kFewTokens, low, next_high, lane);
-        }
+    // The end of an item, or of the part of it in this range: joins the four wavefronts and writes the
+    // rows, or a partial result.
+    auto finish = [&]() {
+        // (worked out here, not kept in registers through the loop)
+        const int tid = opaque(threadIdx.x), le = tid & 63;
         l = sum_quarters(l);
 
         // Join the four wavefronts.
-        __syncthreads();
-        if (lane < 16) {
-            sh_m[wave][lane] = m;
-            sh_l[wave][lane] = l;
+        lds_barrier();
+        if (le < 16) {
+            sh_m[wave][le] = m;
+            sh_l[wave][le] = l;
         }
         if (live) {
 #pragma unroll
@@ -332,23 +238,23 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
 #pragma unroll
                 for (int i = 0; i < VW; i += 4) {
                     f32x4v x = {o[i][r], o[i + 1][r], o[i + 2][r], o[i + 3][r]};
-                    *(f32x4v*)&sh_o[wave][lane & 15][VW * (4 * (lane >> 4) + r) + i] = x;
+                    *(f32x4v*)&sh_o[wave][le & 15][VW * (4 * (le >> 4) + r) + i] = x;
                 }
         }
-        __syncthreads();
-        const int rows = min(kFewRows, q.rows - p.tile * kFewRows);
-        const bool whole = p.unit == 0 && last == units;
-        const int owner = whole ? me : cut.owner(item), behind = whole ? me : cut.owner(item + units - 1);
+        lds_barrier();
+        const int rows = min(kFewRows, it.q.rows - it.tile * kFewRows);
+        const bool whole = first == 0 && k + 1 == it.units;
+        const int owner = whole ? me : cut.owner(item), behind = whole ? me : cut.owner(item + it.units - 1);
         constexpr int kFloats = kFewRows * (DP + 2);  // a pair (maximum, sum) per row, then the rows
-        float* mine = a.part + (int64_t)(2 * me + (p.unit == 0 ? 1 : 0)) * kFloats;
+        float* mine = a.part + (int64_t)(2 * me + (first == 0 ? 1 : 0)) * kFloats;
         auto write = [&](int r, int d, float L, float x, float y) {  // channels d, d + 1 of row r
-            const int rw = p.tile * kFewRows + r;
+            const int rw = it.tile * kFewRows + r;
             const float inv = L != 0.f ? 1.f / L : 0.f;
-            uint16_t* op = (uint16_t*)a.o + (int64_t)(q.first + rw / a.share) * a.o_stride +
-                           (int64_t)(p.head * a.share + rw % a.share) * D + d;
+            uint16_t* op = (uint16_t*)a.o + (int64_t)(it.q.first + rw / a.share) * a.o_stride +
+                           (int64_t)(it.head * a.share + rw % a.share) * D + d;
             if (d < D) *(uint32_t*)op = L != 0.f ? T::pack(x * inv, y * inv) : 0u;
         };
-        for (int i = threadIdx.x; i < rows * (DP / 2); i += 64 * kFewWaves) {
+        for (int i = tid; i < rows * (DP / 2); i += 64 * kFewWaves) {
             const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
             float M = sh_m[0][r];
 #pragma unroll
@@ -369,7 +275,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             }
         }
         if (!whole && arrive_last(a.count + owner, (uint32_t)(behind - owner + 1), &sh_last)) {
-            for (int i = threadIdx.x; i < rows * (DP / 2); i += 64 * kFewWaves) {
+            for (int i = tid; i < rows * (DP / 2); i += 64 * kFewWaves) {
                 const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
                 float M = kNoScore, L = 0.f, x = 0.f, y = 0.f;
                 for (int w = owner; w <= behind; ++w) {
@@ -386,21 +292,144 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                 write(r, d, L, x, y);
             }
         }
+    };
 
-        // The next item.
-        u += last - p.unit;
-        if (u >= end) break;
-        p.unit = 0;
-        if ((++p.tile) * kFewRows >= q.rows) {
-            p.tile = 0;
-            if (++p.head == a.c.heads) {
-                p.head = 0;
-                do {
-                    ++p.seq;
-                    q = read_seq(a, p.seq);
-                } while (q.rows == 0 || q.rows > a.few_limit);
+    F f;
+    {
+        const HeadBase hb(a, it.head, E4M3 ? 1 : 2);
+        const int t0 = it.first_position(k) + 32 * wave;
+        const int e[2] = {entry_of(a, it.seq, t0), entry_of(a, it.seq, t0 + 16)};
+        load_queries();
+        // keys before values, here as in the loop: the wait for the older loads then leaves the younger
+        // ones in flight
+        __builtin_amdgcn_sched_barrier(0);
+        f.load_keys(a, hb, e, t0, it.high, lane);
+        __builtin_amdgcn_sched_barrier(0);
+        f.load_values(a, hb, e, t0, it.low, it.high, lane);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    clear();
+    for (;;) {
+        const int t0 = it.first_position(k) + 32 * wave, low = it.low, high = it.high;
+        // The unit after this one, maybe the next item's first: its loads are issued while this one is
+        // computed, so that an item's end does not drain them.  (Past the range's end nothing is
+        // loaded, with the same instructions: no branch between loads, whose number the waits count.)
+        FewItem nx = it;
+        int nk = k + 1, nitem = item;
+        bool more = item + nk < end;
+        const bool ends = nk == it.units || !more;
+        if (ends && nk == it.units) {
+            nitem = item + it.units + kStart;
+            more = nitem < end;
+            nk = 0;
+            if (more) {
+                next_item<kFewRows, true>(a, &nx.seq, &nx.head, &nx.tile, &nx.q);
+                nx.measure(a);
             }
         }
+        const HeadBase hb(a, nx.head, E4M3 ? 1 : 2);
+        const int nt = nx.first_position(nk) + 32 * wave, next_high = more ? nx.high : 0;
+        const int e[2] = {entry_of(a, nx.seq, nt), entry_of(a, nx.seq, nt + 16)};
+        f32x4v s[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            s[h] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(f.key_operand(h, st), qr[st], s[h]);
+        }
+        f.load_keys(a, hb, e, nt, next_high, lane);
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = s[i / 4][i % 4] * a.scale_log2;
+        const bool masked = t0 < all_low || t0 + 32 > all_high;
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int t = t0 + 16 * (i / 4) + 4 * (lane >> 4) + i % 4;
+                if (t >= see_high || t < see_low) x[i] = -__builtin_inff();
+            }
+        }
+        float most = x[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) most = fmaxf(most, x[i]);
+        if (__any(most > m + kLazy)) {
+            const float to = fmaxf(m, max_quarters(most));
+            const float by = exp2_fast(m - to);
+            m = to;
+            l *= by;
+#pragma unroll
+            for (int i = 0; i < VW; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[i][r] *= by;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = exp2_fast(x[i] - m);
+            l += x[i];
+        }
+        u32x4v pb;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pb[i] = T::pack(x[2 * i], x[2 * i + 1]);
+        bool odd = false;  // an infinity or NaN that some row may not see
+        if (masked) {
+            f.mask_scales(t0, low, high, lane);
+            odd = __any(f.any_odd());
+        }
+        if (!odd) {
+#pragma unroll
+            for (int w = 0; w < VW / 2; ++w) {
+                u32x4v v0, v1;
+                f.value_operands(w, v0, v1);
+                o[2 * w] = T::mfma16(v0, pb, o[2 * w]);
+                o[2 * w + 1] = T::mfma16(v1, pb, o[2 * w + 1]);
+            }
+        } else {
+            // 0 * infinity would be NaN in rows that do not see the token: what is finite as
+            // ever, the rest one token at a time and added only where it is seen
+#pragma unroll
+            for (int w = 0; w < VW / 2; ++w) {
+                u32x4v v0, v1, f0, f1;
+                f.value_operands(w, v0, v1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f0[i] = T::finite(v0[i]);
+                    f1[i] = T::finite(v1[i]);
+                    v0[i] ^= f0[i];
+                    v1[i] ^= f1[i];
+                }
+                o[2 * w] = T::mfma16(f0, pb, o[2 * w]);
+                o[2 * w + 1] = T::mfma16(f1, pb, o[2 * w + 1]);
+#pragma unroll 1
+                for (int j = 0; j < 32; ++j) {
+                    const int t = t0 + 16 * ((j & 7) / 4) + 4 * (j >> 3) + (j & 3);
+                    const bool mine = (lane >> 4) == (j >> 3);
+                    u32x4v b0, b1;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t keep = mine && (j & 7) / 2 == i ? ((j & 1) ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
+                        b0[i] = v0[i] & keep;
+                        b1[i] = v1[i] & keep;
+                    }
+                    const f32x4v z = {0.f, 0.f, 0.f, 0.f};
+                    const f32x4v y0 = T::mfma16(b0, pb, z), y1 = T::mfma16(b1, pb, z);
+                    if (t < see_high && t >= see_low) {
+                        o[2 * w] += y0;
+                        o[2 * w + 1] += y1;
+                    }
+                }
+            }
+        }
+        f.load_values(a, hb, e, nt, nx.low, next_high, lane);
+        if (ends) {
+            finish();
+            if (!more) break;
+            clear();
+            it = nx;
+            first = 0;
+            load_queries();
+        }
+        item = nitem;
+        k = nk;
     }
 }
 

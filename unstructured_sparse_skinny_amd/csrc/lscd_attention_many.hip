@@ -126,14 +126,12 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
     const int G = gridDim.x;
     // consecutive ranges on one XCD (workgroups go to the 8 XCDs in turn): they share keys in its L2
     const int me = (G & 7) == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
-    const int64_t U = total_units<kManyRows, F::kTokens, false>(a, lane);
-    if (U == 0) return;
-    const Cut cut(U, G);
-    int64_t u = cut.begin(me);
-    const int64_t end = cut.begin(me + 1);
-    if (u >= end) return;
-    Place p = find_unit<kManyRows, F::kTokens, false>(a, u, lane);
-    Seq q = read_seq(a, p.seq);
+    Work p;
+    if (!find_work<kManyRows, F::kTokens, false>(a, lane, me, G, &p)) return;
+    const Cut cut = p.cut;
+    int u = p.u;
+    const int end = p.end;
+    Seq& q = p.q;
     const int D = a.c.head_dim;
 
     // LDS offsets of this lane: key chunks by step, value columns by block
@@ -145,8 +143,13 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
         int low, high;
         tile_range<kManyRows>(a, q, p.tile, &low, &high);
         const int units = max(1, (high + F::kTokens - 1) / F::kTokens - low / F::kTokens);
-        const int64_t item = u - p.unit;
-        const int last = (int)min((int64_t)units, p.unit + (end - u));
+        const int item = u - p.unit;  // the slot of the item's first unit
+        if (p.unit < 0) {
+            u = item;
+            p.unit = 0;
+            if (u >= end) break;
+        }
+        const int last = min(units, p.unit + (end - u));
         const int t_base = low / F::kTokens * F::kTokens;
 
         const int row0 = p.tile * kManyRows + 32 * wave, row = row0 + (lane & 31);
@@ -386,17 +389,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
 
         u += last - p.unit;
         if (u >= end) break;
-        p.unit = 0;
-        if ((++p.tile) * kManyRows >= q.rows) {
-            p.tile = 0;
-            if (++p.head == a.c.heads) {
-                p.head = 0;
-                do {
-                    ++p.seq;
-                    q = read_seq(a, p.seq);
-                } while (q.rows <= a.few_limit);
-            }
-        }
+        p.unit = -kStart;
+        next_item<kManyRows, false>(a, &p.seq, &p.head, &p.tile, &q);
     }
 }
 

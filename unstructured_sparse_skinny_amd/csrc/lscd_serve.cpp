@@ -310,6 +310,9 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
         const int64_t units = (span + tokens - 1) / tokens * h->kv_heads;
         return (int)std::min<int64_t>(most, tiles > most ? most : tiles * std::min<int64_t>(units, most));
     };
+    // (slots of work are counted in 32 bits on the device)
+    if ((double)(T * share / lscd::kFewRows + sequences) * ((double)span / 32 + 2) * h->kv_heads >= 2147483648.0)
+        return LSCD_ERROR_NOT_SUPPORTED;
     if (sequences > 1 || !both) {
         hipError_t e = lscd::launch_attention_few(
             a, type, grid(lscd::attention_few_grid(h->cus), lscd::kFewRows, lscd::kFewTokens), (hipStream_t)stream);
