@@ -275,21 +275,55 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             }
         }
         if (!whole && arrive_last(a.count + owner, (uint32_t)(behind - owner + 1), &sh_last)) {
-            for (int i = tid; i < rows * (DP / 2); i += 64 * kFewWaves) {
-                const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
-                float M = kNoScore, L = 0.f, x = 0.f, y = 0.f;
-                for (int w = owner; w <= behind; ++w) {
-                    const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
-                    float m1, l1, x1, y1;
-                    get2(part + 2 * r, &m1, &l1);
-                    get2(part + 2 * kFewRows + r * DP + d, &x1, &y1);
-                    const float to = fmaxf(M, m1), b0 = exp2_fast(M - to), b1 = exp2_fast(m1 - to);
-                    M = to;
-                    L = L * b0 + l1 * b1;
-                    x = x * b0 + x1 * b1;
-                    y = y * b0 + y1 * b1;
+            // The parts in ascending order, 32 at a time: their maxima and sums through LDS, then each
+            // thread's channels, eight loads in flight (a long sequence has a part per workgroup).
+            constexpr int kParts = 32, kMine = kFewRows * (DP / 2) / (64 * kFewWaves);
+            float* pair = &sh_o[0][0][0];
+            float M[kMine], L[kMine], x[kMine], y[kMine];
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                M[j] = kNoScore;
+                L[j] = x[j] = y[j] = 0.f;
+            }
+            auto part_of = [&](int w) { return a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats; };
+            for (int w0 = owner; w0 <= behind; w0 += kParts) {
+                const int n = min(kParts, behind - w0 + 1);
+                lds_barrier();
+                for (int i = tid; i < n * rows; i += 64 * kFewWaves)
+                    get2(part_of(w0 + i / rows) + 2 * (i % rows), pair + 2 * i, pair + 2 * i + 1);
+                lds_barrier();
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) {
+                    const int i = tid + j * 64 * kFewWaves;
+                    if (i >= rows * (DP / 2)) continue;
+                    const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
+                    float to = M[j];
+                    for (int w = 0; w < n; ++w) to = fmaxf(to, pair[2 * (w * rows + r)]);
+                    const float b = exp2_fast(M[j] - to);
+                    M[j] = to;
+                    L[j] *= b;
+                    x[j] *= b;
+                    y[j] *= b;
+                    for (int w1 = 0; w1 < n; w1 += 8) {
+                        float x1[8], y1[8];
+#pragma unroll
+                        for (int w = 0; w < 8; ++w)
+                            get2(part_of(w0 + min(w1 + w, n - 1)) + 2 * kFewRows + r * DP + d, &x1[w], &y1[w]);
+#pragma unroll
+                        for (int w = 0; w < 8; ++w) {
+                            if (w1 + w >= n) break;
+                            const float b1 = exp2_fast(pair[2 * ((w1 + w) * rows + r)] - to);
+                            L[j] += pair[2 * ((w1 + w) * rows + r) + 1] * b1;
+                            x[j] += x1[w] * b1;
+                            y[j] += y1[w] * b1;
+                        }
+                    }
                 }
-                write(r, d, L, x, y);
+            }
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                const int i = tid + j * 64 * kFewWaves;
+                if (i < rows * (DP / 2)) write(i / (DP / 2), 2 * (i % (DP / 2)), L[j], x[j], y[j]);
             }
         }
     };

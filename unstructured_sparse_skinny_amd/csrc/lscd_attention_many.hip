@@ -120,12 +120,12 @@ template <typename T, bool E4M3, int DP>
 __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArgs a) {
     using F = Many<T, E4M3, DP>;
     __shared__ __attribute__((aligned(16))) unsigned char sh[2][2][F::kTile];
-    __shared__ uint32_t sh_last;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5;
     const int G = gridDim.x;
     // consecutive ranges on one XCD (workgroups go to the 8 XCDs in turn): they share keys in its L2
     const int me = (G & 7) == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+    if (tid == 0) a.record[me] = int4{0, 0, 0, 0};
     Work p;
     if (!find_work<kManyRows, F::kTokens, false>(a, lane, me, G, &p)) return;
     const Cut cut = p.cut;
@@ -335,45 +335,22 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
 
         const bool whole = p.unit == 0 && last == units;
         constexpr int64_t kFloats = (int64_t)kManyRows * (DP + 2);
-        bool write = whole;
         if (!whole) {
+            // A part: a pair (maximum, sum) per row, then each lane's values as it holds them.  The
+            // workgroup that has the item's first unit says what there is to join.
             const int owner = cut.owner(item), behind = cut.owner(item + units - 1);
             float* mine = a.part + (int64_t)(2 * me + (p.unit == 0 ? 1 : 0)) * kFloats;
-            // a pair (maximum, sum) per row, then each lane's values as it holds them
-            auto at = [&](int b, int i) { return 2 * kManyRows + (((wave * F::kBlocks + b) * 8 + i / 2) * 64 + lane_e) * 2; };
-            if (half_e == 0) put2(mine + 2 * (32 * wave + lane_e), m, l);
-#pragma unroll
-            for (int b = 0; b < F::kBlocks; ++b)
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) put2(mine + at(b, i), o[b][i], o[b][i + 1]);
-            write = arrive_last(a.count + owner, (uint32_t)(behind - owner + 1), &sh_last);
-            if (write) {
-                m = kNoScore;
-                l = 0.f;
+            if (tid == 0 && owner == me) a.record[me] = int4{behind - owner, p.seq, p.head, p.tile};
+            if (row0 < q.rows) {
+                if (half_e == 0) *(float2*)(mine + 2 * (32 * wave + lane_e)) = float2{m, l};
 #pragma unroll
                 for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
-                for (int w = owner; w <= behind; ++w) {
-                    const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
-                    float m1, l1;
-                    get2(part + 2 * (32 * wave + (lane_e & 31)), &m1, &l1);
-                    const float to = fmaxf(m, m1), b0 = exp2_fast(m - to), b1 = exp2_fast(m1 - to);
-                    m = to;
-                    l = l * b0 + l1 * b1;
-#pragma unroll
-                    for (int b = 0; b < F::kBlocks; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            float x, y;
-                            get2(part + at(b, i), &x, &y);
-                            o[b][i] = o[b][i] * b0 + x * b1;
-                            o[b][i + 1] = o[b][i + 1] * b0 + y * b1;
-                        }
-                }
+                    for (int i = 0; i < 16; i += 4)
+                        *(f32x4v*)(mine + 2 * kManyRows + (((wave * F::kBlocks + b) * 4 + i / 4) * 64 + lane_e) * 4) =
+                            f32x4v{o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
             }
-        }
-        if (write && live) {
+        } else if (live) {
             const float inv = l != 0.f ? 1.f / l : 0.f;
             uint16_t* op = (uint16_t*)a.o + (int64_t)(q.first + opaque(token)) * a.o_stride + (int64_t)opaque(qh) * D;
 #pragma unroll
@@ -394,18 +371,69 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
     }
 }
 
+// Joins the parts of the items that were cut: blockIdx.x is the workgroup that recorded one, blockIdx.y a
+// wavefront's rows and a block of 32 channels, one vector of four values per thread and part.  Parts are
+// 256 rows: joined by an item's last workgroup inside the kernel above, they came one after the other
+// (64 new tokens of 32 heads over 8192 positions: 268 us that way).
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+    constexpr int kBlocks = DP / 32;
+    constexpr int64_t kFloats = (int64_t)kManyRows * (DP + 2);
+    const int4 rec = a.record[blockIdx.x];
+    if (rec.x == 0) return;
+    const int wave = blockIdx.y / kBlocks, b = blockIdx.y % kBlocks, lane = threadIdx.x & 63, i = threadIdx.x >> 6;
+    const Seq q = read_seq(a, rec.y);
+    const int in_tile = 32 * wave + (lane & 31), row = rec.w * kManyRows + in_tile;
+    if (row >= q.rows) return;
+    const int owner = blockIdx.x, behind = owner + rec.x;
+    float m = kNoScore, l = 0.f;
+    f32x4v o = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kBatch = 4;  // parts in flight
+    for (int w0 = owner; w0 <= behind; w0 += kBatch) {
+        float2 ml[kBatch];
+        f32x4v x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int w = min(w0 + j, behind);
+            const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
+            ml[j] = *(const float2*)(part + 2 * in_tile);
+            x[j] = *(const f32x4v*)(part + 2 * kManyRows + ((blockIdx.y * 4 + i) * 64 + lane) * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (w0 + j > behind) break;
+            const float to = fmaxf(m, ml[j].x), b0 = exp2_fast(m - to), b1 = exp2_fast(ml[j].x - to);
+            m = to;
+            l = l * b0 + ml[j].y * b1;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[r] = o[r] * b0 + x[j][r] * b1;
+        }
+    }
+    const int d = 32 * b + 8 * i + 4 * (lane >> 5);
+    if (d >= a.c.head_dim) return;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    u32x2v out = {T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv)};
+    if (l == 0.f) out = u32x2v{0u, 0u};
+    *(u32x2v*)((uint16_t*)a.o + (int64_t)(q.first + row / a.share) * a.o_stride +
+               (int64_t)(rec.z * a.share + row % a.share) * a.c.head_dim + d) = out;
+}
+
+template <typename T, bool E4M3, int DP>
+hipError_t many_run(const AttnArgs& a, int grid, hipStream_t s) {
+    attention_many_kernel<T, E4M3, DP><<<grid, kManyThreads, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    attention_join_kernel<T, DP><<<dim3(grid, kManyWaves * DP / 32), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <typename T, bool E4M3>
 hipError_t many_dim(const AttnArgs& a, int grid, hipStream_t s) {
     const int D = a.c.head_dim;
-    if (D <= 64)
-        attention_many_kernel<T, E4M3, 64><<<grid, kManyThreads, 0, s>>>(a);
-    else if (D <= 96)
-        attention_many_kernel<T, E4M3, 96><<<grid, kManyThreads, 0, s>>>(a);
-    else if (D <= 128)
-        attention_many_kernel<T, E4M3, 128><<<grid, kManyThreads, 0, s>>>(a);
-    else
-        attention_many_kernel<T, E4M3, 256><<<grid, kManyThreads, 0, s>>>(a);
-    return hipGetLastError();
+    if (D <= 64) return many_run<T, E4M3, 64>(a, grid, s);
+    if (D <= 96) return many_run<T, E4M3, 96>(a, grid, s);
+    if (D <= 128) return many_run<T, E4M3, 128>(a, grid, s);
+    return many_run<T, E4M3, 256>(a, grid, s);
 }
 
 }  // namespace

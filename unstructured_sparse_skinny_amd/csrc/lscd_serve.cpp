@@ -52,6 +52,7 @@ void free_attention(lscd_attention_s* h) {
     if (!h) return;
     if (h->part) (void)hipFree(h->part);
     if (h->count) (void)hipFree(h->count);
+    if (h->record) (void)hipFree(h->record);
     delete h;
 }
 
@@ -239,12 +240,13 @@ lscd_status_t lscd_attention_create(int32_t q_heads, int32_t kv_heads, int32_t h
         return LSCD_ERROR_HIP;
     }
     h->cus = cus;
-    const int few = lscd::attention_few_grid(cus), many = lscd::attention_many_grid(cus), most = std::max(few, many);
+    const int few = lscd::attention_few_grid(cus), many = lscd::attention_many_grid(cus);
     const int64_t floats = std::max(2 * few * lscd::attention_few_floats(head_dim),
                                     2 * many * lscd::attention_many_floats(head_dim));
     if ((e = hipMalloc((void**)&h->part, (size_t)floats * 4)) != hipSuccess ||
-        (e = hipMalloc((void**)&h->count, (size_t)most * 4)) != hipSuccess ||
-        (e = hipMemset(h->count, 0, (size_t)most * 4)) != hipSuccess || (e = hipDeviceSynchronize()) != hipSuccess) {
+        (e = hipMalloc((void**)&h->count, (size_t)few * 4)) != hipSuccess ||
+        (e = hipMalloc((void**)&h->record, (size_t)many * sizeof(int4))) != hipSuccess ||
+        (e = hipMemset(h->count, 0, (size_t)few * 4)) != hipSuccess || (e = hipDeviceSynchronize()) != hipSuccess) {
         free_attention(h);
         return status_of(e);
     }
@@ -300,27 +302,31 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
     a.page_log2 = __builtin_ctz((unsigned)cache->page_size);
     a.part = h->part;
     a.count = h->count;
+    a.record = h->record;
     // Sequences of up to 16 query rows are the few-row kernel's, longer ones the other's.  Where no
     // sequence can be longer (or each has one new token, as far as the counts tell), the few-row
     // kernel takes all of them, whatever the device arrays hold.
     const bool both = T * share > lscd::kFewRows && T > sequences;
     a.few_limit = both ? lscd::kFewRows : 0x7FFFFFFF;
-    auto grid = [&](int most, int rows, int tokens) {
-        const int64_t tiles = T * share / rows + sequences;
-        const int64_t units = (span + tokens - 1) / tokens * h->kv_heads;
-        return (int)std::min<int64_t>(most, tiles > most ? most : tiles * std::min<int64_t>(units, most));
+    // Workgroups: no more per item than pay.  An item of U units over W workgroups takes U / W units and
+    // then, in its last one, W parts to join: best at W = sqrt(U * unit / part), with a unit's time over a
+    // part's about 20 for few rows (one query row over 32768 positions: 64 workgroups) and 4 for many,
+    // whose parts are 256 rows.
+    auto grid = [&](int most, int rows, int tokens, double ratio) {
+        const double items = ((double)(T * share) / rows + sequences) * h->kv_heads, units = ceil((double)span / tokens);
+        return (int)std::min<double>(most, items * std::min(units, 1.0 + ceil(sqrt(ratio * units))));
     };
     // (slots of work are counted in 32 bits on the device)
     if ((double)(T * share / lscd::kFewRows + sequences) * ((double)span / 32 + 2) * h->kv_heads >= 2147483648.0)
         return LSCD_ERROR_NOT_SUPPORTED;
     if (sequences > 1 || !both) {
         hipError_t e = lscd::launch_attention_few(
-            a, type, grid(lscd::attention_few_grid(h->cus), lscd::kFewRows, lscd::kFewTokens), (hipStream_t)stream);
+            a, type, grid(lscd::attention_few_grid(h->cus), lscd::kFewRows, lscd::kFewTokens, 20.0), (hipStream_t)stream);
         if (e != hipSuccess) return status_of(e);
     }
     if (both) {
         hipError_t e = lscd::launch_attention_many(
-            a, type, grid(lscd::attention_many_grid(h->cus), lscd::kManyRows, lscd::kManyTokens), (hipStream_t)stream);
+            a, type, grid(lscd::attention_many_grid(h->cus), lscd::kManyRows, lscd::kManyTokens, 4.0), (hipStream_t)stream);
         if (e != hipSuccess) return status_of(e);
     }
     return LSCD_SUCCESS;

@@ -44,7 +44,8 @@ struct AttnArgs {
     int32_t few_limit;       // sequences of at most this many query rows belong to the few-row kernel
     int32_t page_log2;
     float* part;             // partial results: two slots per workgroup
-    uint32_t* count;         // arrivals, one per workgroup; zero between calls
+    uint32_t* count;         // arrivals, one per workgroup; zero between calls (few rows)
+    int4* record;            // cut items, one per workgroup: parts - 1, sequence, key head, row tile (many rows)
 };
 // Workgroups of one launch at most, and floats of one partial result.
 int attention_few_grid(int cus);
@@ -134,4 +135,5 @@ struct lscd_attention_s {
     int32_t q_heads = 0, kv_heads = 0, head_dim = 0;
     float* part = nullptr;
     uint32_t* count = nullptr;
+    int4* record = nullptr;
 };
