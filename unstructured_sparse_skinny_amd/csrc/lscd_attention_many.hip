@@ -23,8 +23,8 @@ typedef __attribute__((address_space(3))) s16x4v lds_s16x4;
 // Instructions that may cross the scheduling barriers below: vector and scalar arithmetic.
 constexpr int kSchedFree = 0x6;
 
-// Tokens of a tile: fewer for heads of more than 128 channels, whose registers would not hold more.
-constexpr int many_tokens(int dp) { return dp <= 128 ? kManyTokens : kManyTokens / 2; }
+// Tokens of a tile: as many as the registers hold, so that a tile's products cover the next one's loads.
+constexpr int many_tokens(int dp) { return dp <= 64 ? 2 * kManyTokens : (dp <= 128 ? kManyTokens : kManyTokens / 2); }
 
 template <typename T, bool E4M3, int DP>
 struct Many {
@@ -371,51 +371,67 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
     }
 }
 
-// Joins the parts of the items that were cut: blockIdx.x is the workgroup that recorded one, blockIdx.y a
-// wavefront's rows and a block of 32 channels, one vector of four values per thread and part.  Parts are
-// 256 rows: joined by an item's last workgroup inside the kernel above, they came one after the other
-// (64 new tokens of 32 heads over 8192 positions: 268 us that way).
+// Joins the parts of the items that were cut (records of G workgroups).  The work, cut items times
+// wavefronts' rows times blocks of 32 channels, is spread over the grid: one vector of four values per
+// thread and part.  Parts are 256 rows: joined by an item's last workgroup inside the kernel above, they
+// came one after the other (64 new tokens of 32 heads over 8192 positions: 268 us that way).
+constexpr int kJoinGrid = 2048, kJoinMasks = 32;
 template <typename T, int DP>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
-    constexpr int kBlocks = DP / 32;
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int G) {
+    constexpr int kBlocks = DP / 32, kSlabs = kManyWaves * kBlocks;
     constexpr int64_t kFloats = (int64_t)kManyRows * (DP + 2);
-    const int4 rec = a.record[blockIdx.x];
-    if (rec.x == 0) return;
-    const int wave = blockIdx.y / kBlocks, b = blockIdx.y % kBlocks, lane = threadIdx.x & 63, i = threadIdx.x >> 6;
-    const Seq q = read_seq(a, rec.y);
-    const int in_tile = 32 * wave + (lane & 31), row = rec.w * kManyRows + in_tile;
-    if (row >= q.rows) return;
-    const int owner = blockIdx.x, behind = owner + rec.x;
-    float m = kNoScore, l = 0.f;
-    f32x4v o = {0.f, 0.f, 0.f, 0.f};
-    constexpr int kBatch = 4;  // parts in flight
-    for (int w0 = owner; w0 <= behind; w0 += kBatch) {
-        float2 ml[kBatch];
-        f32x4v x[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            const int w = min(w0 + j, behind);
-            const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
-            ml[j] = *(const float2*)(part + 2 * in_tile);
-            x[j] = *(const f32x4v*)(part + 2 * kManyRows + ((blockIdx.y * 4 + i) * 64 + lane) * 4);
-        }
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-            if (w0 + j > behind) break;
-            const float to = fmaxf(m, ml[j].x), b0 = exp2_fast(m - to), b1 = exp2_fast(ml[j].x - to);
-            m = to;
-            l = l * b0 + ml[j].y * b1;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) o[r] = o[r] * b0 + x[j][r] * b1;
-        }
+    __shared__ uint64_t sh_mask[kJoinMasks];
+    const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
+    for (int g = i; g * 64 < G; g += 4) {
+        const uint64_t mask = __ballot(g * 64 + lane < G && a.record[min(g * 64 + lane, G - 1)].x != 0);
+        if (lane == 0) sh_mask[g] = mask;
     }
-    const int d = 32 * b + 8 * i + 4 * (lane >> 5);
-    if (d >= a.c.head_dim) return;
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    u32x2v out = {T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv)};
-    if (l == 0.f) out = u32x2v{0u, 0u};
-    *(u32x2v*)((uint16_t*)a.o + (int64_t)(q.first + row / a.share) * a.o_stride +
-               (int64_t)(rec.z * a.share + row % a.share) * a.c.head_dim + d) = out;
+    __syncthreads();
+    int items = 0;
+    for (int g = 0; g * 64 < G; ++g) items += __popcll(sh_mask[g]);
+    for (int work = blockIdx.x; work < items * kSlabs; work += gridDim.x) {
+        const int slab = work % kSlabs, wave = slab / kBlocks, b = slab % kBlocks;
+        int n = work / kSlabs, g = 0;  // the n-th record that is set
+        for (; n >= __popcll(sh_mask[g]); ++g) n -= __popcll(sh_mask[g]);
+        uint64_t mask = sh_mask[g];
+        for (; n > 0; --n) mask &= mask - 1;
+        const int owner = __builtin_amdgcn_readfirstlane(g * 64 + __builtin_ctzll(mask));
+        const int4 rec = a.record[owner];
+        const Seq q = read_seq(a, __builtin_amdgcn_readfirstlane(rec.y));
+        const int in_tile = 32 * wave + (lane & 31), row = rec.w * kManyRows + in_tile, behind = owner + rec.x;
+        if (row >= q.rows) continue;
+        float m = kNoScore, l = 0.f;
+        f32x4v o = {0.f, 0.f, 0.f, 0.f};
+        constexpr int kBatch = 8;  // parts in flight
+        for (int w0 = owner; w0 <= behind; w0 += kBatch) {
+            float2 ml[kBatch];
+            f32x4v x[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (j >= 2 && w0 + j > behind) continue;
+                const int w = min(w0 + j, behind);
+                const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
+                ml[j] = *(const float2*)(part + 2 * in_tile);
+                x[j] = *(const f32x4v*)(part + 2 * kManyRows + ((slab * 4 + i) * 64 + lane) * 4);
+            }
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                if (w0 + j > behind) continue;
+                const float to = fmaxf(m, ml[j].x), b0 = exp2_fast(m - to), b1 = exp2_fast(ml[j].x - to);
+                m = to;
+                l = l * b0 + ml[j].y * b1;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) o[r] = o[r] * b0 + x[j][r] * b1;
+            }
+        }
+        const int d = 32 * b + 8 * i + 4 * (lane >> 5);
+        if (d >= a.c.head_dim) continue;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        u32x2v out = {T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv)};
+        if (l == 0.f) out = u32x2v{0u, 0u};
+        *(u32x2v*)((uint16_t*)a.o + (int64_t)(q.first + row / a.share) * a.o_stride +
+                   (int64_t)(rec.z * a.share + row % a.share) * a.c.head_dim + d) = out;
+    }
 }
 
 template <typename T, bool E4M3, int DP>
@@ -423,7 +439,7 @@ hipError_t many_run(const AttnArgs& a, int grid, hipStream_t s) {
     attention_many_kernel<T, E4M3, DP><<<grid, kManyThreads, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attention_join_kernel<T, DP><<<dim3(grid, kManyWaves * DP / 32), 256, 0, s>>>(a);
+    attention_join_kernel<T, DP><<<kJoinGrid, 256, 0, s>>>(a, grid);
     return hipGetLastError();
 }
 
@@ -438,7 +454,7 @@ hipError_t many_dim(const AttnArgs& a, int grid, hipStream_t s) {
 
 }  // namespace
 
-int attention_many_grid(int cus) { return cus; }
+int attention_many_grid(int cus) { return cus < 64 * kJoinMasks ? cus : 64 * kJoinMasks; }
 int64_t attention_many_floats(int dim) {
     return (int64_t)kManyRows * ((dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : 256) + 2);
 }
