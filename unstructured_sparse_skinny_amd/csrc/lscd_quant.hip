@@ -95,23 +95,35 @@ hipError_t launch_quant_decode(const QuantArgs& a, int type, int kind, uint16_t*
     return type == LSCD_F16 ? decode_kind<F16>(a, kind, w, s) : decode_kind<BF16>(a, kind, w, s);
 }
 
-// The busiest CU's work: its workgroups times (row tiles x units of each, and a fixed part for a
-// workgroup's start, its join and its results); splits along K add partial sums.
+// Row tiles per wavefront and splits along K: the least time by a model of this GPU, in microseconds.
+// A CU moves about 20 KB of codes a microsecond; x costs up to 16 tokens half of what its 256 bytes a
+// token and unit of a wavefront would from HBM.  A workgroup takes about 3 us to start and join, plus one
+// memory latency for each turn of its loads.  More than 16 tokens: a workgroup's round (two units of 4 RT
+// row tiles) measured 0.35 + 0.58 RT (64 tokens) and 0.3 + 0.45 RT (32).  A split adds a launch and its
+// partial sums.  It picks 7 row tiles for 28672 x 7168 (1792 tiles, 7 on every CU), 1 for 5003 x 4099.
 QuantPlan plan_quant(int tiles, int units, int N, int cus) {
     QuantPlan best = {N > 16, 1, 1};
     double cost = 0;
     static const int few[] = {1, 2, 3, 4, 6, 7}, many[] = {1, 2, 3, 4};
     const int* rts = best.shared ? many : few;
-    const int n = N > 32 ? 3 : (best.shared ? 4 : 6),  // (four row tiles of 64 tokens do not fit the registers)
-              wr = best.shared ? 4 : 1, wk = kQuantWaves / wr;
+    const int n = N > 32 ? 3 : (best.shared ? 4 : 6);  // (four row tiles of 64 tokens do not fit the registers)
+    const int wr = best.shared ? 4 : 1, wk = kQuantWaves / wr;
     for (int i = 0; i < n; ++i) {
-        const int64_t groups = (tiles + (int64_t)rts[i] * wr - 1) / (rts[i] * wr);
+        const int rt = rts[i];
+        const int64_t groups = (tiles + (int64_t)rt * wr - 1) / (rt * wr);
         for (int s = 1; s <= 16 && (s == 1 || s * wk <= units); ++s) {
-            const double each = (double)rts[i] * ((units + s * wk - 1) / (s * wk)) + (best.shared ? 8.0 : 4.0);
-            const double c = (double)((groups * s + cus - 1) / cus) * each * (1.0 + (s > 1 ? 0.06 + 0.01 * s : 0.0));
-            if ((i == 0 && s == 1) || c < cost) {
-                cost = c;
-                best.rt = rts[i];
+            const double rounds = (double)((groups * s + cus - 1) / cus), per_wave = (double)((units + s * wk - 1) / (s * wk));
+            double t;
+            if (best.shared) {
+                t = 3.0 + rounds * per_wave * (N > 32 ? 0.35 + 0.58 * rt : 0.3 + 0.45 * rt);
+            } else {
+                const int ahead = rt <= 2 ? 4 : (rt == 3 ? 3 : 2);
+                t = std::max(rounds * per_wave * wk * (rt + N / 8.0) * 0.05, 3.0 + per_wave / ahead);
+            }
+            if (s > 1) t += 4.0 + (double)s * N * tiles * 16 * 8 / 5e6;
+            if ((i == 0 && s == 1) || t < cost) {
+                cost = t;
+                best.rt = rt;
                 best.splits = s;
             }
         }
