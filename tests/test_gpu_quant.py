@@ -97,6 +97,20 @@ def test_whole_numbers_are_exact(kind, N):
     assert torch.equal(y.cpu(), want)
 
 
+@pytest.mark.parametrize("M,K", [(1689, 1645), (3974, 8557)])
+def test_every_number_of_tokens(M, K):
+    """Each number of tokens has its own plan, and fewer tokens may split K into more ranges: the partial
+    sums' room has to hold every plan's (whole numbers: the results are exact, as above)."""
+    say("quant every number of tokens", M, K)
+    h, c, s, z = matrix(M, K, 128, True, "f16", M, whole=True)
+    x = torch.from_numpy(np.random.default_rng(K).integers(-2, 3, (64, K)).astype(np.float64)).half().cuda()
+    want = torch.from_numpy(x.cpu().double().numpy() @ (c * s).T).half()
+    for N in range(1, 65):
+        y = torch.full((N, M), float("nan"), dtype=torch.float16, device="cuda")
+        L.lscd_quant_linear(h, x[:N], y)
+        assert torch.equal(y.cpu(), want[:N]), N
+
+
 @pytest.mark.parametrize("kind", ["f16", "bf16"])
 @pytest.mark.parametrize("group", [32, 64, 128, 384])
 def test_decode(kind, group):

@@ -120,7 +120,8 @@ lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void
         return LSCD_ERROR_NOT_SUPPORTED;
     }
     h->kind = lscd::quant_kind(h->per_unit, zeros != nullptr);
-    for (int n : {16, 32, 64}) {
+    // (every number of tokens has its own plan: fewer may split K further and need more room)
+    for (int n = 1; n <= lscd::kQuantMaxTokens; ++n) {
         const lscd::QuantPlan p = lscd::plan_quant(h->tiles, h->units, n, cus);
         if (p.splits > 1) h->part_floats = std::max(h->part_floats, (int64_t)p.splits * M * n);
     }
