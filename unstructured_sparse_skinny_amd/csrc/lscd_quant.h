@@ -39,7 +39,7 @@ __device__ __forceinline__ uint32_t take_off(uint32_t w, uint32_t less) {
 // -(16 + z) twice: 0xCC00 | z << 6 in float16.
 __device__ __forceinline__ uint32_t less_of(uint32_t z) { return (0xCC00u | z << 6) * 0x00010001u; }
 
-// 8 values of x from column k on: all of them, whatever the alignment; or up to column K, then zeros.
+// 8 values of x, whatever the alignment.
 __device__ __forceinline__ u32x4v load_x(const uint16_t* x) {
     struct __attribute__((packed, aligned(2))) Loose {
         uint32_t w[4];
@@ -47,11 +47,12 @@ __device__ __forceinline__ u32x4v load_x(const uint16_t* x) {
     const Loose v = *(const Loose*)x;
     return u32x4v{v.w[0], v.w[1], v.w[2], v.w[3]};
 }
+// Columns k to k + 7 of a row of fewer than 8: zeros behind its end.
 __device__ __forceinline__ u32x4v load_x_end(const uint16_t* x, int k, int K) {
     u32x4v r = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (k + i < K) r[i / 2] |= (uint32_t)x[i] << (16 * (i & 1));
+        if (k + i < K) r[i / 2] |= (uint32_t)x[k + i] << (16 * (i & 1));
     return r;
 }
 // The same from the row's last 8 values `v`, loaded at column K - 8 where k > K - 8: s = k - (K - 8)

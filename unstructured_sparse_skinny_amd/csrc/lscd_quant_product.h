@@ -43,16 +43,17 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
     const auto cb = tile_buffer(a.codes, rt0, have, (int64_t)a.units * 1024);
     const auto ab = tile_buffer(a.aux, rt0, have, (int64_t)a.units * kQuantRows * A::kBytes);
     const int token = min(lane & 15, a.N - 1);
-    const uint16_t* xp = a.x + token * a.ldx + 8 * g;
-    const int full = min(u1, a.K / kQuantUnit);  // the last unit of a row may not be full
+    const uint16_t* xp = a.x + token * a.ldx;
+    const int whole = a.K / kQuantUnit;  // the last unit of a row may not be full
+    const int last = a.K - 8;            // a row's last 8 values stand in for what reaches past its end
 
     f32x4v acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r] = f32x4v{0.f, 0.f, 0.f, 0.f};
     u32x4v c[kAhead][RT], x[kAhead][4];
     A aux[kAhead][RT];
-    auto load = [&](int i, int u, int end) {
-        const bool on = u < end;
+    auto load = [&](int i, int u) {
+        const bool on = u < u1;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const bool here = on && r < have;  // (the scalar offset is not part of the bounds check)
@@ -62,11 +63,14 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
         }
     };
     auto load_tokens = [&](int i, int u) {
-        const uint16_t* p = xp + (int64_t)min(u, full - 1) * kQuantUnit;
+        const int k = min(u, u1 - 1) * kQuantUnit + 8 * g;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) x[i][s] = load_x(p + 32 * s);
+        for (int s = 0; s < 4; ++s) x[i][s] = load_x(xp + min(k + 32 * s, last));
     };
-    auto compute = [&](int i) {
+    auto compute = [&](int i, int u) {
+        if (u == whole)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) x[i][s] = shift_end(x[i][s], u * kQuantUnit + 32 * s + 8 * g - last);
         const f32x4v none = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < A::kPer; ++p) {
@@ -93,29 +97,29 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
             }
         }
     };
-    if (u0 < full) {
+    if (a.K < 8) {  // (one unit of one wavefront)
+        if (u0 < u1) {
+            load(0, 0);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) x[0][s] = load_x_end(xp, 32 * s + 8 * g, a.K);
+            compute(0, whole + 1);
+        }
+    } else if (u0 < u1) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            load(i, u0 + i, full);
+            load(i, u0 + i);
             load_tokens(i, u0 + i);
             __builtin_amdgcn_sched_barrier(0);
         }
-        for (int u = u0; u < full; u += kAhead) {
+        for (int u = u0; u < u1; u += kAhead) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                if (u + i < full) compute(i);  // (no loads under the branch: the waits count them)
-                load(i, u + i + kAhead, full);
+                if (u + i < u1) compute(i, u + i);  // (no loads under the branch: the waits count them)
+                load(i, u + i + kAhead);
                 load_tokens(i, u + i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-    }
-    if (u0 < u1 && full < u1) {
-        load(0, full, u1);
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-            x[0][s] = load_x_end(xp + (int64_t)full * kQuantUnit + 32 * s, full * kQuantUnit + 32 * s + 8 * g, a.K);
-        compute(0);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
