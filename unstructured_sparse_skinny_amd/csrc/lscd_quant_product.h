@@ -30,7 +30,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const void* p, int
 // per tile and unit) with x straight from the caches, kAhead units in flight, and needs no barrier
 // until the sums are joined through LDS.  x costs 4 KB per unit of a wavefront for 16 tokens (less for
 // fewer: lanes past N repeat a token, the same lines), against RT KB of codes.
-template <typename T, int KIND, int RT>
+template <typename T, int KIND, int RT, typename X>
 __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a) {
     using A = Aux<T, KIND>;
     constexpr int kAhead = RT <= 2 ? 4 : (RT == 3 ? 3 : 2);
@@ -42,7 +42,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
     const int have = min(RT, a.tiles - rt0);
     const auto cb = tile_buffer(a.codes, rt0, have, (int64_t)a.units * 1024);
     const auto ab = tile_buffer(a.aux, rt0, have, (int64_t)a.units * kQuantRows * A::kBytes);
-    const int token = min(lane & 15, a.N - 1);
+    const int token = (lane & 15) < a.N ? lane & 15 : a.spare;
     const uint16_t* xp = a.x + token * a.ldx;
     const int whole = a.K / kQuantUnit;  // the last unit of a row may not be full
     const int last = a.K - 8;            // a row's last 8 values stand in for what reaches past its end
@@ -50,7 +50,8 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
     f32x4v acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r] = f32x4v{0.f, 0.f, 0.f, 0.f};
-    u32x4v c[kAhead][RT], x[kAhead][4];
+    u32x4v c[kAhead][RT];
+    X loaded[kAhead][4];
     A aux[kAhead][RT];
     auto load = [&](int i, int u) {
         const bool on = u < u1;
@@ -65,12 +66,17 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
     auto load_tokens = [&](int i, int u) {
         const int k = min(u, u1 - 1) * kQuantUnit + 8 * g;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) x[i][s] = load_x(xp + min(k + 32 * s, last));
+        for (int s = 0; s < 4; ++s) loaded[i][s].load(xp + min(k + 32 * s, last));
     };
-    auto compute = [&](int i, int u) {
+    auto tokens = [&](int i, int u, u32x4v* x) {
+        const int k = u * kQuantUnit + 8 * g;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) x[s] = loaded[i][s].values(xp + min(k + 32 * s, last));
         if (u == whole)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) x[i][s] = shift_end(x[i][s], u * kQuantUnit + 32 * s + 8 * g - last);
+            for (int s = 0; s < 4; ++s) x[s] = shift_end(x[s], k + 32 * s - last);
+    };
+    auto compute = [&](int i, const u32x4v* x) {
         const f32x4v none = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < A::kPer; ++p) {
@@ -78,7 +84,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
             f32x4v sx = none;
             if (T::bf)
 #pragma unroll
-                for (int s = kSteps * p; s < kSteps * (p + 1); ++s) sx = T::mfma16(x[i][s], ones_of<T>(), sx);
+                for (int s = kSteps * p; s < kSteps * (p + 1); ++s) sx = T::mfma16(x[s], ones_of<T>(), sx);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 const uint32_t z = aux[i][r].zero(p), less = less_of(z);
@@ -89,7 +95,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
                     if (!T::bf)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) w[j] = take_off(w[j], less);
-                    d = T::mfma16(x[i][s], w, d);
+                    d = T::mfma16(x[s], w, d);
                 }
                 const float scale = aux[i][r].scale(p), off = 16.f + (float)z;
 #pragma unroll
@@ -100,9 +106,10 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
     if (a.K < 8) {  // (one unit of one wavefront)
         if (u0 < u1) {
             load(0, 0);
+            u32x4v x[4];
 #pragma unroll
-            for (int s = 0; s < 4; ++s) x[0][s] = load_x_end(xp, 32 * s + 8 * g, a.K);
-            compute(0, whole + 1);
+            for (int s = 0; s < 4; ++s) x[s] = load_x_end(xp, 32 * s + 8 * g, a.K);
+            compute(0, x);
         }
     } else if (u0 < u1) {
 #pragma unroll
@@ -114,7 +121,11 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
         for (int u = u0; u < u1; u += kAhead) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                if (u + i < u1) compute(i, u + i);  // (no loads under the branch: the waits count them)
+                if (u + i < u1) {  // (no loads under the branch: the waits count them)
+                    u32x4v x[4];
+                    tokens(i, u + i, x);
+                    compute(i, x);
+                }
                 load(i, u + i + kAhead);
                 load_tokens(i, u + i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
@@ -318,19 +329,27 @@ void run_many(const QuantArgs& a, int rt, hipStream_t s) {
     else if (rt == 3) quant_many_kernel<T, KIND, NT, 3><<<grid, kQuantThreads, 0, s>>>(a);
     else if constexpr (NT < 4) quant_many_kernel<T, KIND, NT, 4><<<grid, kQuantThreads, 0, s>>>(a);
 }
-template <typename T, int KIND>
+template <typename T, int KIND, typename X>
 void run_few(const QuantArgs& a, int rt, hipStream_t s) {
     const dim3 grid((unsigned)((a.tiles + rt - 1) / rt), (unsigned)a.splits);
-    if (rt == 1) quant_few_kernel<T, KIND, 1><<<grid, kQuantThreads, 0, s>>>(a);
-    else if (rt == 2) quant_few_kernel<T, KIND, 2><<<grid, kQuantThreads, 0, s>>>(a);
-    else if (rt == 3) quant_few_kernel<T, KIND, 3><<<grid, kQuantThreads, 0, s>>>(a);
-    else if (rt == 4) quant_few_kernel<T, KIND, 4><<<grid, kQuantThreads, 0, s>>>(a);
-    else if (rt == 6) quant_few_kernel<T, KIND, 6><<<grid, kQuantThreads, 0, s>>>(a);
-    else quant_few_kernel<T, KIND, 7><<<grid, kQuantThreads, 0, s>>>(a);
+    if (rt == 1) quant_few_kernel<T, KIND, 1, X><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 2) quant_few_kernel<T, KIND, 2, X><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 3) quant_few_kernel<T, KIND, 3, X><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 4) quant_few_kernel<T, KIND, 4, X><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 6) quant_few_kernel<T, KIND, 6, X><<<grid, kQuantThreads, 0, s>>>(a);
+    else quant_few_kernel<T, KIND, 7, X><<<grid, kQuantThreads, 0, s>>>(a);
 }
 template <typename T, int KIND>
-void run_kind(const QuantArgs& a, const QuantPlan& p, hipStream_t s) {
-    if (!p.shared) run_few<T, KIND>(a, p.rt, s);
+void run_kind(QuantArgs a, const QuantPlan& p, hipStream_t s) {
+    // Lanes whose rows begin at odd multiples of 2 bytes, lanes without a token repeating a row that does not.
+    // 5003x4099 (plain loads against OddX): 11.1 against 12.4 us with 2 such lanes, 13.8 against 12.6
+    // with 3; 12288x4097: 13.6 against 12.7 with 2, 16.4 against 13.0 with 3, 31.7 against 17.6 with 8.
+    const bool first = (uintptr_t)a.x % 4, change = a.N > 1 && a.ldx % 2;
+    a.spare = first && change;
+    const int lanes = change ? (a.N + first) / 2 : 16 * first;
+    const bool odd = lanes > 2;
+    if (!p.shared && odd) run_few<T, KIND, OddX>(a, p.rt, s);
+    else if (!p.shared) run_few<T, KIND, EvenX>(a, p.rt, s);
     else if (a.N <= 32) run_many<T, KIND, 2>(a, p.rt, s);
     else run_many<T, KIND, 4>(a, p.rt, s);
 }

@@ -61,7 +61,6 @@ void free_quant(lscd_quant_s* h) {
     if (h->codes) (void)hipFree(h->codes);
     if (h->aux) (void)hipFree(h->aux);
     if (h->part) (void)hipFree(h->part);
-    if (h->count) (void)hipFree(h->count);
     delete h;
 }
 
@@ -76,7 +75,6 @@ lscd::QuantArgs quant_args(const lscd_quant_s* h) {
     a.codes = h->codes;
     a.aux = h->aux;
     a.part = h->part;
-    a.count = h->count;
     a.M = (int32_t)h->M;
     a.K = (int32_t)h->K;
     a.tiles = h->tiles;

@@ -88,10 +88,10 @@ struct QuantArgs {
     const uint16_t* x;
     uint16_t* y;
     float* part;
-    uint32_t* count;
     int64_t ldx, ldy;
     int32_t M, K, N;
     int32_t tiles, units, splits;
+    int32_t spare;           // the row that lanes without a token read
 };
 struct QuantEncodeArgs {
     const uint8_t* q;        // [M][row_bytes]
@@ -125,7 +125,6 @@ struct lscd_quant_s {
     void* aux = nullptr;
     int kind = 0;
     float* part = nullptr;
-    uint32_t* count = nullptr;
     int64_t part_floats = 0;
 };
 
