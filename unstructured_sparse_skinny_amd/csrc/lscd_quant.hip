@@ -1,6 +1,7 @@
 // Matrices of 4-bit codes: encoding into the device layout, decoding, and how a product is split.
 
 #include <algorithm>
+#include <cmath>
 
 #include "lscd_quant.h"
 
@@ -101,12 +102,12 @@ hipError_t launch_quant_decode(const QuantArgs& a, int type, int kind, uint16_t*
 // memory latency for each turn of its loads.  More than 16 tokens: a workgroup's round (two units of 4 RT
 // row tiles) measured 0.35 + 0.58 RT (64 tokens) and 0.3 + 0.45 RT (32).  A split adds a launch and its
 // partial sums.  It picks 7 row tiles for 28672 x 7168 (1792 tiles, 7 on every CU), 1 for 5003 x 4099.
-QuantPlan plan_quant(int tiles, int units, int N, int cus) {
+QuantPlan plan_quant(int tiles, int units, int N, int kind, int cus) {
     QuantPlan best = {N > 16, 1, 1};
     double cost = 0;
     static const int few[] = {1, 2, 3, 4, 6, 7}, many[] = {1, 2, 3, 4};
     const int* rts = best.shared ? many : few;
-    const int n = N > 32 ? 3 : (best.shared ? 4 : 6);  // (four row tiles of 64 tokens do not fit the registers)
+    const int n = N > 32 ? 3 : (best.shared || kind == 4 ? 4 : 6);  // (four row tiles of 64 tokens do not fit the registers)
     const int wr = best.shared ? 4 : 1, wk = kQuantWaves / wr;
     for (int i = 0; i < n; ++i) {
         const int rt = rts[i];
@@ -117,8 +118,9 @@ QuantPlan plan_quant(int tiles, int units, int N, int cus) {
             if (best.shared) {
                 t = 3.0 + rounds * per_wave * (N > 32 ? 0.35 + 0.58 * rt : 0.3 + 0.45 * rt);
             } else {
-                const int ahead = rt <= 2 ? 4 : (rt == 3 ? 3 : 2);
-                t = std::max(rounds * per_wave * wk * (rt + N / 8.0) * 0.05, 3.0 + per_wave / ahead);
+                const int ahead = quant_ahead(rt, kind);
+                const double turns = std::ceil(per_wave / ahead);  // (x is loaded for all of a turn's units)
+                t = std::max(rounds * wk * (per_wave * rt + turns * ahead * N / 8.0) * 0.05, 3.0 + per_wave / ahead);
             }
             if (s > 1) t += 4.0 + (double)s * N * tiles * 16 * 8 / 5e6;
             if ((i == 0 && s == 1) || t < cost) {

@@ -33,7 +33,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const void* p, int
 template <typename T, int KIND, int RT, typename X>
 __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a) {
     using A = Aux<T, KIND>;
-    constexpr int kAhead = RT <= 2 ? 4 : (RT == 3 ? 3 : 2);
+    constexpr int kAhead = quant_ahead(RT, KIND);
     const Unpack<T> unpack;
     __shared__ float sh[kQuantWaves][16][RT * 16 + 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane >> 4;
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
 #pragma unroll
             for (int s = 0; s < 4; ++s) x[s] = shift_end(x[s], k + 32 * s - last);
     };
-    auto compute = [&](int i, const u32x4v* x) {
+    auto multiply = [&](int i, const u32x4v* x) {
         const f32x4v none = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < A::kPer; ++p) {
@@ -103,13 +103,18 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
             }
         }
     };
+    auto compute = [&](int i, int u) {
+        u32x4v x[4];
+        tokens(i, u, x);
+        multiply(i, x);
+    };
     if (a.K < 8) {  // (one unit of one wavefront)
         if (u0 < u1) {
             load(0, 0);
             u32x4v x[4];
 #pragma unroll
             for (int s = 0; s < 4; ++s) x[s] = load_x_end(xp, 32 * s + 8 * g, a.K);
-            compute(0, x);
+            multiply(0, x);
         }
     } else if (u0 < u1) {
 #pragma unroll
@@ -118,19 +123,21 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
             load_tokens(i, u0 + i);
             __builtin_amdgcn_sched_barrier(0);
         }
-        for (int u = u0; u < u1; u += kAhead) {
+        // (no loads under a branch: the waits count them; none for a next turn that is not there: they
+        // would cost a range of a few units as much of x again)
+        int u = u0;
+        for (; u + kAhead < u1; u += kAhead) {
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                if (u + i < u1) {  // (no loads under the branch: the waits count them)
-                    u32x4v x[4];
-                    tokens(i, u + i, x);
-                    compute(i, x);
-                }
+                compute(i, u + i);
                 load(i, u + i + kAhead);
                 load_tokens(i, u + i + kAhead);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (u + i < u1) compute(i, u + i);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -335,9 +342,11 @@ void run_few(const QuantArgs& a, int rt, hipStream_t s) {
     if (rt == 1) quant_few_kernel<T, KIND, 1, X><<<grid, kQuantThreads, 0, s>>>(a);
     else if (rt == 2) quant_few_kernel<T, KIND, 2, X><<<grid, kQuantThreads, 0, s>>>(a);
     else if (rt == 3) quant_few_kernel<T, KIND, 3, X><<<grid, kQuantThreads, 0, s>>>(a);
-    else if (rt == 4) quant_few_kernel<T, KIND, 4, X><<<grid, kQuantThreads, 0, s>>>(a);
-    else if (rt == 6) quant_few_kernel<T, KIND, 6, X><<<grid, kQuantThreads, 0, s>>>(a);
-    else quant_few_kernel<T, KIND, 7, X><<<grid, kQuantThreads, 0, s>>>(a);
+    else if (rt == 4 || KIND == 4) quant_few_kernel<T, KIND, 4, X><<<grid, kQuantThreads, 0, s>>>(a);
+    else if constexpr (KIND < 4) {
+        if (rt == 6) quant_few_kernel<T, KIND, 6, X><<<grid, kQuantThreads, 0, s>>>(a);
+        else quant_few_kernel<T, KIND, 7, X><<<grid, kQuantThreads, 0, s>>>(a);
+    }
 }
 template <typename T, int KIND>
 void run_kind(QuantArgs a, const QuantPlan& p, hipStream_t s) {

@@ -120,7 +120,7 @@ lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void
     h->kind = lscd::quant_kind(h->per_unit, zeros != nullptr);
     // (every number of tokens has its own plan: fewer may split K further and need more room)
     for (int n = 1; n <= lscd::kQuantMaxTokens; ++n) {
-        const lscd::QuantPlan p = lscd::plan_quant(h->tiles, h->units, n, cus);
+        const lscd::QuantPlan p = lscd::plan_quant(h->tiles, h->units, n, h->kind, cus);
         if (p.splits > 1) h->part_floats = std::max(h->part_floats, (int64_t)p.splits * M * n);
     }
     lscd::QuantEncodeArgs a = {};
@@ -170,7 +170,7 @@ lscd_status_t lscd_quant_linear(lscd_quant_t h, const void* x, int64_t ldx, void
         a.x = (const uint16_t*)x + n * ldx;
         a.y = (uint16_t*)y + n * ldy;
         a.N = std::min(N - n, most);
-        const lscd::QuantPlan p = lscd::plan_quant(h->tiles, h->units, a.N, h->cus);
+        const lscd::QuantPlan p = lscd::plan_quant(h->tiles, h->units, a.N, h->kind, h->cus);
         a.splits = p.splits;
         hipError_t e = h->type == LSCD_F16 ? lscd::launch_quant_f16(a, h->kind, p, (hipStream_t)stream)
                                            : lscd::launch_quant_bf16(a, h->kind, p, (hipStream_t)stream);

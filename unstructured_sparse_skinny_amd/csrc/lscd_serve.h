@@ -80,7 +80,10 @@ __host__ __device__ inline int quant_bit(int j, int bit) {
 struct QuantPlan {
     int shared, rt, splits;
 };
-QuantPlan plan_quant(int tiles, int units, int N, int cus);
+QuantPlan plan_quant(int tiles, int units, int N, int kind, int cus);
+// Units that a wavefront has in flight for up to 16 tokens: what the registers hold (records of four words
+// take as many of them as the codes: one unit fewer for 2 and 3 row tiles, and no more than 4 row tiles).
+constexpr int quant_ahead(int rt, int kind) { return rt == 1 ? 4 : (rt == 2 ? (kind == 4 ? 3 : 4) : (rt == 3 && kind < 4 ? 3 : 2)); }
 
 struct QuantArgs {
     const uint32_t* codes;
