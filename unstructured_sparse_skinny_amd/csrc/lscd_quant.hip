@@ -97,17 +97,20 @@ hipError_t launch_quant_decode(const QuantArgs& a, int type, int kind, uint16_t*
 }
 
 // Row tiles per wavefront and splits along K: the least time by a model of this GPU, in microseconds.
-// A CU moves about 20 KB of codes a microsecond; x costs up to 16 tokens half of what its 256 bytes a
-// token and unit of a wavefront would from HBM.  A workgroup takes about 3 us to start and join, plus one
-// memory latency for each turn of its loads.  More than 16 tokens: a workgroup's round (two units of 4 RT
-// row tiles) measured 0.35 + 0.58 RT (64 tokens) and 0.3 + 0.45 RT (32).  A split adds a launch and its
-// partial sums.  It picks 7 row tiles for 28672 x 7168 (1792 tiles, 7 on every CU), 1 for 5003 x 4099.
+// Up to 16 tokens: a CU moves about 20 KB of codes a microsecond; x costs up to half of what its 256 bytes
+// a token and unit of a wavefront would from HBM, and is loaded for all units of a wavefront's turn.  A
+// workgroup takes 1 us to start and join where others run, 3 us and a memory latency for each turn of its
+// loads alone.  More than 16 tokens: a workgroup's round (two units of 4 RT row tiles) measured 0.35 + 0.58
+// RT (64 tokens) and 0.3 + 0.45 RT (32).  A split adds a launch and its partial sums.  It picks 7 row tiles
+// for 28672 x 7168 (1792 tiles, 7 on every CU: 23.0 us at 16 tokens, 38.2 with one), 1 for 4096 x 4096 (6.6
+// us).  More row tiles than 4 with records of four words do not fit the registers (27648 x 9216 x 16 in groups
+// of 32: 722 us with 7, 41.7 with 4); nor do 4 row tiles of 64 tokens.
 QuantPlan plan_quant(int tiles, int units, int N, int kind, int cus) {
     QuantPlan best = {N > 16, 1, 1};
     double cost = 0;
     static const int few[] = {1, 2, 3, 4, 6, 7}, many[] = {1, 2, 3, 4};
     const int* rts = best.shared ? many : few;
-    const int n = N > 32 ? 3 : (best.shared || kind == 4 ? 4 : 6);  // (four row tiles of 64 tokens do not fit the registers)
+    const int n = N > 32 ? 3 : (best.shared || kind == 4 ? 4 : 6);
     const int wr = best.shared ? 4 : 1, wk = kQuantWaves / wr;
     for (int i = 0; i < n; ++i) {
         const int rt = rts[i];
@@ -120,7 +123,7 @@ QuantPlan plan_quant(int tiles, int units, int N, int kind, int cus) {
             } else {
                 const int ahead = quant_ahead(rt, kind);
                 const double turns = std::ceil(per_wave / ahead);  // (x is loaded for all of a turn's units)
-                t = std::max(rounds * wk * (per_wave * rt + turns * ahead * N / 8.0) * 0.05, 3.0 + per_wave / ahead);
+                t = std::max(rounds * (1.0 + wk * (per_wave * rt + turns * ahead * N / 8.0) * 0.05), 3.0 + per_wave / ahead);
             }
             if (s > 1) t += 4.0 + (double)s * N * tiles * 16 * 8 / 5e6;
             if ((i == 0 && s == 1) || t < cost) {
