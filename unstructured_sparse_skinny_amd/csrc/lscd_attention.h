@@ -17,10 +17,14 @@
 //
 // Work is split over all sequences, key heads, row tiles and cached positions at once: the units
 // (one row tile x one stretch of positions) are numbered in that order and cut into equal ranges,
-// one per workgroup, wherever the cuts fall; an item (row tile) cut by a range's end leaves partial
-// results, and the last workgroup to arrive adds them in ascending order, so that results do not
-// depend on who arrives when.  Ragged batches, one long sequence and many short ones all balance,
-// and one launch does it.  Lengths are read on the device: no host copy, no plan.
+// one per workgroup, wherever the cuts fall.  An item (row tile) cut by a range's end leaves partial
+// results (maximum, sum, unnormalised output), which are added in ascending order, so that results do
+// not depend on who arrives when: by the last workgroup to arrive where they are few rows, by a second
+// kernel where they are many.  Ragged batches, one long sequence and many short ones all balance.
+// Lengths are read on the device: no host copy, no plan.
+//
+// Sequences of up to 16 query rows (one MFMA tile) are bound by the reading of their keys and values and
+// go to the kernel for few rows, longer ones to the other; a call whose batch may hold both launches both.
 #pragma once
 
 #include "lscd_serve.h"

