@@ -309,10 +309,11 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
     a.few_limit = both ? lscd::kFewRows : 0x7FFFFFFF;
     // Workgroups: no more per item than pay.  An item of U units over W workgroups takes U / W units and
     // then, in its last one, W parts to join: best at W = sqrt(U * unit / part), with a unit's time over a
-    // part's about 20 for few rows (one query row over 32768 positions: 64 workgroups) and 4 for many,
-    // whose parts are 256 rows.
-    auto grid = [&](int most, int rows, int tokens, double ratio) {
-        const double items = ((double)(T * share) / rows + sequences) * h->kv_heads, units = ceil((double)span / tokens);
+    // part's about 20 over the query rows where they are few (eight query rows over 32768 positions: 39 us with
+    // the workgroups of one row, 29 with theirs) and 4 where they are 256.
+    const double rows = std::min<double>(lscd::kFewRows, ceil((double)(T * share) / sequences));
+    auto grid = [&](int most, int tile, int tokens, double ratio) {
+        const double items = ((double)(T * share) / tile + sequences) * h->kv_heads, units = ceil((double)span / tokens);
         return (int)std::min<double>(most, items * std::min(units, 1.0 + ceil(sqrt(ratio * units))));
     };
     // (slots of work are counted in 32 bits on the device)
@@ -320,7 +321,7 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
         return LSCD_ERROR_NOT_SUPPORTED;
     if (sequences > 1 || !both) {
         hipError_t e = lscd::launch_attention_few(
-            a, type, grid(lscd::attention_few_grid(h->cus), lscd::kFewRows, lscd::kFewTokens, 20.0), (hipStream_t)stream);
+            a, type, grid(lscd::attention_few_grid(h->cus), lscd::kFewRows, lscd::kFewTokens, 20.0 / rows), (hipStream_t)stream);
         if (e != hipSuccess) return status_of(e);
     }
     if (both) {
