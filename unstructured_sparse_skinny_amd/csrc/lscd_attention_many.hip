@@ -11,9 +11,9 @@
 // a 4 x 16 block and get its columns, which is the A operand in the token order that P has.
 // 16-byte chunks are XOR-swizzled by the row so that the lanes of one read spread over the banks.
 //
-// Measured: 2048 new tokens of 32 heads over 16384 positions (515 GFLOP) 535 us, 963 TFLOP/s; a matrix
-// product in bfloat16 reaches 1232 here.  The matrix cores are busy 41 % of the cycles and the vector
-// unit 39 %, and two wavefronts per SIMD overlap little of the two.
+// Measured: 2048 new tokens of 32 heads over 16384 positions (515 GFLOP) 532 to 590 us from one card to
+// the next, 870 to 970 TFLOP/s; a matrix product in bfloat16 reaches 1232.  The matrix cores are busy 41 %
+// of the cycles and the vector unit 39 %, and two wavefronts per SIMD overlap little of the two.
 
 #include "lscd_attention.h"
 
