@@ -137,6 +137,21 @@ def test_strides_and_alignment(kind):
     assert (yw[:, 0] == 3).all() and (yw[:, 1 + M:] == 3).all()
 
 
+def test_strides_of_single_rows_and_columns_do_not_count():
+    """A matrix of one row, or of one byte a row, may have any stride in that direction."""
+    say("quant single rows and columns")
+    for M, K in ((1, 64), (40, 2)):
+        rng = np.random.default_rng(M)
+        codes = torch.from_numpy(rng.integers(0, 256, (M, K // 2)).astype(np.uint8)).cuda()
+        scales = torch.ones((M, 1), dtype=torch.float16, device="cuda")
+        x = torch.from_numpy(rng.integers(-2, 3, (3, K)).astype(np.float64)).half().cuda()
+        odd = codes.as_strided(codes.shape, (1, 1) if M == 1 else (1, 7))
+        y = [torch.empty((3, M), dtype=torch.float16, device="cuda") for _ in range(2)]
+        for c, out in zip((codes, odd), y):
+            L.lscd_quant_linear(L.lscd_quant_encode(c, scales, K, group=64), x, out)
+        assert torch.equal(y[0], y[1])
+
+
 def test_what_is_not_finite_stays_in_its_row():
     say("quant nan rows")
     h, c, s, z = matrix(90, 700, 128, True, "f16", 7)

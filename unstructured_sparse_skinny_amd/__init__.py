@@ -439,7 +439,7 @@ class Quant:
 def lscd_quant_encode(codes, scales, K: int, zeros=None, group: int = 128, stream=None) -> Quant:
     """Lay out a matrix of 4-bit codes: codes uint8 [M][(K + 1) // 2] (low half: even column), scales [M][ceil(K / group)]
     float16 or bfloat16 (the type of the products), zeros uint8 of the scales' shape or None (8)."""
-    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_cuda or codes.stride(1) != 1:
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_cuda or (codes.stride(1) != 1 and codes.shape[1] > 1):
         raise ValueError("codes must be a uint8 CUDA tensor of rows")
     M, groups = codes.shape[0], -(-K // group) if group > 0 else 0
     if scales.dtype not in (torch.float16, torch.bfloat16) or codes.shape[1] != (K + 1) // 2:
@@ -450,7 +450,7 @@ def lscd_quant_encode(codes, scales, K: int, zeros=None, group: int = 128, strea
     if zeros is not None and zeros.dtype != torch.uint8:
         raise ValueError("zeros must be uint8")
     h = ctypes.c_void_p()
-    _check(_lib.lscd_quant_encode(codes.data_ptr(), codes.stride(0), scales.data_ptr(),
+    _check(_lib.lscd_quant_encode(codes.data_ptr(), codes.stride(0) if M > 1 else codes.shape[1], scales.data_ptr(),
                                   None if zeros is None else zeros.data_ptr(), M, K, group, _TYPES[scales.dtype],
                                   _stream_on(stream, codes.device), ctypes.byref(h)), "lscd_quant_encode")
     return Quant(h.value, M, K, group, scales.dtype, codes.device)
