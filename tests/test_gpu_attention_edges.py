@@ -1,0 +1,49 @@
+"""Attention over a paged cache at the ends of its types' ranges and of its arguments.
+
+Tolerances are those of test_gpu_attention (u: unit roundoff, A = sum_j p_j |v_j|), with the floor of small
+float16 weights written out: a weight is rounded to a step of at most 2^-31 of the largest, so to within
+2^-32 of it, which is 2^-32 / sum_j exp(s_j - max s) of the whole.
+"""
+import numpy as np
+import pytest
+
+from oracle import serving as sv
+from tests._util import say
+from tests.test_gpu_attention import TYPES, Batch
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import unstructured_sparse_skinny_amd as L
+
+
+def place(b, which, i, j, value):
+    """Set position j of sequence i (all heads)."""
+    b.tensors[which][b.table[i, j // b.page].long(), :, j % b.page] = value
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("d", [9.5, 12.0, 16.0, 17.5, 20.0])
+def test_weights_far_below_the_largest(kind, n, d):
+    """One position in 32 holds a large score and nothing else; the rest, d nats lower, hold what is there to sum."""
+    say("small weights", kind, n, d)
+    length = 1000
+    b = Batch([(n, length)], 2, 2, 64, 16, kind, kind)
+    b.q.zero_()
+    b.q[:, :, 0] = 1
+    for x, rest in zip(b.tensors, (-d, 1024.0)):
+        x.zero_()
+        for j in range(length):
+            if j % 32:
+                place(b, 0 if rest < 0 else 1, 0, j, torch.tensor([rest] + [0.0] * 63 if rest < 0 else [rest] * 64).to(x))
+    got = b.run(scale=1.0).cpu().double().numpy()
+    o, a, big = sv.attention(b.q.cpu().double().numpy(), b.values(0, 0), b.values(1, 0), 1.0)
+    u, e = sv.ROUNDOFF[kind], 2 * (64 + 8) * 2.0 ** -24 * big[..., None] + 2.0 ** -18
+    tol = u * np.abs(o) + (u + e) * a + sv.TINY[kind]
+    for i in range(n):
+        seen = np.arange(length - n + i + 1) % 32 != 0
+        total = (~seen).sum() + seen.sum() * np.exp(-d)
+        tol[i] += (2.0 ** -32 if kind == "f16" else 0.0) * seen.sum() * 1024 / total
+    assert (np.abs(got - o) <= tol).all(), float((np.abs(got - o) / tol).max())

@@ -12,8 +12,11 @@
 // product: its k index may run over the tokens in any order as long as V^T uses the same one.
 // The maximum is moved only when some score exceeds it by 8 (a factor 256, far inside 16-bit
 // range for P and fp32 for the sums): most tiles then skip the exchange and the rescaling.
-// Sums, maxima and the output accumulate in fp32; P is rounded once to the model's 16-bit type,
-// whose relative step is that of the values it multiplies.
+// Sums, maxima and the output accumulate in fp32.  P is rounded once to the model's 16-bit type for the
+// second product: a step of 2^-11 or 2^-8 of each weight, that of the values it multiplies (a second
+// product with what the rounding leaves out would give every infinity among the values a weight of zero or
+// less).  float16 has few exponents, so its weights are held 2^7 times as large (m is that much less), at
+// most 2^15: they keep their step down to 2^-21 of the largest and are rounded in steps of 2^-31 of it below.
 //
 // Work is split over all sequences, key heads, row tiles and cached positions at once: the units
 // (one row tile x one stretch of positions) are numbered in that order and cut into equal ranges,
@@ -36,7 +39,7 @@ namespace lscd {
 namespace {
 
 constexpr float kNoScore = -1e30f;  // maximum before any score: finite, so that differences stay defined
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 8.f;        // how far a score may exceed the maximum before it is moved
 
 // The rows and positions of one sequence.
 struct Seq {

@@ -391,8 +391,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         float most = x[0];
 #pragma unroll
         for (int i = 1; i < 8; ++i) most = fmaxf(most, x[i]);
-        if (__any(most > m + kLazy)) {
-            const float to = fmaxf(m, max_quarters(most));
+        if (__any(most - m > kLazy + T::kWeightBits)) {
+            const float to = fmaxf(m, max_quarters(most) - T::kWeightBits);
             const float by = exp2_fast(m - to);
             m = to;
             l *= by;

@@ -253,8 +253,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
 #pragma unroll
                 for (int i = 1; i < 16 * kHalves - 1; i += 2) most = max3(most, s[i / 16][i % 16], s[(i + 1) / 16][(i + 1) % 16]);
                 most = max3(most, s[kHalves - 1][15], s[kHalves - 1][15]);
-                if (__any(most * scale > m + kLazy)) {
-                    const float to = fmaxf(m, max_halves(most) * scale);
+                if (__any(most * scale > m + (kLazy + T::kWeightBits))) {
+                    const float to = fmaxf(m, max_halves(most) * scale - T::kWeightBits);
                     const float by = exp2_fast(m - to);
                     m = to;
                     l *= by;

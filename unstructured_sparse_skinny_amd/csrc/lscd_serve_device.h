@@ -27,6 +27,7 @@ __device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cas
 // The two 16-bit types.  A pair of values travels as one 32-bit word.
 struct F16 {
     static constexpr bool bf = false;
+    static constexpr float kWeightBits = 7.f;  // softmax weights are held 2^7 times as large
     __device__ static __forceinline__ float low(uint32_t w) { return (float)__builtin_bit_cast(half2v, w)[0]; }
     __device__ static __forceinline__ float high(uint32_t w) { return (float)__builtin_bit_cast(half2v, w)[1]; }
     __device__ static __forceinline__ uint32_t pack(float a, float b) {  // nearest, ties to even
@@ -62,6 +63,7 @@ struct F16 {
 };
 struct BF16 {
     static constexpr bool bf = true;
+    static constexpr float kWeightBits = 0.f;
     __device__ static __forceinline__ float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
     __device__ static __forceinline__ float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
     __device__ static __forceinline__ uint32_t pack(float a, float b) {
