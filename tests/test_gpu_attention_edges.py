@@ -47,3 +47,13 @@ def test_weights_far_below_the_largest(kind, n, d):
         total = (~seen).sum() + seen.sum() * np.exp(-d)
         tol[i] += (2.0 ** -32 if kind == "f16" else 0.0) * seen.sum() * 1024 / total
     assert (np.abs(got - o) <= tol).all(), float((np.abs(got - o) / tol).max())
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("seqs", [[(1, 3), (1, 20), (1, 300), (5, 40)], [(100, 230)]])
+def test_equal_values_come_out_as_they_are(seqs, kind):
+    """The weights that are summed are those that are multiplied: a mean of equal values is that value."""
+    say("equal values", seqs, kind)
+    b = Batch(seqs, 4, 2, 64, 16, kind, kind, seed=9)
+    b.tensors[1].copy_(torch.linspace(1, 2, 64).to(b.tensors[1]))
+    assert torch.equal(b.run(), torch.linspace(1, 2, 64).to(b.q).expand(b.q.shape))

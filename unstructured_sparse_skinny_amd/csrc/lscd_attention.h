@@ -17,6 +17,7 @@
 // product with what the rounding leaves out would give every infinity among the values a weight of zero or
 // less).  float16 has few exponents, so its weights are held 2^7 times as large (m is that much less), at
 // most 2^15: they keep their step down to 2^-21 of the largest and are rounded in steps of 2^-31 of it below.
+// Both kernels sum the weights as they multiply them.
 //
 // Work is split over all sequences, key heads, row tiles and cached positions at once: the units
 // (one row tile x one stretch of positions) are numbered in that order and cut into equal ranges,

@@ -402,13 +402,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                 for (int r = 0; r < 4; ++r) o[i][r] *= by;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = exp2_fast(x[i] - m);
-            l += x[i];
-        }
+        for (int i = 0; i < 8; ++i) x[i] = exp2_fast(x[i] - m);
         u32x4v pb;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pb[i] = T::pack(x[2 * i], x[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) {
+            pb[i] = T::pack(x[2 * i], x[2 * i + 1]);
+            l = T::add_pair(pb[i], l);  // (as they are multiplied: a mean of equal values is that value)
+        }
         bool odd = false;  // an infinity or NaN that some row may not see
         if (masked) {
             f.mask_scales(t0, low, high, lane);
