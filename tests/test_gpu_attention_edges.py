@@ -57,3 +57,28 @@ def test_equal_values_come_out_as_they_are(seqs, kind):
     b = Batch(seqs, 4, 2, 64, 16, kind, kind, seed=9)
     b.tensors[1].copy_(torch.linspace(1, 2, 64).to(b.tensors[1]))
     assert torch.equal(b.run(), torch.linspace(1, 2, 64).to(b.q).expand(b.q.shape))
+
+
+@pytest.mark.parametrize("kind,scale", [("f16", 2.0 ** 22), ("f16", 2.0 ** 32), ("bf16", 2.0 ** 22), ("bf16", 2.0 ** 60)])
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(kind, scale, n, sign):
+    """Scores far beyond the exponential's range, up to fp32's: equal ones weigh the same, smaller ones nothing.
+
+    Keys are equal but for one position in seven, whose score is far lower: what is left is a mean of the other
+    values, whose weights are equal (error: the output's rounding, and 2^-18 for the sums)."""
+    say("scores of any size", kind, scale, n, sign)
+    length, half = 150, scale ** 0.5
+    b = Batch([(n, length)], 2, 2, 64, 16, kind, kind, seed=3)
+    b.q.zero_()
+    b.q[:, :, :3] = torch.tensor([1.0, 1.0, 0.5]).to(b.q) * 1.1 * sign * (half if kind == "bf16" else 2.0 ** 8)
+    k = torch.tensor([1.0, 0.75, 1.0] + [0.0] * 61) * 1.3 * (half if kind == "bf16" else 2.0 ** 8)
+    for j in range(length):
+        place(b, 0, 0, j, (k * (0.5 if (j % 7 == 3) == (sign > 0) else 1.0)).to(b.q))
+    got = b.run(scale=0.3 if kind == "bf16" else 0.3 * scale / 2 ** 16).cpu().double().numpy()
+    v = b.values(1, 0)
+    for i in range(n):
+        j = np.arange(length - n + i + 1)
+        best = v[j[j % 7 != 3]]
+        want, a = best.mean(0), np.abs(best).mean(0)
+        assert (np.abs(got[i] - want) <= sv.ROUNDOFF[kind] * np.abs(want) + 2.0 ** -18 * a + sv.TINY[kind]).all(), i

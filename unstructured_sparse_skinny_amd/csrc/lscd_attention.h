@@ -41,6 +41,7 @@ namespace {
 
 constexpr float kNoScore = -1e30f;  // maximum before any score: finite, so that differences stay defined
 constexpr float kLazy = 8.f;        // how far a score may exceed the maximum before it is moved
+constexpr float kLarge = 1048576.f;
 
 // The rows and positions of one sequence.
 struct Seq {

@@ -379,7 +379,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         f.load_keys(a, hb, e, nt, next_high, lane);
         float x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = s[i / 4][i % 4] * a.scale_log2;
+        for (int i = 0; i < 8; ++i) x[i] = product(s[i / 4][i % 4], a.scale_log2);
         const bool masked = t0 < all_low || t0 + 32 > all_high;
         if (masked) {
 #pragma unroll

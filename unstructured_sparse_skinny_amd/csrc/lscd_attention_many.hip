@@ -15,6 +15,8 @@
 // the next, 870 to 970 TFLOP/s; a matrix product in bfloat16 reaches 1232.  The matrix cores are busy 41 %
 // of the cycles and the vector unit 39 %, and two wavefronts per SIMD overlap little of the two.
 
+#include <type_traits>
+
 #include "lscd_attention.h"
 
 namespace lscd {
@@ -125,6 +127,7 @@ template <typename T, bool E4M3, int DP>
 __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArgs a) {
     using F = Many<T, E4M3, DP>;
     __shared__ __attribute__((aligned(16))) unsigned char sh[2][2][F::kTile];
+    __shared__ float sh_m[kManyThreads];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int half = lane >> 5;
     const int G = gridDim.x;
@@ -199,7 +202,13 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
         f.look_up(a, p.seq, t0, wave);
         f.load(a, hb, t0, low, high, tid);
         f.look_up(a, p.seq, t0 + F::kTokens, wave);
-        int any_odd = 0;  // an edge tile had infinities or NaN among its values
+        // One fma per weight takes the maximum, which is rounded, from a product that is not: no matter until
+        // the rounding comes near 1, for scores of 2^23.  An item in which this wavefront has had scores of
+        // kLarge rounds the product too: scores become exponents in place, and the maximum waits in LDS (one
+        // register more through the products costs the 256-channel kernels a tenth of their time).
+        bool large = false;
+        float slope = scale;
+        int any_odd = 0;     // an edge tile had infinities or NaN among its values
         auto is_edge = [&](int t) { return t < tile_all_low || t + F::kTokens > tile_all_high; };
         auto put = [&](int buf, int t) {
             const bool edge = is_edge(t);
@@ -253,7 +262,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
 #pragma unroll
                 for (int i = 1; i < 16 * kHalves - 1; i += 2) most = max3(most, s[i / 16][i % 16], s[(i + 1) / 16][(i + 1) % 16]);
                 most = max3(most, s[kHalves - 1][15], s[kHalves - 1][15]);
-                if (__any(most * scale > m + (kLazy + T::kWeightBits))) {
+                if (large) m = sh_m[tid];
+                if (large || __any(most * scale > m + (kLazy + T::kWeightBits))) {
                     const float to = fmaxf(m, max_halves(most) * scale - T::kWeightBits);
                     const float by = exp2_fast(m - to);
                     m = to;
@@ -262,14 +272,24 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
                     for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[b][i] *= by;
+                    large = large || __any(fabsf(m) >= kLarge && m != kNoScore);
+                    if (large) {
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) s[h][i] = product(s[h][i], scale) - m;
+                        sh_m[tid] = m;
+                        m = 0.f;
+                        slope = 1.f;
+                    }
                 }
                 // weights of the 16 tokens of step ks, as the B operand
                 auto weights = [&](int ks) {
                     u32x4v w;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float x = exp2_fast(__builtin_fmaf(s[ks / 2][8 * (ks % 2) + 2 * i], scale, -m));
-                        const float y = exp2_fast(__builtin_fmaf(s[ks / 2][8 * (ks % 2) + 2 * i + 1], scale, -m));
+                        const float x = exp2_fast(__builtin_fmaf(s[ks / 2][8 * (ks % 2) + 2 * i], slope, -m));
+                        const float y = exp2_fast(__builtin_fmaf(s[ks / 2][8 * (ks % 2) + 2 * i + 1], slope, -m));
                         w[i] = T::pack(x, y);
                         l = T::add_pair(w[i], l);
                     }
@@ -299,6 +319,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
             if (k + 1 < last) put(buf ^ 1, t0 + F::kTokens);
             __syncthreads();
         }
+        if (large) m = sh_m[tid];
         l = sum_halves(l);
         // What follows runs once per item: addresses are worked out here, not kept in registers through
         // the loop above (the compiler would move them out of all loops).

@@ -97,6 +97,12 @@ struct BF16 {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32
 
+// a * b rounded, also where a sum follows.
+__device__ __forceinline__ float product(float a, float b) {
+#pragma clang fp contract(off)
+    return a * b;
+}
+
 // x, in a way that the compiler does not see through.
 __device__ __forceinline__ int opaque(int x) {
     asm("" : "+v"(x));
