@@ -59,7 +59,7 @@ def test_equal_values_come_out_as_they_are(seqs, kind):
     assert torch.equal(b.run(), torch.linspace(1, 2, 64).to(b.q).expand(b.q.shape))
 
 
-@pytest.mark.parametrize("kind,scale", [("f16", 2.0 ** 22), ("f16", 2.0 ** 32), ("bf16", 2.0 ** 22), ("bf16", 2.0 ** 60)])
+@pytest.mark.parametrize("kind,scale", [("f16", 2.0 ** 22), ("f16", 2.0 ** 32), ("bf16", 2.0 ** 22), ("bf16", 2.0 ** 60), ("bf16", 2.0 ** 110)])
 @pytest.mark.parametrize("n", [1, 40])
 @pytest.mark.parametrize("sign", [1, -1])
 def test_scores_of_any_size(kind, scale, n, sign):

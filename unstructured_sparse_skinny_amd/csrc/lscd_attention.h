@@ -39,7 +39,8 @@
 namespace lscd {
 namespace {
 
-constexpr float kNoScore = -1e30f;  // maximum before any score: finite, so that differences stay defined
+constexpr float kNoScore = -3.4028234663852886e38f;  // maximum before any score: finite, so that differences stay
+                                                     // defined, and below every finite score
 constexpr float kLazy = 8.f;        // how far a score may exceed the maximum before it is moved
 constexpr float kLarge = 1048576.f;
 
