@@ -496,7 +496,8 @@ lscd_status_t lscd_attention_destroy(lscd_attention_t h);
  *   effect, whatever it holds.
  *   q, o    device, T rows of q_heads * head_dim values of `type`, 16-byte aligned; q_stride,
  *           o_stride elements (a multiple of 8) from one token to the next.  o may not overlap q.
- *   start   device, sequences + 1 ascending numbers, from 0 to T.
+ *   start   device, sequences + 1 ascending numbers, from 0 to T at most; rows of o from start[sequences]
+ *           on are not written (a captured call may have room for more tokens than a replay brings).
  *   length  device, one number for each sequence.
  *   table   device; page j of sequence s is table[s * table_stride + j], table_pages of them.
  *   cache   of the handle's heads and head_dim; of `type` or LSCD_E4M3.

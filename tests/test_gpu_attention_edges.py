@@ -82,3 +82,15 @@ def test_scores_of_any_size(kind, scale, n, sign):
         best = v[j[j % 7 != 3]]
         want, a = best.mean(0), np.abs(best).mean(0)
         assert (np.abs(got[i] - want) <= sv.ROUNDOFF[kind] * np.abs(want) + 2.0 ** -18 * a + sv.TINY[kind]).all(), i
+
+
+@pytest.mark.parametrize("seqs", [[(5, 40)], [(5, 40), (0, 90)], [(1, 40)], [(30, 70), (2, 9)], [(0, 12)]])
+def test_fewer_tokens_than_rows(seqs):
+    """Room for 64 tokens and starts that end before: those tokens are served, the other rows stay."""
+    say("fewer tokens than rows", seqs)
+    b = Batch(seqs, 4, 2, 64, 16, "f16", "f16", seed=21)
+    used, spare = b.T, 64 - b.T
+    q = torch.cat([b.q, torch.full((spare, 4, 64), float("nan"), dtype=torch.float16, device="cuda")])
+    out = b.run(q=q, out=torch.full_like(q, 7.0))
+    b.check(out[:used])
+    assert (out[used:] == 7).all()

@@ -304,9 +304,10 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
     a.record = h->record;
     // Sequences of up to 16 query rows are the few-row kernel's, longer ones the other's.  Where no
     // sequence can be longer (or each has one new token, as far as the counts tell), the few-row
-    // kernel takes all of them, whatever the device arrays hold.
+    // kernel takes all of them, whatever the device arrays hold.  A single sequence that may be long is the
+    // other's, whatever its rows: one launch.
     const bool both = T * share > lscd::kFewRows && T > sequences;
-    a.few_limit = both ? lscd::kFewRows : 0x7FFFFFFF;
+    a.few_limit = !both ? 0x7FFFFFFF : sequences > 1 ? lscd::kFewRows : 0;
     // Workgroups: no more per item than pay.  An item of U units over W workgroups takes U / W units and
     // then, in its last one, W parts to join: best at W = sqrt(U * unit / part), with a unit's time over a
     // part's about 20 over the query rows where they are few (eight query rows over 32768 positions: 39 us with
