@@ -466,7 +466,8 @@ lscd_status_t lscd_cache_write(const lscd_cache_t* cache, const void* k, int64_t
 
 /*
  * lscd_cache_read -- the values in T slots as rows of `type`: the reverse of lscd_cache_write
- * (code times scale, exact unless it leaves the type's normal range).  A slot number that is
+ * (code times scale, exact inside the type's normal range, rounded to its subnormals below and an
+ * infinity above: a float16 value above 63488 is stored as 65536).  A slot number that is
  * negative or past the cache gives zeros.  Same argument rules; any slot may be read any number of
  * times.
  */
@@ -505,7 +506,9 @@ lscd_status_t lscd_attention_destroy(lscd_attention_t h);
  * and replayed with other lengths.  Array contents outside these rules are clamped (tokens to T,
  * lengths to the table, pages to the pool), so that no call reads or writes out of bounds.
  * Scores, softmax and sums are fp32; the softmax weights are rounded once to `type` for the second
- * product.  Results do not depend on timing (partial sums are added in a fixed order) but their
+ * product.  An E4M3 cache's values reach the products in `type`: exact inside its normal range; past its
+ * largest value (65504 in float16) they count as that, below its normal range they are rounded to its
+ * subnormals.  Results do not depend on timing (partial sums are added in a fixed order) but their
  * last bits may depend on the other sequences in the call, which move the points where work is split.
  * INVALID_VALUE: null pointers, misalignment, negative sizes, a scale that is not finite, wrong
  * device.  NOT_SUPPORTED: T * (q_heads / kv_heads) or table_pages * page_size above 2^30, more than

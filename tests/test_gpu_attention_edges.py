@@ -94,3 +94,26 @@ def test_fewer_tokens_than_rows(seqs):
     out = b.run(q=q, out=torch.full_like(q, 7.0))
     b.check(out[:used])
     assert (out[used:] == 7).all()
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("n,length", [(1, 64), (2, 50), (40, 64), (40, 200)])
+def test_codes_past_the_largest_value(kind, n, length):
+    """The largest 16-bit values are stored as codes that stand for a little more (65536 for 65504): they count as the
+    type's largest value, one unit roundoff less (u A, and in the scores what q makes of the difference)."""
+    say("codes past the largest value", kind, n, length)
+    b = Batch([(n, length)], 2, 2, 64, 16, kind, "e4m3", seed=14)
+    top = float(torch.finfo(TYPES[kind]).max)
+    k, v = (torch.randn((length, 2, 64), device="cuda").to(TYPES[kind]) for _ in range(2))
+    k[7, :, 3], k[9, :, 5], v[5, :, 1], v[5, :, 2] = top, -top, top, -top
+    b.q[:, :, 3] = 0.0
+    b.q[:, :, 5] = 2.0 / top
+    place = torch.arange(length, device="cuda")
+    slots = (b.table[0, place // 16] * 16 + place % 16).to(torch.int32)
+    L.lscd_cache_write(b.cache(), k, v, slots)
+    got = b.run().cpu().double().numpy()
+    assert np.abs(b.values(1, 0)).max() > top
+    o, a, big = sv.attention(b.q.cpu().double().numpy(), b.values(0, 0), b.values(1, 0), 64 ** -0.5)
+    u = sv.ROUNDOFF[kind]
+    e = 2 * (64 + 8) * 2.0 ** -24 * big[..., None] + 2 * 64 ** -0.5 * 2 * u + 2.0 ** -18
+    assert (np.abs(got - o) <= u * np.abs(o) + (2 * u + e) * a + sv.TINY[kind]).all()

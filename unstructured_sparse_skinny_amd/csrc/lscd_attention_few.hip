@@ -16,6 +16,8 @@
 // TB/s, which is what a plain read reaches here; one token over 1000 positions of 8 heads 9.4 us, a chain
 // of dependent latencies (tables, keys, values, partial results, their join) rather than its 4 MB.
 
+#include <type_traits>
+
 #include "lscd_attention.h"
 
 namespace lscd {
@@ -116,15 +118,33 @@ struct Few {
         }
     }
 
+    // Whether some key's or value's code times its scale may pass the type's largest value.  (Scales are
+    // positive: they compare as whole numbers.)
+    __device__ __forceinline__ bool top_keys(int h) const { return E4M3 && __any(ks[h] >= T::kTopScale); }
+    __device__ __forceinline__ bool top_values() const {
+        if (!E4M3) return false;
+        uint32_t most = vs[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) most = max(most, vs[j]);
+        return __any(most >= T::kTopScale);
+    }
+    // Word of codes `w` in 16 bits.  TOP: saturated.  (The scale is opaque there, so that the conversions of
+    // the two forms are not taken for the same and moved out of their branches.)
+    template <bool HI, bool TOP>
+    __device__ static __forceinline__ uint32_t from_code(uint32_t w, uint32_t scale) {
+        if (TOP) return saturate<T>(T::template from_e4m3<HI>(w, as_float(opaque(scale))));
+        return T::template from_e4m3<HI>(w, as_float(scale));
+    }
     // The A operand of key half h, step s, in 16 bits.
+    template <bool TOP>
     __device__ __forceinline__ u32x4v key_operand(int h, int s) const {
         u32x4v x;
         if (E4M3) {  // two words of codes per step: channels 16 g + 8 (s % 2) of the 64 of step s / 2
             const uint32_t lo = kr[h][4 * (s / 2) + 2 * (s % 2)], hi = kr[h][4 * (s / 2) + 2 * (s % 2) + 1];
-            x[0] = T::template from_e4m3<false>(lo, as_float(ks[h]));
-            x[1] = T::template from_e4m3<true>(lo, as_float(ks[h]));
-            x[2] = T::template from_e4m3<false>(hi, as_float(ks[h]));
-            x[3] = T::template from_e4m3<true>(hi, as_float(ks[h]));
+            x[0] = from_code<false, TOP>(lo, ks[h]);
+            x[1] = from_code<true, TOP>(lo, ks[h]);
+            x[2] = from_code<false, TOP>(hi, ks[h]);
+            x[3] = from_code<true, TOP>(hi, ks[h]);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = kr[h][4 * s + i];
@@ -373,8 +393,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             s[h] = f32x4v{0.f, 0.f, 0.f, 0.f};
+            auto score = [&](auto top) {
 #pragma unroll
-            for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(f.key_operand(h, st), qr[st], s[h]);
+                for (int st = 0; st < F::kSteps; ++st)
+                    s[h] = T::mfma16(f.template key_operand<decltype(top)::value>(h, st), qr[st], s[h]);
+            };
+            if (f.top_keys(h))
+                score(std::true_type{});
+            else
+                score(std::false_type{});
         }
         f.load_keys(a, hb, e, nt, next_high, lane);
         float x[8];
@@ -409,11 +436,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             pb[i] = T::pack(x[2 * i], x[2 * i + 1]);
             l = T::add_pair(pb[i], l);  // (as they are multiplied: a mean of equal values is that value)
         }
-        bool odd = false;  // an infinity or NaN that some row may not see
+        bool odd = false;  // an infinity or NaN that some row may not see, or a code past the largest value
         if (masked) {
             f.mask_scales(t0, low, high, lane);
             odd = __any(f.any_odd());
         }
+        odd = odd || f.top_values();
         if (!odd) {
 #pragma unroll
             for (int w = 0; w < VW / 2; ++w) {
@@ -424,7 +452,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             }
         } else {
             // 0 * infinity would be NaN in rows that do not see the token: what is finite as
-            // ever, the rest one token at a time and added only where it is seen
+            // ever, the rest one token at a time and added only where it is seen (infinities that codes
+            // became, which have none of their own, as the largest value)
 #pragma unroll
             for (int w = 0; w < VW / 2; ++w) {
                 u32x4v v0, v1, f0, f1;
@@ -435,6 +464,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                     f1[i] = T::finite(v1[i]);
                     v0[i] ^= f0[i];
                     v1[i] ^= f1[i];
+                    if (E4M3) {
+                        v0[i] = saturate<T>(v0[i]);
+                        v1[i] = saturate<T>(v1[i]);
+                    }
                 }
                 o[2 * w] = T::mfma16(f0, pb, o[2 * w]);
                 o[2 * w + 1] = T::mfma16(f1, pb, o[2 * w + 1]);

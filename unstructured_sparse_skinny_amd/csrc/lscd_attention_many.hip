@@ -6,7 +6,7 @@
 // positions for heads of 65 to 128 channels, 128 for less, 32 for more: what the registers hold),
 // double-buffered with one barrier per tile: the next tile's loads are issued before the current
 // one is computed and written to the other buffer after it (codes of an 8-bit cache become 16-bit
-// values on the way; scales are powers of two, so that rounds nothing).  Keys are read back row by
+// values on the way; scales are powers of two, so that this rounds nothing inside the type's range).  Keys are read back row by
 // row (128-bit reads), values as V^T by the transposing LDS read (ds_read_b64_tr_b16): 16 lanes read
 // a 4 x 16 block and get its columns, which is the A operand in the token order that P has.
 // 16-byte chunks are XOR-swizzled by the row so that the lanes of one read spread over the banks.
@@ -94,6 +94,7 @@ struct Many {
             const int row = row_of(i, tid);
             if (kSpare && row >= kTokens) continue;
             if (DP == 96 && c >= DP / (E4M3 ? 16 : 8)) continue;
+            const bool top = E4M3 && __any(max(__builtin_bit_cast(uint32_t, ks[i]), __builtin_bit_cast(uint32_t, vs[i])) >= T::kTopScale);
 #pragma unroll
             for (int h = 0; h < (E4M3 ? 2 : 1); ++h) {
                 u32x4v x = k[i], y = v[i];
@@ -104,6 +105,13 @@ struct Many {
                         x[2 * w + 1] = T::template from_e4m3<true>(k[i][2 * h + w], ks[i]);
                         y[2 * w] = T::template from_e4m3<false>(v[i][2 * h + w], vs[i]);
                         y[2 * w + 1] = T::template from_e4m3<true>(v[i][2 * h + w], vs[i]);
+                    }
+                    if (top) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            x[w] = saturate<T>(x[w]);
+                            y[w] = saturate<T>(y[w]);
+                        }
                     }
                 }
                 if (edge) {
@@ -345,7 +353,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
                         u32x2v x;
                         if (E4M3) {
                             const uint32_t c = __builtin_amdgcn_raw_buffer_load_b32(hb.values(pg), off, 0, 0);
-                            x = u32x2v{T::template from_e4m3<false>(c, vscale), T::template from_e4m3<true>(c, vscale)};
+                            x = u32x2v{saturate<T>(T::template from_e4m3<false>(c, vscale)), saturate<T>(T::template from_e4m3<true>(c, vscale))};
                         } else {
                             x = __builtin_amdgcn_raw_buffer_load_b64(hb.values(pg), off, 0, 0);
                         }

@@ -5,8 +5,9 @@
 // over the finite values (e = 0 where all are zero), code = e4m3(x * 2^-e), nearest with ties to
 // even; the product is exact, so the code is the only rounding.  e4m3 is a floating format: a
 // power of two as the scale costs none of its 4 significant bits, and code * 2^e is exact in the
-// 16-bit types (above their subnormals), so reading back rounds nothing and the attention can use
-// the codes as they are.
+// 16-bit types' normal range, so reading back rounds nothing there and the attention can use the codes
+// as they are.  (A value within 2^-5 of the type's largest may become a code that stands for the next
+// power of two: read back as an infinity, counted by the attention as the largest value.)
 //
 // Both directions move about 3 bytes a value once and compute next to nothing: bound by HBM, and
 // by latency for the few tokens of a decoding step.  A vector of up to 128 channels is one group

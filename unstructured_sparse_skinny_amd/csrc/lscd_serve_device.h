@@ -28,6 +28,8 @@ __device__ __forceinline__ float as_float(uint32_t x) { return __builtin_bit_cas
 struct F16 {
     static constexpr bool bf = false;
     static constexpr float kWeightBits = 7.f;  // softmax weights are held 2^7 times as large
+    static constexpr uint32_t kTopScale = 0x43800000u;  // bits of 2^8, whose codes (up to 448) may pass the largest value
+    static constexpr uint32_t kInfinity = 0x7C00u;
     __device__ static __forceinline__ float low(uint32_t w) { return (float)__builtin_bit_cast(half2v, w)[0]; }
     __device__ static __forceinline__ float high(uint32_t w) { return (float)__builtin_bit_cast(half2v, w)[1]; }
     __device__ static __forceinline__ uint32_t pack(float a, float b) {  // nearest, ties to even
@@ -64,6 +66,8 @@ struct F16 {
 struct BF16 {
     static constexpr bool bf = true;
     static constexpr float kWeightBits = 0.f;
+    static constexpr uint32_t kTopScale = 0x7B800000u;  // 2^120
+    static constexpr uint32_t kInfinity = 0x7F80u;
     __device__ static __forceinline__ float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
     __device__ static __forceinline__ float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
     __device__ static __forceinline__ uint32_t pack(float a, float b) {
@@ -96,6 +100,12 @@ struct BF16 {
 };
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }  // v_exp_f32
+
+// The pair with infinities replaced by the largest value of their sign.
+template <typename T>
+__device__ __forceinline__ uint32_t saturate(uint32_t w) {
+    return w - ((w & 0x7FFFu) == T::kInfinity ? 1u : 0u) - ((w & 0x7FFF0000u) == T::kInfinity << 16 ? 0x10000u : 0u);
+}
 
 // a * b rounded, also where a sum follows.
 __device__ __forceinline__ float product(float a, float b) {
