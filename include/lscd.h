@@ -412,7 +412,9 @@ typedef enum {
  *          any 2-byte alignment (16-byte aligned x rows load faster).
  *   N      0 is a no-op; 1..LSCD_MAX_N, in launches of up to 64 tokens that read the codes once each.
  * Sums are fp32, the scale is applied to each group's sum, y is rounded once (nearest-even).  float16:
- * (code - zero) x is exact; bfloat16: an infinity in x gives NaN.  Sums over a split K are added in a
+ * (code - zero) x is exact; bfloat16: zero times a group's sum of x is taken off after summing, so an
+ * infinity in x gives NaN, and fp32 rounds relative to (32 + code + zero) |x| in place of
+ * |code - zero| |x|.  y may not overlap x.  Sums over a split K are added in a
  * fixed order: bit-reproducible.  Asynchronous, no allocation, graph-capturable; one handle must not
  * run on two streams at once (it owns one workspace).
  *

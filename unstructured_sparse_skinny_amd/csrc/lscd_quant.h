@@ -8,8 +8,13 @@
 // four bits at the top of the fraction of 16.0: one mask-and-or for two codes and a shift for most.
 // float16: 16 + z is then taken off with one packed subtraction, exactly; bfloat16 has no packed
 // arithmetic, so sums of (16 + c) x are kept per group and (16 + z) sum of x is taken off in fp32 once
-// per group (the sums of x are one more product, with ones).  Products of a code and x are exact,
-// sums are fp32, the scale is applied to a group's sum in fp32: the only rounding is y's.
+// per group (the sums of x are one more product, with ones).  These numbers and ones are held 2^-12 times
+// as large, and sums are multiplied by 2^12 when they are written: 128 products of up to 31 then stay below
+// the largest x, whatever x is.
+// Products of a code and x are exact, sums are fp32 and the scale is applied to a group's sum in fp32; y is
+// rounded once to 16 bits.  What fp32 rounds is at most (K + 2 groups + 8) 2^-24 of the sum of the terms'
+// magnitudes: |(c - z) x s| in float16, (32 + c + z) |x s| in bfloat16, where the difference is taken
+// after summing.
 #pragma once
 
 #include "lscd_serve.h"
@@ -18,12 +23,16 @@
 namespace lscd {
 namespace {
 
+// What sums are multiplied by when they are written.
+template <typename T>
+constexpr float kUnit = T::bf ? 4096.f : 1.f;
+
 // The four words (8 values 16 + c) of one word of codes.
 template <typename T>
 struct Unpack {
-    const uint32_t mask, base;  // bfloat16: 16 + c = 0x4180 | c << 3; float16: 0x4C00 | c << 6
+    const uint32_t mask, base;  // bfloat16: (16 + c) 2^-12 = 0x3B80 | c << 3; float16: 16 + c = 0x4C00 | c << 6
     __device__ __forceinline__ Unpack()
-        : mask(scalar_constant(T::bf ? 0x00780078u : 0x03C003C0u)), base(vector_constant(T::bf ? 0x41804180u : 0x4C004C00u)) {}
+        : mask(scalar_constant(T::bf ? 0x00780078u : 0x03C003C0u)), base(vector_constant(T::bf ? 0x3B803B80u : 0x4C004C00u)) {}
     __device__ __forceinline__ u32x4v operator()(uint32_t w) const {
         if (T::bf)
             return u32x4v{(w >> 3 & mask) | base, (w >> 7 & mask) | base, (w << 1 & mask) | base,

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256) void quant_decode_kernel(QuantArgs a, uint16_t
         for (int j = 0; j < 8; ++j) {
             const int64_t k = (int64_t)u * kQuantUnit + 32 * s + 8 * (lane >> 4) + j;
             const uint32_t p = v[j / 2];
-            const float c = (j & 1 ? T::high(p) : T::low(p)) - (16.f + (float)(x >> 16));
+            const float c = (j & 1 ? T::high(p) : T::low(p)) * kUnit<T> - (16.f + (float)(x >> 16));
             if (k < a.K) w[row * a.K + k] = (uint16_t)T::pack(c * T::low(x & 0xFFFFu), 0.f);
         }
     }

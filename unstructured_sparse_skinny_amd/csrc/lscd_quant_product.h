@@ -11,7 +11,8 @@ constexpr int kQuantThreads = 64 * kQuantWaves;
 
 template <typename T>
 __device__ __forceinline__ u32x4v ones_of() {
-    const uint32_t w = T::bf ? 0x3F803F80u : 0x3C003C00u;
+    static_assert(T::bf, "float16 needs no sums of x");
+    const uint32_t w = 0x39803980u;  // 2^-12
     return u32x4v{w, w, w, w};
 }
 
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
         for (int p = 0; p < A::kPer; ++p) {
             constexpr int kSteps = 4 / A::kPer;
             f32x4v sx = none;
-            if (T::bf)
+            if constexpr (T::bf)
 #pragma unroll
                 for (int s = kSteps * p; s < kSteps * (p + 1); ++s) sx = T::mfma16(x[s], ones_of<T>(), sx);
 #pragma unroll
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_few_kernel(QuantArgs a
 #pragma unroll
         for (int w = 0; w < kQuantWaves; ++w) v += sh[w][n][m];
         if (a.splits == 1)
-            a.y[n * a.ldy + row] = (uint16_t)T::pack(v, 0.f);
+            a.y[n * a.ldy + row] = (uint16_t)T::pack(v * kUnit<T>, 0.f);
         else
             a.part[((int64_t)blockIdx.y * a.N + n) * a.M + row] = v;
     }
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs 
             if (s < 3) read(s + 1);
             __builtin_amdgcn_sched_barrier(kFreeOrder);
             const bool first = s % kSteps == 0;
-            if (T::bf)
+            if constexpr (T::bf)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) sx[n] = T::mfma16(x[s & 1][n], ones_of<T>(), first ? none : sx[n]);
 #pragma unroll
@@ -317,7 +318,7 @@ __global__ __launch_bounds__(kQuantThreads, 2) void quant_many_kernel(QuantArgs 
                 const int t = 16 * n + 4 * g + e;
                 if (t >= a.N) continue;
                 if (a.splits == 1)
-                    a.y[t * a.ldy + row] = (uint16_t)T::pack(v[e], 0.f);
+                    a.y[t * a.ldy + row] = (uint16_t)T::pack(v[e] * kUnit<T>, 0.f);
                 else
                     a.part[((int64_t)blockIdx.y * a.N + t) * a.M + row] = v[e];
             }
@@ -332,7 +333,7 @@ __global__ __launch_bounds__(256) void quant_join_kernel(QuantArgs a) {
     if (i >= total) return;
     float v = 0.f;
     for (int s = 0; s < a.splits; ++s) v += a.part[s * total + i];
-    a.y[i / a.M * a.ldy + i % a.M] = (uint16_t)T::pack(v, 0.f);
+    a.y[i / a.M * a.ldy + i % a.M] = (uint16_t)T::pack(v * kUnit<T>, 0.f);
 }
 
 template <typename T, int KIND, int NT>
