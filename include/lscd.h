@@ -456,7 +456,9 @@ typedef struct {
  *          aligned; k_stride, v_stride elements (a multiple of 8) from one token to the next, so
  *          that slices of a fused product's output can be passed.
  *   slots  device, T slot numbers.  A token whose number is negative or past the cache is not
- *          written (padding).  Two tokens in one slot leave either's values, head by head.
+ *          written (padding).  The others have to differ: what a slot holds that one call names twice is
+ *          undefined (codes and scales are separate stores of whichever wavefronts have its tokens, and
+ *          may be of different tokens).  All other slots are as they should be.
  *   E4M3:  per token and head, scale = 2^e with the least e >= -126 such that max |x| <= 448 * 2^e
  *          over the finite values (1 where all are zero), code = x / 2^e rounded to the nearest
  *          e4m3 value, ties to even: the only rounding.  Infinities and NaN are stored as NaN.

@@ -536,7 +536,8 @@ def _same_type(a, b, name):
 
 
 def lscd_cache_write(cache: Cache, k, v, slots, stream=None):
-    """Write the tokens' keys and values (k, v [T][heads][head_dim]) into slots (int32 [T]; negative: none)."""
+    """Write the tokens' keys and values (k, v [T][heads][head_dim]) into slots (int32 [T], all different;
+    negative: none)."""
     pk, sk = _rows(k, "k", cache.heads, cache.head_dim, cache.device)
     pv, sv = _rows(v, "v", cache.heads, cache.head_dim, cache.device)
     T = slots.shape[0]

@@ -75,7 +75,8 @@ __device__ __forceinline__ u32x2v quantise(u32x4v x, float* scale) {
     return codes;
 }
 
-// blockIdx.x: 256 / LANES tokens, blockIdx.y: HEADS heads, blockIdx.z: keys or values.
+// blockIdx.x: 256 / LANES tokens, blockIdx.y: HEADS heads, blockIdx.z: keys or values.  Nothing orders the
+// stores of one token against another's: no two may have one slot.
 template <typename T, bool E4M3, int LANES, int HEADS>
 __global__ __launch_bounds__(kMoveThreads) void cache_write_kernel(CacheMoveArgs a) {
     constexpr int kGroups = kMoveThreads / LANES;
