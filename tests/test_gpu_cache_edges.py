@@ -32,3 +32,26 @@ def test_a_slot_named_twice_leaves_the_others(dim):
         codes, scales = expect_write((x if i == 0 else -x).cpu().double().numpy(), slots, before[i], before[2 + i], page)
         assert np.array_equal(host(c[i]).transpose(0, 2, 1, 3)[once], codes.transpose(0, 2, 1, 3)[once])
         assert np.array_equal(host(c[2 + i]).transpose(0, 2, 1)[once], scales.transpose(0, 2, 1)[once])
+
+
+@pytest.mark.parametrize("T", [2 ** 28 + 40, 2 ** 29 + 40])
+def test_more_tokens_than_a_launch_takes(T):
+    """The last tokens of a call of more than 2^28 and 2^29 are written and read like the first."""
+    say("many tokens", T)
+    c = [torch.zeros((3, 1, 16, 16), dtype=torch.float16, device="cuda") for _ in range(2)]
+    cache = L.Cache(*c)
+    x = torch.empty((T, 1, 16), dtype=torch.float16, device="cuda")
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    at = [0, 2 ** 28 - 1, 2 ** 28, T // 2, T - 2, T - 1]
+    for i, t in enumerate(at):
+        x[t], slots[t] = i + 1, 5 * i
+    L.lscd_cache_write(cache, x, x, slots)
+    want = torch.zeros((48,))
+    want[torch.arange(len(at)) * 5] = torch.arange(len(at)) + 1.0
+    for k in c:
+        assert torch.equal(k.cpu().float(), want.view(3, 1, 16, 1).expand(3, 1, 16, 16))
+    x.fill_(7)
+    L.lscd_cache_read(cache, slots, x, x)
+    for i, t in enumerate(at):
+        assert (x[t] == i + 1).all()
+    assert (x[T - 3] == 0).all() and (x[1] == 0).all()

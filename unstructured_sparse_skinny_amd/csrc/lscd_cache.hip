@@ -157,16 +157,28 @@ __global__ __launch_bounds__(kMoveThreads) void cache_read_kernel(CacheMoveArgs 
 }
 
 template <bool WRITE, typename T, bool E4M3, int LANES>
-hipError_t move_lanes(const CacheMoveArgs& a, hipStream_t s) {
+hipError_t move_lanes(CacheMoveArgs a, hipStream_t s) {
     constexpr int kGroups = kMoveThreads / LANES;
-    // four heads per thread keep four accesses in flight
-    const int64_t bx = (a.T + kGroups - 1) / kGroups;
-    const dim3 grid((unsigned)bx, (unsigned)((a.c.heads + 3) / 4), 2);
-    if (WRITE)
-        cache_write_kernel<T, E4M3, LANES, 4><<<grid, kMoveThreads, 0, s>>>(a);
-    else
-        cache_read_kernel<T, E4M3, LANES, 4><<<grid, kMoveThreads, 0, s>>>(a);
-    return hipGetLastError();
+    // (a dimension of a grid has fewer than 2^32 threads; more are cut off without an error)
+    constexpr int64_t kMost = ((int64_t)1 << 31) / kMoveThreads * kGroups;
+    for (int64_t left = a.T; left > 0; left -= kMost) {
+        a.T = left < kMost ? left : kMost;
+        // four heads per thread keep four accesses in flight
+        const dim3 grid((unsigned)((a.T + kGroups - 1) / kGroups), (unsigned)((a.c.heads + 3) / 4), 2);
+        if (WRITE)
+            cache_write_kernel<T, E4M3, LANES, 4><<<grid, kMoveThreads, 0, s>>>(a);
+        else
+            cache_read_kernel<T, E4M3, LANES, 4><<<grid, kMoveThreads, 0, s>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.slots += kMost;
+        for (int z = 0; z < 2; ++z)
+            if (WRITE)
+                a.in[z] = (const uint16_t*)a.in[z] + kMost * a.stride[z];
+            else
+                a.out[z] = (uint16_t*)a.out[z] + kMost * a.stride[z];
+    }
+    return hipSuccess;
 }
 
 template <bool WRITE, typename T>
