@@ -403,7 +403,8 @@ typedef enum {
  *   scales  device, [M][ceil(K / group)] values of `type` (LSCD_F16 or LSCD_BF16), the type of the
  *           products' x and y too.
  *   zeros   device, [M][ceil(K / group)] bytes 0..15 (the low four bits count), or NULL: 8 throughout.
- *   group   32, 64 or a multiple of 128; M up to 2^30, K up to 2^24 (NOT_SUPPORTED otherwise).
+ *   group   32, 64 or a multiple of 128; M up to 2^25, K up to 2^24, M * K (rows rounded up to 16, columns
+ *           to 512) below 2^37 (NOT_SUPPORTED otherwise).
  *   The handle owns its copy (M * K / 2 bytes, rows rounded up to 16 and columns to 128, and the
  *   scales) and a workspace for products split along K; the arrays are not needed afterwards.
  *

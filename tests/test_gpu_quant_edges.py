@@ -34,3 +34,24 @@ def test_bfloat16_range(N, group, zeros, power):
     L.lscd_quant_linear(h, x, y)
     want = torch.from_numpy(x.cpu().double().numpy() @ (c * s).T).bfloat16()
     assert torch.isfinite(want).all() and torch.equal(y.cpu(), want)
+
+
+def test_most_rows():
+    """As many rows as are supported, every one of them right; one more is refused."""
+    say("quant most rows")
+    M, K = 2 ** 25, 3
+    g = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (M + 1, 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.ones((M + 1, 1), dtype=torch.float16, device="cuda")
+    with pytest.raises(L.LSCDError) as e:
+        L.lscd_quant_encode(codes, scales, K)
+    assert e.value.status == L.LSCD_ERROR_NOT_SUPPORTED
+    h = L.lscd_quant_encode(codes[:M], scales[:M], K)
+    w = (torch.stack([codes[:M] & 15, codes[:M] >> 4], 2).flatten(1)[:, :K].half() - 8)
+    got = torch.full((M, K), 99.0, dtype=torch.float16, device="cuda")
+    assert torch.equal(L.lscd_quant_decode(h, got), w)
+    x = torch.tensor([[1.0, 2.0, -3.0], [5.0, 0.0, 1.0]], dtype=torch.float16, device="cuda")
+    y = torch.full((2, M), 99.0, dtype=torch.float16, device="cuda")
+    L.lscd_quant_linear(h, x, y)
+    for n in range(2):
+        assert torch.equal(y[n], sum(w[:, k] * x[n, k] for k in range(K)))

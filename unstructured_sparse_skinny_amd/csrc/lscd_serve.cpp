@@ -93,8 +93,11 @@ lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void
     if (!codes || !aligned(scales, 2) || M < 1 || K < 1 || group < 1 || row_bytes < (K + 1) / 2 ||
         (type != LSCD_F16 && type != LSCD_BF16))
         return LSCD_ERROR_INVALID_VALUE;
-    if (M > ((int64_t)1 << 30) || K > ((int64_t)1 << 24)) return LSCD_ERROR_NOT_SUPPORTED;
+    if (M > lscd::kQuantMostRows || K > ((int64_t)1 << 24)) return LSCD_ERROR_NOT_SUPPORTED;
     if (group < 32 || (group < 128 ? group != 32 && group != 64 : group % 128)) return LSCD_ERROR_NOT_SUPPORTED;
+    const int32_t tiles = (int32_t)((M + lscd::kQuantRows - 1) / lscd::kQuantRows);
+    const int32_t units = (int32_t)((K + lscd::kQuantUnit - 1) / lscd::kQuantUnit);
+    if ((int64_t)tiles * ((units + 3) / 4) >= ((int64_t)1 << 24)) return LSCD_ERROR_NOT_SUPPORTED;  // (encoded by 256 threads each)
     lscd_quant_s* h = new (std::nothrow) lscd_quant_s();
     if (!h) return LSCD_ERROR_OUT_OF_MEMORY;
     int cus = 0;
@@ -110,13 +113,8 @@ lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void
     h->group = group;
     h->type = type;
     h->per_unit = group >= 128 ? 1 : 128 / group;
-    h->tiles = (int32_t)((M + lscd::kQuantRows - 1) / lscd::kQuantRows);
-    h->units = (int32_t)((K + lscd::kQuantUnit - 1) / lscd::kQuantUnit);
-    const int64_t blocks = (int64_t)h->tiles * ((h->units + 3) / 4);
-    if (blocks >= ((int64_t)1 << 31)) {
-        free_quant(h);
-        return LSCD_ERROR_NOT_SUPPORTED;
-    }
+    h->tiles = tiles;
+    h->units = units;
     h->kind = lscd::quant_kind(h->per_unit, zeros != nullptr);
     // (every number of tokens has its own plan: fewer may split K further and need more room)
     for (int n = 1; n <= lscd::kQuantMaxTokens; ++n) {
@@ -124,9 +122,9 @@ lscd_status_t lscd_quant_encode(const void* codes, int64_t row_bytes, const void
         if (p.splits > 1) h->part_floats = std::max(h->part_floats, (int64_t)p.splits * M * n);
     }
     lscd::QuantEncodeArgs a = {};
-    const int64_t units = (int64_t)h->tiles * h->units;
-    if ((e = hipMalloc((void**)&h->codes, (size_t)units * 1024)) == hipSuccess &&
-        (e = hipMalloc((void**)&h->aux, (size_t)units * 16 * lscd::quant_aux_bytes(h->kind))) == hipSuccess &&
+    const int64_t total = (int64_t)tiles * units;
+    if ((e = hipMalloc((void**)&h->codes, (size_t)total * 1024)) == hipSuccess &&
+        (e = hipMalloc((void**)&h->aux, (size_t)total * 16 * lscd::quant_aux_bytes(h->kind))) == hipSuccess &&
         (!h->part_floats || (e = hipMalloc((void**)&h->part, (size_t)h->part_floats * 4)) == hipSuccess)) {
         a.q = (const uint8_t*)codes;
         a.scales = (const uint16_t*)scales;

@@ -65,6 +65,9 @@ hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStrea
 constexpr int kQuantUnit = 128;
 constexpr int kQuantRows = 16;
 constexpr int kQuantMaxTokens = 64;  // tokens of one launch
+// A dimension of a grid has fewer than 2^32 threads (more are cut off without an error): 512 per row tile in
+// the products, one per result where K was split.
+constexpr int64_t kQuantMostRows = (int64_t)1 << 25;
 constexpr int kQuantWaves = 8;
 
 // Position of bit `bit` (0..3) of code j (0..7) in its word: pair p = j / 2 of codes (low and high
