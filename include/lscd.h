@@ -509,16 +509,18 @@ lscd_status_t lscd_attention_destroy(lscd_attention_t h);
  *   cache   of the handle's heads and head_dim; of `type` or LSCD_E4M3.
  * Lengths stay on the device: the call neither waits nor copies, and can be captured into a graph
  * and replayed with other lengths.  Array contents outside these rules are clamped (tokens to T,
- * lengths to the table, pages to the pool), so that no call reads or writes out of bounds.
+ * lengths to the table, pages to the pool), so that no call reads or writes out of bounds; starts that do
+ * not ascend leave the rows of o undefined.
  * Scores, softmax and sums are fp32; the softmax weights are rounded once to `type` for the second
  * product.  An E4M3 cache's values reach the products in `type`: exact inside its normal range; past its
  * largest value (65504 in float16) they count as that, below its normal range they are rounded to its
  * subnormals.  Results do not depend on timing (partial sums are added in a fixed order) but their
  * last bits may depend on the other sequences in the call, which move the points where work is split.
  * INVALID_VALUE: null pointers, misalignment, negative sizes, a scale that is not finite, wrong
- * device.  NOT_SUPPORTED: T * (q_heads / kv_heads) or table_pages * page_size above 2^30, more than
- * 2^31 stretches of 32 positions over all key heads and tiles of 16 query rows if every sequence filled
- * its table, types that do not fit together.
+ * device.  NOT_SUPPORTED: T * (q_heads / kv_heads) or table_pages * page_size above 2^30; about 2^31 and
+ * more units of work if every sequence filled its table (per key head, 128 positions by 16 query rows, or
+ * from 16 rows a sequence on 256 rows by 128 positions, 64 for heads above 64 channels, 32 above 128);
+ * types that do not fit together.
  */
 lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, const void* q, int64_t q_stride,
                              const int32_t* start, const int32_t* length, const int32_t* table, int64_t table_stride,

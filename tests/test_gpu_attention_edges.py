@@ -117,3 +117,38 @@ def test_codes_past_the_largest_value(kind, n, length):
     u = sv.ROUNDOFF[kind]
     e = 2 * (64 + 8) * 2.0 ** -24 * big[..., None] + 2 * 64 ** -0.5 * 2 * u + 2.0 ** -18
     assert (np.abs(got - o) <= u * np.abs(o) + (2 * u + e) * a + sv.TINY[kind]).all()
+
+
+def test_wide_tables_are_served():
+    """Tables with room for 2^30 positions, of which few are used, and the most work that is counted in advance."""
+    say("wide tables")
+    for n, heads in ((64, 16), (1, 16), (1, 200)):
+        b = Batch([(n, 200)], heads, heads, 16, 1024, "f16", "f16", seed=heads)
+        table = torch.zeros((1, 2 ** 20), dtype=torch.int32, device="cuda")
+        table[:, :b.table.shape[1]] = b.table
+        b.check(b.run())
+        b.table = table
+        b.check(b.run())
+    b = Batch([(1, 200)], 512, 512, 16, 1024, "f16", "f16")
+    b.table = table
+    with pytest.raises(L.LSCDError) as e:
+        b.run()
+    assert e.value.status == L.LSCD_ERROR_NOT_SUPPORTED
+
+
+def test_starts_that_do_not_ascend():
+    """Sequences that name the same tokens again and again, with more work than 31 bits count: the call ends, writes
+    nothing outside its rows, and the next one is right."""
+    say("starts that do not ascend")
+    T, S, pages = 4096, 4096, 1024
+    b = Batch([(T, 5000)], 16, 16, 16, 1024, "f16", "f16", seed=2)
+    clean = b.run()
+    start, length, table = b.start, b.length, b.table
+    b.start = torch.tensor([0, T] * (S // 2) + [0], dtype=torch.int32, device="cuda")
+    b.length = torch.full((S,), 2 ** 30, dtype=torch.int32, device="cuda")
+    b.table = torch.zeros((S, pages), dtype=torch.int32, device="cuda")
+    wide = torch.full((T + 2, 16, 16), 3.0, dtype=torch.float16, device="cuda")
+    b.run(out=wide[1:-1])
+    assert (wide[0] == 3).all() and (wide[-1] == 3).all()
+    b.start, b.length, b.table = start, length, table
+    assert torch.equal(b.run(), clean)

@@ -115,6 +115,9 @@ struct Work {
     int seq, head, tile, unit;
     Seq q;
 };
+// The caller sees to it that sequences which share no token have fewer slots than this.  Starts that do not
+// ascend may make them more: sums saturate, and all workgroups leave.
+constexpr int kMostSlots = 0x7FFFFFFF;
 // Works it out (every wavefront for itself, 64 sequences at a time).  False: there is nothing to do.
 template <int ROWS, int TOKENS, bool FEW>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int lane, int me, int G, Work* w) {
@@ -126,7 +129,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lane, int me, i
     auto scan = [&](int x) {  // inclusive sums over the lanes
         for (int d = 1; d < 64; d <<= 1) {
             const int up = __shfl_up(x, d, 64);
-            if (lane >= d) x += up;
+            if (lane >= d) x = __builtin_elementwise_add_sat(x, up);
         }
         return x;
     };
@@ -135,8 +138,9 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int lane, int me, i
     int U = __builtin_amdgcn_readlane(sum, 63);
     for (int s0 = 64; s0 < a.sequences; s0 += 64) {
         Seq other = {};
-        U += __builtin_amdgcn_readlane(scan(slots_of(s0 + lane, &other) * a.c.heads), 63);
+        U = __builtin_elementwise_add_sat(U, __builtin_amdgcn_readlane(scan(slots_of(s0 + lane, &other) * a.c.heads), 63));
     }
+    if (U == kMostSlots) return false;
     w->cut = Cut(U, G);
     w->u = w->cut.begin(me);
     w->end = w->cut.begin(me + 1);

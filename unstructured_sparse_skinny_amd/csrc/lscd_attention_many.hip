@@ -489,6 +489,7 @@ hipError_t many_dim(const AttnArgs& a, int grid, hipStream_t s) {
 }  // namespace
 
 int attention_many_grid(int cus) { return cus < 64 * kJoinMasks ? cus : 64 * kJoinMasks; }
+int attention_many_tokens(int dim) { return many_tokens(dim <= 64 ? 64 : dim <= 128 ? 128 : 256); }
 int64_t attention_many_floats(int dim) {
     return (int64_t)kManyRows * ((dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : 256) + 2);
 }

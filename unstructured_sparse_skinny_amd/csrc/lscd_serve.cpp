@@ -315,10 +315,16 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
         const double items = ((double)(T * share) / tile + sequences) * h->kv_heads, units = ceil((double)span / tokens);
         return (int)std::min<double>(most, items * std::min(units, 1.0 + ceil(sqrt(ratio * units))));
     };
-    // (slots of work are counted in 32 bits on the device)
-    if ((double)(T * share / lscd::kFewRows + sequences) * ((double)span / 32 + 2) * h->kv_heads >= 2147483648.0)
+    // Slots of work are counted in 31 bits on the device: a row tile has one for each stretch of positions and
+    // two more at most.
+    const bool few = sequences > 1 || !both;
+    auto too_many = [&](int64_t tiles, int tokens) {
+        return (double)(tiles + sequences) * (double)(span / tokens + 2) * h->kv_heads >= 2147483647.0;
+    };
+    if ((few && too_many(both ? 0 : T * share / lscd::kFewRows, lscd::kFewTokens)) ||
+        (both && too_many(T * share / lscd::kManyRows, lscd::attention_many_tokens(h->head_dim))))
         return LSCD_ERROR_NOT_SUPPORTED;
-    if (sequences > 1 || !both) {
+    if (few) {
         hipError_t e = lscd::launch_attention_few(
             a, type, grid(lscd::attention_few_grid(h->cus), lscd::kFewRows, lscd::kFewTokens, 20.0 / rows), (hipStream_t)stream);
         if (e != hipSuccess) return status_of(e);

@@ -50,6 +50,7 @@ struct AttnArgs {
 // Workgroups of one launch at most, and floats of one partial result.
 int attention_few_grid(int cus);
 int attention_many_grid(int cus);
+int attention_many_tokens(int dim);  // positions of one of the many-row kernel's work units
 int64_t attention_few_floats(int dim);
 int64_t attention_many_floats(int dim);
 hipError_t launch_attention_few(const AttnArgs& a, int type, int grid, hipStream_t s);
