@@ -120,7 +120,7 @@ struct Few {
 
     // Whether some key's or value's code times its scale may pass the type's largest value.  (Scales are
     // positive: they compare as whole numbers.)
-    __device__ __forceinline__ bool top_keys(int h) const { return E4M3 && __any(ks[h] >= T::kTopScale); }
+    __device__ __forceinline__ bool top_keys() const { return E4M3 && __any(max(ks[0], ks[1]) >= T::kTopScale); }
     __device__ __forceinline__ bool top_values() const {
         if (!E4M3) return false;
         uint32_t most = vs[0];
@@ -393,15 +393,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             s[h] = f32x4v{0.f, 0.f, 0.f, 0.f};
-            auto score = [&](auto top) {
 #pragma unroll
-                for (int st = 0; st < F::kSteps; ++st)
-                    s[h] = T::mfma16(f.template key_operand<decltype(top)::value>(h, st), qr[st], s[h]);
-            };
-            if (f.top_keys(h))
-                score(std::true_type{});
-            else
-                score(std::false_type{});
+            for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(f.template key_operand<false>(h, st), qr[st], s[h]);
+        }
+        if (f.top_keys()) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s[h] = f32x4v{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(f.template key_operand<true>(h, st), qr[st], s[h]);
+            }
         }
         f.load_keys(a, hb, e, nt, next_high, lane);
         float x[8];
@@ -437,11 +438,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             l = T::add_pair(pb[i], l);  // (as they are multiplied: a mean of equal values is that value)
         }
         bool odd = false;  // an infinity or NaN that some row may not see, or a code past the largest value
-        if (masked) {
+        if (masked || f.top_values()) {
             f.mask_scales(t0, low, high, lane);
             odd = __any(f.any_odd());
         }
-        odd = odd || f.top_values();
         if (!odd) {
 #pragma unroll
             for (int w = 0; w < VW / 2; ++w) {
