@@ -152,3 +152,22 @@ def test_starts_that_do_not_ascend():
     assert (wide[0] == 3).all() and (wide[-1] == 3).all()
     b.start, b.length, b.table = start, length, table
     assert torch.equal(b.run(), clean)
+
+
+def test_strides_of_single_elements_do_not_count():
+    """One sequence's length, one slot and a table of one column may have any stride there."""
+    say("strides of single elements")
+    b = Batch([(1, 10)], 4, 2, 64, 16, "f16", "f16", seed=4)
+    want = b.run()
+    b.length = torch.tensor([10, 99, 99], dtype=torch.int32, device="cuda")[::2][:1]
+    b.table = torch.stack([b.table[:, 0], b.table[:, 0] + 1], 1)[:, ::2]
+    assert torch.equal(b.run(), want)
+    slot = torch.tensor([3, 99, 99], dtype=torch.int32, device="cuda")[::2][:1]
+    k, v = (torch.randn((1, 2, 64), device="cuda").half() for _ in range(2))
+    L.lscd_cache_write(b.cache(), k, v, slot)
+    out = [torch.empty_like(k) for _ in range(2)]
+    L.lscd_cache_read(b.cache(), slot, *out)
+    assert torch.equal(out[0], k) and torch.equal(out[1], v)
+    for t in (torch.arange(4, dtype=torch.int32, device="cuda")[::2], torch.zeros((1, 4), dtype=torch.int32, device="cuda")[:, ::2]):
+        with pytest.raises(ValueError):
+            L._ints(t, "t", t.device, t.dim())

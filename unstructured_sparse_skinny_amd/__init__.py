@@ -524,7 +524,7 @@ def _rows(t, name, heads, dim, device):
 
 
 def _ints(t, name, device, dim=1):
-    if t.dtype != torch.int32 or t.dim() != dim or t.device != device or (t.numel() and t.stride(-1) != 1):
+    if t.dtype != torch.int32 or t.dim() != dim or t.device != device or (t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} must be an int32 tensor of {dim} dimension(s) on the cache's device, last one contiguous")
     return t.data_ptr()
 
