@@ -382,7 +382,8 @@ lscd_status_t lscd_destroy(lscd_handle_t h);
 const char* lscd_status_string(lscd_status_t s);
 
 /* ====================================================================================
- * Serving operators: what stands next to the skinny products in a decoder layer.
+ * Serving operators: what stands next to the skinny products in a decoder layer.  All arrays are
+ * on the current device.
  * Types of activations, weights' scales and cached values.
  * ==================================================================================== */
 typedef enum {

@@ -22,3 +22,14 @@ def encode(M, K, group=128, row_bytes=None):
 def test_largest_matrices(M, K, ok):
     """A grid has fewer than 2^32 threads in a dimension: sizes whose launches would pass that are refused."""
     assert encode(M, K) == (L.LSCD_ERROR_HIP if ok else L.LSCD_ERROR_NOT_SUPPORTED)
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """Every call of the Python layer asks for its stream with its tensors' device."""
+    monkeypatch.setattr(L, "_current_device", lambda: 0)
+    monkeypatch.setattr(L, "_current_raw_stream", lambda index: 70 + index)
+    here, other = L.torch.device("cuda", 0), L.torch.device("cuda", 1)
+    assert L._stream_on(None, here) == 70 and L._stream_on(5, here) == 5
+    for stream in (None, 5):
+        with pytest.raises(ValueError, match="current device"):
+            L._stream_on(stream, other)

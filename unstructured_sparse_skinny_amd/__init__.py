@@ -412,10 +412,14 @@ def lscd_destroy(h: Handle):
 # ---------------------------------------------------------------- serving operators
 
 _current_raw_stream = torch._C._cuda_getCurrentRawStream  # (torch.cuda.current_stream() builds an object: 3 us)
+_current_device = torch._C._cuda_getDevice
 
 
 def _stream_on(stream, device):
-    """The given stream's handle, or that of the device's current one."""
+    """The given stream's handle, or that of the device's current one.  The library works on the current device:
+    tensors of another are refused here, before a kernel of this one would read them."""
+    if device.index != _current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{_current_device()}")
     if stream is None:
         return _current_raw_stream(device.index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
