@@ -43,8 +43,8 @@ struct Many {
     // 16-byte loads: lanes per row (a power of two that covers DP), rows per pass, passes
     static constexpr int kPer = DP <= 64 ? (E4M3 ? 4 : 8) : DP <= 128 ? (E4M3 ? 8 : 16) : (E4M3 ? 16 : 32);
     static constexpr int kPassRows = kManyThreads / kPer;
-    static constexpr int kPasses = kTokens < kPassRows ? 1 : kTokens / kPassRows;
-    static constexpr bool kSpare = kTokens < kPassRows;  // some threads have no row
+    static constexpr int kPasses = kTokens / kPassRows;
+    static_assert(kTokens % kPassRows == 0, "every thread has a row in every pass");
     static_assert(64 / kPer <= 16, "a wavefront's rows of one pass lie in one page");
 
     __device__ static __forceinline__ int key_at(int row, int chunk) {
@@ -73,7 +73,7 @@ struct Many {
         for (int i = 0; i < kPasses; ++i) {
             const int t = t0 + row_of(i, tid), row = t & (a.c.page_size - 1);
             const uint32_t p = page_of(a, entry[i]);
-            const bool on = t < high && t >= low && (!kSpare || row_of(i, tid) < kTokens);
+            const bool on = t < high && t >= low;
             const int at = on && d < D ? (row * D + d) * width : kNoRow;
             k[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.keys(p), at, 0, 0);
             v[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.values(p), at, 0, 0);
@@ -92,7 +92,6 @@ struct Many {
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int row = row_of(i, tid);
-            if (kSpare && row >= kTokens) continue;
             if (DP == 96 && c >= DP / (E4M3 ? 16 : 8)) continue;
             const bool top = E4M3 && __any(max(__builtin_bit_cast(uint32_t, ks[i]), __builtin_bit_cast(uint32_t, vs[i])) >= T::kTopScale);
 #pragma unroll
