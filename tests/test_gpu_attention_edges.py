@@ -171,3 +171,78 @@ def test_strides_of_single_elements_do_not_count():
     for t in (torch.arange(4, dtype=torch.int32, device="cuda")[::2], torch.zeros((1, 4), dtype=torch.int32, device="cuda")[:, ::2]):
         with pytest.raises(ValueError):
             L._ints(t, "t", t.device, t.dim())
+
+
+def test_contents_out_of_range_are_those_of_the_nearest_range():
+    """Lengths past the table, negative ones, pages outside the pool, starts outside the tokens: the result of the
+    clamped arrays, and nothing written beside the output's rows."""
+    say("clamped contents, compared")
+    for n, dim in ((1, 64), (50, 64), (50, 256)):
+        b = Batch([(n, 60), (n, 30), (n, 17)], 4, 2, dim, 16, "f16", "f16", seed=3)
+        wide = torch.full((b.T + 2, 4, dim), 3.0, dtype=torch.float16, device="cuda")
+        keep = b.start.clone(), b.length.clone(), b.table.clone()
+        b.length[0], b.length[2] = 2 ** 31 - 1, -5
+        b.table[0, -1], b.table[1, 0], b.table[1, 1] = -2 ** 31, 2 ** 31 - 1, b.pages
+        b.start[0], b.start[3] = -7, 2 ** 31 - 1
+        b.run(out=wide[1:-1])
+        b.start, b.length, b.table = (x.clone() for x in keep)
+        b.length[0], b.length[2] = b.table.shape[1] * 16, 0
+        b.table[0, b.table[0] < 0] = 0
+        b.table[1, 0], b.table[1, 1] = 0, 0
+        assert torch.equal(wide[1:-1], b.run())
+        assert (wide[0] == 3).all() and (wide[-1] == 3).all()
+
+
+@pytest.mark.parametrize("kind,cache", [("f16", "e4m3"), ("bf16", "bf16")])
+@pytest.mark.parametrize("heads,kv,dim", [(2, 2, 16), (6, 3, 32), (2, 1, 48), (4, 2, 96), (2, 2, 112), (2, 1, 144), (3, 1, 192),
+                                          (2, 2, 240), (8, 1, 256)])
+def test_head_sizes(heads, kv, dim, kind, cache):
+    """Sizes between those of the other tests, decoding and in chunks."""
+    say("head sizes", heads, kv, dim, kind, cache)
+    for seqs in ([(1, 300), (2, 77), (1, 1)], [(70, 200), (0, 9), (33, 33), (1, 150)]):
+        b = Batch(seqs, heads, kv, dim, 16, kind, cache, seed=dim)
+        b.check(b.run())
+        b.check(b.run(window=50), window=50)
+
+
+@pytest.mark.parametrize("kind,cache", [("f16", "f16"), ("bf16", "e4m3")])
+def test_many_sequences_of_both_kinds(kind, cache):
+    """More than 64 sequences, those of few rows and of many among each other and in every block of 64."""
+    say("many sequences", kind, cache)
+    rng = np.random.default_rng(5)
+    new = rng.choice([0, 1, 1, 3, 9, 20, 40, 70], 150)
+    seqs = [(int(n), int(n + rng.integers(0, 90))) for n in new]
+    seqs[10] = (1, 2500)
+    seqs[140] = (40, 2000)
+    b = Batch(seqs, 4, 2, 64, 16, kind, cache, seed=6)
+    out = b.run()
+    b.check(out)
+    for _ in range(2):
+        assert torch.equal(b.run(), out)
+    only = Batch([(max(20, n), length + 20) for n, length in seqs], 4, 2, 64, 16, kind, cache, seed=7)
+    only.check(only.run(window=33), window=33)
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,length", [(1, 33000), (1, 131072), (8, 70000)])
+def test_an_item_of_many_parts(kind, heads, length):
+    """One sequence whose positions go to more workgroups (74, 145 and 39) than are joined at a time, its scores
+    climbing so that every batch of parts rescales those before it."""
+    say("an item of many parts", kind, heads, length)
+    b = Batch([(1, length)], heads, 1, 64, 1024, kind, kind, seed=heads)
+    b.tensors[0].mul_(0.1)
+    pages = b.table[0, :-(-length // 1024)].long()
+    climb = (torch.arange(pages.numel() * 1024, device="cuda") * (30.0 / length)).view(-1, 1024)
+    b.tensors[0][pages, 0, :, 0] = climb.to(b.q.dtype)
+    b.q[:, :, 0] = 8.0
+    out = b.run()
+    q, k, v = b.q[0].double().cpu(), torch.from_numpy(b.values(0, 0))[:, 0], torch.from_numpy(b.values(1, 0))[:, 0]
+    s = (q @ k.t()) * 64 ** -0.5
+    w = torch.softmax(s, 1)
+    o, a = w @ v, w @ v.abs()
+    u, big = sv.ROUNDOFF[kind], ((q.abs() @ k.abs().t()) * 64 ** -0.5).amax(1, keepdim=True)
+    e = 2 * (64 + 8) * 2.0 ** -24 * big + 2.0 ** -18
+    small = 2.0 ** -32 * v.abs().sum(0) / torch.exp(s - s.amax(1, keepdim=True)).sum(1, keepdim=True) if kind == "f16" else 0.0
+    assert ((out[0].double().cpu() - o).abs() <= u * o.abs() + (u + e) * a + small + sv.TINY[kind]).all()
+    for _ in range(3):
+        assert torch.equal(b.run(), out)

@@ -55,3 +55,40 @@ def test_most_rows():
     L.lscd_quant_linear(h, x, y)
     for n in range(2):
         assert torch.equal(y[n], sum(w[:, k] * x[n, k] for k in range(K)))
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
+@pytest.mark.parametrize("M,K", [(300, 8192), (130, 16384), (77, 9001)])
+def test_long_sums_are_exact(M, K, group, zeros, kind):
+    """Whole x and power-of-two scales, sums of thousands of columns below 2^24 of their unit: every output is the
+    rounded result, over splits of K, pipelines of many units, every form by tokens and several launches."""
+    say("quant long sums", M, K, group, zeros, kind)
+    h, c, s, z = matrix(M, K, group, zeros, kind, M, whole=True)
+    x = torch.from_numpy(np.random.default_rng(K).integers(-2, 3, (200, K)).astype(np.float64)).to(TYPES[kind]).cuda()
+    want = torch.from_numpy(x.cpu().double().numpy() @ (c * s).T).to(TYPES[kind])
+    for N in (1, 2, 7, 16, 17, 32, 33, 64, 65, 130, 200):
+        y = torch.full((N, M), float("nan"), dtype=TYPES[kind], device="cuda")
+        L.lscd_quant_linear(h, x[:N], y)
+        assert torch.equal(y.cpu(), want[:N]), N
+
+
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("M,K,N", [(5003, 12288, 16), (2000, 16384, 64), (3000, 7168, 150)])
+def test_error_of_random_sums(M, K, N, kind):
+    """Random x and scales: the error's norm is that of y's rounding (steps of 2 u at fractions of 1 to 2: u / sqrt(3) =
+    0.58 u of a value in the mean square at most) and of fp32 sums, whose rounding errors add up like a random walk:
+    2^-24 sqrt(K + 2 G) of a typical partial sum, which is at most sqrt(2 x 47^2 / 21) of y's in bfloat16 (two sums of
+    terms of up to 47 in place of one of terms of 21 in the mean square)."""
+    say("quant error norm", M, K, N, kind)
+    g = torch.Generator(device="cuda").manual_seed(K)
+    G = K // 128
+    codes = torch.randint(0, 256, (M, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.exp(0.3 * torch.randn((M, G), generator=g, device="cuda") - 4).to(TYPES[kind])
+    x = torch.randn((N, K), generator=g, device="cuda").to(TYPES[kind])
+    y = torch.empty((N, M), dtype=TYPES[kind], device="cuda")
+    L.lscd_quant_linear(L.lscd_quant_encode(codes, scales, K), x, y)
+    w = (torch.stack([codes & 15, codes >> 4], 2).flatten(1).double() - 8) * scales.double().repeat_interleave(128, 1)
+    want = x.double() @ w.t()
+    error = float((y.double() - want).norm() / want.norm())
+    assert error < 0.58 * sv.ROUNDOFF[kind] + 2.0 ** -24 * (K + 2 * G) ** 0.5 * (2 * 47 ** 2 / 21) ** 0.5

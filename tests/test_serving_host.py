@@ -33,3 +33,29 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     for stream in (None, 5):
         with pytest.raises(ValueError, match="current device"):
             L._stream_on(stream, other)
+
+
+@pytest.mark.parametrize("bits", [11, 8])
+@pytest.mark.parametrize("M,K,group", [(300, 8192, 32), (77, 9001, 128), (130, 16384, 64)])
+def test_a_unit_left_out_shows(M, K, group, bits):
+    """The exact comparison of long sums (whole x, power-of-two scales) is sharp: with 128 columns left out of the
+    definition almost every rounded output differs, in both 16-bit types, and so does the norm bound's error."""
+    import numpy as np
+
+    from oracle import serving as sv
+    rng = np.random.default_rng(M)
+    codes = rng.integers(0, 256, (M, (K + 1) // 2)).astype(np.uint8)
+    c, s = sv.quant_weights(codes, 2.0 ** rng.integers(-2, 2, (M, -(-K // group))), None, K, group)
+    x = rng.integers(-2, 3, (5, K)).astype(np.float64)
+    whole = x @ (c * s).T
+    for u in (0, K // 256, (K - 1) // 128):
+        part = x.copy()
+        part[:, 128 * u:128 * (u + 1)] = 0
+        part = part @ (c * s).T
+
+        def rounded(v):
+            f, e = np.frexp(v)
+            return np.ldexp(np.rint(f * 2.0 ** bits), e - bits)
+
+        assert (rounded(part) != rounded(whole)).mean() > (0.9 if 128 * (u + 1) <= K else 0.5)
+        assert np.linalg.norm(part - whole) > 4 * 2.0 ** -bits * np.linalg.norm(whole)
