@@ -30,7 +30,7 @@
 // Sequences of up to 16 query rows (one MFMA tile) are bound by the reading of their keys and values and
 // go to the kernel for few rows, longer ones to the other; a call whose batch may hold both launches both.
 // (Two tiles of 16 in the kernel for few rows, 32 rows a sequence: 64 sequences of 8 key heads over 2048
-// positions 196 us against 112, one sequence over 8192 positions 27 against 23.)
+// positions 189 us against 111, one sequence over 8192 positions 33 against 23.)
 #pragma once
 
 #include "lscd_serve.h"

@@ -12,8 +12,8 @@
 // when the second product is, so that 8 to 16 KB per wavefront are always in flight; the next item's
 // first loads are issued before the present one's end.
 //
-// Measured: 64 sequences of one token over up to 2048 positions of 96 heads (e4m3, 1.72 GB) 312 us, 5.5
-// TB/s, which is what a plain read reaches here; one token over 1000 positions of 8 heads 9.4 us, a chain
+// Measured: 64 sequences of one token over up to 2048 positions of 96 heads (e4m3, 1.72 GB) 313 us, 5.5
+// TB/s, which is what a plain read reaches here; one token over 1000 positions of 8 heads 9.5 us, a chain
 // of dependent latencies (tables, keys, values, partial results, their join) rather than its 4 MB.
 
 #include <type_traits>

@@ -11,9 +11,11 @@
 // a 4 x 16 block and get its columns, which is the A operand in the token order that P has.
 // 16-byte chunks are XOR-swizzled by the row so that the lanes of one read spread over the banks.
 //
-// Measured: 2048 new tokens of 32 heads over 16384 positions (515 GFLOP) 532 to 590 us from one card to
-// the next, 870 to 970 TFLOP/s; a matrix product in bfloat16 reaches 1232.  The matrix cores are busy 41 %
-// of the cycles and the vector unit 39 %, and two wavefronts per SIMD overlap little of the two.
+// Measured: 2048 new tokens of 32 heads over 16384 positions (515 GFLOP) 521 to 590 us from one card to
+// the next, 870 to 990 TFLOP/s; a matrix product in bfloat16 reaches 1232.  The matrix cores are busy 43 %
+// of the cycles and the vector unit 40 %, and two wavefronts per SIMD overlap little of the two.  Heads of
+// 256 channels: 1024 tokens of 16 heads over 8192 positions in 473 us, 270 TFLOP/s, against 98 us and 660 for
+// 128 channels: 54 to 62 registers do not fit and go through memory in the loop.
 
 #include <type_traits>
 

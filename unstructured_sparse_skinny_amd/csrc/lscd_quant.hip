@@ -105,6 +105,7 @@ hipError_t launch_quant_decode(const QuantArgs& a, int type, int kind, uint16_t*
 // for 28672 x 7168 (1792 tiles, 7 on every CU: 23.0 us at 16 tokens, 38.2 with one), 1 for 4096 x 4096 (6.6
 // us).  More row tiles than 4 with records of four words do not fit the registers (27648 x 9216 x 16 in groups
 // of 32: 722 us with 7, 41.7 with 4); nor do 4 row tiles of 64 tokens.
+// (Of the numbers between, 5 is not built: 20480 rows, 5 tiles on every CU, take 6, by the model a seventh slower.)
 QuantPlan plan_quant(int tiles, int units, int N, int kind, int cus) {
     QuantPlan best = {N > 16, 1, 1};
     double cost = 0;

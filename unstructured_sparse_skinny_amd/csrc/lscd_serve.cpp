@@ -309,7 +309,7 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
     // Workgroups: no more per item than pay.  An item of U units over W workgroups takes U / W units and
     // then, in its last one, W parts to join: best at W = sqrt(U * unit / part), with a unit's time over a
     // part's about 20 over the query rows where they are few (eight query rows over 32768 positions: 39 us with
-    // the workgroups of one row, 29 with theirs) and 4 where they are 256.
+    // the workgroups of one row, 26 with theirs) and 4 where they are 256.
     const double rows = std::min<double>(lscd::kFewRows, ceil((double)(T * share) / sequences));
     auto grid = [&](int most, int tile, int tokens, double ratio) {
         const double items = ((double)(T * share) / tile + sequences) * h->kv_heads, units = ceil((double)span / tokens);
