@@ -389,7 +389,8 @@ const char* lscd_status_string(lscd_status_t s);
 typedef enum {
     LSCD_F16 = 0,
     LSCD_BF16 = 1,
-    LSCD_E4M3 = 2  /* 8-bit floating point, 4 significant bits, largest value 448, no infinities */
+    LSCD_E4M3 = 2, /* 8-bit floating point, 4 significant bits, largest value 448, no infinities */
+    LSCD_E2M1 = 3  /* 4-bit floating point, 2 significant bits: 0, 0.5, 1, 1.5, 2, 3, 4, 6 (codes 0..7; 8 is the sign) */
 } lscd_type_t;
 
 /*
@@ -437,6 +438,10 @@ lscd_status_t lscd_quant_destroy(lscd_quant_t h);
  *   k_scale, v_scale  LSCD_E4M3 only (NULL otherwise): [num_pages][heads][page_size] floats,
  *         16-byte aligned; a value is its code times its token's and head's scale.  Scales are
  *         positive powers of two (what lscd_cache_write writes; readers use the exponent only).
+ *   LSCD_E2M1: k, v hold two codes a byte, head_dim / 2 bytes a row, channel c in byte c / 2, the low
+ *         half for even c.  k_scale, v_scale are bytes (cast to float*): [num_pages][heads][page_size][n],
+ *         n = 2, 4 or 8 for head_dim up to 64, 128, 256, 16-byte aligned; channels 32 g .. 32 g + 31 have
+ *         the scale 2^(byte g - 127), 255 makes them NaN.  Bytes from ceil(head_dim / 32) on are not used.
  *   page_size  a power of two, 16..1024.   head_dim  a multiple of 16, 16..256.
  *   heads  1..65535.  num_pages * page_size <= 2^31 - 1 (slots are 32-bit numbers; element
  *         offsets are 64-bit throughout).
@@ -464,6 +469,8 @@ typedef struct {
  *   E4M3:  per token and head, scale = 2^e with the least e >= -126 such that max |x| <= 448 * 2^e
  *          over the finite values (1 where all are zero), code = x / 2^e rounded to the nearest
  *          e4m3 value, ties to even: the only rounding.  Infinities and NaN are stored as NaN.
+ *   E2M1:  the same per token, head and 32 channels with max |x| <= 6 * 2^e over all of them and the nearest
+ *          e2m1 value.  An infinity or NaN among them makes all of them NaN.
  *   16 bits: copied; `type` has to be the cache's (NOT_SUPPORTED otherwise).
  * T = 0 is a no-op.  Asynchronous, no allocation.
  */
@@ -473,9 +480,9 @@ lscd_status_t lscd_cache_write(const lscd_cache_t* cache, const void* k, int64_t
 /*
  * lscd_cache_read -- the values in T slots as rows of `type`: the reverse of lscd_cache_write
  * (code times scale, exact inside the type's normal range, rounded to its subnormals below and an
- * infinity above: a float16 value above 63488 is stored as 65536).  A slot number that is
- * negative or past the cache gives zeros.  Same argument rules; any slot may be read any number of
- * times.
+ * infinity above: a float16 value above 63488 is stored as 65536, in E2M1 one of 57344 and more).  A
+ * slot number that is negative or past the cache gives zeros.  Same argument rules; any slot may be read
+ * any number of times.
  */
 lscd_status_t lscd_cache_read(const lscd_cache_t* cache, const int32_t* slots, int64_t T, void* k, int64_t k_stride,
                               void* v, int64_t v_stride, int32_t type, void* stream);

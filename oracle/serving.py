@@ -48,6 +48,33 @@ def cache_scale(x):
     return 2.0 ** e
 
 
+#: magnitudes of the 4-bit codes 0..7 (8 is the sign bit)
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def e2m1_group(x):
+    """One group of channels in 4 bits: (codes, scale byte), or (None, 255) where a value is not finite."""
+    x = np.asarray(x, dtype=np.float64)
+    if not np.isfinite(x).all():
+        return None, 255
+    most, e = np.abs(x).max(), -126
+    if most == 0:
+        e = 0
+    while most > 6.0 * 2.0 ** e:
+        e += 1
+    far = np.abs(np.abs(x)[:, None] / 2.0 ** e - E2M1[None])
+    near = far == far.min(axis=1, keepdims=True)
+    code = np.array([c[-1] if len(c) == 1 or c[-1] % 2 == 0 else c[0] for c in (np.nonzero(r)[0] for r in near)])
+    return (code + 8 * np.signbit(x)).astype(np.uint8), e + 127
+
+
+def e2m1_values(codes, scales, dim):
+    """Values of packed codes [..][dim / 2] with scale bytes [..][n]: 64 bits, NaN under a scale byte of 255."""
+    c = np.stack([codes & 15, codes >> 4], axis=-1).reshape(*codes.shape[:-1], dim)
+    by = np.where(scales == 255, np.nan, 2.0 ** (scales.astype(np.float64) - 127))
+    return np.where(c > 7, -1.0, 1.0) * E2M1[c & 7] * np.repeat(by, 32, axis=-1)[..., :dim]
+
+
 def attention(q, k, v, scale, causal=True, window=0):
     """One sequence, one query head group: q [n][heads][dim], k, v [len][kv][dim] (64 bits) ->
     (o [n][heads][dim], sum_j p_j |v_j| [n][heads][dim], largest sum of |scale q k| over a row's scores [n][heads])."""

@@ -59,3 +59,15 @@ def test_a_unit_left_out_shows(M, K, group, bits):
 
         assert (rounded(part) != rounded(whole)).mean() > (0.9 if 128 * (u + 1) <= K else 0.5)
         assert np.linalg.norm(part - whole) > 4 * 2.0 ** -bits * np.linalg.norm(whole)
+
+
+def test_e2m1_codes_and_scales():
+    """The 4-bit groups' definition: the scale's steps at 6 * 2^e, ties to the even code, what is not finite."""
+    from oracle import serving as sv
+    import numpy as np
+    codes, byte = sv.e2m1_group([6.0, 5.0, 3.5, 2.5, 1.75, 1.25, 0.75, 0.25, -0.25, -5.01])
+    assert byte == 127 and codes.tolist() == [7, 6, 6, 4, 4, 2, 2, 0, 8, 15]
+    assert sv.e2m1_group([6.01])[1] == 128 and sv.e2m1_group([3.0])[1] == 126 and sv.e2m1_group([0.0])[1] == 127
+    assert sv.e2m1_group([2.0 ** -140])[1] == 1 and sv.e2m1_group([np.inf, 1.0])[1] == 255
+    packed = np.array([[[0x71, 0xF0]]], dtype=np.uint8)
+    assert sv.e2m1_values(packed, np.array([[[128, 0]]], dtype=np.uint8), 4).tolist() == [[[1.0, 12.0, 0.0, -12.0]]]

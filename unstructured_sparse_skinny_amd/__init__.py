@@ -46,7 +46,9 @@ EXPORTS = ("lscd_pack_size", "lscd_pack", "lscd_default_tile_m", "lscd_encode", 
 LSCD_F16 = 0
 LSCD_BF16 = 1
 LSCD_E4M3 = 2
-_TYPES = {torch.float16: LSCD_F16, torch.bfloat16: LSCD_BF16, torch.float8_e4m3fn: LSCD_E4M3}
+LSCD_E2M1 = 3
+#: (uint8: two e2m1 codes a byte)
+_TYPES = {torch.float16: LSCD_F16, torch.bfloat16: LSCD_BF16, torch.float8_e4m3fn: LSCD_E4M3, torch.uint8: LSCD_E2M1}
 
 
 class lscd_info_t(ctypes.Structure):
@@ -492,24 +494,36 @@ def lscd_quant_destroy(h: Quant):
     h.close()
 
 
+def cache_scale_row(head_dim: int) -> int:
+    """Scales of one head vector in a cache of 4-bit codes: one for 32 channels, rounded up to 2, 4 or 8."""
+    return 2 if head_dim <= 64 else 4 if head_dim <= 128 else 8
+
+
 class Cache:
     """A paged cache over the caller's tensors (lscd_cache_t): k, v [pages][heads][page_size][head_dim] in
-    float16, bfloat16 or float8_e4m3fn; the last with k_scale, v_scale float32 [pages][heads][page_size]."""
+    float16, bfloat16 or float8_e4m3fn, the last with k_scale, v_scale float32 [pages][heads][page_size]; or uint8
+    [pages][heads][page_size][head_dim / 2], two e2m1 codes a byte, with k_scale, v_scale uint8 (exponent + 127)
+    [pages][heads][page_size][cache_scale_row(head_dim)]."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None):
-        scaled = k.dtype == torch.float8_e4m3fn
+        packed = k.dtype == torch.uint8
+        scaled = packed or k.dtype == torch.float8_e4m3fn
         if k.dtype not in _TYPES or v.dtype != k.dtype or k.dim() != 4 or k.shape != v.shape:
             raise ValueError("k and v must be tensors of one type and shape [pages][heads][page_size][head_dim]")
         if scaled != (k_scale is not None) or scaled != (v_scale is not None):
-            raise ValueError("k_scale and v_scale go with float8_e4m3fn keys and values")
+            raise ValueError("k_scale and v_scale go with float8_e4m3fn or uint8 keys and values")
         for t in (k_scale, v_scale) if scaled else ():
-            if t.dtype != torch.float32 or tuple(t.shape) != tuple(k.shape[:3]):
+            if packed and (t.dtype != torch.uint8 or tuple(t.shape) != (*k.shape[:3], cache_scale_row(2 * k.shape[3]))):
+                raise ValueError("scales must be uint8 [pages][heads][page_size][2, 4 or 8]")
+            if not packed and (t.dtype != torch.float32 or tuple(t.shape) != tuple(k.shape[:3])):
                 raise ValueError("scales must be float32 [pages][heads][page_size]")
         self.tensors = (k, v, k_scale, v_scale)
         for t in self.tensors:
             if t is not None and not (t.is_cuda and t.is_contiguous() and t.device == k.device):
                 raise ValueError("the cache's tensors must be contiguous and on one CUDA device")
         pages, self.heads, page_size, self.head_dim = k.shape
+        self.page_size = page_size
+        self.head_dim *= 2 if packed else 1
         self.dtype, self.device = k.dtype, k.device
         self.struct = lscd_cache_t(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if scaled else None,
                                    v_scale.data_ptr() if scaled else None, pages, self.heads, page_size, self.head_dim,

@@ -16,12 +16,14 @@ lscd_status_t status_of(hipError_t e) {
 }
 bool aligned(const void* p, uintptr_t n) { return p && ((uintptr_t)p & (n - 1)) == 0; }
 
+bool scaled_form(int32_t type) { return type == LSCD_E4M3 || type == LSCD_E2M1; }
+
 lscd_status_t check_cache(const lscd_cache_t* c) {
     if (!c || !aligned(c->k, 16) || !aligned(c->v, 16) || c->num_pages < 1 || c->heads < 1 || c->page_size < 1 ||
         c->head_dim < 1)
         return LSCD_ERROR_INVALID_VALUE;
-    if (c->type != LSCD_F16 && c->type != LSCD_BF16 && c->type != LSCD_E4M3) return LSCD_ERROR_INVALID_VALUE;
-    const bool scaled = c->type == LSCD_E4M3;
+    if (c->type != LSCD_F16 && c->type != LSCD_BF16 && !scaled_form(c->type)) return LSCD_ERROR_INVALID_VALUE;
+    const bool scaled = scaled_form(c->type);
     if (scaled ? !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16) : c->k_scale || c->v_scale)
         return LSCD_ERROR_INVALID_VALUE;
     if (c->page_size < 16 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)) || c->head_dim % 16 ||
@@ -40,7 +42,7 @@ lscd_status_t check_move(const lscd_cache_t* c, const void* k, int64_t ks, const
     lscd_status_t st = check_cache(c);
     if (st != LSCD_SUCCESS) return st;
     if (T < 0 || (type != LSCD_F16 && type != LSCD_BF16)) return LSCD_ERROR_INVALID_VALUE;
-    if (c->type != LSCD_E4M3 && c->type != type) return LSCD_ERROR_NOT_SUPPORTED;
+    if (!scaled_form(c->type) && c->type != type) return LSCD_ERROR_NOT_SUPPORTED;
     if (T == 0) return LSCD_SUCCESS;
     const int64_t width = (int64_t)c->heads * c->head_dim;
     if (bad_rows(k, ks, width) || bad_rows(v, vs, width) || !aligned(slots, 4)) return LSCD_ERROR_INVALID_VALUE;

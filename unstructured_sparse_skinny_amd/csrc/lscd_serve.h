@@ -11,6 +11,14 @@
 namespace lscd {
 
 // ---------------------------------------------------------------- paged cache
+// How a cache holds its values: 16 bits, e4m3 with a float scale a token and head, e2m1 with a byte (exponent
+// + 127) for every 32 channels.
+enum CacheForm { kForm16 = 0, kForm8 = 1, kForm4 = 2 };
+inline int cache_form(int type) { return type == LSCD_E4M3 ? kForm8 : type == LSCD_E2M1 ? kForm4 : kForm16; }
+constexpr int form_bits(int form) { return form == kForm4 ? 4 : form == kForm8 ? 8 : 16; }
+constexpr int kScaleGroup = 32;
+// Bytes of one token's and head's scales of an e2m1 cache: one for 32 channels, so that a row is one aligned word.
+constexpr int scale_row(int dim) { return dim <= 64 ? 2 : dim <= 128 ? 4 : 8; }
 // Copies of T tokens between rows of `type` ([T][heads][dim], strides in elements) and slots.
 struct CacheMoveArgs {
     lscd_cache_t c;

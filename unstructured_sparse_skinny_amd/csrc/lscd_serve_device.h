@@ -1,5 +1,5 @@
 // Device-side building blocks of the serving operators: the two 16-bit types, matrix
-// instructions on them, e4m3 conversion, wavefront helpers.
+// instructions on them, e4m3 and e2m1 conversion, wavefront helpers.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -29,6 +29,7 @@ struct F16 {
     static constexpr bool bf = false;
     static constexpr float kWeightBits = 7.f;  // softmax weights are held 2^7 times as large
     static constexpr uint32_t kTopScale = 0x43800000u;  // bits of 2^8, whose codes (up to 448) may pass the largest value
+    static constexpr uint32_t kTopScale4 = 127u + 14u;  // the same of e2m1 codes (up to 6), as the exponent + 127
     static constexpr uint32_t kInfinity = 0x7C00u;
     __device__ static __forceinline__ float low(uint32_t w) { return (float)__builtin_bit_cast(half2v, w)[0]; }
     __device__ static __forceinline__ float high(uint32_t w) { return (float)__builtin_bit_cast(half2v, w)[1]; }
@@ -40,6 +41,12 @@ struct F16 {
     template <bool HI>
     __device__ static __forceinline__ uint32_t from_e4m3(uint32_t w, float scale) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, scale, HI));
+    }
+    // the two e2m1 codes of byte B of w, times the power of two `scale` (its exponent alone counts: sign and
+    // fraction may be anything); NaN where the exponent is that of infinity
+    template <int B>
+    __device__ static __forceinline__ uint32_t from_e2m1(uint32_t w, float scale) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, scale, B));
     }
     __device__ static __forceinline__ f32x4v mfma16(u32x4v a, u32x4v b, f32x4v c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8v, a), __builtin_bit_cast(half8v, b), c, 0,
@@ -67,6 +74,7 @@ struct BF16 {
     static constexpr bool bf = true;
     static constexpr float kWeightBits = 0.f;
     static constexpr uint32_t kTopScale = 0x7B800000u;  // 2^120
+    static constexpr uint32_t kTopScale4 = 127u + 126u;
     static constexpr uint32_t kInfinity = 0x7F80u;
     __device__ static __forceinline__ float low(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
     __device__ static __forceinline__ float high(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
@@ -77,6 +85,10 @@ struct BF16 {
     template <bool HI>
     __device__ static __forceinline__ uint32_t from_e4m3(uint32_t w, float scale) {
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, scale, HI));
+    }
+    template <int B>
+    __device__ static __forceinline__ uint32_t from_e2m1(uint32_t w, float scale) {
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, B));
     }
     __device__ static __forceinline__ f32x4v mfma16(u32x4v a, u32x4v b, f32x4v c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8v, a), __builtin_bit_cast(bf8v, b), c, 0, 0,
