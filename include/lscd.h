@@ -514,13 +514,13 @@ lscd_status_t lscd_attention_destroy(lscd_attention_t h);
  *           on are not written (a captured call may have room for more tokens than a replay brings).
  *   length  device, one number for each sequence.
  *   table   device; page j of sequence s is table[s * table_stride + j], table_pages of them.
- *   cache   of the handle's heads and head_dim; of `type` or LSCD_E4M3.
+ *   cache   of the handle's heads and head_dim; of `type`, LSCD_E4M3 or LSCD_E2M1.
  * Lengths stay on the device: the call neither waits nor copies, and can be captured into a graph
  * and replayed with other lengths.  Array contents outside these rules are clamped (tokens to T,
  * lengths to the table, pages to the pool), so that no call reads or writes out of bounds; starts that do
  * not ascend leave the rows of o undefined.
  * Scores, softmax and sums are fp32; the softmax weights are rounded once to `type` for the second
- * product.  An E4M3 cache's values reach the products in `type`: exact inside its normal range; past its
+ * product.  An E4M3 or E2M1 cache's values reach the products in `type`: exact inside its normal range; past its
  * largest value (65504 in float16) they count as that, below its normal range they are rounded to its
  * subnormals.  Results do not depend on timing (partial sums are added in a fixed order) but their
  * last bits may depend on the other sequences in the call, which move the points where work is split.
@@ -534,6 +534,18 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
                              const int32_t* start, const int32_t* length, const int32_t* table, int64_t table_stride,
                              int32_t table_pages, int32_t sequences, int64_t T, float scale, int32_t causal,
                              int32_t window, void* o, int64_t o_stride, int32_t type, void* stream);
+
+/*
+ * lscd_attention_lse -- lscd_attention (the same o, bit for bit) that also writes, for every token and query
+ *   head, the logarithm of its sum: lse = ln sum over the positions seen of exp(scale * q . k), -infinity where
+ *   none is seen.  With it, outputs over several caches can be joined and softmax weights be worked out again
+ *   (exp(scale * q . k - lse)).
+ *   lse    device, [T][q_heads] floats; rows from start[sequences] on are not written.
+ */
+lscd_status_t lscd_attention_lse(lscd_attention_t h, const lscd_cache_t* cache, const void* q, int64_t q_stride,
+                                 const int32_t* start, const int32_t* length, const int32_t* table, int64_t table_stride,
+                                 int32_t table_pages, int32_t sequences, int64_t T, float scale, int32_t causal,
+                                 int32_t window, void* o, int64_t o_stride, float* lse, int32_t type, void* stream);
 
 #ifdef __cplusplus
 }

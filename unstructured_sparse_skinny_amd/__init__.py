@@ -41,7 +41,7 @@ EXPORTS = ("lscd_pack_size", "lscd_pack", "lscd_default_tile_m", "lscd_encode", 
            "lscd_status_string", "lscd_stream_read", "lscd_spmm_noalloc", "lscd_linear_times",
            "lscd_quant_encode", "lscd_quant_linear", "lscd_quant_decode", "lscd_quant_destroy",
            "lscd_cache_write", "lscd_cache_read",
-           "lscd_attention_create", "lscd_attention", "lscd_attention_destroy")
+           "lscd_attention_create", "lscd_attention", "lscd_attention_lse", "lscd_attention_destroy")
 
 LSCD_F16 = 0
 LSCD_BF16 = 1
@@ -117,6 +117,7 @@ def _load():
         "lscd_attention_create": [I32, I32, I32, P(VP)],
         "lscd_attention_destroy": [VP],
         "lscd_attention": [VP, VP, VP, I64, VP, VP, VP, I64, I32, I32, I64, ctypes.c_float, I32, I32, VP, I64, I32, VP],
+        "lscd_attention_lse": [VP, VP, VP, I64, VP, VP, VP, I64, I32, I32, I64, ctypes.c_float, I32, I32, VP, I64, VP, I32, VP],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -547,6 +548,12 @@ def _ints(t, name, device, dim=1):
     return t.data_ptr()
 
 
+def _lse(t, T, heads, device):
+    if t.dtype != torch.float32 or tuple(t.shape) != (T, heads) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"lse must be a contiguous float32 tensor [{T}][{heads}] on the cache's device")
+    return t.data_ptr()
+
+
 def _same_type(a, b, name):
     if a.dtype != b.dtype or a.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError(f"{name} must both be float16 or both be bfloat16")
@@ -599,10 +606,11 @@ def lscd_attention_create(q_heads: int, kv_heads: int, head_dim: int) -> Attenti
 
 
 def lscd_attention(h: Attention, cache: Cache, q, start, length, table, out, scale=None, causal=True, window=0,
-                   stream=None):
+                   stream=None, lse=None):
     """Attention of the new tokens q [T][q_heads][head_dim] of a batch of sequences over their cached positions:
     sequence s has the tokens start[s] .. start[s + 1] - 1 (int32) as the last of its length[s] positions, which lie
-    in the pages table[s] (int32 [sequences][pages]).  scale defaults to head_dim ** -0.5."""
+    in the pages table[s] (int32 [sequences][pages]).  scale defaults to head_dim ** -0.5.  lse (float32
+    [T][q_heads]): where the logarithm of each row's sum of exponentials goes too (lscd_attention_lse)."""
     pq, sq = _rows(q, "q", h.q_heads, h.head_dim, cache.device)
     po, so = _rows(out, "out", h.q_heads, h.head_dim, cache.device)
     S, T = length.shape[0], q.shape[0]
@@ -610,10 +618,15 @@ def lscd_attention(h: Attention, cache: Cache, q, start, length, table, out, sca
         raise ValueError("start must have one entry more than length, table as many rows, out as many tokens as q")
     dev = cache.device
     pt = _ints(table, "table", dev, 2)
-    _check(_lib.lscd_attention(h.ptr, cache.ptr, pq, sq, _ints(start, "start", dev), _ints(length, "length", dev), pt,
-                               table.stride(0) if S > 1 else table.shape[1], table.shape[1], S, T,
-                               h.head_dim ** -0.5 if scale is None else scale, causal, window, po, so,
-                               _same_type(q, out, "q and out"), _stream_on(stream, dev)), "lscd_attention")
+    args = (h.ptr, cache.ptr, pq, sq, _ints(start, "start", dev), _ints(length, "length", dev), pt,
+            table.stride(0) if S > 1 else table.shape[1], table.shape[1], S, T,
+            h.head_dim ** -0.5 if scale is None else scale, causal, window, po, so)
+    kind = _same_type(q, out, "q and out")
+    if lse is None:
+        _check(_lib.lscd_attention(*args, kind, _stream_on(stream, dev)), "lscd_attention")
+    else:
+        _check(_lib.lscd_attention_lse(*args, _lse(lse, T, h.q_heads, dev), kind, _stream_on(stream, dev)),
+               "lscd_attention_lse")
     return out
 
 

@@ -17,7 +17,8 @@
 // product with what the rounding leaves out would give every infinity among the values a weight of zero or
 // less).  float16 has few exponents, so its weights are held 2^7 times as large (m is that much less), at
 // most 2^15: they keep their step down to 2^-21 of the largest and are rounded in steps of 2^-31 of it below.
-// Both kernels sum the weights as they multiply them.
+// Both kernels sum the weights as they multiply them.  Where the logarithm of a row's sum is asked for (lse),
+// they sum the weights before that rounding too: ln of the sum as rounded would be off by up to 2^-9 in bfloat16.
 //
 // Work is split over all sequences, key heads, row tiles and cached positions at once: the units
 // (one row tile x one stretch of positions) are numbered in that order and cut into equal ranges,
@@ -43,6 +44,12 @@ constexpr float kNoScore = -3.4028234663852886e38f;  // maximum before any score
                                                      // defined, and below every finite score
 constexpr float kLazy = 8.f;        // how far a score may exceed the maximum before it is moved
 constexpr float kLarge = 1048576.f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Natural logarithm of a row's sum of exponentials: sum * 2^m, -infinity where there are none.
+__device__ __forceinline__ float log_of_sum(float m, float sum) {
+    return sum != 0.f ? (m + __builtin_amdgcn_logf(sum)) * kLn2 : -__builtin_inff();
+}
 
 // The rows and positions of one sequence.
 struct Seq {
@@ -202,26 +209,28 @@ __device__ __forceinline__ uint32_t page_of(const AttnArgs& a, int entry) {
 // One key head's part of the cache: its block of page 0, and the bytes from a page's to the next's.
 struct HeadBase {
     const uint8_t *k, *v;
-    const float *ks, *vs;
+    const uint8_t *ks, *vs;
     uint64_t page, page_scales;
     int block, block_scales;  // bytes of one page's block
-    __device__ __forceinline__ HeadBase(const AttnArgs& a, int head, int width) {
-        block = a.c.page_size * a.c.head_dim * width;
-        block_scales = a.c.page_size * 4;
-        page = (uint64_t)a.c.heads * block;
-        page_scales = (uint64_t)a.c.heads * block_scales;
-        k = (const uint8_t*)a.c.k + (uint64_t)head * block;
-        v = (const uint8_t*)a.c.v + (uint64_t)head * block;
-        ks = a.c.k_scale + (uint64_t)head * a.c.page_size;
-        vs = a.c.v_scale + (uint64_t)head * a.c.page_size;
+    // BITS: of one value; SCALES: bytes of one token's scales
+    template <int BITS, int SCALES>
+    __device__ __forceinline__ void set(const lscd_cache_t& c, int head) {
+        block = c.page_size * c.head_dim / 8 * BITS;
+        block_scales = c.page_size * SCALES;
+        page = (uint64_t)c.heads * block;
+        page_scales = (uint64_t)c.heads * block_scales;
+        k = (const uint8_t*)c.k + (uint64_t)head * block;
+        v = (const uint8_t*)c.v + (uint64_t)head * block;
+        ks = (const uint8_t*)c.k_scale + (uint64_t)head * block_scales;
+        vs = (const uint8_t*)c.v_scale + (uint64_t)head * block_scales;
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t keys(uint32_t p) const { return buffer_of(k + p * page, block); }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t values(uint32_t p) const { return buffer_of(v + p * page, block); }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t key_scales(uint32_t p) const {
-        return buffer_of((const uint8_t*)ks + p * page_scales, block_scales);
+        return buffer_of(ks + p * page_scales, block_scales);
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t value_scales(uint32_t p) const {
-        return buffer_of((const uint8_t*)vs + p * page_scales, block_scales);
+        return buffer_of(vs + p * page_scales, block_scales);
     }
 };
 

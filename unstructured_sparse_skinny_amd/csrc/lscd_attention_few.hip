@@ -25,16 +25,30 @@ namespace {
 
 constexpr int kFewWaves = 4;
 
-// DP: channels padded to 64, 128 or 256.
-template <typename T, bool E4M3, int DP>
+// FORM: how the cache holds its values.  DP: channels padded to 64, 128 or 256.
+template <typename T, int FORM, int DP>
 struct Few {
+    static constexpr bool kScaled = FORM != kForm16;
+    static constexpr int kBits = form_bits(FORM);
+    static constexpr int kScaleBytes = FORM == kForm4 ? scale_row(DP) : 4;  // of one token's scales
     static constexpr int kSteps = DP / 32;  // MFMA steps over the channels of q . k
     static constexpr int VW = DP / 16;      // channels per lane of a value row
-    static constexpr int kKeyRegs = E4M3 ? DP / 16 : DP / 8;        // words of one 16-token key tile per lane
-    static constexpr int kValWords = E4M3 ? VW / 4 : VW / 2;        // words of one value row per lane
+    static constexpr int kKeyRegs = DP * kBits / 128;                       // words of one 16-token key tile per lane
+    static constexpr int kValWords = VW * kBits >= 32 ? VW * kBits / 32 : 1;  // words of one value row per lane
+    static constexpr int kKeyScales = FORM == kForm4 && DP == 256 ? 2 : 1;    // scales of one key tile per lane
+    // 1 as a scale is loaded
+    static constexpr uint32_t kOne = FORM == kForm4 ? 127u : 0x3F800000u, kTop = FORM == kForm4 ? T::kTopScale4 : T::kTopScale;
     uint32_t kr[2][kKeyRegs];
     uint32_t vr[8][kValWords];
-    uint32_t ks[2], vs[8];  // scales as loaded (e4m3)
+    uint32_t ks[2][kKeyScales], vs[8];  // scales as loaded: bits of a float (e4m3), exponent + 127 (e2m1)
+
+    // A key row of 4-bit codes lies in the four lane groups as 16 channels each, of 64 (DP 64), or as 32 each, of
+    // 128: the lane's channels of unit u of them have one scale.  Rows that end in the middle of 32 channels are
+    // loaded to their end, 16 channels too early; the query has zeros there.
+    __device__ static __forceinline__ int unit_channel(int u, int g) { return DP == 64 ? 16 * g : 128 * u + 32 * g; }
+    __device__ static __forceinline__ int unit_start(int u, int g, int D) {
+        return DP == 64 ? unit_channel(u, g) : min(unit_channel(u, g), D - 32);
+    }
 
     // 32 positions from t0 on, in the pages of the table entries e; positions from `high` on are zero
     // (lanes without a position read outside the descriptor, which costs no traffic).
@@ -47,7 +61,7 @@ struct Few {
             const uint32_t p = page_of(a, e[h]);
             const bool on = t + (lane & 15) < high;
             const auto rs = hb.keys(p);
-            if (E4M3) {
+            if (FORM == kForm8) {
 #pragma unroll
                 for (int u = 0; u < DP / 64; ++u) {
                     const int d = 64 * u + 16 * (lane >> 4);
@@ -55,7 +69,24 @@ struct Few {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
                 }
-                ks[h] = __builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0);
+                ks[h][0] = __builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0);
+            } else if (FORM == kForm4) {
+#pragma unroll
+                for (int u = 0; u < kKeyScales; ++u) {
+                    const int d = unit_channel(u, lane >> 4);
+                    const int at = on && d < D ? (row * D + unit_start(u, lane >> 4, D)) / 2 : kNoRow;
+                    if constexpr (DP == 64) {
+                        const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
+                        kr[h][0] = x[0];
+                        kr[h][1] = x[1];
+                    } else {
+                        const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
+                    }
+                    ks[h][u] = __builtin_amdgcn_raw_buffer_load_b8(hb.key_scales(p),
+                                                                   on && d < D ? row * kScaleBytes + d / kScaleGroup : kNoRow, 0, 0);
+                }
             } else {
 #pragma unroll
                 for (int s = 0; s < kSteps; ++s) {
@@ -72,14 +103,13 @@ struct Few {
     // Positions outside [low, high) are zero (their scales are left out by value_scale).
     __device__ __forceinline__ void load_values(const AttnArgs& a, const HeadBase& hb, const int (&e)[2], int t0, int low,
                                                 int high, int lane) {
-        constexpr int W = E4M3 ? 1 : 2;
         const int D = a.c.head_dim, g = lane >> 4, d = VW * (lane & 15);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int t = t0 + 16 * h, r0 = (t & (a.c.page_size - 1)) + 4 * g;
             const uint32_t p = page_of(a, e[h]);
             const auto rs = hb.values(p);
-            if (E4M3) {
+            if (FORM == kForm8) {
                 const u32x4v sc = __builtin_amdgcn_raw_buffer_load_b128(hb.value_scales(p), r0 * 4, 0, 0);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) vs[4 * h + j] = sc[j];
@@ -91,9 +121,11 @@ struct Few {
                 constexpr int kPer = kValWords < 4 ? kValWords : 4;  // words of one load
 #pragma unroll
                 for (int w = 0; w < kValWords; w += kPer) {
-                    const int at = d + w * 4 / W;
-                    const int off = on && at < D ? ((r0 + j) * D + at) * W : kNoRow;
-                    if constexpr (kPer == 1) {
+                    const int at = d + w * 32 / kBits;
+                    const int off = on && at < D ? ((r0 + j) * D + at) * kBits / 8 : kNoRow;
+                    if constexpr (VW * kBits == 16) {
+                        vr[4 * h + j][w] = __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0);
+                    } else if constexpr (kPer == 1) {
                         vr[4 * h + j][w] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
                     } else if constexpr (kPer == 2) {
                         const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
@@ -105,28 +137,36 @@ struct Few {
                         for (int i = 0; i < 4; ++i) vr[4 * h + j][w + i] = x[i];
                     }
                 }
+                if (FORM == kForm4)
+                    vs[4 * h + j] = __builtin_amdgcn_raw_buffer_load_b8(hb.value_scales(p), 
+                                                                      d < D ? (r0 + j) * kScaleBytes + d / kScaleGroup : kNoRow, 0, 0);
             }
         }
     }
     // A position that was not loaded has zeros for codes, but any scale: 1 instead.
     __device__ __forceinline__ void mask_scales(int t0, int low, int high, int lane) {
-        if (!E4M3) return;
+        if (!kScaled) return;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int pos = t0 + 16 * (j / 4) + 4 * (lane >> 4) + j % 4;
-            if (pos >= high || pos < low) vs[j] = 0x3F800000u;
+            if (pos >= high || pos < low) vs[j] = kOne;
         }
     }
 
     // Whether some key's or value's code times its scale may pass the type's largest value.  (Scales are
     // positive: they compare as whole numbers.)
-    __device__ __forceinline__ bool top_keys() const { return E4M3 && __any(max(ks[0], ks[1]) >= T::kTopScale); }
+    __device__ __forceinline__ bool top_keys() const {
+        if (!kScaled) return false;
+        uint32_t most = max(ks[0][0], ks[1][0]);
+        if (kKeyScales == 2) most = max(most, max(ks[0][kKeyScales - 1], ks[1][kKeyScales - 1]));
+        return __any(most >= kTop);
+    }
     __device__ __forceinline__ bool top_values() const {
-        if (!E4M3) return false;
+        if (!kScaled) return false;
         uint32_t most = vs[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) most = max(most, vs[j]);
-        return __any(most >= T::kTopScale);
+        return __any(most >= kTop);
     }
     // Word of codes `w` in 16 bits.  TOP: saturated.  (The scale is opaque there, so that the conversions of
     // the two forms are not taken for the same and moved out of their branches.)
@@ -135,29 +175,51 @@ struct Few {
         if (TOP) return saturate<T>(T::template from_e4m3<HI>(w, as_float(opaque(scale))));
         return T::template from_e4m3<HI>(w, as_float(scale));
     }
+    template <int B, bool TOP>
+    __device__ static __forceinline__ uint32_t from_code4(uint32_t w, uint32_t scale) {
+        if (TOP) return saturate<T>(T::template from_e2m1<B>(w, as_float(opaque(scale << 23))));
+        return T::template from_e2m1<B>(w, as_float(scale << 23));
+    }
     // The A operand of key half h, step s, in 16 bits.
     template <bool TOP>
     __device__ __forceinline__ u32x4v key_operand(int h, int s) const {
         u32x4v x;
-        if (E4M3) {  // two words of codes per step: channels 16 g + 8 (s % 2) of the 64 of step s / 2
+        if constexpr (FORM == kForm4) {  // one word of codes per step
+            x[0] = from_code4<0, TOP>(kr[h][s], ks[h][s / 4]);
+            x[1] = from_code4<1, TOP>(kr[h][s], ks[h][s / 4]);
+            x[2] = from_code4<2, TOP>(kr[h][s], ks[h][s / 4]);
+            x[3] = from_code4<3, TOP>(kr[h][s], ks[h][s / 4]);
+        } else if constexpr (FORM == kForm8) {  // two words of codes per step: channels 16 g + 8 (s % 2) of the 64 of step s / 2
             const uint32_t lo = kr[h][4 * (s / 2) + 2 * (s % 2)], hi = kr[h][4 * (s / 2) + 2 * (s % 2) + 1];
-            x[0] = from_code<false, TOP>(lo, ks[h]);
-            x[1] = from_code<true, TOP>(lo, ks[h]);
-            x[2] = from_code<false, TOP>(hi, ks[h]);
-            x[3] = from_code<true, TOP>(hi, ks[h]);
+            x[0] = from_code<false, TOP>(lo, ks[h][0]);
+            x[1] = from_code<true, TOP>(lo, ks[h][0]);
+            x[2] = from_code<false, TOP>(hi, ks[h][0]);
+            x[3] = from_code<true, TOP>(hi, ks[h][0]);
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i] = kr[h][4 * s + i];
         }
         return x;
     }
-    // The channel that step s, lane group g begins with (the q operand uses the same order).
-    __device__ static __forceinline__ int step_channel(int s, int g) {
-        return E4M3 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+    // The channel that step s, lane group g begins with (the q operand uses the same order); D and more where it
+    // has none.
+    __device__ static __forceinline__ int step_channel(int s, int g, int D) {
+        if (FORM == kForm4) {
+            const int d = unit_start(s / 4, g, D) + 8 * (s % 4);
+            return d < unit_channel(s / 4, g) ? D : d;
+        }
+        return FORM == kForm8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
     }
     // Word of channels 2w, 2w+1 of value row j in 16 bits.
     __device__ __forceinline__ uint32_t value_word(int j, int w) const {
-        if (E4M3) return w % 2 ? T::template from_e4m3<true>(vr[j][w / 2], as_float(vs[j])) : T::template from_e4m3<false>(vr[j][w / 2], as_float(vs[j]));
+        if (FORM == kForm4) {
+            const uint32_t c = vr[j][w / 4];
+            return w % 4 == 0   ? from_code4<0, false>(c, vs[j])
+                   : w % 4 == 1 ? from_code4<1, false>(c, vs[j])
+                   : w % 4 == 2 ? from_code4<2, false>(c, vs[j])
+                                : from_code4<3, false>(c, vs[j]);
+        }
+        if (FORM == kForm8) return w % 2 ? T::template from_e4m3<true>(vr[j][w / 2], as_float(vs[j])) : T::template from_e4m3<false>(vr[j][w / 2], as_float(vs[j]));
         return vr[j][w];
     }
     // The A operands of channels 2w and 2w + 1 of every lane: tokens in pairs.
@@ -191,12 +253,13 @@ struct FewItem {
     __device__ __forceinline__ int first_position(int unit) const { return (low / kFewTokens + unit) * kFewTokens; }
 };
 
-template <typename T, bool E4M3, int DP>
+// LSE: the logarithms of the rows' sums are written too.
+template <typename T, int FORM, int DP, bool LSE>
 __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs a) {
-    using F = Few<T, E4M3, DP>;
+    using F = Few<T, FORM, DP>;
     constexpr int VW = F::VW;
     __shared__ float sh_o[kFewWaves][kFewRows][DP];
-    __shared__ float sh_m[kFewWaves][kFewRows], sh_l[kFewWaves][kFewRows];
+    __shared__ float sh_m[kFewWaves][kFewRows], sh_l[kFewWaves][kFewRows], sh_f[LSE ? kFewWaves : 1][kFewRows];
     __shared__ uint32_t sh_last;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int me = blockIdx.x;
@@ -222,7 +285,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         const uint16_t* qp = (const uint16_t*)a.q + (int64_t)(it.q.first + (live ? token : 0)) * a.q_stride + (int64_t)qh * D;
 #pragma unroll
         for (int s = 0; s < F::kSteps; ++s) {
-            const int d = F::step_channel(s, lane >> 4);
+            const int d = F::step_channel(s, lane >> 4, D);
             qr[s] = u32x4v{0u, 0u, 0u, 0u};
             if (live && d < D) qr[s] = *(const u32x4v*)(qp + d);
         }
@@ -235,11 +298,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         all_low = a.window ? it.q.len - it.q.n + tok1 - a.window + 1 : 0;
     };
 
-    float m = kNoScore, l = 0.f;
+    float m = kNoScore, l = 0.f, full = 0.f;  // full: the sum before the weights' rounding (LSE)
     f32x4v o[VW];
     auto clear = [&]() {
         m = kNoScore;
-        l = 0.f;
+        l = full = 0.f;
 #pragma unroll
         for (int i = 0; i < VW; ++i) o[i] = f32x4v{0.f, 0.f, 0.f, 0.f};
     };
@@ -250,12 +313,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         // (worked out here, not kept in registers through the loop)
         const int tid = opaque(threadIdx.x), le = tid & 63;
         l = sum_quarters(l);
+        if (LSE) full = sum_quarters(full);
 
         // Join the four wavefronts.
         lds_barrier();
         if (le < 16) {
             sh_m[wave][le] = m;
             sh_l[wave][le] = l;
+            if (LSE) sh_f[wave][le] = full;
         }
         if (live) {
 #pragma unroll
@@ -270,7 +335,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         const int rows = min(kFewRows, it.q.rows - it.tile * kFewRows);
         const bool whole = first == 0 && k + 1 == it.units;
         const int owner = whole ? me : cut.owner(item), behind = whole ? me : cut.owner(item + it.units - 1);
-        constexpr int kFloats = kFewRows * (DP + 2);  // a pair (maximum, sum) per row, then the rows
+        // a pair (maximum, sum) per row, then the rows, then (LSE) a pair (full sum, -) per row
+        constexpr int kFull = kFewRows * (DP + 2), kFloats = kFull + (LSE ? 2 * kFewRows : 0);
         float* mine = a.part + (int64_t)(2 * me + (first == 0 ? 1 : 0)) * kFloats;
         auto write = [&](int r, int d, float L, float x, float y) {  // channels d, d + 1 of row r
             const int rw = it.tile * kFewRows + r;
@@ -278,6 +344,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             uint16_t* op = (uint16_t*)a.o + (int64_t)(it.q.first + rw / a.share) * a.o_stride +
                            (int64_t)(it.head * a.share + rw % a.share) * D + d;
             if (d < D) *(uint32_t*)op = L != 0.f ? T::pack(x * inv, y * inv) : 0u;
+        };
+        auto write_log = [&](int r, float M, float L) {
+            const int rw = it.tile * kFewRows + r;
+            a.lse[(int64_t)(it.q.first + rw / a.share) * a.q_heads + it.head * a.share + rw % a.share] = log_of_sum(M, L);
         };
         for (int i = tid; i < rows * (DP / 2); i += 64 * kFewWaves) {
             const int r = i / (DP / 2), d = 2 * (i % (DP / 2));
@@ -292,11 +362,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                 x += by * sh_o[w][r][d];
                 y += by * sh_o[w][r][d + 1];
             }
+            float all = 0.f;
+            if (LSE && d == 0)
+#pragma unroll
+                for (int w = 0; w < kFewWaves; ++w) all += exp2_fast(sh_m[w][r] - M) * sh_f[w][r];
             if (whole) {
                 write(r, d, L, x, y);
+                if (LSE && d == 0) write_log(r, M, all);
             } else {
                 put2(mine + 2 * kFewRows + r * DP + d, x, y);
                 if (d == 0) put2(mine + 2 * r, M, L);
+                if (LSE && d == 0) put2(mine + kFull + 2 * r, all, 0.f);
             }
         }
         if (!whole && arrive_last(a.count + owner, (uint32_t)(behind - owner + 1), &sh_last)) {
@@ -304,11 +380,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             // thread's channels, eight loads in flight (a long sequence has a part per workgroup).
             constexpr int kParts = 32, kMine = kFewRows * (DP / 2) / (64 * kFewWaves);
             float* pair = &sh_o[0][0][0];
-            float M[kMine], L[kMine], x[kMine], y[kMine];
+            float M[kMine], L[kMine], x[kMine], y[kMine], all[kMine];
 #pragma unroll
             for (int j = 0; j < kMine; ++j) {
                 M[j] = kNoScore;
-                L[j] = x[j] = y[j] = 0.f;
+                L[j] = x[j] = y[j] = all[j] = 0.f;
             }
             auto part_of = [&](int w) { return a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats; };
             for (int w0 = owner; w0 <= behind; w0 += kParts) {
@@ -329,6 +405,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                     L[j] *= b;
                     x[j] *= b;
                     y[j] *= b;
+                    if (LSE && d == 0) {
+                        all[j] *= b;
+                        for (int w = 0; w < n; ++w) {
+                            float one, none;
+                            get2(part_of(w0 + w) + kFull + 2 * r, &one, &none);
+                            all[j] += one * exp2_fast(pair[2 * (w * rows + r)] - to);
+                        }
+                    }
                     for (int w1 = 0; w1 < n; w1 += 8) {
                         float x1[8], y1[8];
 #pragma unroll
@@ -349,13 +433,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             for (int j = 0; j < kMine; ++j) {
                 const int i = tid + j * 64 * kFewWaves;
                 if (i < rows * (DP / 2)) write(i / (DP / 2), 2 * (i % (DP / 2)), L[j], x[j], y[j]);
+                if (LSE && i < rows * (DP / 2) && i % (DP / 2) == 0) write_log(i / (DP / 2), M[j], all[j]);
             }
         }
     };
 
     F f;
     {
-        const HeadBase hb(a, it.head, E4M3 ? 1 : 2);
+        HeadBase hb;
+        hb.set<F::kBits, F::kScaleBytes>(a.c, it.head);
         const int t0 = it.first_position(k) + 32 * wave;
         const int e[2] = {entry_of(a, it.seq, t0), entry_of(a, it.seq, t0 + 16)};
         load_queries();
@@ -386,7 +472,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                 nx.measure(a);
             }
         }
-        const HeadBase hb(a, nx.head, E4M3 ? 1 : 2);
+        HeadBase hb;
+        hb.set<F::kBits, F::kScaleBytes>(a.c, nx.head);
         const int nt = nx.first_position(nk) + 32 * wave, next_high = more ? nx.high : 0;
         const int e[2] = {entry_of(a, nx.seq, nt), entry_of(a, nx.seq, nt + 16)};
         f32x4v s[2];
@@ -424,13 +511,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
             const float by = exp2_fast(m - to);
             m = to;
             l *= by;
+            if (LSE) full *= by;
 #pragma unroll
             for (int i = 0; i < VW; ++i)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[i][r] *= by;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = exp2_fast(x[i] - m);
+        for (int i = 0; i < 8; ++i) {
+            x[i] = exp2_fast(x[i] - m);
+            if (LSE) full += x[i];
+        }
         u32x4v pb;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -464,7 +555,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                     f1[i] = T::finite(v1[i]);
                     v0[i] ^= f0[i];
                     v1[i] ^= f1[i];
-                    if (E4M3) {
+                    if (F::kScaled) {
                         v0[i] = saturate<T>(v0[i]);
                         v1[i] = saturate<T>(v1[i]);
                     }
@@ -505,27 +596,39 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
     }
 }
 
-template <typename T, bool E4M3>
+template <typename T, int FORM, bool LSE>
 hipError_t few_dim(const AttnArgs& a, int grid, hipStream_t s) {
     const int D = a.c.head_dim;
     if (D <= 64)
-        attention_few_kernel<T, E4M3, 64><<<grid, 64 * kFewWaves, 0, s>>>(a);
+        attention_few_kernel<T, FORM, 64, LSE><<<grid, 64 * kFewWaves, 0, s>>>(a);
     else if (D <= 128)
-        attention_few_kernel<T, E4M3, 128><<<grid, 64 * kFewWaves, 0, s>>>(a);
+        attention_few_kernel<T, FORM, 128, LSE><<<grid, 64 * kFewWaves, 0, s>>>(a);
     else
-        attention_few_kernel<T, E4M3, 256><<<grid, 64 * kFewWaves, 0, s>>>(a);
+        attention_few_kernel<T, FORM, 256, LSE><<<grid, 64 * kFewWaves, 0, s>>>(a);
     return hipGetLastError();
+}
+
+template <typename T, int FORM>
+hipError_t few_form(const AttnArgs& a, int grid, hipStream_t s) {
+    return a.lse ? few_dim<T, FORM, true>(a, grid, s) : few_dim<T, FORM, false>(a, grid, s);
+}
+
+template <typename T>
+hipError_t few_type(const AttnArgs& a, int grid, hipStream_t s) {
+    switch (cache_form(a.c.type)) {
+        case kForm8: return few_form<T, kForm8>(a, grid, s);
+        case kForm4: return few_form<T, kForm4>(a, grid, s);
+        default: return few_form<T, kForm16>(a, grid, s);
+    }
 }
 
 }  // namespace
 
 int attention_few_grid(int cus) { return 2 * cus; }
-int64_t attention_few_floats(int dim) { return kFewRows * ((dim <= 64 ? 64 : dim <= 128 ? 128 : 256) + 2); }
+int64_t attention_few_floats(int dim) { return kFewRows * ((dim <= 64 ? 64 : dim <= 128 ? 128 : 256) + 4); }
 
 hipError_t launch_attention_few(const AttnArgs& a, int type, int grid, hipStream_t s) {
-    const bool e = a.c.type == LSCD_E4M3;
-    if (type == LSCD_F16) return e ? few_dim<F16, true>(a, grid, s) : few_dim<F16, false>(a, grid, s);
-    return e ? few_dim<BF16, true>(a, grid, s) : few_dim<BF16, false>(a, grid, s);
+    return type == LSCD_F16 ? few_type<F16>(a, grid, s) : few_type<BF16>(a, grid, s);
 }
 
 }  // namespace lscd

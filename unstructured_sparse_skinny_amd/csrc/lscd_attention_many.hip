@@ -35,15 +35,20 @@ constexpr int kSchedFree = 0x6;
 // Tokens of a tile: as many as the registers hold, so that a tile's products cover the next one's loads.
 constexpr int many_tokens(int dp) { return dp <= 64 ? 2 * kManyTokens : (dp <= 128 ? kManyTokens : kManyTokens / 2); }
 
-template <typename T, bool E4M3, int DP>
+template <typename T, int FORM, int DP>
 struct Many {
+    static constexpr bool kScaled = FORM != kForm16;
+    static constexpr int kBits = form_bits(FORM);
+    static constexpr int kScaleBytes = FORM == kForm4 ? scale_row(DP) : 4;  // of one token's scales
     static constexpr int kSteps = DP / 16;    // MFMA steps over the channels of q . k
     static constexpr int kBlocks = DP / 32;   // 32-channel blocks of the output
     static constexpr int kRow = DP * 2;       // bytes of an LDS row
     static constexpr int kTokens = many_tokens(DP);
     static constexpr int kTile = kTokens * kRow;
-    // 16-byte loads: lanes per row (a power of two that covers DP), rows per pass, passes
-    static constexpr int kPer = DP <= 64 ? (E4M3 ? 4 : 8) : DP <= 128 ? (E4M3 ? 8 : 16) : (E4M3 ? 16 : 32);
+    // Loads of 16 bytes (8 of 4-bit codes, so that a tile has a row for every thread): channels of one, lanes per
+    // row (a power of two that covers DP), rows per pass, passes
+    static constexpr int kLoad = kScaled ? 16 : 8;
+    static constexpr int kPer = (DP <= 64 ? 64 : DP <= 128 ? 128 : 256) / kLoad;
     static constexpr int kPassRows = kManyThreads / kPer;
     static constexpr int kPasses = kTokens / kPassRows;
     static_assert(kTokens % kPassRows == 0, "every thread has a row in every pass");
@@ -59,7 +64,7 @@ struct Many {
     __device__ static __forceinline__ int val_at(int row, int chunk) { return row * kRow + ((chunk ^ val_swizzle(row)) << 4); }
 
     u32x4v k[kPasses], v[kPasses];
-    float ks[kPasses], vs[kPasses];
+    uint32_t ks[kPasses], vs[kPasses];  // as loaded: bits of a float (e4m3), exponent + 127 (e2m1)
     int entry[kPasses];  // table entries of the next tile to load
 
     __device__ __forceinline__ static int row_of(int pass, int tid) { return pass * kPassRows + tid / kPer; }
@@ -70,20 +75,49 @@ struct Many {
     }
     // Loads the tile whose entries look_up() found; rows from `high` on are zero.
     __device__ __forceinline__ void load(const AttnArgs& a, const HeadBase& hb, int t0, int low, int high, int tid) {
-        const int D = a.c.head_dim, width = E4M3 ? 1 : 2, d = (tid % kPer) * (E4M3 ? 16 : 8);
+        const int D = a.c.head_dim, d = (tid % kPer) * kLoad;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int t = t0 + row_of(i, tid), row = t & (a.c.page_size - 1);
             const uint32_t p = page_of(a, entry[i]);
             const bool on = t < high && t >= low;
-            const int at = on && d < D ? (row * D + d) * width : kNoRow;
-            k[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.keys(p), at, 0, 0);
-            v[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.values(p), at, 0, 0);
-            if (E4M3) {
-                ks[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0));
-                vs[i] = as_float(__builtin_amdgcn_raw_buffer_load_b32(hb.value_scales(p), on ? row * 4 : kNoRow, 0, 0));
+            const int at = on && d < D ? (row * D + d) * kBits / 8 : kNoRow;
+            if constexpr (FORM == kForm4) {
+                const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(hb.keys(p), at, 0, 0);
+                const u32x2v y = __builtin_amdgcn_raw_buffer_load_b64(hb.values(p), at, 0, 0);
+                k[i] = u32x4v{x[0], x[1], 0u, 0u};
+                v[i] = u32x4v{y[0], y[1], 0u, 0u};
+                const int by = on && d < D ? row * kScaleBytes + d / kScaleGroup : kNoRow;
+                ks[i] = __builtin_amdgcn_raw_buffer_load_b8(hb.key_scales(p), by, 0, 0);
+                vs[i] = __builtin_amdgcn_raw_buffer_load_b8(hb.value_scales(p), by, 0, 0);
+            } else {
+                k[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.keys(p), at, 0, 0);
+                v[i] = __builtin_amdgcn_raw_buffer_load_b128(hb.values(p), at, 0, 0);
+            }
+            if (FORM == kForm8) {
+                ks[i] = __builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0);
+                vs[i] = __builtin_amdgcn_raw_buffer_load_b32(hb.value_scales(p), on ? row * 4 : kNoRow, 0, 0);
             }
         }
+    }
+    // The h-th 8 of a load's values in 16 bits.
+    __device__ static __forceinline__ u32x4v widen(u32x4v x, uint32_t scale, int h) {
+        if constexpr (FORM == kForm4) {
+            const uint32_t w = x[h];
+            const float by = as_float(scale << 23);
+            x[0] = T::template from_e2m1<0>(w, by);
+            x[1] = T::template from_e2m1<1>(w, by);
+            x[2] = T::template from_e2m1<2>(w, by);
+            x[3] = T::template from_e2m1<3>(w, by);
+        } else if constexpr (FORM == kForm8) {
+            const uint32_t lo = x[2 * h], hi = x[2 * h + 1];
+            const float by = as_float(scale);
+            x[0] = T::template from_e4m3<false>(lo, by);
+            x[1] = T::template from_e4m3<true>(lo, by);
+            x[2] = T::template from_e4m3<false>(hi, by);
+            x[3] = T::template from_e4m3<true>(hi, by);
+        }
+        return x;
     }
     // Writes the loaded tile as 16-bit values.  `edge`: some row may not see some position; such a row's
     // weight is 0, but 0 * infinity is NaN, so infinities and NaN among the values become zeros (the kernel
@@ -94,25 +128,16 @@ struct Many {
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int row = row_of(i, tid);
-            if (DP == 96 && c >= DP / (E4M3 ? 16 : 8)) continue;
-            const bool top = E4M3 && __any(max(__builtin_bit_cast(uint32_t, ks[i]), __builtin_bit_cast(uint32_t, vs[i])) >= T::kTopScale);
+            if (DP == 96 && c >= DP / kLoad) continue;
+            const bool top = kScaled && __any(max(ks[i], vs[i]) >= (FORM == kForm4 ? T::kTopScale4 : T::kTopScale));
 #pragma unroll
-            for (int h = 0; h < (E4M3 ? 2 : 1); ++h) {
-                u32x4v x = k[i], y = v[i];
-                if (E4M3) {
+            for (int h = 0; h < kLoad / 8; ++h) {
+                u32x4v x = widen(k[i], ks[i], h), y = widen(v[i], vs[i], h);
+                if (kScaled && top) {
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        x[2 * w] = T::template from_e4m3<false>(k[i][2 * h + w], ks[i]);
-                        x[2 * w + 1] = T::template from_e4m3<true>(k[i][2 * h + w], ks[i]);
-                        y[2 * w] = T::template from_e4m3<false>(v[i][2 * h + w], vs[i]);
-                        y[2 * w + 1] = T::template from_e4m3<true>(v[i][2 * h + w], vs[i]);
-                    }
-                    if (top) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            x[w] = saturate<T>(x[w]);
-                            y[w] = saturate<T>(y[w]);
-                        }
+                    for (int w = 0; w < 4; ++w) {
+                        x[w] = saturate<T>(x[w]);
+                        y[w] = saturate<T>(y[w]);
                     }
                 }
                 if (edge) {
@@ -123,7 +148,7 @@ struct Many {
                         y[w] = f;
                     }
                 }
-                const int chunk = E4M3 ? 2 * c + h : c;
+                const int chunk = kLoad / 8 * c + h;
                 *(u32x4v*)(kb + key_at(row, chunk)) = x;
                 *(u32x4v*)(vb + val_at(row, chunk)) = y;
             }
@@ -132,9 +157,10 @@ struct Many {
     }
 };
 
-template <typename T, bool E4M3, int DP>
+// LSE: the logarithms of the rows' sums are written too.
+template <typename T, int FORM, int DP, bool LSE>
 __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArgs a) {
-    using F = Many<T, E4M3, DP>;
+    using F = Many<T, FORM, DP>;
     __shared__ __attribute__((aligned(16))) unsigned char sh[2][2][F::kTile];
     __shared__ float sh_m[kManyThreads];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -198,7 +224,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
         const int tile_all_high = a.causal ? min(q.len - q.n + end0 + 1, q.len) : q.len;
         const int tile_all_low = a.window ? q.len - q.n + end1 - a.window + 1 : 0;
 
-        float m = kNoScore, l = 0.f;
+        float m = kNoScore, l = 0.f, full = 0.f;  // full: the sum before the weights' rounding (LSE)
         f32x16v o[F::kBlocks];
 #pragma unroll
         for (int b = 0; b < F::kBlocks; ++b)
@@ -206,7 +232,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
             for (int i = 0; i < 16; ++i) o[b][i] = 0.f;
 
         F f;
-        const HeadBase hb(a, p.head, E4M3 ? 1 : 2);
+        HeadBase hb;
+        hb.set<F::kBits, F::kScaleBytes>(a.c, p.head);
         int t0 = t_base + p.unit * F::kTokens;
         f.look_up(a, p.seq, t0, wave);
         f.load(a, hb, t0, low, high, tid);
@@ -277,6 +304,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
                     const float by = exp2_fast(m - to);
                     m = to;
                     l *= by;
+                    if (LSE) full *= by;
 #pragma unroll
                     for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
@@ -301,6 +329,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
                         const float y = exp2_fast(__builtin_fmaf(s[ks / 2][8 * (ks % 2) + 2 * i + 1], slope, -m));
                         w[i] = T::pack(x, y);
                         l = T::add_pair(w[i], l);
+                        if (LSE) full += x + y;
                     }
                     return w;
                 };
@@ -330,6 +359,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
         }
         if (large) m = sh_m[tid];
         l = sum_halves(l);
+        if (LSE) full = sum_halves(full);
         // What follows runs once per item: addresses are worked out here, not kept in registers through
         // the loop above (the compiler would move them out of all loops).
         const int lane_e = opaque(lane), half_e = lane_e >> 5;
@@ -343,16 +373,21 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
                 const int at = t & (a.c.page_size - 1);
                 const bool seen = t < see_high && t >= see_low;
                 float vscale = 1.f;
-                if (E4M3)
+                if (FORM == kForm8)
                     vscale = as_float(__builtin_amdgcn_raw_buffer_load_b32(hb.value_scales(pg), seen ? at * 4 : kNoRow, 0, 0));
 #pragma unroll
                 for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; i += 4) {
                         const int d = 32 * b + 8 * (i / 4) + 4 * half_e;
-                        const int off = seen && d < D ? (at * D + d) * (E4M3 ? 1 : 2) : kNoRow;
+                        const int off = seen && d < D ? (at * D + d) * F::kBits / 8 : kNoRow;
                         u32x2v x;
-                        if (E4M3) {
+                        if constexpr (FORM == kForm4) {
+                            const uint32_t c = __builtin_amdgcn_raw_buffer_load_b16(hb.values(pg), off, 0, 0);
+                            const int by = seen && d < D ? at * F::kScaleBytes + d / kScaleGroup : kNoRow;
+                            vscale = as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b8(hb.value_scales(pg), by, 0, 0) << 23);
+                            x = u32x2v{saturate<T>(T::template from_e2m1<0>(c, vscale)), saturate<T>(T::template from_e2m1<1>(c, vscale))};
+                        } else if constexpr (FORM == kForm8) {
                             const uint32_t c = __builtin_amdgcn_raw_buffer_load_b32(hb.values(pg), off, 0, 0);
                             x = u32x2v{saturate<T>(T::template from_e4m3<false>(c, vscale)), saturate<T>(T::template from_e4m3<true>(c, vscale))};
                         } else {
@@ -369,15 +404,16 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
         }
 
         const bool whole = p.unit == 0 && last == units;
-        constexpr int64_t kFloats = (int64_t)kManyRows * (DP + 2);
+        constexpr int64_t kFull = (int64_t)kManyRows * (DP + 2), kFloats = kFull + (LSE ? kManyRows : 0);
         if (!whole) {
-            // A part: a pair (maximum, sum) per row, then each lane's values as it holds them.  The
-            // workgroup that has the item's first unit says what there is to join.
+            // A part: a pair (maximum, sum) per row, then each lane's values as it holds them, then (LSE) a full
+            // sum per row.  The workgroup that has the item's first unit says what there is to join.
             const int owner = cut.owner(item), behind = cut.owner(item + units - 1);
             float* mine = a.part + (int64_t)(2 * me + (p.unit == 0 ? 1 : 0)) * kFloats;
             if (tid == 0 && owner == me) a.record[me] = int4{behind - owner, p.seq, p.head, p.tile};
             if (row0 < q.rows) {
                 if (half_e == 0) *(float2*)(mine + 2 * (32 * wave + lane_e)) = float2{m, l};
+                if (LSE && half_e == 0) mine[kFull + 32 * wave + lane_e] = full;
 #pragma unroll
                 for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
@@ -388,6 +424,7 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
         } else if (live) {
             const float inv = l != 0.f ? 1.f / l : 0.f;
             uint16_t* op = (uint16_t*)a.o + (int64_t)(q.first + opaque(token)) * a.o_stride + (int64_t)opaque(qh) * D;
+            if (LSE && half_e == 0) a.lse[(int64_t)(q.first + opaque(token)) * a.q_heads + opaque(qh)] = log_of_sum(m, full);
 #pragma unroll
             for (int b = 0; b < F::kBlocks; ++b)
 #pragma unroll
@@ -411,10 +448,10 @@ __global__ __launch_bounds__(kManyThreads, 2) void attention_many_kernel(AttnArg
 // thread and part.  Parts are 256 rows: joined by an item's last workgroup inside the kernel above, they
 // came one after the other (64 new tokens of 32 heads over 8192 positions: 268 us that way).
 constexpr int kJoinGrid = 2048, kJoinMasks = 32;
-template <typename T, int DP>
+template <typename T, int DP, bool LSE>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int G) {
     constexpr int kBlocks = DP / 32, kSlabs = kManyWaves * kBlocks;
-    constexpr int64_t kFloats = (int64_t)kManyRows * (DP + 2);
+    constexpr int64_t kFull = (int64_t)kManyRows * (DP + 2), kFloats = kFull + (LSE ? kManyRows : 0);
     __shared__ uint64_t sh_mask[kJoinMasks];
     const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
     for (int g = i; g * 64 < G; g += 4) {
@@ -435,11 +472,12 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int G) 
         const Seq q = read_seq(a, __builtin_amdgcn_readfirstlane(rec.y));
         const int in_tile = 32 * wave + (lane & 31), row = rec.w * kManyRows + in_tile, behind = owner + rec.x;
         if (row >= q.rows) continue;
-        float m = kNoScore, l = 0.f;
+        float m = kNoScore, l = 0.f, full = 0.f;
         f32x4v o = {0.f, 0.f, 0.f, 0.f};
         constexpr int kBatch = 8;  // parts in flight
         for (int w0 = owner; w0 <= behind; w0 += kBatch) {
             float2 ml[kBatch];
+            float sum[kBatch];
             f32x4v x[kBatch];
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) {
@@ -447,6 +485,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int G) 
                 const int w = min(w0 + j, behind);
                 const float* part = a.part + (int64_t)(2 * w + (w == owner ? 1 : 0)) * kFloats;
                 ml[j] = *(const float2*)(part + 2 * in_tile);
+                if (LSE) sum[j] = part[kFull + in_tile];
                 x[j] = *(const f32x4v*)(part + 2 * kManyRows + ((slab * 4 + i) * 64 + lane) * 4);
             }
 #pragma unroll
@@ -455,11 +494,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int G) 
                 const float to = fmaxf(m, ml[j].x), b0 = exp2_fast(m - to), b1 = exp2_fast(ml[j].x - to);
                 m = to;
                 l = l * b0 + ml[j].y * b1;
+                if (LSE) full = full * b0 + sum[j] * b1;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) o[r] = o[r] * b0 + x[j][r] * b1;
             }
         }
         const int d = 32 * b + 8 * i + 4 * (lane >> 5);
+        if (LSE && d == 0)
+            a.lse[(int64_t)(q.first + row / a.share) * a.q_heads + rec.z * a.share + row % a.share] = log_of_sum(m, full);
         if (d >= a.c.head_dim) continue;
         const float inv = l != 0.f ? 1.f / l : 0.f;
         u32x2v out = {T::pack(o[0] * inv, o[1] * inv), T::pack(o[2] * inv, o[3] * inv)};
@@ -469,22 +511,36 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, int G) 
     }
 }
 
-template <typename T, bool E4M3, int DP>
+template <typename T, int FORM, int DP, bool LSE>
 hipError_t many_run(const AttnArgs& a, int grid, hipStream_t s) {
-    attention_many_kernel<T, E4M3, DP><<<grid, kManyThreads, 0, s>>>(a);
+    attention_many_kernel<T, FORM, DP, LSE><<<grid, kManyThreads, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attention_join_kernel<T, DP><<<kJoinGrid, 256, 0, s>>>(a, grid);
+    attention_join_kernel<T, DP, LSE><<<kJoinGrid, 256, 0, s>>>(a, grid);
     return hipGetLastError();
 }
 
-template <typename T, bool E4M3>
+template <typename T, int FORM, bool LSE>
 hipError_t many_dim(const AttnArgs& a, int grid, hipStream_t s) {
     const int D = a.c.head_dim;
-    if (D <= 64) return many_run<T, E4M3, 64>(a, grid, s);
-    if (D <= 96) return many_run<T, E4M3, 96>(a, grid, s);
-    if (D <= 128) return many_run<T, E4M3, 128>(a, grid, s);
-    return many_run<T, E4M3, 256>(a, grid, s);
+    if (D <= 64) return many_run<T, FORM, 64, LSE>(a, grid, s);
+    if (D <= 96) return many_run<T, FORM, 96, LSE>(a, grid, s);
+    if (D <= 128) return many_run<T, FORM, 128, LSE>(a, grid, s);
+    return many_run<T, FORM, 256, LSE>(a, grid, s);
+}
+
+template <typename T, int FORM>
+hipError_t many_form(const AttnArgs& a, int grid, hipStream_t s) {
+    return a.lse ? many_dim<T, FORM, true>(a, grid, s) : many_dim<T, FORM, false>(a, grid, s);
+}
+
+template <typename T>
+hipError_t many_type(const AttnArgs& a, int grid, hipStream_t s) {
+    switch (cache_form(a.c.type)) {
+        case kForm8: return many_form<T, kForm8>(a, grid, s);
+        case kForm4: return many_form<T, kForm4>(a, grid, s);
+        default: return many_form<T, kForm16>(a, grid, s);
+    }
 }
 
 }  // namespace
@@ -492,13 +548,11 @@ hipError_t many_dim(const AttnArgs& a, int grid, hipStream_t s) {
 int attention_many_grid(int cus) { return cus < 64 * kJoinMasks ? cus : 64 * kJoinMasks; }
 int attention_many_tokens(int dim) { return many_tokens(dim <= 64 ? 64 : dim <= 128 ? 128 : 256); }
 int64_t attention_many_floats(int dim) {
-    return (int64_t)kManyRows * ((dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : 256) + 2);
+    return (int64_t)kManyRows * ((dim <= 64 ? 64 : dim <= 96 ? 96 : dim <= 128 ? 128 : 256) + 3);
 }
 
 hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStream_t s) {
-    const bool e = a.c.type == LSCD_E4M3;
-    if (type == LSCD_F16) return e ? many_dim<F16, true>(a, grid, s) : many_dim<F16, false>(a, grid, s);
-    return e ? many_dim<BF16, true>(a, grid, s) : many_dim<BF16, false>(a, grid, s);
+    return type == LSCD_F16 ? many_type<F16>(a, grid, s) : many_type<BF16>(a, grid, s);
 }
 
 }  // namespace lscd

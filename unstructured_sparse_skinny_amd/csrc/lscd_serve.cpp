@@ -66,6 +66,11 @@ void free_quant(lscd_quant_s* h) {
     delete h;
 }
 
+lscd_status_t attend(lscd_attention_t h, const lscd_cache_t* cache, const void* q, int64_t q_stride, const int32_t* start,
+                     const int32_t* length, const int32_t* table, int64_t table_stride, int32_t table_pages,
+                     int32_t sequences, int64_t T, float scale, int32_t causal, int32_t window, void* o, int64_t o_stride,
+                     float* lse, int32_t type, void* stream);
+
 lscd_status_t check_quant(const lscd_quant_s* h) {
     int device = 0;
     if (hipGetDevice(&device) != hipSuccess) return LSCD_ERROR_HIP;
@@ -262,6 +267,27 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
                              const int32_t* start, const int32_t* length, const int32_t* table, int64_t table_stride,
                              int32_t table_pages, int32_t sequences, int64_t T, float scale, int32_t causal,
                              int32_t window, void* o, int64_t o_stride, int32_t type, void* stream) {
+    return attend(h, cache, q, q_stride, start, length, table, table_stride, table_pages, sequences, T, scale, causal, window,
+                  o, o_stride, nullptr, type, stream);
+}
+
+lscd_status_t lscd_attention_lse(lscd_attention_t h, const lscd_cache_t* cache, const void* q, int64_t q_stride,
+                                 const int32_t* start, const int32_t* length, const int32_t* table, int64_t table_stride,
+                                 int32_t table_pages, int32_t sequences, int64_t T, float scale, int32_t causal,
+                                 int32_t window, void* o, int64_t o_stride, float* lse, int32_t type, void* stream) {
+    if (T > 0 && sequences > 0 && !aligned(lse, 4)) return LSCD_ERROR_INVALID_VALUE;
+    return attend(h, cache, q, q_stride, start, length, table, table_stride, table_pages, sequences, T, scale, causal, window,
+                  o, o_stride, lse, type, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+lscd_status_t attend(lscd_attention_t h, const lscd_cache_t* cache, const void* q, int64_t q_stride, const int32_t* start,
+                     const int32_t* length, const int32_t* table, int64_t table_stride, int32_t table_pages,
+                     int32_t sequences, int64_t T, float scale, int32_t causal, int32_t window, void* o, int64_t o_stride,
+                     float* lse, int32_t type, void* stream) {
     if (!h) return LSCD_ERROR_INVALID_VALUE;
     lscd_status_t st = check_cache(cache);
     if (st != LSCD_SUCCESS) return st;
@@ -269,7 +295,7 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
     if ((type != LSCD_F16 && type != LSCD_BF16) || T < 0 || sequences < 0 || table_pages < 0 || window < 0 ||
         !isfinite(scale))
         return LSCD_ERROR_INVALID_VALUE;
-    if (cache->type != LSCD_E4M3 && cache->type != type) return LSCD_ERROR_NOT_SUPPORTED;
+    if (!scaled_form(cache->type) && cache->type != type) return LSCD_ERROR_NOT_SUPPORTED;
     if (T == 0 || sequences == 0) return LSCD_SUCCESS;
     const int64_t width = (int64_t)h->q_heads * h->head_dim;
     if (bad_rows(q, q_stride, width) || bad_rows(o, o_stride, width) || !aligned(start, 4) || !aligned(length, 4) ||
@@ -284,6 +310,7 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
     a.c = *cache;
     a.q = q;
     a.o = o;
+    a.lse = lse;
     a.q_stride = q_stride;
     a.o_stride = o_stride;
     a.table_stride = table_stride;
@@ -339,4 +366,4 @@ lscd_status_t lscd_attention(lscd_attention_t h, const lscd_cache_t* cache, cons
     return LSCD_SUCCESS;
 }
 
-}  // extern "C"
+}  // namespace

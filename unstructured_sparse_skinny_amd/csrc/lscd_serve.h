@@ -54,6 +54,7 @@ struct AttnArgs {
     float* part;             // partial results: two slots per workgroup
     uint32_t* count;         // arrivals, one per workgroup; zero between calls (few rows)
     int4* record;            // cut items, one per workgroup: parts - 1, sequence, key head, row tile (many rows)
+    float* lse;              // [T][q_heads], or null
 };
 // Workgroups of one launch at most, and floats of one partial result.
 int attention_few_grid(int cus);
