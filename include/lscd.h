@@ -547,6 +547,26 @@ lscd_status_t lscd_attention_lse(lscd_attention_t h, const lscd_cache_t* cache, 
                                  int32_t table_pages, int32_t sequences, int64_t T, float scale, int32_t causal,
                                  int32_t window, void* o, int64_t o_stride, float* lse, int32_t type, void* stream);
 
+/*
+ * lscd_cache_weigh -- how much the new tokens look at each cached position: for every sequence, its new tokens'
+ *   rows and each key head, the sum of the softmax weights exp(scale * q . k - lse) of the rows (tokens x query
+ *   heads of the key head) that see the position is put into (new tokens' positions) or added to (the others)
+ *   weight[slot].  Nothing else is written.  Arguments as in lscd_attention (q_heads a multiple of the cache's
+ *   heads; lse as lscd_attention_lse wrote it for the same rows); it follows it in a layer.
+ *   lse     device, [T][q_heads] floats.  A row of -infinity gives nothing.
+ *   weight  device, [num_pages][heads][page_size] floats, 16-byte aligned.
+ * No two sequences of a call may share a page of which one's new tokens see a position (sums would be lost).
+ * Sums are fp32, in a fixed order: bit-reproducible for the same call.  A weight is off by about 2^-24 of the
+ * largest score and of lse, relative.  Array contents outside the rules are clamped as in lscd_attention;
+ * positions in pages outside the pool have no weight.
+ * Asynchronous, no allocation, no workspace, graph-capturable.
+ * NOT_SUPPORTED as lscd_attention, with units of 16 query rows by 32 positions; q_heads above 65535.
+ */
+lscd_status_t lscd_cache_weigh(const lscd_cache_t* cache, const void* q, int64_t q_stride, int32_t q_heads,
+                               const float* lse, const int32_t* start, const int32_t* length, const int32_t* table,
+                               int64_t table_stride, int32_t table_pages, int32_t sequences, int64_t T, float scale,
+                               int32_t causal, int32_t window, float* weight, int32_t type, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

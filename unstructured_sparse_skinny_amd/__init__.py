@@ -40,7 +40,7 @@ EXPORTS = ("lscd_pack_size", "lscd_pack", "lscd_default_tile_m", "lscd_encode", 
            "lscd_linear_path", "lscd_set_linear_crossover", "lscd_linear_model", "lscd_tune_dense", "lscd_destroy",
            "lscd_status_string", "lscd_stream_read", "lscd_spmm_noalloc", "lscd_linear_times",
            "lscd_quant_encode", "lscd_quant_linear", "lscd_quant_decode", "lscd_quant_destroy",
-           "lscd_cache_write", "lscd_cache_read",
+           "lscd_cache_write", "lscd_cache_read", "lscd_cache_weigh",
            "lscd_attention_create", "lscd_attention", "lscd_attention_lse", "lscd_attention_destroy")
 
 LSCD_F16 = 0
@@ -114,6 +114,7 @@ def _load():
         "lscd_quant_destroy": [VP],
         "lscd_cache_write": [VP, VP, I64, VP, I64, VP, I64, I32, VP],
         "lscd_cache_read": [VP, VP, I64, VP, I64, VP, I64, I32, VP],
+        "lscd_cache_weigh": [VP, VP, I64, I32, VP, VP, VP, VP, I64, I32, I32, I64, ctypes.c_float, I32, I32, VP, I32, VP],
         "lscd_attention_create": [I32, I32, I32, P(VP)],
         "lscd_attention_destroy": [VP],
         "lscd_attention": [VP, VP, VP, I64, VP, VP, VP, I64, I32, I32, I64, ctypes.c_float, I32, I32, VP, I64, I32, VP],
@@ -628,6 +629,31 @@ def lscd_attention(h: Attention, cache: Cache, q, start, length, table, out, sca
         _check(_lib.lscd_attention_lse(*args, _lse(lse, T, h.q_heads, dev), kind, _stream_on(stream, dev)),
                "lscd_attention_lse")
     return out
+
+
+def _weights(t, cache):
+    if t.dtype != torch.float32 or tuple(t.shape) != (cache.struct.num_pages, cache.heads, cache.page_size) or \
+            not t.is_contiguous() or t.device != cache.device:
+        raise ValueError("weight must be a contiguous float32 tensor [pages][heads][page_size] on the cache's device")
+    return t.data_ptr()
+
+
+def lscd_cache_weigh(cache: Cache, q, lse, start, length, table, weight, scale=None, causal=True, window=0, stream=None):
+    """Put into (new tokens' positions) or add to (the others) weight [pages][heads][page_size] (float32) the softmax
+    weights that the new tokens q [T][q_heads][head_dim] give to the cached positions; lse [T][q_heads] as
+    lscd_attention wrote it for the same arguments."""
+    heads, T, S, dev = q.shape[1] if q.dim() == 3 else 0, q.shape[0], length.shape[0], cache.device
+    pq, sq = _rows(q, "q", heads, cache.head_dim, dev)
+    if q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be float16 or bfloat16")
+    if start.shape[0] != S + 1 or table.shape[0] != S:
+        raise ValueError("start must have one entry more than length, table as many rows")
+    pt = _ints(table, "table", dev, 2)
+    _check(_lib.lscd_cache_weigh(cache.ptr, pq, sq, heads, _lse(lse, T, heads, dev), _ints(start, "start", dev),
+                                 _ints(length, "length", dev), pt, table.stride(0) if S > 1 else table.shape[1],
+                                 table.shape[1], S, T, cache.head_dim ** -0.5 if scale is None else scale, causal, window,
+                                 _weights(weight, cache), _TYPES[q.dtype], _stream_on(stream, dev)), "lscd_cache_weigh")
+    return weight
 
 
 def lscd_attention_destroy(h: Attention):

@@ -25,79 +25,16 @@ namespace {
 
 constexpr int kFewWaves = 4;
 
-// FORM: how the cache holds its values.  DP: channels padded to 64, 128 or 256.
 template <typename T, int FORM, int DP>
-struct Few {
-    static constexpr bool kScaled = FORM != kForm16;
-    static constexpr int kBits = form_bits(FORM);
-    static constexpr int kScaleBytes = FORM == kForm4 ? scale_row(DP) : 4;  // of one token's scales
-    static constexpr int kSteps = DP / 32;  // MFMA steps over the channels of q . k
+struct Few : Keys<T, FORM, DP> {
+    using K = Keys<T, FORM, DP>;
+    using K::kBits;
+    using K::kScaleBytes;
+    using K::kScaled;
     static constexpr int VW = DP / 16;      // channels per lane of a value row
-    static constexpr int kKeyRegs = DP * kBits / 128;                       // words of one 16-token key tile per lane
     static constexpr int kValWords = VW * kBits >= 32 ? VW * kBits / 32 : 1;  // words of one value row per lane
-    static constexpr int kKeyScales = FORM == kForm4 && DP == 256 ? 2 : 1;    // scales of one key tile per lane
-    // 1 as a scale is loaded
-    static constexpr uint32_t kOne = FORM == kForm4 ? 127u : 0x3F800000u, kTop = FORM == kForm4 ? T::kTopScale4 : T::kTopScale;
-    uint32_t kr[2][kKeyRegs];
     uint32_t vr[8][kValWords];
-    uint32_t ks[2][kKeyScales], vs[8];  // scales as loaded: bits of a float (e4m3), exponent + 127 (e2m1)
-
-    // A key row of 4-bit codes lies in the four lane groups as 16 channels each, of 64 (DP 64), or as 32 each, of
-    // 128: the lane's channels of unit u of them have one scale.  Rows that end in the middle of 32 channels are
-    // loaded to their end, 16 channels too early; the query has zeros there.
-    __device__ static __forceinline__ int unit_channel(int u, int g) { return DP == 64 ? 16 * g : 128 * u + 32 * g; }
-    __device__ static __forceinline__ int unit_start(int u, int g, int D) {
-        return DP == 64 ? unit_channel(u, g) : min(unit_channel(u, g), D - 32);
-    }
-
-    // 32 positions from t0 on, in the pages of the table entries e; positions from `high` on are zero
-    // (lanes without a position read outside the descriptor, which costs no traffic).
-    __device__ __forceinline__ void load_keys(const AttnArgs& a, const HeadBase& hb, const int (&e)[2], int t0, int high,
-                                              int lane) {
-        const int D = a.c.head_dim;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int t = t0 + 16 * h, row = (t & (a.c.page_size - 1)) + (lane & 15);
-            const uint32_t p = page_of(a, e[h]);
-            const bool on = t + (lane & 15) < high;
-            const auto rs = hb.keys(p);
-            if (FORM == kForm8) {
-#pragma unroll
-                for (int u = 0; u < DP / 64; ++u) {
-                    const int d = 64 * u + 16 * (lane >> 4);
-                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? row * D + d : kNoRow, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
-                }
-                ks[h][0] = __builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0);
-            } else if (FORM == kForm4) {
-#pragma unroll
-                for (int u = 0; u < kKeyScales; ++u) {
-                    const int d = unit_channel(u, lane >> 4);
-                    const int at = on && d < D ? (row * D + unit_start(u, lane >> 4, D)) / 2 : kNoRow;
-                    if constexpr (DP == 64) {
-                        const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
-                        kr[h][0] = x[0];
-                        kr[h][1] = x[1];
-                    } else {
-                        const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
-                    }
-                    ks[h][u] = __builtin_amdgcn_raw_buffer_load_b8(hb.key_scales(p),
-                                                                   on && d < D ? row * kScaleBytes + d / kScaleGroup : kNoRow, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    const int d = 32 * s + 8 * (lane >> 4);
-                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? (row * D + d) * 2 : kNoRow, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) kr[h][4 * s + i] = x[i];
-                }
-            }
-        }
-    }
+    uint32_t vs[8];  // scales as loaded
 
     // Value rows of lane group g: positions 4g .. 4g+3 of each of the two 16-position halves.
     // Positions outside [low, high) are zero (their scales are left out by value_scale).
@@ -138,7 +75,7 @@ struct Few {
                     }
                 }
                 if (FORM == kForm4)
-                    vs[4 * h + j] = __builtin_amdgcn_raw_buffer_load_b8(hb.value_scales(p), 
+                    vs[4 * h + j] = __builtin_amdgcn_raw_buffer_load_b8(hb.value_scales(p),
                                                                       d < D ? (r0 + j) * kScaleBytes + d / kScaleGroup : kNoRow, 0, 0);
             }
         }
@@ -149,75 +86,26 @@ struct Few {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int pos = t0 + 16 * (j / 4) + 4 * (lane >> 4) + j % 4;
-            if (pos >= high || pos < low) vs[j] = kOne;
+            if (pos >= high || pos < low) vs[j] = K::kOne;
         }
     }
 
-    // Whether some key's or value's code times its scale may pass the type's largest value.  (Scales are
-    // positive: they compare as whole numbers.)
-    __device__ __forceinline__ bool top_keys() const {
-        if (!kScaled) return false;
-        uint32_t most = max(ks[0][0], ks[1][0]);
-        if (kKeyScales == 2) most = max(most, max(ks[0][kKeyScales - 1], ks[1][kKeyScales - 1]));
-        return __any(most >= kTop);
-    }
+    // top_keys() of the values.
     __device__ __forceinline__ bool top_values() const {
         if (!kScaled) return false;
         uint32_t most = vs[0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) most = max(most, vs[j]);
-        return __any(most >= kTop);
-    }
-    // Word of codes `w` in 16 bits.  TOP: saturated.  (The scale is opaque there, so that the conversions of
-    // the two forms are not taken for the same and moved out of their branches.)
-    template <bool HI, bool TOP>
-    __device__ static __forceinline__ uint32_t from_code(uint32_t w, uint32_t scale) {
-        if (TOP) return saturate<T>(T::template from_e4m3<HI>(w, as_float(opaque(scale))));
-        return T::template from_e4m3<HI>(w, as_float(scale));
-    }
-    template <int B, bool TOP>
-    __device__ static __forceinline__ uint32_t from_code4(uint32_t w, uint32_t scale) {
-        if (TOP) return saturate<T>(T::template from_e2m1<B>(w, as_float(opaque(scale << 23))));
-        return T::template from_e2m1<B>(w, as_float(scale << 23));
-    }
-    // The A operand of key half h, step s, in 16 bits.
-    template <bool TOP>
-    __device__ __forceinline__ u32x4v key_operand(int h, int s) const {
-        u32x4v x;
-        if constexpr (FORM == kForm4) {  // one word of codes per step
-            x[0] = from_code4<0, TOP>(kr[h][s], ks[h][s / 4]);
-            x[1] = from_code4<1, TOP>(kr[h][s], ks[h][s / 4]);
-            x[2] = from_code4<2, TOP>(kr[h][s], ks[h][s / 4]);
-            x[3] = from_code4<3, TOP>(kr[h][s], ks[h][s / 4]);
-        } else if constexpr (FORM == kForm8) {  // two words of codes per step: channels 16 g + 8 (s % 2) of the 64 of step s / 2
-            const uint32_t lo = kr[h][4 * (s / 2) + 2 * (s % 2)], hi = kr[h][4 * (s / 2) + 2 * (s % 2) + 1];
-            x[0] = from_code<false, TOP>(lo, ks[h][0]);
-            x[1] = from_code<true, TOP>(lo, ks[h][0]);
-            x[2] = from_code<false, TOP>(hi, ks[h][0]);
-            x[3] = from_code<true, TOP>(hi, ks[h][0]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = kr[h][4 * s + i];
-        }
-        return x;
-    }
-    // The channel that step s, lane group g begins with (the q operand uses the same order); D and more where it
-    // has none.
-    __device__ static __forceinline__ int step_channel(int s, int g, int D) {
-        if (FORM == kForm4) {
-            const int d = unit_start(s / 4, g, D) + 8 * (s % 4);
-            return d < unit_channel(s / 4, g) ? D : d;
-        }
-        return FORM == kForm8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+        return __any(most >= K::kTop);
     }
     // Word of channels 2w, 2w+1 of value row j in 16 bits.
     __device__ __forceinline__ uint32_t value_word(int j, int w) const {
         if (FORM == kForm4) {
             const uint32_t c = vr[j][w / 4];
-            return w % 4 == 0   ? from_code4<0, false>(c, vs[j])
-                   : w % 4 == 1 ? from_code4<1, false>(c, vs[j])
-                   : w % 4 == 2 ? from_code4<2, false>(c, vs[j])
-                                : from_code4<3, false>(c, vs[j]);
+            return w % 4 == 0   ? K::template from_code4<0, false>(c, vs[j])
+                   : w % 4 == 1 ? K::template from_code4<1, false>(c, vs[j])
+                   : w % 4 == 2 ? K::template from_code4<2, false>(c, vs[j])
+                                : K::template from_code4<3, false>(c, vs[j]);
         }
         if (FORM == kForm8) return w % 2 ? T::template from_e4m3<true>(vr[j][w / 2], as_float(vs[j])) : T::template from_e4m3<false>(vr[j][w / 2], as_float(vs[j]));
         return vr[j][w];

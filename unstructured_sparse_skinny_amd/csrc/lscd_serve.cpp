@@ -71,6 +71,43 @@ lscd_status_t attend(lscd_attention_t h, const lscd_cache_t* cache, const void* 
                      int32_t sequences, int64_t T, float scale, int32_t causal, int32_t window, void* o, int64_t o_stride,
                      float* lse, int32_t type, void* stream);
 
+// The arguments of query rows over cached positions, checked and put into *a.  (Where there is nothing to do, the
+// pointers are not looked at.)
+lscd_status_t check_rows(const lscd_cache_t* cache, const void* q, int64_t q_stride, int32_t q_heads, const int32_t* start,
+                         const int32_t* length, const int32_t* table, int64_t table_stride, int32_t table_pages,
+                         int32_t sequences, int64_t T, float scale, int32_t causal, int32_t window, int32_t type,
+                         lscd::AttnArgs* a) {
+    lscd_status_t st = check_cache(cache);
+    if (st != LSCD_SUCCESS) return st;
+    if ((type != LSCD_F16 && type != LSCD_BF16) || T < 0 || sequences < 0 || table_pages < 0 || window < 0 ||
+        !isfinite(scale) || q_heads < 1 || q_heads % cache->heads)
+        return LSCD_ERROR_INVALID_VALUE;
+    if (!scaled_form(cache->type) && cache->type != type) return LSCD_ERROR_NOT_SUPPORTED;
+    if (T == 0 || sequences == 0) return LSCD_SUCCESS;
+    if (bad_rows(q, q_stride, (int64_t)q_heads * cache->head_dim) || !aligned(start, 4) || !aligned(length, 4) ||
+        !aligned(table, 4) || table_pages < 1 || table_stride < table_pages)
+        return LSCD_ERROR_INVALID_VALUE;
+    const int64_t share = q_heads / cache->heads, span = (int64_t)table_pages * cache->page_size;
+    if (T > ((int64_t)1 << 30) / share || span > ((int64_t)1 << 30)) return LSCD_ERROR_NOT_SUPPORTED;
+    a->c = *cache;
+    a->q = q;
+    a->q_stride = q_stride;
+    a->table_stride = table_stride;
+    a->start = start;
+    a->length = length;
+    a->table = table;
+    a->table_pages = table_pages;
+    a->sequences = sequences;
+    a->q_heads = q_heads;
+    a->share = (int32_t)share;
+    a->causal = causal != 0;
+    a->window = (int32_t)std::min<int64_t>(window, (int64_t)1 << 30);
+    a->T = T;
+    a->scale_log2 = scale * 1.4426950408889634f;
+    a->page_log2 = __builtin_ctz((unsigned)cache->page_size);
+    return LSCD_SUCCESS;
+}
+
 lscd_status_t check_quant(const lscd_quant_s* h) {
     int device = 0;
     if (hipGetDevice(&device) != hipSuccess) return LSCD_ERROR_HIP;
@@ -280,6 +317,29 @@ lscd_status_t lscd_attention_lse(lscd_attention_t h, const lscd_cache_t* cache, 
                   o, o_stride, lse, type, stream);
 }
 
+lscd_status_t lscd_cache_weigh(const lscd_cache_t* cache, const void* q, int64_t q_stride, int32_t q_heads,
+                               const float* lse, const int32_t* start, const int32_t* length, const int32_t* table,
+                               int64_t table_stride, int32_t table_pages, int32_t sequences, int64_t T, float scale,
+                               int32_t causal, int32_t window, float* weight, int32_t type, void* stream) {
+    lscd::AttnArgs a = {};
+    lscd_status_t st = check_rows(cache, q, q_stride, q_heads, start, length, table, table_stride, table_pages, sequences, T,
+                                  scale, causal, window, type, &a);
+    if (st != LSCD_SUCCESS || T == 0 || sequences == 0) return st;
+    if (!aligned(lse, 4) || !aligned(weight, 16)) return LSCD_ERROR_INVALID_VALUE;
+    if (q_heads > 65535) return LSCD_ERROR_NOT_SUPPORTED;
+    // Slots of work are counted in 31 bits on the device.
+    const double span = (double)table_pages * cache->page_size;
+    if (((double)(T * a.share) / lscd::kFewRows + sequences) * (span / lscd::kWeighTokens + 1) * cache->heads >= 2147483647.0)
+        return LSCD_ERROR_NOT_SUPPORTED;
+    int device = 0, cus = 0;
+    hipError_t e = hipGetDevice(&device);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
+    if (e != hipSuccess || cus <= 0) return LSCD_ERROR_HIP;
+    a.row_lse = lse;
+    a.weight = weight;
+    return status_of(lscd::launch_weigh(a, type, cus, (hipStream_t)stream));
+}
+
 }  // extern "C"
 
 namespace {
@@ -292,40 +352,19 @@ lscd_status_t attend(lscd_attention_t h, const lscd_cache_t* cache, const void* 
     lscd_status_t st = check_cache(cache);
     if (st != LSCD_SUCCESS) return st;
     if (cache->heads != h->kv_heads || cache->head_dim != h->head_dim) return LSCD_ERROR_INVALID_VALUE;
-    if ((type != LSCD_F16 && type != LSCD_BF16) || T < 0 || sequences < 0 || table_pages < 0 || window < 0 ||
-        !isfinite(scale))
-        return LSCD_ERROR_INVALID_VALUE;
-    if (!scaled_form(cache->type) && cache->type != type) return LSCD_ERROR_NOT_SUPPORTED;
+    lscd::AttnArgs a = {};
+    st = check_rows(cache, q, q_stride, h->q_heads, start, length, table, table_stride, table_pages, sequences, T, scale,
+                    causal, window, type, &a);
+    if (st != LSCD_SUCCESS) return st;
     if (T == 0 || sequences == 0) return LSCD_SUCCESS;
-    const int64_t width = (int64_t)h->q_heads * h->head_dim;
-    if (bad_rows(q, q_stride, width) || bad_rows(o, o_stride, width) || !aligned(start, 4) || !aligned(length, 4) ||
-        !aligned(table, 4) || table_pages < 1 || table_stride < table_pages)
-        return LSCD_ERROR_INVALID_VALUE;
-    const int64_t share = h->q_heads / h->kv_heads, span = (int64_t)table_pages * cache->page_size;
-    if (T > ((int64_t)1 << 30) / share || span > ((int64_t)1 << 30)) return LSCD_ERROR_NOT_SUPPORTED;
+    if (bad_rows(o, o_stride, (int64_t)h->q_heads * h->head_dim)) return LSCD_ERROR_INVALID_VALUE;
+    const int64_t share = a.share, span = (int64_t)table_pages * cache->page_size;
     int device = 0;
     if (hipGetDevice(&device) != hipSuccess) return LSCD_ERROR_HIP;
     if (device != h->device) return LSCD_ERROR_INVALID_VALUE;
-    lscd::AttnArgs a = {};
-    a.c = *cache;
-    a.q = q;
     a.o = o;
     a.lse = lse;
-    a.q_stride = q_stride;
     a.o_stride = o_stride;
-    a.table_stride = table_stride;
-    a.start = start;
-    a.length = length;
-    a.table = table;
-    a.table_pages = table_pages;
-    a.sequences = sequences;
-    a.q_heads = h->q_heads;
-    a.share = (int32_t)share;
-    a.causal = causal != 0;
-    a.window = (int32_t)std::min<int64_t>(window, (int64_t)1 << 30);
-    a.T = T;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.page_log2 = __builtin_ctz((unsigned)cache->page_size);
     a.part = h->part;
     a.count = h->count;
     a.record = h->record;

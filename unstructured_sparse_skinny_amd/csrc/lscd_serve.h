@@ -55,6 +55,8 @@ struct AttnArgs {
     uint32_t* count;         // arrivals, one per workgroup; zero between calls (few rows)
     int4* record;            // cut items, one per workgroup: parts - 1, sequence, key head, row tile (many rows)
     float* lse;              // [T][q_heads], or null
+    const float* row_lse;    // the same as an input (weigh)
+    float* weight;           // [num_pages][heads][page_size] (weigh)
 };
 // Workgroups of one launch at most, and floats of one partial result.
 int attention_few_grid(int cus);
@@ -63,6 +65,8 @@ int attention_many_tokens(int dim);  // positions of one of the many-row kernel'
 int64_t attention_few_floats(int dim);
 int64_t attention_many_floats(int dim);
 hipError_t launch_attention_few(const AttnArgs& a, int type, int grid, hipStream_t s);
+hipError_t launch_weigh(const AttnArgs& a, int type, int cus, hipStream_t s);
+constexpr int kWeighTokens = 32;  // positions of one of its work units
 hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStream_t s);
 
 // ---------------------------------------------------------------- quantised product
