@@ -567,6 +567,30 @@ lscd_status_t lscd_cache_weigh(const lscd_cache_t* cache, const void* q, int64_t
                                int64_t table_stride, int32_t table_pages, int32_t sequences, int64_t T, float scale,
                                int32_t causal, int32_t window, float* weight, int32_t type, void* stream);
 
+/*
+ * lscd_cache_evict -- cut sequences to `keep` positions: of every sequence of more and every key head, the last
+ *   `recent` positions stay and, of the others, the keep - recent with the largest weights (the lower position
+ *   where weights are equal; NaN counts as the largest).  Each head keeps its own: its i-th kept position's keys,
+ *   values, scales and weight move to the i-th position of the pages of `to`, or in place.  The caller goes on
+ *   with length min(length, keep); positions already are in the keys, and later tokens see all that is kept.
+ *   Nothing else is written; in place, a sequence of up to `keep` positions stays as it is; with `to` it is
+ *   copied whole.
+ *   weight  device, [num_pages][heads][page_size] floats as lscd_cache_weigh adds them up, 16-byte aligned.
+ *   length, table  as in lscd_attention.
+ *   to      device; page j of sequence s is to[s * to_stride + j], to_pages of them, enough for `keep`
+ *           positions.  No page of it may be one that the call reads or that it names twice.  NULL (or `table`
+ *           itself): in place; a page of a sequence that is cut may then not be another sequence's too.
+ *   kept    device, [sequences][heads][keep]: the positions kept, ascending, then -1.
+ *   keep    1 and more;  recent  0..keep.
+ * Lengths outside the table are clamped to it; a page outside the pool is read as page 0 and not written.
+ * Asynchronous, no allocation, no workspace, graph-capturable.  NOT_SUPPORTED: table_pages * page_size above
+ * 2^30; sequences * heads * (keep / 32, or in place 1 and two for 128 bytes of a row) of 2^22 and more.
+ */
+lscd_status_t lscd_cache_evict(const lscd_cache_t* cache, float* weight, const int32_t* length, const int32_t* table,
+                               int64_t table_stride, int32_t table_pages, const int32_t* to, int64_t to_stride,
+                               int32_t to_pages, int32_t sequences, int32_t keep, int32_t recent, int32_t* kept,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif

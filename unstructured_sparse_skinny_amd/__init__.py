@@ -40,7 +40,7 @@ EXPORTS = ("lscd_pack_size", "lscd_pack", "lscd_default_tile_m", "lscd_encode", 
            "lscd_linear_path", "lscd_set_linear_crossover", "lscd_linear_model", "lscd_tune_dense", "lscd_destroy",
            "lscd_status_string", "lscd_stream_read", "lscd_spmm_noalloc", "lscd_linear_times",
            "lscd_quant_encode", "lscd_quant_linear", "lscd_quant_decode", "lscd_quant_destroy",
-           "lscd_cache_write", "lscd_cache_read", "lscd_cache_weigh",
+           "lscd_cache_write", "lscd_cache_read", "lscd_cache_weigh", "lscd_cache_evict",
            "lscd_attention_create", "lscd_attention", "lscd_attention_lse", "lscd_attention_destroy")
 
 LSCD_F16 = 0
@@ -115,6 +115,7 @@ def _load():
         "lscd_cache_write": [VP, VP, I64, VP, I64, VP, I64, I32, VP],
         "lscd_cache_read": [VP, VP, I64, VP, I64, VP, I64, I32, VP],
         "lscd_cache_weigh": [VP, VP, I64, I32, VP, VP, VP, VP, I64, I32, I32, I64, ctypes.c_float, I32, I32, VP, I32, VP],
+        "lscd_cache_evict": [VP, VP, VP, VP, I64, I32, VP, I64, I32, I32, I32, I32, VP, VP],
         "lscd_attention_create": [I32, I32, I32, P(VP)],
         "lscd_attention_destroy": [VP],
         "lscd_attention": [VP, VP, VP, I64, VP, VP, VP, I64, I32, I32, I64, ctypes.c_float, I32, I32, VP, I64, I32, VP],
@@ -654,6 +655,25 @@ def lscd_cache_weigh(cache: Cache, q, lse, start, length, table, weight, scale=N
                                  table.shape[1], S, T, cache.head_dim ** -0.5 if scale is None else scale, causal, window,
                                  _weights(weight, cache), _TYPES[q.dtype], _stream_on(stream, dev)), "lscd_cache_weigh")
     return weight
+
+
+def lscd_cache_evict(cache: Cache, weight, length, table, keep: int, recent: int = 0, to=None, kept=None, stream=None):
+    """Cut every sequence to its last `recent` positions and those of the others with the largest weights, `keep` in
+    all for each key head, moved in their order to the front of its pages (in place) or of those of `to` (int32
+    [sequences][pages]).  Returns the positions kept, int32 [sequences][heads][keep], -1 behind them."""
+    S, dev = length.shape[0], cache.device
+    if table.shape[0] != S or (to is not None and to.shape[0] != S):
+        raise ValueError("tables must have a row for every length")
+    if kept is None:
+        kept = torch.empty((S, cache.heads, max(keep, 0)), dtype=torch.int32, device=dev)
+    if kept.dtype != torch.int32 or tuple(kept.shape) != (S, cache.heads, keep) or not kept.is_contiguous() or kept.device != dev:
+        raise ValueError(f"kept must be a contiguous int32 tensor [{S}][{cache.heads}][{keep}] on the cache's device")
+    wide = [0, 0] if to is None else [to.stride(0) if S > 1 else to.shape[1], to.shape[1]]
+    _check(_lib.lscd_cache_evict(cache.ptr, _weights(weight, cache), _ints(length, "length", dev), _ints(table, "table", dev, 2),
+                                 table.stride(0) if S > 1 else table.shape[1], table.shape[1],
+                                 None if to is None else _ints(to, "to", dev, 2), *wide, S, keep, recent, kept.data_ptr(),
+                                 _stream_on(stream, dev)), "lscd_cache_evict")
+    return kept
 
 
 def lscd_attention_destroy(h: Attention):

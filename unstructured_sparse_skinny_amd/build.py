@@ -24,7 +24,8 @@ SOURCES = ["csrc/lscd_skinny64.hip", "csrc/lscd_skinny32.hip", "csrc/lscd_skinny
            "csrc/lscd_bitmap.hip", "csrc/lscd_wide.hip", "csrc/lscd_kernels.hip", "csrc/lscd_encode_dev.hip",
            "csrc/lscd_attention_many.hip", "csrc/lscd_quant_bf16.hip", "csrc/lscd_quant_f16.hip",
            "csrc/lscd_quant.hip",
-           "csrc/lscd_attention_few.hip", "csrc/lscd_weigh.hip", "csrc/lscd_cache.hip", "csrc/lscd_serve.cpp",
+           "csrc/lscd_attention_few.hip", "csrc/lscd_weigh.hip", "csrc/lscd_evict.hip",
+           "csrc/lscd_cache.hip", "csrc/lscd_serve.cpp",
            "csrc/lscd_api.cpp", "csrc/lscd_linear.cpp", "csrc/lscd_pack.cpp"]
 # Device sources of each format's product (their hash identifies the kernels behind a committed
 # measurement of that format; the split-K reduction and the shared helpers belong to all).

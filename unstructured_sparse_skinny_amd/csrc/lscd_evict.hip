@@ -1,0 +1,289 @@
+// Eviction from a paged cache: of every sequence and key head, the last positions and those of the others with
+// the largest weights are kept and moved, in their order, to the front of the sequence's pages (or of others).
+//
+// Which ones: one workgroup per sequence and head finds the k-th largest weight among n by its digits, 11, 11 and
+// 10 bits from the top: a histogram in LDS says in which digit's bin the k-th lies, and the next digit is looked
+// at among that bin's weights only.  Weights are compared as whole numbers in the order of their values.  With the
+// threshold known, every wavefront counts what of its stretch is above it and equal to it, and then writes the
+// positions in order: equal ones from the lowest position on until there are k.  Nothing depends on the order of
+// the histogram's atomics.
+//
+// Moving: position i of the front takes the i-th position kept, which is i or more.  Into other pages the rows are
+// independent.  In place, a workgroup takes a column of the rows (128 bytes of keys or values, or the scales and
+// weights) from the front to the back: it reads as many rows as its registers hold before it writes them, and what
+// it writes lies before everything that is still to be read.
+
+#include "lscd_serve.h"
+#include "lscd_serve_device.h"
+
+namespace lscd {
+namespace {
+
+constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / 64;
+constexpr int kBins = 2048;
+
+// Order of the weights: larger values have larger keys, zeros are equal, NaN counts as the largest.
+__device__ __forceinline__ uint32_t key_of(float w) {
+    if (w != w) return 0xFFFFFFFFu;
+    const uint32_t b = __builtin_bit_cast(uint32_t, w + 0.f);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+struct Kept {
+    int len, all, first;  // the sequence's positions; how many stay; the first of the last ones, which stay anyway
+    __device__ __forceinline__ Kept(const EvictArgs& a, int s) {
+        len = (int)min(max((int64_t)a.length[s], (int64_t)0), (int64_t)a.table_pages * a.c.page_size);
+        all = min(len, a.keep);
+        first = len - min(a.recent, all);
+    }
+};
+
+// The page that a table names (page 0 for an entry outside the pool).
+__device__ __forceinline__ int64_t page_at(const EvictArgs& a, const int32_t* table, int64_t stride, int s, int page) {
+    const int32_t e = table[s * stride + page];
+    return (uint32_t)e < (uint32_t)a.c.num_pages ? e : 0;
+}
+
+// KEYS: weights that LDS holds; longer sequences are read again for every digit.
+template <int KEYS>
+__global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(EvictArgs a) {
+    __shared__ uint32_t keys[KEYS];
+    __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t sums[2 * kSelectWaves];
+    __shared__ uint32_t found[2];  // a digit, and how many of its bin are wanted
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int s = blockIdx.x / a.c.heads, h = blockIdx.x % a.c.heads;
+    const Kept kp(a, s);
+    int32_t* out = a.kept + ((int64_t)s * a.c.heads + h) * a.keep;
+    for (int i = kp.all + tid; i < a.keep; i += kSelectThreads) out[i] = -1;
+    const int n = kp.first, k = kp.all - (kp.len - kp.first);  // k of the first n
+    for (int i = tid; i < kp.len - n; i += kSelectThreads) out[k + i] = n + i;
+    if (k == n) {
+        for (int i = tid; i < n; i += kSelectThreads) out[i] = i;
+        return;
+    }
+    if (k == 0) return;
+    auto load = [&](int j) {
+        const int64_t p = page_at(a, a.table, a.table_stride, s, j >> a.page_log2);
+        return key_of(a.weight[(p * a.c.heads + h) * a.c.page_size + (j & (a.c.page_size - 1))]);
+    };
+    const bool held = n <= KEYS;
+    if (held)
+        for (int j = tid; j < n; j += kSelectThreads) keys[j] = load(j);
+    auto key = [&](int j) { return held ? keys[j] : load(j); };
+
+    uint32_t prefix = 0, mask = 0;  // the digits found, and their bits
+    uint32_t want = (uint32_t)k;
+    for (int digit = 0; digit < 3; ++digit) {
+        const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bins = digit == 2 ? 1024 : 2048;
+        for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+        __syncthreads();
+        for (int j = tid; j < n; j += kSelectThreads) {
+            const uint32_t x = key(j);
+            if ((x & mask) == prefix) atomicAdd(&hist[(x >> shift) & (bins - 1)], 1u);
+        }
+        __syncthreads();
+        // two bins a thread, from the top: how many keys lie above and in them
+        const int top = kBins - 1 - 2 * tid;
+        const uint32_t c0 = hist[top], c1 = hist[top - 1];
+        uint32_t sum = c0 + c1;
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t up = __shfl_up(sum, d, 64);
+            if (lane >= d) sum += up;
+        }
+        if (lane == 63) sums[wave] = sum;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w) sum += sums[w];
+        const uint32_t above = sum - c0 - c1;
+        if (above < want && want <= sum) {
+            const bool upper = want <= above + c0;
+            found[0] = upper ? top : top - 1;
+            found[1] = want - above - (upper ? 0u : c0);
+        }
+        __syncthreads();
+        prefix |= found[0] << shift;
+        mask |= (uint32_t)(bins - 1) << shift;
+        want = found[1];
+    }
+    // `prefix` is the k-th largest key, `want` how many keys equal to it are kept.  Stretches of whole wavefronts:
+    const int per = (n + kSelectThreads - 1) / kSelectThreads * 64;
+    const int low = min(wave * per, n), high = min(low + per, n);
+    uint32_t more = 0, same = 0;
+    for (int j0 = low; j0 < high; j0 += 64) {
+        const bool on = j0 + lane < high;
+        const uint32_t x = on ? key(j0 + lane) : 0u;
+        more += __popcll(__ballot(on && x > prefix));
+        same += __popcll(__ballot(on && x == prefix));
+    }
+    if (lane == 0) {
+        sums[wave] = more;
+        sums[kSelectWaves + wave] = same;
+    }
+    __syncthreads();
+    more = same = 0;
+    for (int w = 0; w < wave; ++w) {
+        more += sums[w];
+        same += sums[kSelectWaves + w];
+    }
+    const uint64_t below = ((uint64_t)1 << lane) - 1;
+    for (int j0 = low; j0 < high; j0 += 64) {
+        const bool on = j0 + lane < high;
+        const uint32_t x = on ? key(j0 + lane) : 0u;
+        const uint64_t gt = __ballot(on && x > prefix), eq = __ballot(on && x == prefix);
+        const uint32_t g = more + __popcll(gt & below), e = same + __popcll(eq & below);
+        if (on && (x > prefix || (x == prefix && e < want))) out[g + min(e, want)] = j0 + lane;
+        more += __popcll(gt);
+        same += __popcll(eq);
+    }
+}
+
+// A row of the cache: its number among all rows of all heads, or -1.
+__device__ __forceinline__ int64_t row_at(const EvictArgs& a, const int32_t* table, int64_t stride, int s, int h, int i) {
+    const int32_t e = table[s * stride + (i >> a.page_log2)];
+    if ((uint32_t)e >= (uint32_t)a.c.num_pages) return -1;
+    return ((int64_t)e * a.c.heads + h) * a.c.page_size + (i & (a.c.page_size - 1));
+}
+
+// A scale row (1, 2, 4 or 8 bytes; 0: there are none) from one row to another.
+__device__ __forceinline__ void move_scale(void* p, int bytes, int64_t from, int64_t to) {
+    if (bytes == 8)
+        ((uint64_t*)p)[to] = ((const uint64_t*)p)[from];
+    else if (bytes == 4)
+        ((uint32_t*)p)[to] = ((const uint32_t*)p)[from];
+    else if (bytes == 2)
+        ((uint16_t*)p)[to] = ((const uint16_t*)p)[from];
+}
+
+// Into other pages: a workgroup takes kMoveRows kept rows of the keys or the values of one sequence and head.
+constexpr int kMoveRows = 64, kMoveThreads = 256;
+template <typename U>
+__global__ __launch_bounds__(kMoveThreads) void evict_copy_kernel(EvictArgs a, int chunks) {
+    __shared__ int64_t src[kMoveRows], dst[kMoveRows];
+    const int tid = threadIdx.x, z = blockIdx.x & 1;
+    const int chunk = (blockIdx.x >> 1) % chunks, sh = (blockIdx.x >> 1) / chunks;
+    const int s = sh / a.c.heads, h = sh % a.c.heads, i0 = chunk * kMoveRows;
+    const int rows = min(Kept(a, s).all - i0, kMoveRows);
+    if (rows <= 0) return;
+    if (tid < rows) {
+        const int from = a.kept[((int64_t)s * a.c.heads + h) * a.keep + i0 + tid];
+        const int64_t p = page_at(a, a.table, a.table_stride, s, from >> a.page_log2);
+        src[tid] = (p * a.c.heads + h) * a.c.page_size + (from & (a.c.page_size - 1));
+        dst[tid] = row_at(a, a.to, a.to_stride, s, h, i0 + tid);
+        if (dst[tid] >= 0) {
+            if (z == 0) a.weight[dst[tid]] = a.weight[src[tid]];
+            move_scale(z ? a.c.v_scale : a.c.k_scale, a.scale_bytes, src[tid], dst[tid]);
+        }
+    }
+    __syncthreads();
+    const int units = a.row_bytes / (int)sizeof(U);
+    U* data = (U*)(z ? a.c.v : a.c.k);
+#pragma unroll 4
+    for (int i = tid; i < rows * units; i += kMoveThreads) {
+        const int r = i / units, u = i % units;
+        if (dst[r] >= 0) data[dst[r] * units + u] = data[src[r] * units + u];
+    }
+}
+
+// In place: see above.  blockIdx.x: sequence and head, and a column: kColumn bytes of the keys, of the values, or
+// (the last) scales and weights.
+constexpr int kInPlaceThreads = 1024, kColumn = 128, kAhead = 4;
+template <typename U>
+__global__ __launch_bounds__(kInPlaceThreads) void evict_in_place_kernel(EvictArgs a, int columns) {
+    const int tid = threadIdx.x;
+    const int column = blockIdx.x % (2 * columns + 1), sh = blockIdx.x / (2 * columns + 1);
+    const int s = sh / a.c.heads, h = sh % a.c.heads;
+    const Kept kp(a, s);
+    if (kp.len <= a.keep) return;
+    const int32_t* kept = a.kept + ((int64_t)s * a.c.heads + h) * a.keep;
+    auto source = [&](int i) {
+        const int from = kept[i];
+        return (page_at(a, a.table, a.table_stride, s, from >> a.page_log2) * a.c.heads + h) * a.c.page_size +
+               (from & (a.c.page_size - 1));
+    };
+    // Reads of a round are complete before its writes begin; nothing of a later round's reads is written before.
+    auto all_read = [&]() {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __syncthreads();
+    };
+    if (column == 2 * columns) {
+        for (int i0 = 0; i0 < kp.all; i0 += kInPlaceThreads) {
+            const int i = i0 + tid;
+            const int64_t to = i < kp.all ? row_at(a, a.table, a.table_stride, s, h, i) : -1;
+            const int64_t from = to >= 0 ? source(i) : 0;
+            float w = 0.f;
+            uint64_t x[2] = {0, 0};
+            if (to >= 0) {
+                w = a.weight[from];
+                for (int z = 0; z < 2; ++z) {
+                    const void* p = z ? a.c.v_scale : a.c.k_scale;
+                    if (a.scale_bytes == 8) x[z] = ((const uint64_t*)p)[from];
+                    if (a.scale_bytes == 4) x[z] = ((const uint32_t*)p)[from];
+                    if (a.scale_bytes == 2) x[z] = ((const uint16_t*)p)[from];
+                }
+            }
+            all_read();
+            if (to >= 0) {
+                a.weight[to] = w;
+                for (int z = 0; z < 2; ++z) {
+                    void* p = z ? a.c.v_scale : a.c.k_scale;
+                    if (a.scale_bytes == 8) ((uint64_t*)p)[to] = x[z];
+                    if (a.scale_bytes == 4) ((uint32_t*)p)[to] = (uint32_t)x[z];
+                    if (a.scale_bytes == 2) ((uint16_t*)p)[to] = (uint16_t)x[z];
+                }
+            }
+        }
+        return;
+    }
+    const int units = a.row_bytes / (int)sizeof(U), wide = kColumn / (int)sizeof(U);
+    const int u0 = column % columns * wide, mine = min(wide, units - u0);  // units of this column
+    const int r = tid / mine, u = u0 + tid % mine, per = kInPlaceThreads / mine;
+    U* data = (U*)(column >= columns ? a.c.v : a.c.k);
+    for (int i0 = 0; i0 < kp.all; i0 += kAhead * per) {
+        int64_t to[kAhead];
+        U x[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            x[j] = U{};
+            const int i = i0 + j * per + r;
+            to[j] = r < per && i < kp.all ? row_at(a, a.table, a.table_stride, s, h, i) : -1;
+            if (to[j] >= 0) x[j] = data[source(i) * units + u];
+        }
+        all_read();
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (to[j] >= 0) data[to[j] * units + u] = x[j];
+    }
+}
+
+int move_chunks(const EvictArgs& a) { return (a.keep + kMoveRows - 1) / kMoveRows; }
+int move_columns(const EvictArgs& a) { return (a.row_bytes + kColumn - 1) / kColumn; }
+
+template <typename U>
+hipError_t move(const EvictArgs& a, hipStream_t s) {
+    const unsigned groups = (unsigned)evict_workgroups(a);
+    if (a.to)
+        evict_copy_kernel<U><<<groups, kMoveThreads, 0, s>>>(a, move_chunks(a));
+    else
+        evict_in_place_kernel<U><<<groups, kInPlaceThreads, 0, s>>>(a, move_columns(a));
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t evict_workgroups(const EvictArgs& a) {
+    return (int64_t)a.sequences * a.c.heads * (a.to ? 2 * (int64_t)move_chunks(a) : 2 * move_columns(a) + 1);
+}
+
+hipError_t launch_evict(const EvictArgs& a, hipStream_t s) {
+    const unsigned pairs = (unsigned)((int64_t)a.sequences * a.c.heads);
+    // (two workgroups a CU with the smaller one)
+    if ((int64_t)a.table_pages * a.c.page_size <= 16384)
+        evict_select_kernel<16384><<<pairs, kSelectThreads, 0, s>>>(a);
+    else
+        evict_select_kernel<36864><<<pairs, kSelectThreads, 0, s>>>(a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    return a.row_bytes % 16 ? move<u32x2v>(a, s) : move<u32x4v>(a, s);
+}
+
+}  // namespace lscd

@@ -340,6 +340,42 @@ lscd_status_t lscd_cache_weigh(const lscd_cache_t* cache, const void* q, int64_t
     return status_of(lscd::launch_weigh(a, type, cus, (hipStream_t)stream));
 }
 
+lscd_status_t lscd_cache_evict(const lscd_cache_t* cache, float* weight, const int32_t* length, const int32_t* table,
+                               int64_t table_stride, int32_t table_pages, const int32_t* to, int64_t to_stride,
+                               int32_t to_pages, int32_t sequences, int32_t keep, int32_t recent, int32_t* kept,
+                               void* stream) {
+    lscd_status_t st = check_cache(cache);
+    if (st != LSCD_SUCCESS) return st;
+    if (sequences < 0 || keep < 1 || recent < 0 || recent > keep) return LSCD_ERROR_INVALID_VALUE;
+    if (sequences == 0) return LSCD_SUCCESS;
+    if (!aligned(weight, 16) || !aligned(length, 4) || !aligned(table, 4) || !aligned(kept, 4) || table_pages < 1 ||
+        table_stride < table_pages || ((uintptr_t)to & 3))
+        return LSCD_ERROR_INVALID_VALUE;
+    const int64_t page = cache->page_size;
+    if (to && (to_pages < 1 || to_stride < to_pages || to_pages * page < keep)) return LSCD_ERROR_INVALID_VALUE;
+    if (table_pages * page > ((int64_t)1 << 30)) return LSCD_ERROR_NOT_SUPPORTED;
+    lscd::EvictArgs a = {};
+    a.c = *cache;
+    a.weight = weight;
+    a.length = length;
+    a.table = table;
+    a.to = to == table ? nullptr : to;
+    a.table_stride = table_stride;
+    a.to_stride = to_stride;
+    a.kept = kept;
+    a.table_pages = table_pages;
+    a.sequences = sequences;
+    a.keep = keep;
+    a.recent = recent;
+    a.page_log2 = __builtin_ctz((unsigned)page);
+    a.row_bytes = cache->head_dim * lscd::form_bits(lscd::cache_form(cache->type)) / 8;
+    a.scale_bytes = cache->type == LSCD_E4M3 ? 4 : cache->type == LSCD_E2M1 ? lscd::scale_row(cache->head_dim) : 0;
+    // (a dimension of a grid has fewer than 2^32 threads, 1024 of them a workgroup at most)
+    if ((int64_t)sequences * cache->heads >= ((int64_t)1 << 22) || lscd::evict_workgroups(a) >= ((int64_t)1 << 22))
+        return LSCD_ERROR_NOT_SUPPORTED;
+    return status_of(lscd::launch_evict(a, (hipStream_t)stream));
+}
+
 }  // extern "C"
 
 namespace {

@@ -69,6 +69,23 @@ hipError_t launch_weigh(const AttnArgs& a, int type, int cus, hipStream_t s);
 constexpr int kWeighTokens = 32;  // positions of one of its work units
 hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStream_t s);
 
+// ---------------------------------------------------------------- eviction
+struct EvictArgs {
+    lscd_cache_t c;
+    float* weight;                // [num_pages][heads][page_size]
+    const int32_t* length;
+    const int32_t* table;
+    const int32_t* to;            // other pages, or null: the same
+    int64_t table_stride, to_stride;
+    int32_t* kept;                // [sequences][heads][keep]
+    int32_t table_pages, sequences, keep, recent;
+    int32_t page_log2;
+    int32_t row_bytes, scale_bytes;  // of one position and head of keys or values, and of its scales
+};
+// Workgroups of its largest launch.
+int64_t evict_workgroups(const EvictArgs& a);
+hipError_t launch_evict(const EvictArgs& a, hipStream_t s);
+
 // ---------------------------------------------------------------- quantised product
 // Device layout of the codes: row tiles of 16 rows, units of 128 columns, [row tile][unit][64 lanes]
 // [4 words].  Lane l of a unit has row l % 16; word s its 8 codes of columns 32 s + 8 (l / 16) + 0..7,
