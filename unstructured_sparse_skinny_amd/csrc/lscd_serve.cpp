@@ -337,7 +337,10 @@ lscd_status_t lscd_cache_weigh(const lscd_cache_t* cache, const void* q, int64_t
     if (e != hipSuccess || cus <= 0) return LSCD_ERROR_HIP;
     a.row_lse = lse;
     a.weight = weight;
-    return status_of(lscd::launch_weigh(a, type, cus, (hipStream_t)stream));
+    // The same choice as for attention: one launch where no sequence can have many rows, or there is only one.
+    const bool both = T * a.share > lscd::kWeighRows && T > sequences;
+    a.few_limit = !both ? 0x7FFFFFFF : sequences > 1 ? lscd::kWeighRows : 0;
+    return status_of(lscd::launch_weigh(a, type, cus, !both ? 1 : sequences > 1 ? 3 : 2, (hipStream_t)stream));
 }
 
 lscd_status_t lscd_cache_evict(const lscd_cache_t* cache, float* weight, const int32_t* length, const int32_t* table,

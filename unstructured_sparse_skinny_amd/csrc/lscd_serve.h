@@ -65,8 +65,9 @@ int attention_many_tokens(int dim);  // positions of one of the many-row kernel'
 int64_t attention_few_floats(int dim);
 int64_t attention_many_floats(int dim);
 hipError_t launch_attention_few(const AttnArgs& a, int type, int grid, hipStream_t s);
-hipError_t launch_weigh(const AttnArgs& a, int type, int cus, hipStream_t s);
+hipError_t launch_weigh(const AttnArgs& a, int type, int cus, int which, hipStream_t s);
 constexpr int kWeighTokens = 32;  // positions of one of its work units
+constexpr int kWeighRows = 64;    // sequences of more query rows go to its kernel for many
 hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStream_t s);
 
 // ---------------------------------------------------------------- eviction

@@ -24,7 +24,8 @@ static_assert(kWeighTokens == 32, "a unit is two key tiles of 16 positions");
 struct Stretch {
     int low, high, units, cost;
     __device__ __forceinline__ void measure(const AttnArgs& a, const Seq& q) {
-        high = q.rows > 0 ? q.len : 0;  // (the last token sees all with or without causality)
+        // (the last token sees all with or without causality)
+        high = q.rows > 0 && q.rows <= a.few_limit ? q.len : 0;
         low = a.window ? min(max(q.len - q.n - a.window + 1, 0), high) : 0;
         units = high > low ? (high + kWeighTokens - 1) / kWeighTokens - low / kWeighTokens : 0;
         cost = (q.rows + kFewRows - 1) / kFewRows;
@@ -179,31 +180,308 @@ __global__ __launch_bounds__(64 * kWeighWaves) void weigh_few_kernel(AttnArgs a)
     }
 }
 
+// Many rows: a workgroup has kBlockTokens positions, whose keys its four wavefronts all hold in registers (as
+// 16-bit values) while they stream the query rows past them, 32 at a time and every wavefront its own; at the end
+// the four sums of each position are added.  A wavefront brings its next rows into its part of LDS by loads that
+// pass no registers, and reads them back as it needs them: no barrier inside the loop.  Per 32 rows and 128
+// positions of 128 channels that is 8 KB of LDS read against 32 matrix instructions of 32 cycles, and 64
+// exponentials of 16 cycles with two more instructions each beside them, which bound it.
+template <typename T, int FORM, int DP>
+struct Block {
+    static constexpr int kTiles = DP <= 128 ? 4 : 2;       // key tiles of 32 positions: what the registers hold
+    static constexpr int kTokens = 32 * kTiles;
+    static constexpr int kSteps = DP / 16;                 // matrix instructions of a tile
+    static constexpr int kChunks = DP / 8;                 // 16-byte chunks of a query row
+    static constexpr int kRowMask = DP == 96 ? 3 : DP == 64 ? 7 : 15;
+    static constexpr int kTile = 32 * DP * 2;              // bytes of 32 query rows
+    static constexpr int kBits = form_bits(FORM);
+    static constexpr int kScaleBytes = FORM == kForm4 ? scale_row(DP) : 4;
+
+    // The chunk of channels that step s has in the lanes of half `half`: what one load of a key row brings.
+    __device__ static __forceinline__ int chunk(int s, int half) {
+        return FORM == kForm4 ? 8 * (s / 4) + 4 * half + s % 4 : FORM == kForm8 ? 4 * (s / 2) + 2 * half + s % 2 : 2 * s + half;
+    }
+
+    u32x4v key[kTiles][kSteps];
+
+    // Positions t0 .. of the lane's columns; zeros outside [low, high) and behind a row's end.
+    __device__ __forceinline__ void load(const AttnArgs& a, int seq, int head, int t0, int low, int high, int lane) {
+        const int D = a.c.head_dim, half = lane >> 5, page = a.c.page_size;
+        const int bytes = D * kBits / 8;
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) {
+            const int t = t0 + 32 * i + (lane & 31);
+            const bool on = t >= low && t < high;
+            const uint32_t p = on ? page_of(a, a.table[seq * a.table_stride + (t >> a.page_log2)]) : 0u;
+            const int64_t row = ((int64_t)p * a.c.heads + head) * page + (t & (page - 1));
+            const uint8_t* k = (const uint8_t*)a.c.k + row * bytes;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int d = 8 * chunk(s, half);
+                u32x4v x = {0u, 0u, 0u, 0u};
+                if (on && d < D) {
+                    if constexpr (FORM == kForm4) {
+                        const uint32_t w = *(const uint32_t*)(k + d / 2);
+                        const uint32_t by = ((const uint8_t*)a.c.k_scale)[row * scale_row(D) + d / kScaleGroup];
+                        const float scale = as_float(by << 23);
+                        x = u32x4v{T::template from_e2m1<0>(w, scale), T::template from_e2m1<1>(w, scale),
+                                   T::template from_e2m1<2>(w, scale), T::template from_e2m1<3>(w, scale)};
+                    } else if constexpr (FORM == kForm8) {
+                        const u32x2v w = *(const u32x2v*)(k + d);
+                        const float scale = a.c.k_scale[row];
+                        x = u32x4v{T::template from_e4m3<false>(w[0], scale), T::template from_e4m3<true>(w[0], scale),
+                                   T::template from_e4m3<false>(w[1], scale), T::template from_e4m3<true>(w[1], scale)};
+                    } else {
+                        x = *(const u32x4v*)(k + 2 * d);
+                    }
+                    if constexpr (FORM != kForm16)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x[j] = saturate<T>(x[j]);
+                }
+                key[i][s] = x;
+            }
+        }
+    }
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+
+// The units of the kernel for many rows: kTokens positions of one sequence and key head.
+template <int TOKENS>
+__device__ __forceinline__ int block_units(const AttnArgs& a, const Seq& q, int* low, int* high) {
+    const bool mine = q.rows > a.few_limit;
+    *high = mine ? q.len : 0;
+    *low = a.window ? min(max(q.len - q.n - a.window + 1, 0), *high) : 0;
+    return *high > *low ? (*high + TOKENS - 1) / TOKENS - *low / TOKENS : 0;
+}
+
+template <typename T, int FORM, int DP>
+__global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArgs a) {
+    using F = Block<T, FORM, DP>;
+    __shared__ __attribute__((aligned(16))) unsigned char rows[kWeighWaves][F::kTile];
+    __shared__ float logs[kWeighWaves][32];
+    __shared__ int highs[kWeighWaves][32], lows[kWeighWaves][32];
+    __shared__ int64_t places[kWeighWaves][32];
+    __shared__ float sums[kWeighWaves][F::kTokens];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
+    const int G = gridDim.x, D = a.c.head_dim;
+    // consecutive units on one XCD (workgroups go to the 8 XCDs in turn): they share query rows in its L2
+    const int me = (G & 7) == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+
+    auto scan = [&](int x) {  // inclusive sums over the lanes
+        for (int d = 1; d < 64; d <<= 1) {
+            const int up = __shfl_up(x, d, 64);
+            if (lane >= d) x = __builtin_elementwise_add_sat(x, up);
+        }
+        return x;
+    };
+    for (int u = me;; u += G) {
+        // the sequence of unit u
+        Seq q = {};
+        int seq = 0, head = 0, unit = 0, before = 0;
+        bool none = true;
+        for (int s0 = 0; s0 < a.sequences && none; s0 += 64) {
+            int low, high, per = 0;
+            Seq x = {};
+            if (s0 + lane < a.sequences) {
+                x = read_seq(a, s0 + lane);
+                per = block_units<F::kTokens>(a, x, &low, &high);
+            }
+            const int sum = scan(per * a.c.heads);
+            const uint64_t past = __ballot(__builtin_elementwise_add_sat(before, sum) > u);
+            if (past) {
+                const int l = __builtin_ctzll(past);
+                const int ph = __builtin_amdgcn_readlane(per, l);
+                const int rest = u - (before + __builtin_amdgcn_readlane(sum, l) - ph * a.c.heads);
+                seq = s0 + l;
+                head = rest / ph;
+                unit = rest % ph;
+                q.first = __builtin_amdgcn_readlane(x.first, l);
+                q.n = __builtin_amdgcn_readlane(x.n, l);
+                q.len = __builtin_amdgcn_readlane(x.len, l);
+                q.rows = __builtin_amdgcn_readlane(x.rows, l);
+                none = false;
+            }
+            before = __builtin_elementwise_add_sat(before, __builtin_amdgcn_readlane(sum, 63));
+        }
+        if (none) return;
+        int low, high;
+        block_units<F::kTokens>(a, q, &low, &high);
+        const int t0 = (low / F::kTokens + unit) * F::kTokens;
+        F f;
+        f.load(a, seq, head, t0, low, high, lane);
+
+        // the rows that may see some of it: tiles [r0, r1) of 32
+        const int base = q.len - q.n;
+        const int64_t first = a.causal ? (int64_t)max(0, t0 - base) * a.share : 0;
+        const int64_t last = a.window ? min((int64_t)q.rows, max((int64_t)0, (int64_t)t0 + F::kTokens - 1 + a.window - base) * a.share) : q.rows;
+        const int r0 = (int)(first / 32), r1 = (int)((last + 31) / 32);
+        unsigned char* mine = rows[wave];
+        // What lane l says about row l % 32 of a tile: where it begins in q, its logarithm, the positions that it sees.
+        int64_t place = 0;
+        float row_log = 0.f;
+        int row_high = 0, row_low = 0;
+        auto describe = [&](int tile) {
+            const int row = tile * 32 + (lane & 31), tk = min(row, q.rows - 1) / a.share, hs = min(row, q.rows - 1) - tk * a.share;
+            const bool on = row < q.rows;
+            place = (int64_t)(q.first + tk) * a.q_stride + (int64_t)(head * a.share + hs) * D;
+            const float x = a.row_lse[(int64_t)(q.first + tk) * a.q_heads + head * a.share + hs];
+            row_log = on && x != -__builtin_inff() ? x * kLog2e : __builtin_inff();
+            row_high = on ? (a.causal ? min(base + tk + 1, q.len) : q.len) : 0;
+            row_low = a.window ? base + tk - a.window + 1 : 0;
+        };
+        // Brings the rows that were described: their channels swizzled by the row, so that the lanes of a read spread
+        // over the banks; what lies behind a row's end meets zeros of the keys.
+        auto bring = [&]() {
+            if (lane < 32) places[wave][lane] = place;
+            const int l = opaque(lane);  // (worked out here, not kept in registers through the loop)
+#pragma unroll
+            for (int i = 0; i < F::kTile / 1024; ++i) {
+                const int at = i * 64 + l, r = at / F::kChunks;
+                const int c = (at % F::kChunks) ^ (r & F::kRowMask);
+                const uint16_t* p = (const uint16_t*)a.q + places[wave][r] + (8 * c < D ? 8 * c : 0);
+                __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)(mine + i * 1024), 16, 0, 0);
+            }
+        };
+        auto query = [&](int s, int l) {
+            const int r = l & 31;
+            return *(const u32x4v*)(mine + r * DP * 2 + ((F::chunk(s, l >> 5) ^ (r & F::kRowMask)) << 4));
+        };
+        float sum[F::kTiles];
+#pragma unroll
+        for (int i = 0; i < F::kTiles; ++i) sum[i] = 0.f;
+        if (r0 + wave < r1) {
+            describe(r0 + wave);
+            bring();
+        }
+        for (int tile = r0 + wave; tile < r1; tile += kWeighWaves) {
+            if (lane < 32) {
+                logs[wave][lane] = row_log;
+                highs[wave][lane] = row_high;
+                lows[wave][lane] = row_low;
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            const int l = opaque(lane);
+            // (all of a row in registers where they are enough, so that the next rows may come at once)
+            constexpr bool kHeld = DP <= 128;
+            u32x4v qr[kHeld ? F::kSteps : 1];
+            if (kHeld)
+#pragma unroll
+                for (int s = 0; s < F::kSteps; ++s) qr[s] = query(s, l);
+            f32x4v log[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) log[j] = *(const f32x4v*)&logs[wave][8 * j + 4 * half];
+            // some row does not see some position (or is none)
+            const int tok0 = tile * 32 / a.share, tok1 = min(tile * 32 + 31, q.rows - 1) / a.share;
+            const bool masked = tile * 32 + 32 > q.rows || t0 < low || t0 + F::kTokens > high ||
+                                (a.causal && t0 + F::kTokens > base + tok0 + 1) || (a.window && t0 < base + tok1 - a.window + 1);
+            const bool more = tile + kWeighWaves < r1;
+            if (kHeld && more) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                describe(tile + kWeighWaves);
+                bring();
+            }
+#pragma unroll
+            for (int i = 0; i < F::kTiles; i += 2) {
+                f32x16v s[2];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[0][j] = s[1][j] = 0.f;
+#pragma unroll
+                for (int st = 0; st < F::kSteps; ++st) {
+                    const u32x4v x = kHeld ? qr[kHeld ? st : 0] : query(st, l);
+                    s[0] = T::mfma32(x, f.key[i][st], s[0]);
+                    s[1] = T::mfma32(x, f.key[i + 1][st], s[1]);
+                }
+                if (!masked) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            sum[i + h] += exp2_fast(__builtin_fmaf(s[h][j], a.scale_log2, -log[j / 4][j % 4]));
+                } else {
+                    const int t = t0 + 32 * i + (lane & 31);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int r = 8 * (j / 4) + 4 * half + j % 4;
+                        const int to = highs[wave][r], from = lows[wave][r];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float p = exp2_fast(__builtin_fmaf(s[h][j], a.scale_log2, -log[j / 4][j % 4]));
+                            sum[i + h] += t + 32 * h < to && t + 32 * h >= from ? p : 0.f;
+                        }
+                    }
+                }
+            }
+            if (!kHeld && more) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                describe(tile + kWeighWaves);
+                bring();
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < F::kTiles; ++i) {
+            const float x = sum_halves(sum[i]);
+            if (lane < 32) sums[wave][32 * i + lane] = x;
+        }
+        __syncthreads();
+        if (tid < F::kTokens) {
+            const int t = t0 + tid;
+            float x = sums[0][tid];
+#pragma unroll
+            for (int w = 1; w < kWeighWaves; ++w) x += sums[w][tid];
+            if (t >= low && t < high) {
+                const int entry = a.table[seq * a.table_stride + (t >> a.page_log2)];
+                if ((uint32_t)entry < (uint32_t)a.c.num_pages) {
+                    float* w = a.weight + ((int64_t)entry * a.c.heads + head) * a.c.page_size + (t & (a.c.page_size - 1));
+                    *w = (t < base ? *w : 0.f) + x;
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, int FORM, int DP>
+hipError_t weigh_run(const AttnArgs& a, int cus, int which, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    if (which & 1) {
+        weigh_few_kernel<T, FORM, (DP == 96 ? 128 : DP)><<<4 * cus, 64 * kWeighWaves, 0, s>>>(a);
+        e = hipGetLastError();
+    }
+    if (e == hipSuccess && (which & 2)) {
+        weigh_many_kernel<T, FORM, DP><<<2 * cus, 64 * kWeighWaves, 0, s>>>(a);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
 template <typename T, int FORM>
-hipError_t weigh_dim(const AttnArgs& a, int grid, hipStream_t s) {
+hipError_t weigh_dim(const AttnArgs& a, int cus, int which, hipStream_t s) {
     const int D = a.c.head_dim;
-    if (D <= 64)
-        weigh_few_kernel<T, FORM, 64><<<grid, 64 * kWeighWaves, 0, s>>>(a);
-    else if (D <= 128)
-        weigh_few_kernel<T, FORM, 128><<<grid, 64 * kWeighWaves, 0, s>>>(a);
-    else
-        weigh_few_kernel<T, FORM, 256><<<grid, 64 * kWeighWaves, 0, s>>>(a);
-    return hipGetLastError();
+    if (D <= 64) return weigh_run<T, FORM, 64>(a, cus, which, s);
+    // (4-bit rows are read 64 channels at a time)
+    if (D <= 96 && FORM != kForm4) return weigh_run<T, FORM, (FORM == kForm4 ? 128 : 96)>(a, cus, which, s);
+    if (D <= 128) return weigh_run<T, FORM, 128>(a, cus, which, s);
+    return weigh_run<T, FORM, 256>(a, cus, which, s);
 }
 
 template <typename T>
-hipError_t weigh_type(const AttnArgs& a, int grid, hipStream_t s) {
+hipError_t weigh_type(const AttnArgs& a, int cus, int which, hipStream_t s) {
     switch (cache_form(a.c.type)) {
-        case kForm8: return weigh_dim<T, kForm8>(a, grid, s);
-        case kForm4: return weigh_dim<T, kForm4>(a, grid, s);
-        default: return weigh_dim<T, kForm16>(a, grid, s);
+        case kForm8: return weigh_dim<T, kForm8>(a, cus, which, s);
+        case kForm4: return weigh_dim<T, kForm4>(a, cus, which, s);
+        default: return weigh_dim<T, kForm16>(a, cus, which, s);
     }
 }
 
 }  // namespace
 
-hipError_t launch_weigh(const AttnArgs& a, int type, int cus, hipStream_t s) {
-    return type == LSCD_F16 ? weigh_type<F16>(a, 4 * cus, s) : weigh_type<BF16>(a, 4 * cus, s);
+// which: 1 the kernel for few rows, 2 the one for many, 3 both.
+hipError_t launch_weigh(const AttnArgs& a, int type, int cus, int which, hipStream_t s) {
+    return type == LSCD_F16 ? weigh_type<F16>(a, cus, which, s) : weigh_type<BF16>(a, cus, which, s);
 }
 
 }  // namespace lscd
