@@ -336,6 +336,10 @@ lscd_status_t lscd_cache_weigh(const lscd_cache_t* cache, const void* q, int64_t
     if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, device);
     if (e != hipSuccess || cus <= 0) return LSCD_ERROR_HIP;
     a.row_lse = lse;
+    uint32_t bits = 0;  // 2^bits >= share: magic = ceil(2^(31 + bits) / share) has 32 bits
+    while (((int64_t)1 << bits) < a.share) ++bits;
+    a.share_shift = 31 + bits;
+    a.share_magic = (uint32_t)((((uint64_t)1 << a.share_shift) + a.share - 1) / a.share);
     a.weight = weight;
     // The same choice as for attention: one launch where no sequence can have many rows, or there is only one.
     const bool both = T * a.share > lscd::kWeighRows && T > sequences;

@@ -56,6 +56,7 @@ struct AttnArgs {
     int4* record;            // cut items, one per workgroup: parts - 1, sequence, key head, row tile (many rows)
     float* lse;              // [T][q_heads], or null
     const float* row_lse;    // the same as an input (weigh)
+    uint32_t share_magic, share_shift;  // x / share = x * magic >> shift for x below 2^31 (weigh)
     float* weight;           // [num_pages][heads][page_size] (weigh)
 };
 // Workgroups of one launch at most, and floats of one partial result.

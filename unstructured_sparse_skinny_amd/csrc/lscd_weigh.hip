@@ -191,9 +191,9 @@ struct Block {
     static constexpr int kTiles = DP <= 128 ? 4 : 2;       // key tiles of 32 positions: what the registers hold
     static constexpr int kTokens = 32 * kTiles;
     static constexpr int kSteps = DP / 16;                 // matrix instructions of a tile
-    static constexpr int kChunks = DP / 8;                 // 16-byte chunks of a query row
-    static constexpr int kRowMask = DP == 96 ? 3 : DP == 64 ? 7 : 15;
-    static constexpr int kTile = 32 * DP * 2;              // bytes of 32 query rows
+    static constexpr int kChunks = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;  // 16-byte chunks of a query row in LDS
+    static constexpr int kRowMask = DP <= 64 ? 7 : 15;
+    static constexpr int kRow = 16 * kChunks, kTile = 32 * kRow;  // bytes of a query row and of 32
     static constexpr int kBits = form_bits(FORM);
     static constexpr int kScaleBytes = FORM == kForm4 ? scale_row(DP) : 4;
 
@@ -262,7 +262,7 @@ __global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArg
     __shared__ __attribute__((aligned(16))) unsigned char rows[kWeighWaves][F::kTile];
     __shared__ float logs[kWeighWaves][32];
     __shared__ int highs[kWeighWaves][32], lows[kWeighWaves][32];
-    __shared__ int64_t places[kWeighWaves][32];
+    __shared__ const uint16_t* places[kWeighWaves][32];
     __shared__ float sums[kWeighWaves][F::kTokens];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
     const int G = gridDim.x, D = a.c.head_dim;
@@ -318,35 +318,36 @@ __global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArg
         const int64_t last = a.window ? min((int64_t)q.rows, max((int64_t)0, (int64_t)t0 + F::kTokens - 1 + a.window - base) * a.share) : q.rows;
         const int r0 = (int)(first / 32), r1 = (int)((last + 31) / 32);
         unsigned char* mine = rows[wave];
-        // What lane l says about row l % 32 of a tile: where it begins in q, its logarithm, the positions that it sees.
-        int64_t place = 0;
+        // What lane l says about row l % 32 of a tile: where it is, its logarithm, the positions that it sees.
+        const uint16_t* place = nullptr;
         float row_log = 0.f;
         int row_high = 0, row_low = 0;
         auto describe = [&](int tile) {
-            const int row = tile * 32 + (lane & 31), tk = min(row, q.rows - 1) / a.share, hs = min(row, q.rows - 1) - tk * a.share;
+            const int row = tile * 32 + (lane & 31), tk = (int)((uint64_t)(uint32_t)min(row, q.rows - 1) * a.share_magic >> a.share_shift);
+            const int hs = min(row, q.rows - 1) - tk * a.share;
             const bool on = row < q.rows;
-            place = (int64_t)(q.first + tk) * a.q_stride + (int64_t)(head * a.share + hs) * D;
+            place = (const uint16_t*)a.q + (int64_t)(q.first + tk) * a.q_stride + (int64_t)(head * a.share + hs) * D;
             const float x = a.row_lse[(int64_t)(q.first + tk) * a.q_heads + head * a.share + hs];
             row_log = on && x != -__builtin_inff() ? x * kLog2e : __builtin_inff();
             row_high = on ? (a.causal ? min(base + tk + 1, q.len) : q.len) : 0;
             row_low = a.window ? base + tk - a.window + 1 : 0;
         };
-        // Brings the rows that were described: their channels swizzled by the row, so that the lanes of a read spread
-        // over the banks; what lies behind a row's end meets zeros of the keys.
+        // Brings the rows that were described: their chunks swizzled by the row, so that the lanes of a read spread
+        // over the banks; chunks behind a row's end (its last one again) meet zeros of the keys.
         auto bring = [&]() {
             if (lane < 32) places[wave][lane] = place;
-            const int l = opaque(lane);  // (worked out here, not kept in registers through the loop)
+            const int l = opaque(lane), r = l / F::kChunks;  // (worked out here, not kept in registers through the loop)
+            const int at = (l % F::kChunks ^ r) << 4, most = 2 * D - 16;
+            constexpr int kRows = 64 / F::kChunks;  // of one load
 #pragma unroll
             for (int i = 0; i < F::kTile / 1024; ++i) {
-                const int at = i * 64 + l, r = at / F::kChunks;
-                const int c = (at % F::kChunks) ^ (r & F::kRowMask);
-                const uint16_t* p = (const uint16_t*)a.q + places[wave][r] + (8 * c < D ? 8 * c : 0);
+                const uint8_t* p = (const uint8_t*)places[wave][i * kRows + r] + (uint32_t)min(at ^ ((i * kRows & F::kRowMask) << 4), most);
                 __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)(mine + i * 1024), 16, 0, 0);
             }
         };
         auto query = [&](int s, int l) {
             const int r = l & 31;
-            return *(const u32x4v*)(mine + r * DP * 2 + ((F::chunk(s, l >> 5) ^ (r & F::kRowMask)) << 4));
+            return *(const u32x4v*)(mine + r * F::kRow + ((F::chunk(s, l >> 5) ^ (r & F::kRowMask)) << 4));
         };
         float sum[F::kTiles];
 #pragma unroll
@@ -373,9 +374,7 @@ __global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArg
 #pragma unroll
             for (int j = 0; j < 4; ++j) log[j] = *(const f32x4v*)&logs[wave][8 * j + 4 * half];
             // some row does not see some position (or is none)
-            const int tok0 = tile * 32 / a.share, tok1 = min(tile * 32 + 31, q.rows - 1) / a.share;
-            const bool masked = tile * 32 + 32 > q.rows || t0 < low || t0 + F::kTokens > high ||
-                                (a.causal && t0 + F::kTokens > base + tok0 + 1) || (a.window && t0 < base + tok1 - a.window + 1);
+            const bool masked = __any(row_high < t0 + F::kTokens || row_low > t0);
             const bool more = tile + kWeighWaves < r1;
             if (kHeld && more) {
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
