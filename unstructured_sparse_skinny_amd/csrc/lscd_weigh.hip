@@ -95,8 +95,8 @@ __device__ __forceinline__ bool find_weigh(const AttnArgs& a, int lane, int me, 
     return true;
 }
 
-// The unit after this one; false past the range's end.
-__device__ __forceinline__ bool next_unit(const AttnArgs& a, WeighWork* w) {
+// To the unit that w names, which may be another head's or sequence's first; false past the range's end.
+__device__ __forceinline__ bool settle(const AttnArgs& a, WeighWork* w) {
     if (w->u >= w->end) return false;
     if (w->unit < w->st.units) return true;
     w->unit = 0;
@@ -110,73 +110,117 @@ __device__ __forceinline__ bool next_unit(const AttnArgs& a, WeighWork* w) {
     return true;
 }
 
+__device__ __forceinline__ int share_of(const AttnArgs& a, int row) {  // row / a.share
+    return (int)((uint64_t)(uint32_t)row * a.share_magic >> a.share_shift);
+}
+
+// Few rows: bound by the reading of the keys.  A wavefront issues the next unit's loads before it computes the
+// present one, and keeps its query rows while sequence and head stay the same.
 template <typename T, int FORM, int DP>
 __global__ __launch_bounds__(64 * kWeighWaves) void weigh_few_kernel(AttnArgs a) {
     using F = Keys<T, FORM, DP>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     WeighWork w;
-    if (!find_weigh(a, lane, blockIdx.x * kWeighWaves + wave, gridDim.x * kWeighWaves, &w)) return;
+    if (!find_weigh(a, lane, blockIdx.x * kWeighWaves + wave, gridDim.x * kWeighWaves, &w) || !settle(a, &w)) return;
     const int D = a.c.head_dim, g = lane >> 4;
-    while (next_unit(a, &w)) {
+
+    // A unit's keys, and the place of the lane's position's weight (lanes 0 .. 31) with what it has.
+    struct Unit {
+        F f;
+        float* at;
+        float old;
+    };
+    auto load = [&](const WeighWork& w, bool more, Unit* x) {
         const int t0 = (w.st.low / kWeighTokens + w.unit) * kWeighTokens;
         const int e[2] = {entry_of(a, w.seq, t0), entry_of(a, w.seq, t0 + 16)};
         HeadBase hb;
         hb.set<F::kBits, F::kScaleBytes>(a.c, w.head);
-        F f;
-        f.load_keys(a, hb, e, t0, w.st.high, lane);
-        // the weights of the lane's position (lanes 0 .. 31)
-        const int mine = t0 + (lane & 31), page = a.c.page_size;
-        const int entry = lane & 16 ? e[1] : e[0];
-        const int64_t at = ((int64_t)page_of(a, entry) * a.c.heads + w.head) * page + (mine & (page - 1));
-        const bool own = lane < 32 && mine >= w.st.low && mine < w.st.high && (uint32_t)entry < (uint32_t)a.c.num_pages;
-        const float old = own && mine < w.q.len - w.q.n ? a.weight[at] : 0.f;
+        x->f.load_keys(a, hb, e, t0, more ? w.st.high : 0, lane);
+        const int t = t0 + (lane & 31), page = a.c.page_size, entry = lane & 16 ? e[1] : e[0];
+        const bool own = more && lane < 32 && t >= w.st.low && t < w.st.high && (uint32_t)entry < (uint32_t)a.c.num_pages;
+        x->at = own ? a.weight + ((int64_t)entry * a.c.heads + w.head) * page + (t & (page - 1)) : nullptr;
+        x->old = own && t < w.q.len - w.q.n ? *x->at : 0.f;
+    };
+    // The query rows of a tile; rows that are none repeat the last one, and weigh nothing.
+    u32x4v qr[F::kSteps];
+    float log[4];  // of the rows whose scores the lane has, in units of log2
+    int see_high[4], see_low[4], all_high, all_low;
+    auto queries = [&](const WeighWork& w, int tile) {
+        auto row = [&](int r, int* token, int* head) {
+            const int x = min(tile * kFewRows + r, w.q.rows - 1);
+            *token = share_of(a, x);
+            *head = w.head * a.share + x - *token * a.share;
+        };
+        int token, head;
+        row(lane & 15, &token, &head);
+        const uint16_t* qp = (const uint16_t*)a.q + (int64_t)(w.q.first + token) * a.q_stride + (int64_t)head * D;
+#pragma unroll
+        for (int s = 0; s < F::kSteps; ++s) {
+            const int d = F::step_channel(s, g, D);
+            qr[s] = u32x4v{0u, 0u, 0u, 0u};
+            if (d < D) qr[s] = *(const u32x4v*)(qp + d);
+        }
+        all_high = w.q.len;
+        all_low = 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            row(4 * g + r, &token, &head);
+            const float x = a.row_lse[(int64_t)(w.q.first + token) * a.q_heads + head];
+            log[r] = tile * kFewRows + 4 * g + r < w.q.rows && x != -__builtin_inff() ? x * kLog2e : __builtin_inff();
+            const int pos = w.q.len - w.q.n + token;
+            see_high[r] = a.causal ? min(pos + 1, w.q.len) : w.q.len;
+            see_low[r] = a.window ? pos - a.window + 1 : 0;
+        }
+        // what every row sees: the first one's end, the last one's begin
+        if (a.causal) all_high = __builtin_amdgcn_readfirstlane(see_high[0]);
+        if (a.window) all_low = __builtin_amdgcn_readlane(see_low[3], 48);
+    };
+
+    Unit x;
+    load(w, true, &x);
+    int seq = -1, head = -1;
+    bool more = true;
+    while (more) {
+        WeighWork nw = w;
+        nw.u += w.st.cost;
+        ++nw.unit;
+        more = settle(a, &nw);
+        const bool single = w.st.cost == 1;
+        if (single && (w.seq != seq || w.head != head)) queries(w, 0);
+        seq = single ? w.seq : -1;
+        head = w.head;
+        Unit nx;
+        load(more ? nw : w, more, &nx);
+        const int t0 = (w.st.low / kWeighTokens + w.unit) * kWeighTokens;
         float sum[2] = {0.f, 0.f};
+        const bool top = x.f.top_keys();
         for (int tile = 0; tile < w.st.cost; ++tile) {
-            const int row = tile * kFewRows + (lane & 15);
-            const bool live = row < w.q.rows;
-            const int token = row / a.share;
-            const uint16_t* qp = (const uint16_t*)a.q + (int64_t)(w.q.first + (live ? token : 0)) * a.q_stride +
-                                 (int64_t)(w.head * a.share + row % a.share) * D;
-            u32x4v qr[F::kSteps];
-#pragma unroll
-            for (int s = 0; s < F::kSteps; ++s) {
-                const int d = F::step_channel(s, g, D);
-                qr[s] = u32x4v{0u, 0u, 0u, 0u};
-                if (live && d < D) qr[s] = *(const u32x4v*)(qp + d);
-            }
-            float lse[4];  // of the rows whose scores the lane has, in units of log2; rows that are none weigh nothing
-            int see_high[4], see_low[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int rw = tile * kFewRows + 4 * g + r, tk = rw / a.share, pos = w.q.len - w.q.n + tk;
-                const bool on = rw < w.q.rows;
-                const float x = on ? a.row_lse[(int64_t)(w.q.first + tk) * a.q_heads + w.head * a.share + rw % a.share] : -__builtin_inff();
-                lse[r] = x == -__builtin_inff() ? __builtin_inff() : x * kLog2e;
-                see_high[r] = on ? (a.causal ? min(pos + 1, w.q.len) : w.q.len) : 0;
-                see_low[r] = a.window ? pos - a.window + 1 : 0;
-            }
-            const bool top = f.top_keys();
+            if (!single) queries(w, tile);
+            const bool masked = t0 < all_low || t0 + kWeighTokens > all_high;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 f32x4v s = {0.f, 0.f, 0.f, 0.f};
                 if (!top)
 #pragma unroll
-                    for (int st = 0; st < F::kSteps; ++st) s = T::mfma16(qr[st], f.template key_operand<false>(h, st), s);
+                    for (int st = 0; st < F::kSteps; ++st) s = T::mfma16(qr[st], x.f.template key_operand<false>(h, st), s);
                 else
 #pragma unroll
-                    for (int st = 0; st < F::kSteps; ++st) s = T::mfma16(qr[st], f.template key_operand<true>(h, st), s);
-                const int t = t0 + 16 * h + (lane & 15);
+                    for (int st = 0; st < F::kSteps; ++st) s = T::mfma16(qr[st], x.f.template key_operand<true>(h, st), s);
+                float p[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float p = exp2_fast(__builtin_fmaf(s[r], a.scale_log2, -lse[r]));
-                    sum[h] += t < see_high[r] && t >= see_low[r] ? p : 0.f;
+                for (int r = 0; r < 4; ++r) p[r] = exp2_fast(__builtin_fmaf(s[r], a.scale_log2, -log[r]));
+                if (masked) {
+                    const int t = t0 + 16 * h + (lane & 15);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) p[r] = t < see_high[r] && t >= see_low[r] ? p[r] : 0.f;
                 }
+                sum[h] += (p[0] + p[1]) + (p[2] + p[3]);
             }
         }
-        const float x = sum_quarters(sum[0]), y = sum_quarters(sum[1]);
-        if (own) a.weight[at] = old + (lane & 16 ? y : x);
-        w.u += w.st.cost;
-        ++w.unit;
+        const float y = sum_quarters(sum[0]), z = sum_quarters(sum[1]);
+        if (x.at) *x.at = x.old + (lane & 16 ? z : y);
+        x = nx;
+        w = nw;
     }
 }
 
@@ -323,7 +367,7 @@ __global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArg
         float row_log = 0.f;
         int row_high = 0, row_low = 0;
         auto describe = [&](int tile) {
-            const int row = tile * 32 + (lane & 31), tk = (int)((uint64_t)(uint32_t)min(row, q.rows - 1) * a.share_magic >> a.share_shift);
+            const int row = tile * 32 + (lane & 31), tk = share_of(a, min(row, q.rows - 1));
             const int hs = min(row, q.rows - 1) - tk * a.share;
             const bool on = row < q.rows;
             place = (const uint16_t*)a.q + (int64_t)(q.first + tk) * a.q_stride + (int64_t)(head * a.share + hs) * D;
