@@ -236,9 +236,10 @@ struct HeadBase {
 
 // Key rows of 16 positions as an operand of the 16 x 16 x 32 matrix instructions, straight from memory: the
 // lane's row is position lane % 16, its channels are those of step_channel().  FORM: how the cache holds its
-// values.  DP: channels padded to 64, 128 or 256.
-template <typename T, int FORM, int DP>
+// values.  DP: channels padded to 64, 128 or 256.  TILES: of 16 positions.
+template <typename T, int FORM, int DP, int TILES = 2>
 struct Keys {
+    static constexpr int kTiles = TILES;
     static constexpr bool kScaled = FORM != kForm16;
     static constexpr int kBits = form_bits(FORM);
     static constexpr int kScaleBytes = FORM == kForm4 ? scale_row(DP) : 4;  // of one token's scales
@@ -247,8 +248,8 @@ struct Keys {
     static constexpr int kKeyScales = FORM == kForm4 && DP == 256 ? 2 : 1;    // scales of one key tile per lane
     // 1 as a scale is loaded
     static constexpr uint32_t kOne = FORM == kForm4 ? 127u : 0x3F800000u, kTop = FORM == kForm4 ? T::kTopScale4 : T::kTopScale;
-    uint32_t kr[2][kKeyRegs];
-    uint32_t ks[2][kKeyScales];  // scales as loaded: bits of a float (e4m3), exponent + 127 (e2m1)
+    uint32_t kr[TILES][kKeyRegs];
+    uint32_t ks[TILES][kKeyScales];  // scales as loaded: bits of a float (e4m3), exponent + 127 (e2m1)
 
     // A key row of 4-bit codes lies in the four lane groups as 16 channels each, of 64 (DP 64), or as 32 each, of
     // 128: the lane's channels of unit u of them have one scale.  Rows that end in the middle of 32 channels are
@@ -258,52 +259,56 @@ struct Keys {
         return DP == 64 ? unit_channel(u, g) : min(unit_channel(u, g), D - 32);
     }
 
-    // 32 positions from t0 on, in the pages of the table entries e; positions from `high` on are zero
-    // (lanes without a position read outside the descriptor, which costs no traffic).
-    __device__ __forceinline__ void load_keys(const AttnArgs& a, const HeadBase& hb, const int (&e)[2], int t0, int high,
-                                              int lane) {
-        const int D = a.c.head_dim;
+    // Tile h: 16 positions from row `row` of a page on, whose keys and scales the descriptors are of; lanes whose
+    // position is not `on` have zeros (they read outside the descriptor, which costs no traffic).  Offsets are the
+    // lane's, which do not change, and the tile's first row's, a scalar.
+    __device__ __forceinline__ void load_tile(int h, __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t scales, int D, int row,
+                                              bool on, int lane) {
+        const int r = lane & 15, g = lane >> 4, at = row * D * kBits / 8;
+        if (FORM == kForm8) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int t = t0 + 16 * h, row = (t & (a.c.page_size - 1)) + (lane & 15);
-            const uint32_t p = page_of(a, e[h]);
-            const bool on = t + (lane & 15) < high;
-            const auto rs = hb.keys(p);
-            if (FORM == kForm8) {
+            for (int u = 0; u < DP / 64; ++u) {
+                const int d = 64 * u + 16 * g;
+                const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? r * D + d : kNoRow, at, 0);
 #pragma unroll
-                for (int u = 0; u < DP / 64; ++u) {
-                    const int d = 64 * u + 16 * (lane >> 4);
-                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? row * D + d : kNoRow, 0, 0);
+                for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
+            }
+            ks[h][0] = __builtin_amdgcn_raw_buffer_load_b32(scales, on ? r * 4 : kNoRow, row * 4, 0);
+        } else if (FORM == kForm4) {
+#pragma unroll
+            for (int u = 0; u < kKeyScales; ++u) {
+                const int d = unit_channel(u, g);
+                const int off = on && d < D ? (r * D + unit_start(u, g, D)) / 2 : kNoRow;
+                if constexpr (DP == 64) {
+                    const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, off, at, 0);
+                    kr[h][0] = x[0];
+                    kr[h][1] = x[1];
+                } else {
+                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, off, at, 0);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
                 }
-                ks[h][0] = __builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0);
-            } else if (FORM == kForm4) {
-#pragma unroll
-                for (int u = 0; u < kKeyScales; ++u) {
-                    const int d = unit_channel(u, lane >> 4);
-                    const int at = on && d < D ? (row * D + unit_start(u, lane >> 4, D)) / 2 : kNoRow;
-                    if constexpr (DP == 64) {
-                        const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, at, 0, 0);
-                        kr[h][0] = x[0];
-                        kr[h][1] = x[1];
-                    } else {
-                        const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
-                    }
-                    ks[h][u] = __builtin_amdgcn_raw_buffer_load_b8(hb.key_scales(p),
-                                                                   on && d < D ? row * kScaleBytes + d / kScaleGroup : kNoRow, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    const int d = 32 * s + 8 * (lane >> 4);
-                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? (row * D + d) * 2 : kNoRow, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) kr[h][4 * s + i] = x[i];
-                }
+                ks[h][u] = __builtin_amdgcn_raw_buffer_load_b8(
+                    scales, on && d < D ? r * kScaleBytes + d / kScaleGroup : kNoRow, row * kScaleBytes, 0);
             }
+        } else {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const int d = 32 * s + 8 * g;
+                const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? (r * D + d) * 2 : kNoRow, at, 0);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kr[h][4 * s + i] = x[i];
+            }
+        }
+    }
+    // 16 TILES positions from t0 on, in the pages of the table entries e; positions from `high` on are zero.
+    __device__ __forceinline__ void load_keys(const AttnArgs& a, const HeadBase& hb, const int (&e)[TILES], int t0, int high,
+                                              int lane) {
+#pragma unroll
+        for (int h = 0; h < TILES; ++h) {
+            const int t = t0 + 16 * h;
+            const uint32_t p = page_of(a, e[h]);
+            load_tile(h, hb.keys(p), hb.key_scales(p), a.c.head_dim, t & (a.c.page_size - 1), t + (lane & 15) < high, lane);
         }
     }
 
@@ -311,8 +316,11 @@ struct Keys {
     // compare as whole numbers.)
     __device__ __forceinline__ bool top_keys() const {
         if (!kScaled) return false;
-        uint32_t most = max(ks[0][0], ks[1][0]);
-        if (kKeyScales == 2) most = max(most, max(ks[0][kKeyScales - 1], ks[1][kKeyScales - 1]));
+        uint32_t most = 0u;
+#pragma unroll
+        for (int h = 0; h < TILES; ++h)
+#pragma unroll
+            for (int u = 0; u < kKeyScales; ++u) most = max(most, ks[h][u]);
         return __any(most >= kTop);
     }
     // Word of codes `w` in 16 bits.  TOP: saturated.  (The scale is opaque there, so that the conversions of

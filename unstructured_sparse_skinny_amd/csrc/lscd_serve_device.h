@@ -186,6 +186,15 @@ __device__ __forceinline__ float sum_halves(float x) {
     both_halves(x, &a, &b);
     return a + b;
 }
+// x summed over the lanes l, l ^ 32 in the lower half, y in the upper; over l, l ^ 16 in the even quarters, the odd ones
+__device__ __forceinline__ float add_halves(float x, float y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y), false, false);
+    return as_float(r[0]) + as_float(r[1]);
+}
+__device__ __forceinline__ float add_quarters(float x, float y) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, y), false, false);
+    return as_float(r[0]) + as_float(r[1]);
+}
 __device__ __forceinline__ float max_quarters(float x) {
     float a, b;
     both_quarters(x, &a, &b);

@@ -7,7 +7,7 @@
 // S = Q K^T on the matrix cores: a lane then holds scores of one position and of four rows, whose sum is taken in
 // the lane and over its quarters.  Products are exact and sums fp32, as in the attention.
 //
-// The units (stretches of kWeighTokens positions of one sequence and key head) are numbered sequence after
+// The units (stretches of positions of one sequence and key head) are numbered sequence after
 // sequence, head after head, and cut into equal ranges by what they cost, one for each wavefront; a unit belongs
 // to the range in which its first slot lies.
 
@@ -17,33 +17,38 @@ namespace lscd {
 namespace {
 
 constexpr int kWeighWaves = 4;
-static_assert(kWeighTokens == 32, "a unit is two key tiles of 16 positions");
+// Key tiles of 16 positions in a unit of the kernel for few rows: the fewer bytes a row has, the more of them.
+constexpr int weigh_tiles(int form, int dp) { return form == kForm4 && dp <= 128 ? 4 : 2; }
+static_assert(kWeighTokens == 32, "no unit is smaller");
 
 // What the rows of a sequence see together: positions [low, high), in `units` stretches; a unit costs a slot for
 // every tile of 16 rows.
+template <int TOKENS>
 struct Stretch {
     int low, high, units, cost;
     __device__ __forceinline__ void measure(const AttnArgs& a, const Seq& q) {
         // (the last token sees all with or without causality)
         high = q.rows > 0 && q.rows <= a.few_limit ? q.len : 0;
         low = a.window ? min(max(q.len - q.n - a.window + 1, 0), high) : 0;
-        units = high > low ? (high + kWeighTokens - 1) / kWeighTokens - low / kWeighTokens : 0;
+        units = high > low ? (high + TOKENS - 1) / TOKENS - low / TOKENS : 0;
         cost = (q.rows + kFewRows - 1) / kFewRows;
     }
 };
 
 // Where a range begins: the first unit whose first slot is in it.
+template <int TOKENS>
 struct WeighWork {
     int u, end;  // that slot; the range's end
     int seq, head, unit;
     Seq q;
-    Stretch st;
+    Stretch<TOKENS> st;
 };
-__device__ __forceinline__ bool find_weigh(const AttnArgs& a, int lane, int me, int G, WeighWork* w) {
+template <int TOKENS>
+__device__ __forceinline__ bool find_weigh(const AttnArgs& a, int lane, int me, int G, WeighWork<TOKENS>* w) {
     auto slots_of = [&](int s, Seq* q) {
         if (s >= a.sequences) return 0;
         *q = read_seq(a, s);
-        Stretch st;
+        Stretch<TOKENS> st;
         st.measure(a, *q);
         return st.units * st.cost;
     };
@@ -96,7 +101,8 @@ __device__ __forceinline__ bool find_weigh(const AttnArgs& a, int lane, int me, 
 }
 
 // To the unit that w names, which may be another head's or sequence's first; false past the range's end.
-__device__ __forceinline__ bool settle(const AttnArgs& a, WeighWork* w) {
+template <int TOKENS>
+__device__ __forceinline__ bool settle(const AttnArgs& a, WeighWork<TOKENS>* w) {
     if (w->u >= w->end) return false;
     if (w->unit < w->st.units) return true;
     w->unit = 0;
@@ -114,38 +120,79 @@ __device__ __forceinline__ int share_of(const AttnArgs& a, int row) {  // row / 
     return (int)((uint64_t)(uint32_t)row * a.share_magic >> a.share_shift);
 }
 
-// Few rows: bound by the reading of the keys.  A wavefront issues the next unit's loads before it computes the
-// present one, and keeps its query rows while sequence and head stay the same.
+// Where the pages of a sequence hold one key head: lane l has the addresses of its keys, scales and weights in the
+// page of table entry base + l, worked out for 64 pages at a time and read from there as scalars.
+struct Window {
+    int seq, head, base;
+    uint32_t k_lo, k_hi, s_lo, s_hi, w_lo, w_hi;  // weights: null for a page outside the pool
+
+    template <int BITS, int SCALES>
+    __device__ __forceinline__ void fill(const AttnArgs& a, int sq, int hd, int page, int lane) {
+        seq = sq;
+        head = hd;
+        base = page;
+        const int32_t e = a.table[seq * a.table_stride + min(page + lane, a.table_pages - 1)];
+        const int64_t row = ((int64_t)page_of(a, e) * a.c.heads + head) * a.c.page_size;  // the page's first
+        const uint64_t k = (uint64_t)a.c.k + row * (a.c.head_dim * BITS / 8), s = (uint64_t)a.c.k_scale + row * SCALES;
+        const uint64_t w = (uint32_t)e < (uint32_t)a.c.num_pages ? (uint64_t)(a.weight + row) : 0;
+        k_lo = (uint32_t)k;
+        k_hi = (uint32_t)(k >> 32);
+        s_lo = (uint32_t)s;
+        s_hi = (uint32_t)(s >> 32);
+        w_lo = (uint32_t)w;
+        w_hi = (uint32_t)(w >> 32);
+    }
+    __device__ static __forceinline__ uint64_t at(uint32_t lo, uint32_t hi, int page) {
+        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, page) << 32 | (uint32_t)__builtin_amdgcn_readlane(lo, page);
+    }
+};
+
+// Few rows: bound by the reading of the keys.  A wavefront loads the next unit's keys into the registers of the
+// present one's as soon as its products are issued, before the exponentials, and keeps its query rows while
+// sequence and head stay the same.
 template <typename T, int FORM, int DP>
-__global__ __launch_bounds__(64 * kWeighWaves) void weigh_few_kernel(AttnArgs a) {
-    using F = Keys<T, FORM, DP>;
+__global__ __launch_bounds__(64 * kWeighWaves, (DP <= 64 || (FORM == kForm4 && DP <= 128) ? 4 : DP <= 128 ? 3 : 2)) void weigh_few_kernel(AttnArgs a) {
+    constexpr int kTiles = weigh_tiles(FORM, DP), kTokens = 16 * kTiles;
+    using F = Keys<T, FORM, DP, kTiles>;
+    using Work = WeighWork<kTokens>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    WeighWork w;
+    Work w;
     if (!find_weigh(a, lane, blockIdx.x * kWeighWaves + wave, gridDim.x * kWeighWaves, &w) || !settle(a, &w)) return;
     const int D = a.c.head_dim, g = lane >> 4;
+    const int row_bytes = D * F::kBits / 8, key_block = a.c.page_size * row_bytes, scale_block = a.c.page_size * F::kScaleBytes;
 
-    // A unit's keys, and the place of the lane's position's weight (lanes 0 .. 31) with what it has.
-    struct Unit {
-        F f;
-        float* at;
-        float old;
+    F f;
+    Window win;
+    win.seq = -1;
+    // (past the range's end nothing is loaded, by the same instructions: the waits count them)
+    auto load_keys = [&](const Work& w, bool more) {
+        const int t0 = (w.st.low / kTokens + w.unit) * kTokens;
+        if (w.seq != win.seq || w.head != win.head || ((t0 + kTokens - 1) >> a.page_log2) - win.base >= 64)
+            win.fill<F::kBits, F::kScaleBytes>(a, w.seq, w.head, t0 >> a.page_log2, lane);
+        const int high = more ? w.st.high : 0;
+#pragma unroll
+        for (int h = 0; h < kTiles; ++h) {
+            const int t = t0 + 16 * h, i = (t >> a.page_log2) - win.base;
+            f.load_tile(h, buffer_of((const void*)Window::at(win.k_lo, win.k_hi, i), key_block),
+                        F::kScaled ? buffer_of((const void*)Window::at(win.s_lo, win.s_hi, i), scale_block) : buffer_of(nullptr, 0),
+                        D, t & (a.c.page_size - 1), t + (lane & 15) < high, lane);
+        }
     };
-    auto load = [&](const WeighWork& w, bool more, Unit* x) {
-        const int t0 = (w.st.low / kWeighTokens + w.unit) * kWeighTokens;
-        const int e[2] = {entry_of(a, w.seq, t0), entry_of(a, w.seq, t0 + 16)};
-        HeadBase hb;
-        hb.set<F::kBits, F::kScaleBytes>(a.c, w.head);
-        x->f.load_keys(a, hb, e, t0, more ? w.st.high : 0, lane);
-        const int t = t0 + (lane & 31), page = a.c.page_size, entry = lane & 16 ? e[1] : e[0];
-        const bool own = more && lane < 32 && t >= w.st.low && t < w.st.high && (uint32_t)entry < (uint32_t)a.c.num_pages;
-        x->at = own ? a.weight + ((int64_t)entry * a.c.heads + w.head) * page + (t & (page - 1)) : nullptr;
-        x->old = own && t < w.q.len - w.q.n ? *x->at : 0.f;
+    // The place of the lane's position's weight (as many lanes as positions), null if it has none, and what is there.
+    float* place = nullptr;
+    float old = 0.f;
+    auto load_weight = [&](const Work& w) {
+        const int t = (w.st.low / kTokens + w.unit) * kTokens + (lane & (kTokens - 1)), i = (t >> a.page_log2) - win.base;
+        const uint64_t at = (uint64_t)(uint32_t)__shfl((int)win.w_hi, i, 64) << 32 | (uint32_t)__shfl((int)win.w_lo, i, 64);
+        const bool own = lane < kTokens && t >= w.st.low && t < w.st.high && at != 0;
+        place = own ? (float*)at + (t & (a.c.page_size - 1)) : nullptr;
+        old = *(own ? place : a.weight);
     };
     // The query rows of a tile; rows that are none repeat the last one, and weigh nothing.
     u32x4v qr[F::kSteps];
     float log[4];  // of the rows whose scores the lane has, in units of log2
     int see_high[4], see_low[4], all_high, all_low;
-    auto queries = [&](const WeighWork& w, int tile) {
+    auto queries = [&](const Work& w, int tile) {
         auto row = [&](int r, int* token, int* head) {
             const int x = min(tile * kFewRows + r, w.q.rows - 1);
             *token = share_of(a, x);
@@ -176,51 +223,71 @@ __global__ __launch_bounds__(64 * kWeighWaves) void weigh_few_kernel(AttnArgs a)
         if (a.window) all_low = __builtin_amdgcn_readlane(see_low[3], 48);
     };
 
-    Unit x;
-    load(w, true, &x);
-    int seq = -1, head = -1;
-    bool more = true;
-    while (more) {
-        WeighWork nw = w;
-        nw.u += w.st.cost;
-        ++nw.unit;
-        more = settle(a, &nw);
-        const bool single = w.st.cost == 1;
-        if (single && (w.seq != seq || w.head != head)) queries(w, 0);
-        seq = single ? w.seq : -1;
-        head = w.head;
-        Unit nx;
-        load(more ? nw : w, more, &nx);
-        const int t0 = (w.st.low / kWeighTokens + w.unit) * kWeighTokens;
-        float sum[2] = {0.f, 0.f};
-        const bool top = x.f.top_keys();
-        for (int tile = 0; tile < w.st.cost; ++tile) {
-            if (!single) queries(w, tile);
-            const bool masked = t0 < all_low || t0 + kWeighTokens > all_high;
+    // Scores of the tile of rows in qr with the keys in f, and what they weigh.
+    f32x4v s[kTiles];
+    auto products = [&]() {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                f32x4v s = {0.f, 0.f, 0.f, 0.f};
-                if (!top)
+        for (int h = 0; h < kTiles; ++h) s[h] = f32x4v{0.f, 0.f, 0.f, 0.f};
+        if (!f.top_keys()) {
 #pragma unroll
-                    for (int st = 0; st < F::kSteps; ++st) s = T::mfma16(qr[st], x.f.template key_operand<false>(h, st), s);
-                else
+            for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-                    for (int st = 0; st < F::kSteps; ++st) s = T::mfma16(qr[st], x.f.template key_operand<true>(h, st), s);
-                float p[4];
+                for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(qr[st], f.template key_operand<false>(h, st), s[h]);
+        } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) p[r] = exp2_fast(__builtin_fmaf(s[r], a.scale_log2, -log[r]));
-                if (masked) {
-                    const int t = t0 + 16 * h + (lane & 15);
+            for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) p[r] = t < see_high[r] && t >= see_low[r] ? p[r] : 0.f;
-                }
-                sum[h] += (p[0] + p[1]) + (p[2] + p[3]);
+                for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(qr[st], f.template key_operand<true>(h, st), s[h]);
+        }
+    };
+    float sum[kTiles];
+    auto weigh = [&](int t0) {
+#pragma unroll
+        for (int h = 0; h < kTiles; ++h)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[h][r] = exp2_fast(__builtin_fmaf(s[h][r], a.scale_log2, -log[r]));
+        if (t0 < all_low || t0 + kTokens > all_high) {
+#pragma unroll
+            for (int h = 0; h < kTiles; ++h) {
+                const int t = t0 + 16 * h + (lane & 15);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[h][r] = t < see_high[r] && t >= see_low[r] ? s[h][r] : 0.f;
             }
         }
-        const float y = sum_quarters(sum[0]), z = sum_quarters(sum[1]);
-        if (x.at) *x.at = x.old + (lane & 16 ? z : y);
-        x = nx;
+#pragma unroll
+        for (int h = 0; h < kTiles; ++h) sum[h] += (s[h][0] + s[h][1]) + (s[h][2] + s[h][3]);
+    };
+
+    load_keys(w, true);
+    load_weight(w);
+    int seq = -1, head = -1;
+    for (;;) {
+        Work nw = w;
+        nw.u += w.st.cost;
+        ++nw.unit;
+        const bool more = settle(a, &nw);
+        if (!more) nw = w;
+        const int t0 = (w.st.low / kTokens + w.unit) * kTokens, last = w.st.cost - 1;
+#pragma unroll
+        for (int h = 0; h < kTiles; ++h) sum[h] = 0.f;
+        for (int tile = 0; tile < last; ++tile) {
+            queries(w, tile);
+            products();
+            weigh(t0);
+        }
+        if (last || w.seq != seq || w.head != head) queries(w, last);
+        seq = last ? -1 : w.seq;
+        head = w.head;
+        products();
+        load_keys(nw, more);
+        weigh(t0);
+        // the sums over the four quarters, that of tile h in quarter h (of two tiles: in h and h + 2)
+        float y = add_quarters(sum[0], sum[1]);
+        y = kTiles == 4 ? add_halves(y, add_quarters(sum[kTiles - 2], sum[kTiles - 1])) : sum_halves(y);
+        if (place) *place = (t0 + (lane & (kTokens - 1)) < w.q.len - w.q.n ? old : 0.f) + y;
+        if (!more) break;
         w = nw;
+        load_weight(w);
     }
 }
 
@@ -491,7 +558,7 @@ template <typename T, int FORM, int DP>
 hipError_t weigh_run(const AttnArgs& a, int cus, int which, hipStream_t s) {
     hipError_t e = hipSuccess;
     if (which & 1) {
-        weigh_few_kernel<T, FORM, (DP == 96 ? 128 : DP)><<<4 * cus, 64 * kWeighWaves, 0, s>>>(a);
+        weigh_few_kernel<T, FORM, (DP == 96 ? 128 : DP)><<<8 * cus, 64 * kWeighWaves, 0, s>>>(a);
         e = hipGetLastError();
     }
     if (e == hipSuccess && (which & 2)) {
