@@ -291,20 +291,22 @@ __global__ __launch_bounds__(64 * kWeighWaves, (DP <= 64 || (FORM == kForm4 && D
     }
 }
 
-// Many rows: a workgroup has kBlockTokens positions, whose keys its four wavefronts all hold in registers (as
-// 16-bit values) while they stream the query rows past them, 32 at a time and every wavefront its own; at the end
-// the four sums of each position are added.  A wavefront brings its next rows into its part of LDS by loads that
-// pass no registers, and reads them back as it needs them: no barrier inside the loop.  Per 32 rows and 128
+// Many rows: a workgroup has a block of positions, whose keys its four wavefronts all hold in registers (as 16-bit
+// values) while they stream the query rows past them, 64 at a time and every wavefront its own; at the end the
+// four sums of each position are added.  A wavefront brings its next rows into its part of LDS by loads that pass
+// no registers, 32 rows as soon as those before them are read: no barrier inside the loop.  Per 32 rows and 128
 // positions of 128 channels that is 8 KB of LDS read against 32 matrix instructions of 32 cycles, and 64
 // exponentials of 16 cycles with two more instructions each beside them, which bound it.
-template <typename T, int FORM, int DP>
+// TILES: key tiles of 32 positions, what the registers hold (4, or 2 of 256 channels), or 1 where there would be
+// fewer blocks than compute units.
+template <typename T, int FORM, int DP, int TILES>
 struct Block {
-    static constexpr int kTiles = DP <= 128 ? 4 : 2;       // key tiles of 32 positions: what the registers hold
+    static constexpr int kTiles = TILES;
     static constexpr int kTokens = 32 * kTiles;
     static constexpr int kSteps = DP / 16;                 // matrix instructions of a tile
     static constexpr int kChunks = DP <= 64 ? 8 : DP <= 128 ? 16 : 32;  // 16-byte chunks of a query row in LDS
     static constexpr int kRowMask = DP <= 64 ? 7 : 15;
-    static constexpr int kRow = 16 * kChunks, kTile = 32 * kRow;  // bytes of a query row and of 32
+    static constexpr int kRow = 16 * kChunks, kHalf = 32 * kRow;  // bytes of a query row and of 32
     static constexpr int kBits = form_bits(FORM);
     static constexpr int kScaleBytes = FORM == kForm4 ? scale_row(DP) : 4;
 
@@ -355,8 +357,13 @@ struct Block {
     }
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(1))) const void global_void;
+// 16 bytes a lane from memory into LDS, lane after lane from `to` on (a byte offset, the same in all lanes).  In
+// assembly: the compiler would wait for every such load before any later read of LDS.  What reads the bytes waits
+// for vmcnt by itself.
+typedef __attribute__((address_space(3))) const void lds_void;
+__device__ __forceinline__ void load_to_lds(const void* from, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory", "m0");
+}
 
 // The units of the kernel for many rows: kTokens positions of one sequence and key head.
 template <int TOKENS>
@@ -367,18 +374,16 @@ __device__ __forceinline__ int block_units(const AttnArgs& a, const Seq& q, int*
     return *high > *low ? (*high + TOKENS - 1) / TOKENS - *low / TOKENS : 0;
 }
 
-template <typename T, int FORM, int DP>
+template <typename T, int FORM, int DP, int TILES>
 __global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArgs a) {
-    using F = Block<T, FORM, DP>;
-    __shared__ __attribute__((aligned(16))) unsigned char rows[kWeighWaves][F::kTile];
-    __shared__ float logs[kWeighWaves][32];
-    __shared__ int highs[kWeighWaves][32], lows[kWeighWaves][32];
-    __shared__ const uint16_t* places[kWeighWaves][32];
+    using F = Block<T, FORM, DP, TILES>;
+    __shared__ __attribute__((aligned(16))) unsigned char rows[kWeighWaves][2][F::kHalf];
+    __shared__ float logs[kWeighWaves][64];
+    __shared__ int highs[kWeighWaves][64], lows[kWeighWaves][64];
+    __shared__ const uint16_t* places[kWeighWaves][64];
     __shared__ float sums[kWeighWaves][F::kTokens];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = lane >> 5;
-    const int G = gridDim.x, D = a.c.head_dim;
-    // consecutive units on one XCD (workgroups go to the 8 XCDs in turn): they share query rows in its L2
-    const int me = (G & 7) == 0 ? (blockIdx.x & 7) * (G >> 3) + (blockIdx.x >> 3) : blockIdx.x;
+    const int D = a.c.head_dim;
 
     auto scan = [&](int x) {  // inclusive sums over the lanes
         for (int d = 1; d < 64; d <<= 1) {
@@ -387,20 +392,29 @@ __global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArg
         }
         return x;
     };
-    for (int u = me;; u += G) {
+    auto units_of = [&](int s, Seq* q) {
+        if (s >= a.sequences) return 0;
+        int low, high;
+        *q = read_seq(a, s);
+        return block_units<F::kTokens>(a, *q, &low, &high);
+    };
+    int U = 0;
+    for (int s0 = 0; s0 < a.sequences; s0 += 64) {
+        Seq x = {};
+        U = __builtin_elementwise_add_sat(U, __builtin_amdgcn_readlane(scan(units_of(s0 + lane, &x) * a.c.heads), 63));
+    }
+    if (U == kMostSlots) return;
+    // Consecutive units on one XCD (workgroups go to the 8 XCDs in turn): they share query rows in its L2.
+    const int xcds = (gridDim.x & 7) == 0 ? 8 : 1, per_xcd = (U + xcds - 1) / xcds;
+    const int begin = blockIdx.x % xcds * per_xcd, end = min(begin + per_xcd, U);
+    for (int u = begin + blockIdx.x / xcds; u < end; u += gridDim.x / xcds) {
         // the sequence of unit u
         Seq q = {};
         int seq = 0, head = 0, unit = 0, before = 0;
-        bool none = true;
-        for (int s0 = 0; s0 < a.sequences && none; s0 += 64) {
-            int low, high, per = 0;
+        for (int s0 = 0;; s0 += 64) {
             Seq x = {};
-            if (s0 + lane < a.sequences) {
-                x = read_seq(a, s0 + lane);
-                per = block_units<F::kTokens>(a, x, &low, &high);
-            }
-            const int sum = scan(per * a.c.heads);
-            const uint64_t past = __ballot(__builtin_elementwise_add_sat(before, sum) > u);
+            const int per = units_of(s0 + lane, &x), sum = scan(per * a.c.heads);
+            const uint64_t past = __ballot(before + sum > u);
             if (past) {
                 const int l = __builtin_ctzll(past);
                 const int ph = __builtin_amdgcn_readlane(per, l);
@@ -412,124 +426,155 @@ __global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArg
                 q.n = __builtin_amdgcn_readlane(x.n, l);
                 q.len = __builtin_amdgcn_readlane(x.len, l);
                 q.rows = __builtin_amdgcn_readlane(x.rows, l);
-                none = false;
+                break;
             }
-            before = __builtin_elementwise_add_sat(before, __builtin_amdgcn_readlane(sum, 63));
+            before += __builtin_amdgcn_readlane(sum, 63);
         }
-        if (none) return;
         int low, high;
         block_units<F::kTokens>(a, q, &low, &high);
         const int t0 = (low / F::kTokens + unit) * F::kTokens;
         F f;
         f.load(a, seq, head, t0, low, high, lane);
 
-        // the rows that may see some of it: tiles [r0, r1) of 32
+        // the rows that may see some of it: tiles [r0, r1) of 64
         const int base = q.len - q.n;
         const int64_t first = a.causal ? (int64_t)max(0, t0 - base) * a.share : 0;
         const int64_t last = a.window ? min((int64_t)q.rows, max((int64_t)0, (int64_t)t0 + F::kTokens - 1 + a.window - base) * a.share) : q.rows;
-        const int r0 = (int)(first / 32), r1 = (int)((last + 31) / 32);
-        unsigned char* mine = rows[wave];
-        // What lane l says about row l % 32 of a tile: where it is, its logarithm, the positions that it sees.
+        const int r0 = (int)(first / 64), r1 = (int)((last + 63) / 64);
+        // What lane l says about row l of a tile: where it is, its logarithm, the positions that it sees.
         const uint16_t* place = nullptr;
         float row_log = 0.f;
         int row_high = 0, row_low = 0;
         auto describe = [&](int tile) {
-            const int row = tile * 32 + (lane & 31), tk = share_of(a, min(row, q.rows - 1));
-            const int hs = min(row, q.rows - 1) - tk * a.share;
+            const int row = tile * 64 + lane, at = min(row, q.rows - 1), tk = share_of(a, at), hs = at - tk * a.share;
             const bool on = row < q.rows;
             place = (const uint16_t*)a.q + (int64_t)(q.first + tk) * a.q_stride + (int64_t)(head * a.share + hs) * D;
             const float x = a.row_lse[(int64_t)(q.first + tk) * a.q_heads + head * a.share + hs];
-            row_log = on && x != -__builtin_inff() ? x * kLog2e : __builtin_inff();
+            row_log = x;  // (not looked at before the rows are: that would wait for it)
             row_high = on ? (a.causal ? min(base + tk + 1, q.len) : q.len) : 0;
             row_low = a.window ? base + tk - a.window + 1 : 0;
+            places[wave][lane] = place;
         };
-        // Brings the rows that were described: their chunks swizzled by the row, so that the lanes of a read spread
-        // over the banks; chunks behind a row's end (its last one again) meet zeros of the keys.
-        auto bring = [&]() {
-            if (lane < 32) places[wave][lane] = place;
+        // Brings the rows of half p that were described: their chunks swizzled by the row, so that the lanes of a read
+        // spread over the banks; chunks behind a row's end (its last one again) meet zeros of the keys.
+        auto bring = [&](int p) {
+            const uint32_t to = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void*)rows[wave][p]);
             const int l = opaque(lane), r = l / F::kChunks;  // (worked out here, not kept in registers through the loop)
             const int at = (l % F::kChunks ^ r) << 4, most = 2 * D - 16;
             constexpr int kRows = 64 / F::kChunks;  // of one load
+            constexpr int kBatch = F::kHalf / 1024 < 8 ? F::kHalf / 1024 : 8;  // addresses read at a time
 #pragma unroll
-            for (int i = 0; i < F::kTile / 1024; ++i) {
-                const uint8_t* p = (const uint8_t*)places[wave][i * kRows + r] + (uint32_t)min(at ^ ((i * kRows & F::kRowMask) << 4), most);
-                __builtin_amdgcn_global_load_lds((global_void*)p, (lds_void*)(mine + i * 1024), 16, 0, 0);
+            for (int i0 = 0; i0 < F::kHalf / 1024; i0 += kBatch) {
+                const uint8_t* from[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) from[i] = (const uint8_t*)places[wave][32 * p + (i0 + i) * kRows + r];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    load_to_lds(from[i] + (uint32_t)min(at ^ (((i0 + i) * kRows & F::kRowMask) << 4), most), to + (i0 + i) * 1024);
             }
-        };
-        auto query = [&](int s, int l) {
-            const int r = l & 31;
-            return *(const u32x4v*)(mine + r * F::kRow + ((F::chunk(s, l >> 5) ^ (r & F::kRowMask)) << 4));
         };
         float sum[F::kTiles];
 #pragma unroll
         for (int i = 0; i < F::kTiles; ++i) sum[i] = 0.f;
-        if (r0 + wave < r1) {
-            describe(r0 + wave);
-            bring();
-        }
-        for (int tile = r0 + wave; tile < r1; tile += kWeighWaves) {
-            if (lane < 32) {
-                logs[wave][lane] = row_log;
-                highs[wave][lane] = row_high;
-                lows[wave][lane] = row_low;
-            }
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        // 32 rows, half p of a tile; next: what brings the rows that come where they were
+        auto half_tile = [&](int p, bool masked, auto next) {
             const int l = opaque(lane);
+            auto query = [&](int s) {
+                const int r = l & 31;
+                return *(const u32x4v*)(rows[wave][p] + r * F::kRow + ((F::chunk(s, l >> 5) ^ (r & F::kRowMask)) << 4));
+            };
             // (all of a row in registers where they are enough, so that the next rows may come at once)
             constexpr bool kHeld = DP <= 128;
             u32x4v qr[kHeld ? F::kSteps : 1];
             if (kHeld)
 #pragma unroll
-                for (int s = 0; s < F::kSteps; ++s) qr[s] = query(s, l);
+                for (int s = 0; s < F::kSteps; ++s) qr[s] = query(s);
             f32x4v log[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) log[j] = *(const f32x4v*)&logs[wave][8 * j + 4 * half];
-            // some row does not see some position (or is none)
-            const bool masked = __any(row_high < t0 + F::kTokens || row_low > t0);
-            const bool more = tile + kWeighWaves < r1;
-            if (kHeld && more) {
+            for (int j = 0; j < 4; ++j) log[j] = *(const f32x4v*)&logs[wave][32 * p + 8 * j + 4 * half];
+            auto ahead = [&]() {
                 asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
                 __builtin_amdgcn_sched_barrier(0);
-                describe(tile + kWeighWaves);
-                bring();
-            }
+                next();
+            };
+            if (kHeld) ahead();
+            auto product = [&](int i, int st, f32x16v& s) {
+                if (st == 0)
 #pragma unroll
-            for (int i = 0; i < F::kTiles; i += 2) {
+                    for (int j = 0; j < 16; ++j) s[j] = 0.f;
+                s = T::mfma32(kHeld ? qr[kHeld ? st : 0] : query(st), f.key[i][st], s);
+            };
+            auto weigh = [&](int i, int j, const f32x16v& s) {
+                sum[i] += exp2_fast(__builtin_fmaf(s[j], a.scale_log2, -log[j / 4][j % 4]));
+            };
+            if (!masked) {
+                // a tile's products between the exponentials of the tile before it
                 f32x16v s[2];
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[0][j] = s[1][j] = 0.f;
+                for (int st = 0; st < F::kSteps; ++st) product(0, st, s[0]);
 #pragma unroll
-                for (int st = 0; st < F::kSteps; ++st) {
-                    const u32x4v x = kHeld ? qr[kHeld ? st : 0] : query(st, l);
-                    s[0] = T::mfma32(x, f.key[i][st], s[0]);
-                    s[1] = T::mfma32(x, f.key[i + 1][st], s[1]);
+                for (int i = 0; i < F::kTiles; ++i) {
+                    const bool then = i + 1 < F::kTiles;
+                    if (then)
+#pragma unroll
+                        for (int st = 0; st < F::kSteps; ++st) product(i + 1, st, s[(i + 1) & 1]);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) weigh(i, j, s[i & 1]);
+                    if (then) {
+#pragma unroll
+                        for (int st = 0; st < F::kSteps; ++st) {
+                            __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                            __builtin_amdgcn_sched_group_barrier(0x402, 48 / F::kSteps, 0);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                if (!masked) {
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
+                for (int i = 0; i < F::kTiles; ++i) {
+                    f32x16v s;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            sum[i + h] += exp2_fast(__builtin_fmaf(s[h][j], a.scale_log2, -log[j / 4][j % 4]));
-                } else {
+                    for (int st = 0; st < F::kSteps; ++st) product(i, st, s);
                     const int t = t0 + 32 * i + (lane & 31);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const int r = 8 * (j / 4) + 4 * half + j % 4;
+                        const int r = 32 * p + 8 * (j / 4) + 4 * half + j % 4;
                         const int to = highs[wave][r], from = lows[wave][r];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float p = exp2_fast(__builtin_fmaf(s[h][j], a.scale_log2, -log[j / 4][j % 4]));
-                            sum[i + h] += t + 32 * h < to && t + 32 * h >= from ? p : 0.f;
-                        }
+                        const float x = exp2_fast(__builtin_fmaf(s[j], a.scale_log2, -log[j / 4][j % 4]));
+                        sum[i] += t < to && t >= from ? x : 0.f;
                     }
                 }
             }
-            if (!kHeld && more) {
-                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                __builtin_amdgcn_sched_barrier(0);
+            if (!kHeld) ahead();
+        };
+        if (r0 + wave < r1) {
+            describe(r0 + wave);
+            bring(0);
+            bring(1);
+        }
+        for (int tile = r0 + wave; tile < r1; tile += kWeighWaves) {
+            // (here the first half's rows have come, too)
+            logs[wave][lane] = tile * 64 + lane < q.rows && row_log != -__builtin_inff() ? row_log * kLog2e : __builtin_inff();
+            highs[wave][lane] = row_high;
+            lows[wave][lane] = row_low;
+            // some row does not see some position (or is none)
+            const uint64_t masked = __ballot(row_high < t0 + F::kTokens || row_low > t0);
+            const bool more = tile + kWeighWaves < r1;
+            constexpr int kLoads = F::kHalf / 1024;
+            asm volatile("s_waitcnt vmcnt(%0)" ::"i"(kLoads) : "memory");  // all but the second half's
+            half_tile(0, (uint32_t)masked != 0, [&]() {
+                if (!more) return;
                 describe(tile + kWeighWaves);
-                bring();
-            }
+                bring(0);
+            });
+            if (more)
+                asm volatile("s_waitcnt vmcnt(%0)" ::"i"(kLoads) : "memory");  // all but the next first half's
+            else
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            half_tile(1, masked >> 32 != 0, [&]() {
+                if (more) bring(1);
+            });
         }
 #pragma unroll
         for (int i = 0; i < F::kTiles; ++i) {
@@ -562,7 +607,14 @@ hipError_t weigh_run(const AttnArgs& a, int cus, int which, hipStream_t s) {
         e = hipGetLastError();
     }
     if (e == hipSuccess && (which & 2)) {
-        weigh_many_kernel<T, FORM, DP><<<2 * cus, 64 * kWeighWaves, 0, s>>>(a);
+        constexpr int kTiles = DP <= 128 ? 4 : 2;
+        const double blocks = (double)a.sequences * a.c.heads * ((double)a.table_pages * a.c.page_size / (32 * kTiles) + 1);
+        // (blocks of 32 positions where those of 128 would leave CUs idle, as far as the table's width tells: 128 blocks
+        // of 1500 tokens x 4 heads 77 against 48 us, 192 74 against 75, 256 73 against 95)
+        if (blocks < 0.75 * cus)
+            weigh_many_kernel<T, FORM, DP, 1><<<2 * cus, 64 * kWeighWaves, 0, s>>>(a);
+        else
+            weigh_many_kernel<T, FORM, DP, kTiles><<<2 * cus, 64 * kWeighWaves, 0, s>>>(a);
         e = hipGetLastError();
     }
     return e;
