@@ -68,7 +68,10 @@ int64_t attention_many_floats(int dim);
 hipError_t launch_attention_few(const AttnArgs& a, int type, int grid, hipStream_t s);
 hipError_t launch_weigh(const AttnArgs& a, int type, int cus, int which, hipStream_t s);
 constexpr int kWeighTokens = 32;  // positions of one of its work units
-constexpr int kWeighRows = 64;    // sequences of more query rows go to its kernel for many
+// Sequences of more query rows go to its kernel for many.  (The other one over 16-bit caches, 32 sequences over 3000
+// positions: 128 rows 122 us against 170, 192 167 against 178, 256 213 against 188; 4 sequences: 128 rows 26 against
+// 29, 256 47 against 31.)
+constexpr int kWeighRows = 128;
 hipError_t launch_attention_many(const AttnArgs& a, int type, int grid, hipStream_t s);
 
 // ---------------------------------------------------------------- eviction
