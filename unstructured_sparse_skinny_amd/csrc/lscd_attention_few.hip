@@ -25,6 +25,51 @@ namespace {
 
 constexpr int kFewWaves = 4;
 
+// Where the tiles of 16 positions lie that a wavefront has in 32 units of one sequence and key head: lane 2 u + h
+// holds the addresses of its keys and scales in unit start + u, half h; read from there as scalars.  The values' lie
+// as far from them as the two arrays do.  (4-bit codes: addresses worked out anew for every unit were a third of
+// the vector unit's work.)
+template <int BITS, int SCALES>
+struct Tiles {
+    int seq, head, start;
+    uint32_t page;                   // of the lane's tile
+    uint32_t lo, hi, scale_lo, scale_hi;
+
+    __device__ __forceinline__ void find(const AttnArgs& a, int sq, int hd, int unit, int wave, int lane) {
+        if (sq != seq || (uint32_t)(unit - start) >= 32u) {
+            seq = sq;
+            start = unit;
+            head = -1;
+            const int t = (start + (lane >> 1)) * kFewTokens + 32 * wave + 16 * (lane & 1);
+            page = page_of(a, a.table[seq * a.table_stride + min(t >> a.page_log2, a.table_pages - 1)]);
+        }
+        if (hd != head) {
+            head = hd;
+            const uint64_t row = ((uint64_t)page * (uint32_t)a.c.heads + (uint32_t)head) * (uint32_t)a.c.page_size;
+            const uint64_t k = (uint64_t)a.c.k + row * (uint32_t)(a.c.head_dim * BITS / 8), s = (uint64_t)a.c.k_scale + row * SCALES;
+            lo = (uint32_t)k;
+            hi = (uint32_t)(k >> 32);
+            scale_lo = (uint32_t)s;
+            scale_hi = (uint32_t)(s >> 32);
+        }
+    }
+    __device__ static __forceinline__ uint64_t at(uint32_t lo, uint32_t hi, int i) {
+        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane(hi, i) << 32 | (uint32_t)__builtin_amdgcn_readlane(lo, i);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t keys(const AttnArgs& a, int i) const {
+        return buffer_of((const void*)at(lo, hi, i), a.c.page_size * a.c.head_dim / 8 * BITS);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t values(const AttnArgs& a, int i) const {
+        return buffer_of((const void*)(at(lo, hi, i) + ((uint64_t)a.c.v - (uint64_t)a.c.k)), a.c.page_size * a.c.head_dim / 8 * BITS);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t key_scales(const AttnArgs& a, int i) const {
+        return buffer_of((const void*)at(scale_lo, scale_hi, i), a.c.page_size * SCALES);
+    }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t value_scales(const AttnArgs& a, int i) const {
+        return buffer_of((const void*)(at(scale_lo, scale_hi, i) + ((uint64_t)a.c.v_scale - (uint64_t)a.c.k_scale)), a.c.page_size * SCALES);
+    }
+};
+
 template <typename T, int FORM, int DP>
 struct Few : Keys<T, FORM, DP> {
     using K = Keys<T, FORM, DP>;
@@ -60,9 +105,7 @@ struct Few : Keys<T, FORM, DP> {
                 for (int w = 0; w < kValWords; w += kPer) {
                     const int at = d + w * 32 / kBits;
                     const int off = on && at < D ? ((r0 + j) * D + at) * kBits / 8 : kNoRow;
-                    if constexpr (VW * kBits == 16) {
-                        vr[4 * h + j][w] = __builtin_amdgcn_raw_buffer_load_b16(rs, off, 0, 0);
-                    } else if constexpr (kPer == 1) {
+                    if constexpr (kPer == 1) {
                         vr[4 * h + j][w] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0);
                     } else if constexpr (kPer == 2) {
                         const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, off, 0, 0);
@@ -74,12 +117,52 @@ struct Few : Keys<T, FORM, DP> {
                         for (int i = 0; i < 4; ++i) vr[4 * h + j][w + i] = x[i];
                     }
                 }
-                if (FORM == kForm4)
-                    vs[4 * h + j] = __builtin_amdgcn_raw_buffer_load_b8(hb.value_scales(p),
-                                                                      d < D ? (r0 + j) * kScaleBytes + d / kScaleGroup : kNoRow, 0, 0);
             }
         }
     }
+    // 4-bit codes: 32 positions from t0 on, in tiles i and i + 1.  WHOLE: all of them are loaded.
+    template <bool WHOLE>
+    __device__ __forceinline__ void load_value_tiles(const AttnArgs& a, const Tiles<kBits, kScaleBytes>& tiles, int i, int t0, int low,
+                                                     int high, int lane) {
+        const int D = a.c.head_dim, g = lane >> 4, d = VW * (lane & 15), step = D / 2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = (t0 + 16 * h) & (a.c.page_size - 1);
+            const auto rs = tiles.values(a, i + h), scales = tiles.value_scales(a, i + h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int pos = t0 + 16 * h + 4 * g + j;
+                const bool on = d < D && (WHOLE || (pos < high && pos >= low));
+                const int off = on ? 4 * g * step + d / 2 : kNoRow, at = (row + j) * step;
+                if constexpr (VW == 4) {
+                    vr[4 * h + j][0] = __builtin_amdgcn_raw_buffer_load_b16(rs, off, at, 0);
+                } else if constexpr (VW == 8) {
+                    vr[4 * h + j][0] = __builtin_amdgcn_raw_buffer_load_b32(rs, off, at, 0);
+                } else if constexpr (VW == 16) {
+                    const u32x2v x = __builtin_amdgcn_raw_buffer_load_b64(rs, off, at, 0);
+                    vr[4 * h + j][0] = x[0];
+                    vr[4 * h + j][kValWords - 1] = x[1];
+                }
+                vs[4 * h + j] = __builtin_amdgcn_raw_buffer_load_b8(scales, on ? 4 * g * kScaleBytes + d / kScaleGroup : kNoRow,
+                                                                    (row + j) * kScaleBytes, 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void load_values(const AttnArgs& a, const Tiles<kBits, kScaleBytes>& tiles, int i, int t0, int low,
+                                                int high, int lane) {
+        if (t0 >= low && t0 + 32 <= high)  // (as many loads either way: the waits count them)
+            load_value_tiles<true>(a, tiles, i, t0, low, high, lane);
+        else
+            load_value_tiles<false>(a, tiles, i, t0, low, high, lane);
+    }
+    __device__ __forceinline__ void load_keys(const AttnArgs& a, const Tiles<kBits, kScaleBytes>& tiles, int i, int t0, int high,
+                                              int lane) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            this->load_tile(h, tiles.keys(a, i + h), tiles.key_scales(a, i + h), a.c.head_dim, (t0 + 16 * h) & (a.c.page_size - 1),
+                            t0 + 16 * h + (lane & 15) < high, lane);
+    }
+    using K::load_keys;
     // A position that was not loaded has zeros for codes, but any scale: 1 instead.
     __device__ __forceinline__ void mask_scales(int t0, int low, int high, int lane) {
         if (!kScaled) return;
@@ -120,6 +203,8 @@ struct Few : Keys<T, FORM, DP> {
         }
     }
     __device__ __forceinline__ bool any_odd() const {
+        // (4-bit codes are finite: their scales say what may not be; conversions here would be kept for the products)
+        if (FORM == kForm4) return top_values();
         bool odd = false;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -138,12 +223,13 @@ struct FewItem {
         tile_range<kFewRows>(a, q, tile, &low, &high);
         units = max(1, (high + kFewTokens - 1) / kFewTokens - low / kFewTokens);
     }
-    __device__ __forceinline__ int first_position(int unit) const { return (low / kFewTokens + unit) * kFewTokens; }
+    __device__ __forceinline__ int place(int unit) const { return low / kFewTokens + unit; }  // among all of the sequence
+    __device__ __forceinline__ int first_position(int unit) const { return place(unit) * kFewTokens; }
 };
 
 // LSE: the logarithms of the rows' sums are written too.
 template <typename T, int FORM, int DP, bool LSE>
-__global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kFewWaves, (FORM == kForm4 && DP <= 128 ? 3 : 1)) void attention_few_kernel(AttnArgs a) {
     using F = Few<T, FORM, DP>;
     constexpr int VW = F::VW;
     __shared__ float sh_o[kFewWaves][kFewRows][DP];
@@ -327,18 +413,29 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
     };
 
     F f;
+    constexpr bool kTiled = FORM == kForm4;
+    Tiles<F::kBits, F::kScaleBytes> tiles;
+    tiles.seq = tiles.start = -1;
     {
         HeadBase hb;
         hb.set<F::kBits, F::kScaleBytes>(a.c, it.head);
         const int t0 = it.first_position(k) + 32 * wave;
-        const int e[2] = {entry_of(a, it.seq, t0), entry_of(a, it.seq, t0 + 16)};
+        int e[2] = {0, 0};
+        if constexpr (kTiled) {
+            tiles.find(a, it.seq, it.head, it.place(k), wave, lane);
+        } else {
+            e[0] = entry_of(a, it.seq, t0);
+            e[1] = entry_of(a, it.seq, t0 + 16);
+        }
         load_queries();
         // keys before values, here as in the loop: the wait for the older loads then leaves the younger
         // ones in flight
         __builtin_amdgcn_sched_barrier(0);
-        f.load_keys(a, hb, e, t0, it.high, lane);
+        if constexpr (kTiled) f.load_keys(a, tiles, 0, t0, it.high, lane);
+        else f.load_keys(a, hb, e, t0, it.high, lane);
         __builtin_amdgcn_sched_barrier(0);
-        f.load_values(a, hb, e, t0, it.low, it.high, lane);
+        if constexpr (kTiled) f.load_values(a, tiles, 0, t0, it.low, it.high, lane);
+        else f.load_values(a, hb, e, t0, it.low, it.high, lane);
         __builtin_amdgcn_sched_barrier(0);
     }
     clear();
@@ -363,7 +460,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
         HeadBase hb;
         hb.set<F::kBits, F::kScaleBytes>(a.c, nx.head);
         const int nt = nx.first_position(nk) + 32 * wave, next_high = more ? nx.high : 0;
-        const int e[2] = {entry_of(a, nx.seq, nt), entry_of(a, nx.seq, nt + 16)};
+        int e[2] = {0, 0};
+        if constexpr (!kTiled) {
+            e[0] = entry_of(a, nx.seq, nt);
+            e[1] = entry_of(a, nx.seq, nt + 16);
+        }
         f32x4v s[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -379,7 +480,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                 for (int st = 0; st < F::kSteps; ++st) s[h] = T::mfma16(f.template key_operand<true>(h, st), qr[st], s[h]);
             }
         }
-        f.load_keys(a, hb, e, nt, next_high, lane);
+        int ni = 0;
+        if constexpr (kTiled) {
+            tiles.find(a, nx.seq, nx.head, nx.place(nk), wave, lane);
+            ni = 2 * (nx.place(nk) - tiles.start);
+            f.load_keys(a, tiles, ni, nt, next_high, lane);
+        } else {
+            f.load_keys(a, hb, e, nt, next_high, lane);
+        }
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = product(s[i / 4][i % 4], a.scale_log2);
@@ -470,7 +578,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void attention_few_kernel(AttnArgs 
                 }
             }
         }
-        f.load_values(a, hb, e, nt, nx.low, next_high, lane);
+        if constexpr (kTiled) f.load_values(a, tiles, ni, nt, nx.low, next_high, lane);
+        else f.load_values(a, hb, e, nt, nx.low, next_high, lane);
         if (ends) {
             finish();
             if (!more) break;
@@ -512,7 +621,10 @@ hipError_t few_type(const AttnArgs& a, int grid, hipStream_t s) {
 
 }  // namespace
 
-int attention_few_grid(int cus) { return 2 * cus; }
+// As many as run at once; over 4-bit codes three run on a CU, and twice as many even out what they wait for (64
+// sequences of up to 2048 positions: 235 us with 6 a CU, 245 with 3, 283 with 4).
+int attention_few_grid(int cus, int type, int dim) { return cache_form(type) == kForm4 && dim <= 128 ? 6 * cus : 2 * cus; }
+
 int64_t attention_few_floats(int dim) { return kFewRows * ((dim <= 64 ? 64 : dim <= 128 ? 128 : 256) + 4); }
 
 hipError_t launch_attention_few(const AttnArgs& a, int type, int grid, hipStream_t s) {

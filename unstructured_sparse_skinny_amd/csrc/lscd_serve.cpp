@@ -281,7 +281,7 @@ lscd_status_t lscd_attention_create(int32_t q_heads, int32_t kv_heads, int32_t h
         return LSCD_ERROR_HIP;
     }
     h->cus = cus;
-    const int few = lscd::attention_few_grid(cus), many = lscd::attention_many_grid(cus);
+    const int few = lscd::attention_few_grid(cus, LSCD_E2M1, head_dim), many = lscd::attention_many_grid(cus);
     const int64_t floats = std::max(2 * few * lscd::attention_few_floats(head_dim),
                                     2 * many * lscd::attention_many_floats(head_dim));
     if ((e = hipMalloc((void**)&h->part, (size_t)floats * 4)) != hipSuccess ||
@@ -437,7 +437,7 @@ lscd_status_t attend(lscd_attention_t h, const lscd_cache_t* cache, const void* 
         return LSCD_ERROR_NOT_SUPPORTED;
     if (few) {
         hipError_t e = lscd::launch_attention_few(
-            a, type, grid(lscd::attention_few_grid(h->cus), lscd::kFewRows, lscd::kFewTokens, 20.0 / rows), (hipStream_t)stream);
+            a, type, grid(lscd::attention_few_grid(h->cus, cache->type, h->head_dim), lscd::kFewRows, lscd::kFewTokens, 20.0 / rows), (hipStream_t)stream);
         if (e != hipSuccess) return status_of(e);
     }
     if (both) {

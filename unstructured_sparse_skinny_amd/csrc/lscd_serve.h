@@ -60,7 +60,7 @@ struct AttnArgs {
     float* weight;           // [num_pages][heads][page_size] (weigh)
 };
 // Workgroups of one launch at most, and floats of one partial result.
-int attention_few_grid(int cus);
+int attention_few_grid(int cus, int type, int dim);  // by the cache's type
 int attention_many_grid(int cus);
 int attention_many_tokens(int dim);  // positions of one of the many-row kernel's work units
 int64_t attention_few_floats(int dim);
