@@ -302,13 +302,36 @@ struct Keys {
         }
     }
     // 16 TILES positions from t0 on, in the pages of the table entries e; positions from `high` on are zero.
+    // (Not by load_tile: with its scalar offsets the attention over e4m3 heads of 64 channels took 231 us in place of
+    // 216, one sequence over 32768 positions 28.7 in place of 26.0.)
     __device__ __forceinline__ void load_keys(const AttnArgs& a, const HeadBase& hb, const int (&e)[TILES], int t0, int high,
                                               int lane) {
+        static_assert(FORM != kForm4, "4-bit codes are loaded tile by tile");
+        const int D = a.c.head_dim;
 #pragma unroll
         for (int h = 0; h < TILES; ++h) {
-            const int t = t0 + 16 * h;
+            const int t = t0 + 16 * h, row = (t & (a.c.page_size - 1)) + (lane & 15);
             const uint32_t p = page_of(a, e[h]);
-            load_tile(h, hb.keys(p), hb.key_scales(p), a.c.head_dim, t & (a.c.page_size - 1), t + (lane & 15) < high, lane);
+            const bool on = t + (lane & 15) < high;
+            const auto rs = hb.keys(p);
+            if (FORM == kForm8) {
+#pragma unroll
+                for (int u = 0; u < DP / 64; ++u) {
+                    const int d = 64 * u + 16 * (lane >> 4);
+                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? row * D + d : kNoRow, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kr[h][4 * u + i] = x[i];
+                }
+                ks[h][0] = __builtin_amdgcn_raw_buffer_load_b32(hb.key_scales(p), on ? row * 4 : kNoRow, 0, 0);
+            } else {
+#pragma unroll
+                for (int s = 0; s < kSteps; ++s) {
+                    const int d = 32 * s + 8 * (lane >> 4);
+                    const u32x4v x = __builtin_amdgcn_raw_buffer_load_b128(rs, on && d < D ? (row * D + d) * 2 : kNoRow, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kr[h][4 * s + i] = x[i];
+                }
+            }
         }
     }
 
