@@ -19,7 +19,6 @@
 namespace lscd {
 namespace {
 
-constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / 64;
 constexpr int kBins = 2048;
 
 // Order of the weights: larger values have larger keys, zeros are equal, NaN counts as the largest.
@@ -44,14 +43,15 @@ __device__ __forceinline__ int64_t page_at(const EvictArgs& a, const int32_t* ta
     return (uint32_t)e < (uint32_t)a.c.num_pages ? e : 0;
 }
 
-// KEYS: weights that LDS holds; longer sequences are read again for every digit.
-template <int KEYS>
-__global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(EvictArgs a) {
-    __shared__ uint32_t keys[KEYS];
+// PER: weights that a thread holds; longer sequences (of the first positions more than THREADS x PER) are read
+// again for every digit.  A wavefront has one stretch of positions, 64 after 64.
+template <int THREADS, int PER>
+__global__ __launch_bounds__(THREADS) void evict_select_kernel(EvictArgs a) {
+    constexpr int kSelectThreads = THREADS, kSelectWaves = THREADS / 64, kMine = kBins / THREADS;  // (bins of a thread)
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t sums[2 * kSelectWaves];
     __shared__ uint32_t found[2];  // a digit, and how many of its bin are wanted
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int s = blockIdx.x / a.c.heads, h = blockIdx.x % a.c.heads;
     const Kept kp(a, s);
     int32_t* out = a.kept + ((int64_t)s * a.c.heads + h) * a.keep;
@@ -63,14 +63,49 @@ __global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(EvictArgs 
         return;
     }
     if (k == 0) return;
-    auto load = [&](int j) {
-        const int64_t p = page_at(a, a.table, a.table_stride, s, j >> a.page_log2);
-        return key_of(a.weight[(p * a.c.heads + h) * a.c.page_size + (j & (a.c.page_size - 1))]);
+
+    const int steps = (n + kSelectThreads - 1) / kSelectThreads;
+    const int low = min(wave * steps * 64, n), high = min(low + steps * 64, n);
+    auto entry = [&](int i) { return page_at(a, a.table, a.table_stride, s, min(low + i * 64 + lane, n - 1) >> a.page_log2); };
+    auto weight = [&](int64_t page, int i) {
+        return a.weight[(page * a.c.heads + h) * a.c.page_size + (min(low + i * 64 + lane, n - 1) & (a.c.page_size - 1))];
     };
-    const bool held = n <= KEYS;
-    if (held)
-        for (int j = tid; j < n; j += kSelectThreads) keys[j] = load(j);
-    auto key = [&](int j) { return held ? keys[j] : load(j); };
+    const bool held = steps <= PER;
+    uint32_t keys[PER];
+    if (held) {
+        constexpr int kBatch = PER <= 16 ? PER : 12;  // loads in flight
+        static_assert(PER % kBatch == 0, "whole batches");
+#pragma unroll
+        for (int i0 = 0; i0 < PER; i0 += kBatch) {
+            if (i0 >= steps) break;
+            int64_t page[kBatch];
+            float w[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) page[i] = entry(i0 + i);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) w[i] = weight(page[i], i0 + i);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) keys[i0 + i] = key_of(w[i]);
+        }
+    }
+    // f(position, key, whether there is one) for every step of the wavefront's stretch
+    auto each = [&](auto f) {
+        if (held) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (i < steps) f(low + i * 64 + lane, keys[i], low + i * 64 + lane < high);
+        } else {
+            for (int i = 0; i < steps; ++i) f(low + i * 64 + lane, key_of(weight(entry(i), i)), low + i * 64 + lane < high);
+        }
+    };
+    // the sum of what the wavefronts before this one have put into x
+    auto before = [&](const uint32_t* x) {
+        const uint32_t mine = x[lane % kSelectWaves];
+        uint32_t sum = 0;
+#pragma unroll
+        for (int w = 0; w < kSelectWaves - 1; ++w) sum += w < wave ? __builtin_amdgcn_readlane(mine, w) : 0u;
+        return sum;
+    };
 
     uint32_t prefix = 0, mask = 0;  // the digits found, and their bits
     uint32_t want = (uint32_t)k;
@@ -78,63 +113,60 @@ __global__ __launch_bounds__(kSelectThreads) void evict_select_kernel(EvictArgs 
         const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bins = digit == 2 ? 1024 : 2048;
         for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
         __syncthreads();
-        for (int j = tid; j < n; j += kSelectThreads) {
-            const uint32_t x = key(j);
-            if ((x & mask) == prefix) atomicAdd(&hist[(x >> shift) & (bins - 1)], 1u);
-        }
+        each([&](int, uint32_t x, bool on) {
+            if (on && (x & mask) == prefix) atomicAdd(&hist[(x >> shift) & (bins - 1)], 1u);
+        });
         __syncthreads();
-        // two bins a thread, from the top: how many keys lie above and in them
-        const int top = kBins - 1 - 2 * tid;
-        const uint32_t c0 = hist[top], c1 = hist[top - 1];
-        uint32_t sum = c0 + c1;
+        // a few bins a thread, from the top: how many keys lie above and in them
+        const int top = kBins - 1 - kMine * tid;
+        uint32_t count[kMine], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            count[i] = hist[top - i];
+            sum += count[i];
+        }
+        const uint32_t mine = sum;
         for (int d = 1; d < 64; d <<= 1) {
             const uint32_t up = __shfl_up(sum, d, 64);
             if (lane >= d) sum += up;
         }
         if (lane == 63) sums[wave] = sum;
         __syncthreads();
-        for (int w = 0; w < wave; ++w) sum += sums[w];
-        const uint32_t above = sum - c0 - c1;
-        if (above < want && want <= sum) {
-            const bool upper = want <= above + c0;
-            found[0] = upper ? top : top - 1;
-            found[1] = want - above - (upper ? 0u : c0);
+        uint32_t above = before(sums) + sum - mine;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            if (above < want && want <= above + count[i]) {
+                found[0] = top - i;
+                found[1] = want - above;
+            }
+            above += count[i];
         }
         __syncthreads();
         prefix |= found[0] << shift;
         mask |= (uint32_t)(bins - 1) << shift;
         want = found[1];
     }
-    // `prefix` is the k-th largest key, `want` how many keys equal to it are kept.  Stretches of whole wavefronts:
-    const int per = (n + kSelectThreads - 1) / kSelectThreads * 64;
-    const int low = min(wave * per, n), high = min(low + per, n);
+    // `prefix` is the k-th largest key, `want` how many keys equal to it are kept
     uint32_t more = 0, same = 0;
-    for (int j0 = low; j0 < high; j0 += 64) {
-        const bool on = j0 + lane < high;
-        const uint32_t x = on ? key(j0 + lane) : 0u;
+    each([&](int, uint32_t x, bool on) {
         more += __popcll(__ballot(on && x > prefix));
         same += __popcll(__ballot(on && x == prefix));
-    }
+    });
     if (lane == 0) {
         sums[wave] = more;
         sums[kSelectWaves + wave] = same;
     }
     __syncthreads();
-    more = same = 0;
-    for (int w = 0; w < wave; ++w) {
-        more += sums[w];
-        same += sums[kSelectWaves + w];
-    }
+    more = before(sums);
+    same = before(sums + kSelectWaves);
     const uint64_t below = ((uint64_t)1 << lane) - 1;
-    for (int j0 = low; j0 < high; j0 += 64) {
-        const bool on = j0 + lane < high;
-        const uint32_t x = on ? key(j0 + lane) : 0u;
+    each([&](int j, uint32_t x, bool on) {
         const uint64_t gt = __ballot(on && x > prefix), eq = __ballot(on && x == prefix);
         const uint32_t g = more + __popcll(gt & below), e = same + __popcll(eq & below);
-        if (on && (x > prefix || (x == prefix && e < want))) out[g + min(e, want)] = j0 + lane;
+        if (on && (x > prefix || (x == prefix && e < want))) out[g + min(e, want)] = j;
         more += __popcll(gt);
         same += __popcll(eq);
-    }
+    });
 }
 
 // A row of the cache: its number among all rows of all heads, or -1.
@@ -276,11 +308,14 @@ int64_t evict_workgroups(const EvictArgs& a) {
 
 hipError_t launch_evict(const EvictArgs& a, hipStream_t s) {
     const unsigned pairs = (unsigned)((int64_t)a.sequences * a.c.heads);
-    // (two workgroups a CU with the smaller one)
-    if ((int64_t)a.table_pages * a.c.page_size <= 16384)
-        evict_select_kernel<16384><<<pairs, kSelectThreads, 0, s>>>(a);
+    // (what the registers of 16 wavefronts hold; few where that is enough, as far as the tables' width tells)
+    const int64_t span = (int64_t)a.table_pages * a.c.page_size;
+    if (span <= 256 * 16)
+        evict_select_kernel<256, 16><<<pairs, 256, 0, s>>>(a);
+    else if (span <= 1024 * 16)
+        evict_select_kernel<1024, 16><<<pairs, 1024, 0, s>>>(a);
     else
-        evict_select_kernel<36864><<<pairs, kSelectThreads, 0, s>>>(a);
+        evict_select_kernel<1024, 36><<<pairs, 1024, 0, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return a.row_bytes % 16 ? move<u32x2v>(a, s) : move<u32x4v>(a, s);
