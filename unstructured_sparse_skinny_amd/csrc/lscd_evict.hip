@@ -72,20 +72,24 @@ __global__ __launch_bounds__(THREADS) void evict_select_kernel(EvictArgs a) {
     };
     const bool held = steps <= PER;
     uint32_t keys[PER];
+    // The keys of steps i0 .. i0 + kBatch - 1 into x: all loads in flight together.
+    constexpr int kBatch = PER <= 16 ? PER : 12;
+    static_assert(PER % kBatch == 0, "whole batches");
+    auto load = [&](int i0, uint32_t* x) {
+        int64_t page[kBatch];
+        float w[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) page[i] = entry(i0 + i);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) w[i] = weight(page[i], i0 + i);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) x[i] = key_of(w[i]);
+    };
     if (held) {
-        constexpr int kBatch = PER <= 16 ? PER : 12;  // loads in flight
-        static_assert(PER % kBatch == 0, "whole batches");
 #pragma unroll
         for (int i0 = 0; i0 < PER; i0 += kBatch) {
             if (i0 >= steps) break;
-            int64_t page[kBatch];
-            float w[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) page[i] = entry(i0 + i);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) w[i] = weight(page[i], i0 + i);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) keys[i0 + i] = key_of(w[i]);
+            load(i0, keys + i0);
         }
     }
     // f(position, key, whether there is one) for every step of the wavefront's stretch
@@ -95,7 +99,12 @@ __global__ __launch_bounds__(THREADS) void evict_select_kernel(EvictArgs a) {
             for (int i = 0; i < PER; ++i)
                 if (i < steps) f(low + i * 64 + lane, keys[i], low + i * 64 + lane < high);
         } else {
-            for (int i = 0; i < steps; ++i) f(low + i * 64 + lane, key_of(weight(entry(i), i)), low + i * 64 + lane < high);
+            for (int i0 = 0; i0 < steps; i0 += kBatch) {
+                uint32_t x[kBatch];
+                load(i0, x);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) f(low + (i0 + i) * 64 + lane, x[i], low + (i0 + i) * 64 + lane < high);
+            }
         }
     };
     // the sum of what the wavefronts before this one have put into x
@@ -207,12 +216,20 @@ __global__ __launch_bounds__(kMoveThreads) void evict_copy_kernel(EvictArgs a, i
         }
     }
     __syncthreads();
-    const int units = a.row_bytes / (int)sizeof(U);
+    const int units = a.row_bytes / (int)sizeof(U), per = kMoveThreads / units;  // rows of a pass
+    const int r0 = tid / units, u = tid % units;
+    if (r0 >= per) return;
     U* data = (U*)(z ? a.c.v : a.c.k);
-#pragma unroll 4
-    for (int i = tid; i < rows * units; i += kMoveThreads) {
-        const int r = i / units, u = i % units;
-        if (dst[r] >= 0) data[dst[r] * units + u] = data[src[r] * units + u];
+    constexpr int kAtOnce = 4;
+    for (int r = r0; r < rows; r += kAtOnce * per) {  // (rows behind the last are read again and not written)
+        U x[kAtOnce];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) x[j] = data[src[min(r + j * per, rows - 1)] * units + u];
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+            const int64_t to = r + j * per < rows ? dst[r + j * per] : -1;
+            if (to >= 0) data[to * units + u] = x[j];
+        }
     }
 }
 
@@ -221,6 +238,8 @@ __global__ __launch_bounds__(kMoveThreads) void evict_copy_kernel(EvictArgs a, i
 constexpr int kInPlaceThreads = 1024, kColumn = 128, kAhead = 4;
 template <typename U>
 __global__ __launch_bounds__(kInPlaceThreads) void evict_in_place_kernel(EvictArgs a, int columns) {
+    constexpr int kRows = kInPlaceThreads * kAhead;  // of one round at most
+    __shared__ int64_t src[kRows], dst[kRows];
     const int tid = threadIdx.x;
     const int column = blockIdx.x % (2 * columns + 1), sh = blockIdx.x / (2 * columns + 1);
     const int s = sh / a.c.heads, h = sh % a.c.heads;
@@ -271,19 +290,22 @@ __global__ __launch_bounds__(kInPlaceThreads) void evict_in_place_kernel(EvictAr
     const int r = tid / mine, u = u0 + tid % mine, per = kInPlaceThreads / mine;
     U* data = (U*)(column >= columns ? a.c.v : a.c.k);
     for (int i0 = 0; i0 < kp.all; i0 += kAhead * per) {
-        int64_t to[kAhead];
+        // where the round's rows are and go, worked out together; rows behind the last repeat it and go nowhere
+        for (int i = tid; i < kAhead * per; i += kInPlaceThreads) {
+            src[i] = source(min(i0 + i, kp.all - 1));
+            dst[i] = i0 + i < kp.all ? row_at(a, a.table, a.table_stride, s, h, i0 + i) : -1;
+        }
+        __syncthreads();
         U x[kAhead];
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            x[j] = U{};
-            const int i = i0 + j * per + r;
-            to[j] = r < per && i < kp.all ? row_at(a, a.table, a.table_stride, s, h, i) : -1;
-            if (to[j] >= 0) x[j] = data[source(i) * units + u];
-        }
+        for (int j = 0; j < kAhead; ++j) x[j] = data[src[j * per + min(r, per - 1)] * units + u];
         all_read();
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j)
-            if (to[j] >= 0) data[to[j] * units + u] = x[j];
+        for (int j = 0; j < kAhead; ++j) {
+            const int64_t to = r < per ? dst[j * per + r] : -1;
+            if (to >= 0) data[to * units + u] = x[j];
+        }
+        __syncthreads();  // (src and dst are read)
     }
 }
 
