@@ -265,3 +265,16 @@ def test_nothing_to_do_and_refusals():
         with pytest.raises(ValueError):
             L.lscd_cache_evict(c, weight, length, table, 32, **kw)
     assert all(torch.equal(x.cpu(), y) for x, y in zip(p.bytes, p.raw)) and torch.equal(p.w.cpu(), p.weight)
+
+
+def test_twice_in_place_is_once():
+    """A sequence that has been cut stays as it is when the call is made again with its new length."""
+    say("twice")
+    p = Pool([400, 90], 64, 2, 64, 16, "e4m3", seed=8)
+    cache = p.device()
+    L.lscd_cache_evict(cache, p.w, *p.args, 64, 10)
+    p.args[0].clamp_(max=64)
+    before, w = [x.clone() for x in p.bytes], p.w.clone()
+    kept = L.lscd_cache_evict(cache, p.w, *p.args, 64, 10)
+    assert torch.equal(kept, torch.arange(64, device="cuda", dtype=torch.int32).expand(2, 2, 64))
+    assert all(torch.equal(x, y) for x, y in zip(before, p.bytes)) and torch.equal(p.w, w)

@@ -289,3 +289,40 @@ def test_nothing_to_do_and_refusals():
     three = b.q[:, :3].contiguous()                          # not a multiple of the cache's two heads
     assert status(c, three, w.lse[:, :3].contiguous(), *good[3:]) == L.LSCD_ERROR_INVALID_VALUE
     assert torch.equal(w.old, before)
+
+
+def test_many_sequences():
+    """More than 64 sequences of both kinds, idle ones among them, in one call."""
+    say("many sequences")
+    seqs = [(i % 3, 20 + 7 * i % 90) for i in range(70)] + [(45, 200), (0, 0), (1, 300)] + [(i % 2, 33 + i) for i in range(60)] + [(90, 90)]
+    w = Weights(Batch4(seqs, 4, 1, 64, 16, "f16", "e2m1", seed=2))
+    w.check(w.run())
+
+
+@pytest.mark.parametrize("n", [0, 1, 9, 33])
+def test_one_sequence_with_room_for_more(n):
+    """A captured call's room: 40 rows of 4 heads in q, fewer new tokens in `start`; rows behind them do not count."""
+    say("room", n)
+    b = Batch4([(n, 150)], 4, 1, 64, 16, "f16", "f16", seed=3)
+    w = Weights(b)
+    want = w.run()
+    w.check(want)
+    b.q = torch.cat([b.q, torch.full((40 - n, 4, 64), float("nan"), device="cuda").half()])
+    w.lse = torch.cat([w.lse, torch.zeros((40 - n, 4), device="cuda")])
+    got = w.run()
+    # (another kernel may serve it: the sums' order differs)
+    assert torch.allclose(got, want, rtol=2.0 ** -18, atol=1e-9)
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_keys_past_the_largest_count_as_the_largest(n):
+    """As in the attention: a key's 65536 is 65504, so that a query of zeros there sees zero."""
+    say("largest keys", n)
+    b = Batch4([(n, 70)], 2, 2, 64, 16, "f16", "e2m1", seed=5)
+    b.q[:, :, 32:] = 0
+    clean = Weights(b)
+    want = clean.run()
+    b.tensors[2][..., 1] = 127 + 14
+    b.tensors[0][..., 16:] = 0x77
+    got = clean.run()
+    assert torch.isfinite(got).all() and torch.equal(got, want)
