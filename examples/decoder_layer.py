@@ -2,12 +2,16 @@
 
     python examples/decoder_layer.py                       # 4096 channels, 32 heads, 4 sequences
     python examples/decoder_layer.py --hidden 12288 --heads 96 --prompt 500
+    python examples/decoder_layer.py --cache e2m1 --keep 64   # 4-bit cache, prompts cut to 64 positions
 
 The layer is OPT's without biases (normalisation, attention, normalisation, a ReLU MLP; random
 weights): the QKV product runs on pruned weights (lscd_spmm), new keys and values go into a paged 8-bit
 cache (lscd_cache_write), attention reads it (lscd_attention), and the output projection and the MLP run
 on 4-bit weights (lscd_quant_linear).  A batch of prompts of different lengths goes through in one call,
-then every sequence decodes one token at a time, as one captured graph that is replayed.
+then every sequence decodes one token at a time, as one captured graph that is replayed.  With --keep,
+the prompt's attention also says how much each position is looked at (lscd_cache_weigh), and longer
+prompts are cut to the last quarter of what is kept and the positions with the largest weights
+(lscd_cache_evict) before decoding.
 """
 import argparse
 import os
@@ -31,7 +35,7 @@ def quantise_weights(w, group=128):
 
 
 class Layer:
-    def __init__(self, hidden=4096, heads=32, sparsity=0.7, pages=256, page=16, seed=0, device="cuda"):
+    def __init__(self, hidden=4096, heads=32, sparsity=0.7, pages=256, page=16, seed=0, device="cuda", cache="e4m3"):
         g = torch.Generator(device=device).manual_seed(seed)
 
         def weight(m, k):
@@ -47,19 +51,28 @@ class Layer:
             setattr(self, name, L.lscd_quant_encode(codes, scale, k, zero))
             self.dense[name] = torch.empty((m, k), device=device, dtype=torch.float16)
             L.lscd_quant_decode(getattr(self, name), self.dense[name])   # (what a plain layer is compared on)
-        shape = (pages, heads, page, self.dim)
-        self.cache = L.Cache(*(torch.zeros(shape, device=device, dtype=torch.float8_e4m3fn) for _ in range(2)),
-                             *(torch.ones(shape[:3], device=device) for _ in range(2)))
+        shape = (pages, heads, page)
+        if cache == "e2m1":
+            self.cache = L.Cache(*(torch.zeros((*shape, n), device=device, dtype=torch.uint8)
+                                   for n in 2 * [self.dim // 2] + 2 * [L.cache_scale_row(self.dim)]))
+        else:
+            self.cache = L.Cache(*(torch.zeros((*shape, self.dim), device=device, dtype=torch.float8_e4m3fn) for _ in range(2)),
+                                 *(torch.ones(shape, device=device) for _ in range(2)))
+        self.weight = torch.zeros(shape, device=device)   # what lscd_cache_weigh adds up
         self.attention = L.lscd_attention_create(heads, heads, self.dim)
 
-    def __call__(self, x, slots, start, length, table, b=None):
-        """x [T][hidden]: new tokens of all sequences; slots: where each goes.  b: buffers to use again."""
+    def __call__(self, x, slots, start, length, table, b=None, weigh=False):
+        """x [T][hidden]: new tokens of all sequences; slots: where each goes.  b: buffers to use again.  weigh: add
+        up how much the cached positions are looked at."""
         T, D = x.shape[0], self.hidden
         b = b if b is not None else self.buffers(T)
         L.lscd_spmm(self.qkv, torch.nn.functional.layer_norm(x, (D,)), b["qkv"])
         q, k, v = b["qkv"].view(T, 3, self.heads, self.dim).unbind(1)
         L.lscd_cache_write(self.cache, k, v, slots)
-        L.lscd_attention(self.attention, self.cache, q, start, length, table, b["mixed"].view(T, self.heads, self.dim))
+        lse = torch.empty((T, self.heads), device=x.device) if weigh else None
+        L.lscd_attention(self.attention, self.cache, q, start, length, table, b["mixed"].view(T, self.heads, self.dim), lse=lse)
+        if weigh:
+            L.lscd_cache_weigh(self.cache, q, lse, start, length, table, self.weight)
         L.lscd_quant_linear(self.out, b["mixed"], b["out"])
         x = x + b["out"]
         L.lscd_quant_linear(self.up, torch.nn.functional.layer_norm(x, (D,)), b["up"])
@@ -85,8 +98,9 @@ class Layer:
         return torch.cat(out)
 
 
-def serve(layer, prompts, steps, seed=1):
-    """Prompts (their lengths), then `steps` tokens for each sequence: all layer inputs and outputs, by sequence."""
+def serve(layer, prompts, steps, seed=1, keep=0):
+    """Prompts (their lengths), then `steps` tokens for each sequence: all layer inputs and outputs, by sequence.
+    keep: cut longer prompts to so many positions before decoding."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     S, page = len(prompts), layer.page
     wide = (max(prompts) + steps + page - 1) // page
@@ -100,9 +114,13 @@ def serve(layer, prompts, steps, seed=1):
     start = [0]
     for n in prompts:
         start.append(start[-1] + n)
-    y = layer(x, slots_of([(s, p) for s, n in enumerate(prompts) for p in range(n)]), ints(start), ints(prompts), table)
+    y = layer(x, slots_of([(s, p) for s, n in enumerate(prompts) for p in range(n)]), ints(start), ints(prompts), table,
+              weigh=keep > 0)
     xs = [[x[start[s]:start[s + 1]]] for s in range(S)]
     ys = [[y[start[s]:start[s + 1]]] for s in range(S)]
+    if keep:
+        L.lscd_cache_evict(layer.cache, layer.weight, ints(prompts), table, keep, recent=keep // 4)
+        prompts = [min(n, keep) for n in prompts]
     # decoding: one graph, its inputs updated between replays
     token, slots = torch.zeros((S, layer.hidden), device="cuda", dtype=torch.float16), slots_of(list(enumerate(prompts)))
     one, length, b = ints(list(range(S + 1))), ints([n + 1 for n in prompts]), layer.buffers(S)
@@ -129,11 +147,13 @@ def main():
     p.add_argument("--sequences", type=int, default=4)
     p.add_argument("--prompt", type=int, default=200)
     p.add_argument("--steps", type=int, default=8)
+    p.add_argument("--cache", choices=("e4m3", "e2m1"), default="e4m3")
+    p.add_argument("--keep", type=int, default=0)
     a = p.parse_args()
     prompts = [max(1, a.prompt - 37 * s) for s in range(a.sequences)]
     pages = a.sequences * ((a.prompt + a.steps + 15) // 16)
-    layer = Layer(a.hidden, a.heads, pages=pages)
-    xs, ys, graph = serve(layer, prompts, a.steps)
+    layer = Layer(a.hidden, a.heads, pages=pages, cache=a.cache)
+    xs, ys, graph = serve(layer, prompts, a.steps, keep=a.keep)
     want = layer.plain(torch.cat(xs), [len(v) for v in xs])
     error = float((torch.cat(ys).float() - want).norm() / want.norm())
     begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
@@ -143,7 +163,7 @@ def main():
     end.record()
     torch.cuda.synchronize()
     print(f"{sum(prompts)} prompt tokens and {a.steps} x {a.sequences} decoded ones; against a plain float32 layer without "
-          f"a cache: {error:.2e} (the 8-bit cache's part); one decoding step {begin.elapsed_time(end) / 20 * 1e3:.0f} us")
+          f"a cache: {error:.2e} (the cache's part{', and what was dropped' if a.keep else ''}); one decoding step {begin.elapsed_time(end) / 20 * 1e3:.0f} us")
 
 
 if __name__ == "__main__":

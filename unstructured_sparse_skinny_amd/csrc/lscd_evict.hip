@@ -10,8 +10,13 @@
 //
 // Moving: position i of the front takes the i-th position kept, which is i or more.  Into other pages the rows are
 // independent.  In place, a workgroup takes a column of the rows (128 bytes of keys or values, or the scales and
-// weights) from the front to the back: it reads as many rows as its registers hold before it writes them, and what
-// it writes lies before everything that is still to be read.
+// weights) from the front to the back: it reads some rows into registers before it writes them, and what it writes
+// lies before everything that is still to be read.
+//
+// Measured: one sequence of 16384 positions of 8 heads (16 bits) cut to 4096 in 26 us, 18.5 of them to choose (eight
+// workgroups: 5 us to read the weights, 3 to 6 for a digit) and 7 to move; in place 44.  64 sequences of 100 to 4096
+// positions cut to 1024 (e4m3, 247 MB) in 71 us, 12 to choose and 57 to move; in place 49.  131072 positions, whose
+// weights are read from memory for every digit, cut to 32768: 250 us, in place 403 (32 columns of rows for 256 CUs).
 
 #include "lscd_serve.h"
 #include "lscd_serve_device.h"

@@ -7,9 +7,14 @@
 // S = Q K^T on the matrix cores: a lane then holds scores of one position and of four rows, whose sum is taken in
 // the lane and over its quarters.  Products are exact and sums fp32, as in the attention.
 //
-// The units (stretches of positions of one sequence and key head) are numbered sequence after
-// sequence, head after head, and cut into equal ranges by what they cost, one for each wavefront; a unit belongs
-// to the range in which its first slot lies.
+// Few rows: the units (stretches of positions of one sequence and key head) are numbered sequence after sequence,
+// head after head, and cut into equal ranges by what they cost, one for each wavefront; a unit belongs to the range
+// in which its first slot lies.  Twice as many wavefronts as run at once even out what they wait for (64 sequences
+// of one token over up to 2048 positions of 96 heads, 4-bit codes: 114 us, 121 with half as many).
+//
+// Measured: those 497 MB in 114 us, 4.4 TB/s; 1500 tokens of 32 heads over 8000 positions of 8 (89 GFLOP and 348
+// million exponentials) in 119 us, 750 TFLOP/s; 4096 over 16384 in 561 us, 858 TFLOP/s.  Heads of 256 channels: 273
+// us for the 1500, one workgroup a CU.
 
 #include "lscd_attention.h"
 
