@@ -71,3 +71,63 @@ def test_e2m1_codes_and_scales():
     assert sv.e2m1_group([2.0 ** -140])[1] == 1 and sv.e2m1_group([np.inf, 1.0])[1] == 255
     packed = np.array([[[0x71, 0xF0]]], dtype=np.uint8)
     assert sv.e2m1_values(packed, np.array([[[128, 0]]], dtype=np.uint8), 4).tolist() == [[[1.0, 12.0, 0.0, -12.0]]]
+
+
+def cache_of(kind=None, **more):
+    c = dict(k=0x1000, v=0x2000, k_scale=0x3000, v_scale=0x4000, num_pages=8, heads=2, page_size=16, head_dim=64, type=L.LSCD_E2M1)
+    c.update(more)
+    return L.lscd_cache_t(*c.values())
+
+
+def weigh_status(cache=None, **more):
+    """Status of lscd_cache_weigh for arrays that are not there."""
+    a = dict(q=0x5000, q_stride=256, q_heads=4, lse=0x6000, start=0x7000, length=0x7100, table=0x7200, table_stride=4,
+             table_pages=4, sequences=3, T=5, scale=0.1, causal=1, window=0, weight=0x8000, type=L.LSCD_F16)
+    a.update(more)
+    return L._lib.lscd_cache_weigh(ctypes.byref(cache if cache is not None else cache_of()), *a.values(), None)
+
+
+def evict_status(cache=None, **more):
+    a = dict(weight=0x8000, length=0x7100, table=0x7200, table_stride=4, table_pages=4, to=None, to_stride=0, to_pages=0,
+             sequences=3, keep=20, recent=4, kept=0x9000)
+    a.update(more)
+    return L._lib.lscd_cache_evict(ctypes.byref(cache if cache is not None else cache_of()), *a.values(), None)
+
+
+CACHES = [dict(k=None), dict(k_scale=None), dict(k=0x1008), dict(v_scale=0x4004), dict(num_pages=0), dict(type=7)]
+LIMITS = [dict(page_size=24), dict(head_dim=40), dict(head_dim=272), dict(heads=65536), dict(num_pages=2 ** 28)]
+
+
+@pytest.mark.parametrize("call", [weigh_status, evict_status])
+def test_caches_are_checked(call):
+    for bad in CACHES:
+        assert call(cache_of(**bad)) == L.LSCD_ERROR_INVALID_VALUE, bad
+    for bad in LIMITS:
+        assert call(cache_of(**bad)) == L.LSCD_ERROR_NOT_SUPPORTED, bad
+
+
+def test_weigh_refuses():
+    for bad in (dict(q=None), dict(q=0x5008), dict(q_stride=255), dict(q_stride=128), dict(q_heads=3), dict(q_heads=0), dict(lse=None),
+                dict(lse=0x6002), dict(weight=None), dict(weight=0x8004), dict(start=None), dict(length=0x7102), dict(table=None),
+                dict(table_pages=0), dict(table_stride=3), dict(T=-1), dict(sequences=-1), dict(window=-1),
+                dict(scale=float("nan")), dict(type=L.LSCD_E4M3)):
+        assert weigh_status(**bad) == L.LSCD_ERROR_INVALID_VALUE, bad
+    assert weigh_status(cache_of(type=L.LSCD_BF16, k_scale=None, v_scale=None)) == L.LSCD_ERROR_NOT_SUPPORTED
+    assert weigh_status(T=2 ** 31) == L.LSCD_ERROR_NOT_SUPPORTED
+    assert weigh_status(table_pages=2 ** 27, table_stride=2 ** 27) == L.LSCD_ERROR_NOT_SUPPORTED
+    # 2^31 units: 16 query rows by 32 positions, a key head each
+    assert weigh_status(T=2 ** 24, table_pages=2 ** 14, table_stride=2 ** 14) == L.LSCD_ERROR_NOT_SUPPORTED
+    for nothing in (dict(T=0), dict(sequences=0), dict(T=0, q=None, lse=None, weight=None, table=None)):
+        assert weigh_status(**nothing) == L.LSCD_SUCCESS, nothing
+
+
+def test_evict_refuses():
+    for bad in (dict(keep=0), dict(recent=-1), dict(recent=21), dict(sequences=-1), dict(weight=None), dict(weight=0x8008),
+                dict(length=None), dict(table=0x7202), dict(table_pages=0), dict(table_stride=3), dict(kept=None), dict(kept=0x9001),
+                dict(to=0xA002, to_stride=4, to_pages=4), dict(to=0xA000, to_stride=4, to_pages=1),
+                dict(to=0xA000, to_stride=1, to_pages=2), dict(to=0xA000, to_stride=0, to_pages=0)):
+        assert evict_status(**bad) == L.LSCD_ERROR_INVALID_VALUE, bad
+    assert evict_status(table_pages=2 ** 27, table_stride=2 ** 27) == L.LSCD_ERROR_NOT_SUPPORTED
+    assert evict_status(sequences=2 ** 21) == L.LSCD_ERROR_NOT_SUPPORTED
+    assert evict_status(sequences=2 ** 30, cache=cache_of(heads=65535)) == L.LSCD_ERROR_NOT_SUPPORTED
+    assert evict_status(sequences=0, weight=None, kept=None, table=None) == L.LSCD_SUCCESS
