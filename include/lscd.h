@@ -581,6 +581,7 @@ lscd_status_t lscd_cache_weigh(const lscd_cache_t* cache, const void* q, int64_t
  *           positions.  No page of it may be one that the call reads or that it names twice.  NULL (or `table`
  *           itself): in place; a page of a sequence that is cut may then not be another sequence's too.
  *   kept    device, [sequences][heads][keep]: the positions kept, ascending, then -1.
+ *           Rows are moved by what it says: nothing else may write it before the call's work is done.
  *   keep    1 and more;  recent  0..keep.
  * Lengths outside the table are clamped to it; a page outside the pool is read as page 0 and not written.
  * Asynchronous, no allocation, no workspace, graph-capturable.  NOT_SUPPORTED: table_pages * page_size above

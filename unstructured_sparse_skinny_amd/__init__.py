@@ -430,6 +430,17 @@ def _stream_on(stream, device):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
+def _empty_on(stream, shape, dtype, device):
+    """torch.empty on the stream that a call works on: memory of another stream's pool may still be in use there, and
+    would go back to it, for its next allocation, while the call's kernels work."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class Quant:
     """Owner of an lscd_quant_t (an M x K matrix of 4-bit codes); freed by lscd_quant_destroy (or when collected)."""
 
@@ -660,19 +671,21 @@ def lscd_cache_weigh(cache: Cache, q, lse, start, length, table, weight, scale=N
 def lscd_cache_evict(cache: Cache, weight, length, table, keep: int, recent: int = 0, to=None, kept=None, stream=None):
     """Cut every sequence to its last `recent` positions and those of the others with the largest weights, `keep` in
     all for each key head, moved in their order to the front of its pages (in place) or of those of `to` (int32
-    [sequences][pages]).  Returns the positions kept, int32 [sequences][heads][keep], -1 behind them."""
+    [sequences][pages]).  Returns the positions kept, int32 [sequences][heads][keep], -1 behind them.  The kernels that
+    move read them there: `kept` stays as it is until they are done (one that is not given is allocated on `stream`)."""
     S, dev = length.shape[0], cache.device
+    on = _stream_on(stream, dev)
     if table.shape[0] != S or (to is not None and to.shape[0] != S):
         raise ValueError("tables must have a row for every length")
     if kept is None:
-        kept = torch.empty((S, cache.heads, max(keep, 0)), dtype=torch.int32, device=dev)
+        kept = _empty_on(stream, (S, cache.heads, max(keep, 0)), torch.int32, dev)
     if kept.dtype != torch.int32 or tuple(kept.shape) != (S, cache.heads, keep) or not kept.is_contiguous() or kept.device != dev:
         raise ValueError(f"kept must be a contiguous int32 tensor [{S}][{cache.heads}][{keep}] on the cache's device")
     wide = [0, 0] if to is None else [to.stride(0) if S > 1 else to.shape[1], to.shape[1]]
     _check(_lib.lscd_cache_evict(cache.ptr, _weights(weight, cache), _ints(length, "length", dev), _ints(table, "table", dev, 2),
                                  table.stride(0) if S > 1 else table.shape[1], table.shape[1],
                                  None if to is None else _ints(to, "to", dev, 2), *wide, S, keep, recent, kept.data_ptr(),
-                                 _stream_on(stream, dev)), "lscd_cache_evict")
+                                 on), "lscd_cache_evict")
     return kept
 
 

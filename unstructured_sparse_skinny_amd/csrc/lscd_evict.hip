@@ -190,6 +190,9 @@ __device__ __forceinline__ int64_t row_at(const EvictArgs& a, const int32_t* tab
     return ((int64_t)e * a.c.heads + h) * a.c.page_size + (i & (a.c.page_size - 1));
 }
 
+// A position read back from `kept`, which is the caller's memory: clamped, whatever it holds by now.
+__device__ __forceinline__ int within(int from, int len) { return (int)min((uint32_t)from, (uint32_t)len - 1u); }
+
 // A scale row (1, 2, 4 or 8 bytes; 0: there are none) from one row to another.
 __device__ __forceinline__ void move_scale(void* p, int bytes, int64_t from, int64_t to) {
     if (bytes == 8)
@@ -208,10 +211,11 @@ __global__ __launch_bounds__(kMoveThreads) void evict_copy_kernel(EvictArgs a, i
     const int tid = threadIdx.x, z = blockIdx.x & 1;
     const int chunk = (blockIdx.x >> 1) % chunks, sh = (blockIdx.x >> 1) / chunks;
     const int s = sh / a.c.heads, h = sh % a.c.heads, i0 = chunk * kMoveRows;
-    const int rows = min(Kept(a, s).all - i0, kMoveRows);
+    const Kept kp(a, s);
+    const int rows = min(kp.all - i0, kMoveRows);
     if (rows <= 0) return;
     if (tid < rows) {
-        const int from = a.kept[((int64_t)s * a.c.heads + h) * a.keep + i0 + tid];
+        const int from = within(a.kept[((int64_t)s * a.c.heads + h) * a.keep + i0 + tid], kp.len);
         const int64_t p = page_at(a, a.table, a.table_stride, s, from >> a.page_log2);
         src[tid] = (p * a.c.heads + h) * a.c.page_size + (from & (a.c.page_size - 1));
         dst[tid] = row_at(a, a.to, a.to_stride, s, h, i0 + tid);
@@ -252,7 +256,7 @@ __global__ __launch_bounds__(kInPlaceThreads) void evict_in_place_kernel(EvictAr
     if (kp.len <= a.keep) return;
     const int32_t* kept = a.kept + ((int64_t)s * a.c.heads + h) * a.keep;
     auto source = [&](int i) {
-        const int from = kept[i];
+        const int from = within(kept[i], kp.len);
         return (page_at(a, a.table, a.table_stride, s, from >> a.page_log2) * a.c.heads + h) * a.c.page_size +
                (from & (a.c.page_size - 1));
     };
