@@ -584,8 +584,8 @@ lscd_status_t lscd_cache_weigh(const lscd_cache_t* cache, const void* q, int64_t
  *           Rows are moved by what it says: nothing else may write it before the call's work is done.
  *   keep    1 and more;  recent  0..keep.
  * Lengths outside the table are clamped to it; a page outside the pool is read as page 0 and not written.
- * Asynchronous, no allocation, no workspace, graph-capturable.  NOT_SUPPORTED: table_pages * page_size above
- * 2^30; sequences * heads * (keep / 32, or in place 1 and two for 128 bytes of a row) of 2^22 and more.
+ * Asynchronous, no allocation, no workspace, graph-capturable.  NOT_SUPPORTED: table_pages * page_size or keep
+ * above 2^30; sequences * heads * (keep / 32, or in place 1 and two for 128 bytes of a row) of 2^22 and more.
  */
 lscd_status_t lscd_cache_evict(const lscd_cache_t* cache, float* weight, const int32_t* length, const int32_t* table,
                                int64_t table_stride, int32_t table_pages, const int32_t* to, int64_t to_stride,

@@ -131,3 +131,10 @@ def test_evict_refuses():
     assert evict_status(sequences=2 ** 21) == L.LSCD_ERROR_NOT_SUPPORTED
     assert evict_status(sequences=2 ** 30, cache=cache_of(heads=65535)) == L.LSCD_ERROR_NOT_SUPPORTED
     assert evict_status(sequences=0, weight=None, kept=None, table=None) == L.LSCD_SUCCESS
+
+
+def test_evict_refuses_more_than_it_counts():
+    """Numbers of positions past 2^30, whose loops and launches would pass 31 bits, in place and into other pages."""
+    for keep in (2 ** 30 + 1, 2 ** 31 - 64, 2 ** 31 - 1):
+        for more in (dict(), dict(recent=keep), dict(to=0xA000, to_stride=2 ** 27, to_pages=2 ** 27)):
+            assert evict_status(sequences=1, keep=keep, **{"recent": 0, **more}) == L.LSCD_ERROR_NOT_SUPPORTED, (keep, more)

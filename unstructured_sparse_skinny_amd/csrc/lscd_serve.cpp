@@ -360,7 +360,8 @@ lscd_status_t lscd_cache_evict(const lscd_cache_t* cache, float* weight, const i
         return LSCD_ERROR_INVALID_VALUE;
     const int64_t page = cache->page_size;
     if (to && (to_pages < 1 || to_stride < to_pages || to_pages * page < keep)) return LSCD_ERROR_INVALID_VALUE;
-    if (table_pages * page > ((int64_t)1 << 30)) return LSCD_ERROR_NOT_SUPPORTED;
+    // (positions, and those that are kept, are counted in 31 bits with what a workgroup takes at a time behind them)
+    if (table_pages * page > ((int64_t)1 << 30) || keep > (1 << 30)) return LSCD_ERROR_NOT_SUPPORTED;
     lscd::EvictArgs a = {};
     a.c = *cache;
     a.weight = weight;
