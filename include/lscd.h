@@ -553,7 +553,7 @@ lscd_status_t lscd_attention_lse(lscd_attention_t h, const lscd_cache_t* cache, 
  *   heads of the key head) that see the position is put into (new tokens' positions) or added to (the others)
  *   weight[slot].  Nothing else is written.  Arguments as in lscd_attention (q_heads a multiple of the cache's
  *   heads; lse as lscd_attention_lse wrote it for the same rows); it follows it in a layer.
- *   lse     device, [T][q_heads] floats.  A row of -infinity gives nothing.
+ *   lse     device, [T][q_heads] floats.  A row of -infinity gives nothing, whatever its query and the keys hold.
  *   weight  device, [num_pages][heads][page_size] floats, 16-byte aligned.
  * No two sequences of a call may share a page of which one's new tokens see a position (sums would be lost).
  * Sums are fp32, in a fixed order: bit-reproducible for the same call.  A weight is off by about 2^-24 of the

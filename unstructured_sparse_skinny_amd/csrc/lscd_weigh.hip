@@ -193,7 +193,8 @@ __global__ __launch_bounds__(64 * kWeighWaves, (DP <= 64 || (FORM == kForm4 && D
         place = own ? (float*)at + (t & (a.c.page_size - 1)) : nullptr;
         old = *(own ? place : a.weight);
     };
-    // The query rows of a tile; rows that are none repeat the last one, and weigh nothing.
+    // The query rows of a tile; rows that are none repeat the last one, and weigh nothing.  One whose logarithm is
+    // -infinity sees nothing: 2^(score - infinity) would be NaN where the score is.
     u32x4v qr[F::kSteps];
     float log[4];  // of the rows whose scores the lane has, in units of log2
     int see_high[4], see_low[4], all_high, all_low;
@@ -214,18 +215,22 @@ __global__ __launch_bounds__(64 * kWeighWaves, (DP <= 64 || (FORM == kForm4 && D
         }
         all_high = w.q.len;
         all_low = 0;
+        bool out = false;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             row(4 * g + r, &token, &head);
             const float x = a.row_lse[(int64_t)(w.q.first + token) * a.q_heads + head];
-            log[r] = tile * kFewRows + 4 * g + r < w.q.rows && x != -__builtin_inff() ? x * kLog2e : __builtin_inff();
+            const bool none = x == -__builtin_inff();
+            out |= none;
+            log[r] = tile * kFewRows + 4 * g + r < w.q.rows ? x * kLog2e : __builtin_inff();
             const int pos = w.q.len - w.q.n + token;
-            see_high[r] = a.causal ? min(pos + 1, w.q.len) : w.q.len;
+            see_high[r] = none ? 0 : a.causal ? min(pos + 1, w.q.len) : w.q.len;
             see_low[r] = a.window ? pos - a.window + 1 : 0;
         }
         // what every row sees: the first one's end, the last one's begin
         if (a.causal) all_high = __builtin_amdgcn_readfirstlane(see_high[0]);
         if (a.window) all_low = __builtin_amdgcn_readlane(see_low[3], 48);
+        if (__any(out)) all_high = 0;
     };
 
     // Scores of the tile of rows in qr with the keys in f, and what they weigh.
@@ -560,7 +565,8 @@ __global__ __launch_bounds__(64 * kWeighWaves, 2) void weigh_many_kernel(AttnArg
         }
         for (int tile = r0 + wave; tile < r1; tile += kWeighWaves) {
             // (here the first half's rows have come, too)
-            logs[wave][lane] = tile * 64 + lane < q.rows && row_log != -__builtin_inff() ? row_log * kLog2e : __builtin_inff();
+            if (row_log == -__builtin_inff()) row_high = 0;  // (it sees nothing: 2^(score - infinity) may be NaN)
+            logs[wave][lane] = tile * 64 + lane < q.rows ? row_log * kLog2e : __builtin_inff();
             highs[wave][lane] = row_high;
             lows[wave][lane] = row_low;
             // some row does not see some position (or is none)
