@@ -51,3 +51,26 @@ def test_a_result_that_nobody_keeps():
         junk = [torch.full((3, 2, 2048), 5, dtype=torch.int32, device="cuda") for _ in range(4)]
         s.synchronize()
         assert len(junk) == 4 and all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(p.bytes, want[1]))
+
+
+def stream_of(t):
+    """The stream whose pool a tensor's memory is of."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+
+
+def test_every_way_to_name_a_stream():
+    """None, a stream, its handle, and the default stream's, which is 0: from under another current stream."""
+    say("ways to name a stream")
+    p, s, other = Pool([300], 64, 2, 16, 16, "f16", seed=1), torch.cuda.Stream(), torch.cuda.Stream()
+    want = p.expect(3, True)[0]
+    assert stream_of(torch.empty(5, device="cuda")) == torch.cuda.current_stream().cuda_stream == 0
+    for stream, handle in ((None, other.cuda_stream), (s, s.cuda_stream), (s.cuda_stream, s.cuda_stream), (0, 0),
+                           (torch.cuda.default_stream(), 0)):
+        cache, to = p.device(), p.to.cuda()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            kept = L.lscd_cache_evict(cache, p.w, *p.args, 64, 3, to=to, stream=stream)
+        torch.cuda.synchronize()
+        assert stream_of(kept) == handle and np.array_equal(kept.cpu().numpy(), want)

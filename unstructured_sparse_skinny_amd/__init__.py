@@ -435,8 +435,8 @@ def _empty_on(stream, shape, dtype, device):
     would go back to it, for its next allocation, while the call's kernels work."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # (torch makes a new stream of a handle of 0, which is the default one's)
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
