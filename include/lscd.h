@@ -556,6 +556,8 @@ lscd_status_t lscd_attention_lse(lscd_attention_t h, const lscd_cache_t* cache, 
  *   lse     device, [T][q_heads] floats.  A row of -infinity gives nothing, whatever its query and the keys hold.
  *   weight  device, [num_pages][heads][page_size] floats, 16-byte aligned.
  * No two sequences of a call may share a page of which one's new tokens see a position (sums would be lost).
+ * What is added to is the slot's former weight, whoever left it: of a position that was written but was new in no
+ * call (of a prompt whose last part alone is weighed, or of tokens decoded without), clear it before.
  * Sums are fp32, in a fixed order: bit-reproducible for the same call.  A weight is off by about 2^-24 of the
  * largest score and of lse, relative.  Array contents outside the rules are clamped as in lscd_attention;
  * positions in pages outside the pool have no weight.

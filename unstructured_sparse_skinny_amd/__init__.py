@@ -653,7 +653,8 @@ def _weights(t, cache):
 def lscd_cache_weigh(cache: Cache, q, lse, start, length, table, weight, scale=None, causal=True, window=0, stream=None):
     """Put into (new tokens' positions) or add to (the others) weight [pages][heads][page_size] (float32) the softmax
     weights that the new tokens q [T][q_heads][head_dim] give to the cached positions; lse [T][q_heads] as
-    lscd_attention wrote it for the same arguments."""
+    lscd_attention wrote it for the same arguments (-infinity: the row gives nothing).  Positions that are new in no
+    call have to be cleared before, or the sums are added to what their slots' former owners left."""
     heads, T, S, dev = q.shape[1] if q.dim() == 3 else 0, q.shape[0], length.shape[0], cache.device
     pq, sq = _rows(q, "q", heads, cache.head_dim, dev)
     if q.dtype not in (torch.float16, torch.bfloat16):
