@@ -558,9 +558,10 @@ lscd_status_t lscd_attention_lse(lscd_attention_t h, const lscd_cache_t* cache, 
  * No two sequences of a call may share a page of which one's new tokens see a position (sums would be lost).
  * What is added to is the slot's former weight, whoever left it: of a position that was written but was new in no
  * call (of a prompt whose last part alone is weighed, or of tokens decoded without), clear it before.
- * Sums are fp32, in a fixed order: bit-reproducible for the same call.  A weight is off by about 2^-24 of the
- * largest score and of lse, relative.  Array contents outside the rules are clamped as in lscd_attention;
- * positions in pages outside the pool have no weight.
+ * Sums are fp32, in a fixed order: bit-reproducible for the same call.  With B the sum over the channels of
+ * |scale * q k|, a row's weight is off by at most (head_dim + 8) 2^-24 B + 2^-22 (B + |lse| + 1) of itself (for the
+ * lse given), the sum of R rows by R 2^-24 more, and what is added to by 2^-23 of the result.  Array contents outside
+ * the rules are clamped as in lscd_attention; positions in pages outside the pool have no weight.
  * Asynchronous, no allocation, no workspace, graph-capturable.
  * NOT_SUPPORTED as lscd_attention, with units of 16 query rows by 32 positions; q_heads above 65535.
  */
