@@ -14,10 +14,12 @@
 //
 // Measured: 64 sequences of one token over up to 2048 positions of 96 heads (e4m3, 1.72 GB) 313 us, 5.5
 // TB/s, which is what a plain read reaches here; one token over 1000 positions of 8 heads 9.5 us, a chain
-// of dependent latencies (tables, keys, values, partial results, their join) rather than its 4 MB.  The same 64
-// sequences over 4-bit codes (889 MB) 236 us, 3.8 TB/s: conversions, transpositions and softmax take as much of the
-// vector unit for half the bytes (about 250 vector instructions for 32 positions), and what is left waits, with three
-// wavefronts on a SIMD.
+// of dependent latencies (tables, keys, values, partial results, their join) rather than its 4 MB (12.4 with the
+// rows' logarithms: the join fetches the parts' sums one after the other).  The same 64 sequences over 4-bit codes
+// (889 MB) 236 us, 3.8 TB/s, which nothing is full at: the vector unit is busy 43 % of the time, CUs have wavefronts
+// for 77 % of it (the ranges are of equal size, and end unevenly), 2.7 to a SIMD then, and one of these waits for loads
+// for 47 % of its time and for its turn to issue for 18.  (20 loads bring 32 positions' 4.3 KB; over e4m3 16 loads
+// bring 8.3, and CUs have wavefronts for 95 % of the time.)
 
 #include <type_traits>
 

@@ -14,9 +14,11 @@
 // lies before everything that is still to be read.
 //
 // Measured: one sequence of 16384 positions of 8 heads (16 bits) cut to 4096 in 26 us, 18.5 of them to choose (eight
-// workgroups: 5 us to read the weights, 3 to 6 for a digit) and 7 to move; in place 44.  64 sequences of 100 to 4096
-// positions cut to 1024 (e4m3, 247 MB) in 71 us, 12 to choose and 57 to move; in place 49.  131072 positions, whose
-// weights are read from memory for every digit, cut to 32768: 250 us, in place 403 (32 columns of rows for 256 CUs).
+// workgroups on 256 CUs, whose passes wait for each other: 5 us to read the weights, 3 to 6 for a digit) and 7 to
+// move; in place 40 (40 workgroups, a memory latency and a drain a round).  64 sequences of 100 to 4096 positions cut to
+// 1024 (e4m3, 247 MB) in 71 us, 12 to choose and 57 to move; in place 52.  131072 positions, whose weights are read
+// from memory five times (three digits, a count, the writing), cut to 32768: 270 us, in place 415.  4-bit codes: 23 us
+// and 56, in place 30 and 31.
 
 #include "lscd_serve.h"
 #include "lscd_serve_device.h"

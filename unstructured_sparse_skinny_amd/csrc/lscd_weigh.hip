@@ -13,8 +13,9 @@
 // of one token over up to 2048 positions of 96 heads, 4-bit codes: 114 us, 121 with half as many).
 //
 // Measured: those 497 MB in 114 us, 4.4 TB/s; 1500 tokens of 32 heads over 8000 positions of 8 (89 GFLOP and 348
-// million exponentials) in 119 us, 750 TFLOP/s; 4096 over 16384 in 561 us, 858 TFLOP/s.  Heads of 256 channels: 273
-// us for the 1500, one workgroup a CU.
+// million exponentials) in 121 us, 740 TFLOP/s; 4096 over 16384 in 561 us, 858 TFLOP/s.  Over e4m3 122 us, over e2m1
+// 123, in float16 125; heads of 64 channels 82, of 256 277, one workgroup a CU.  One token each over 16-bit caches 365 us
+// (1.72 GB, 4.7 TB/s), over e4m3 207 (914 MB, 4.4 TB/s).
 
 #include "lscd_attention.h"
 
@@ -621,7 +622,8 @@ hipError_t weigh_run(const AttnArgs& a, int cus, int which, hipStream_t s) {
         constexpr int kTiles = DP <= 128 ? 4 : 2;
         const double blocks = (double)a.sequences * a.c.heads * ((double)a.table_pages * a.c.page_size / (32 * kTiles) + 1);
         // (blocks of 32 positions where those of 128 would leave CUs idle, as far as the table's width tells: 128 blocks
-        // of 1500 tokens x 4 heads 77 against 48 us, 192 74 against 75, 256 73 against 95)
+        // of 1500 tokens x 4 heads 77 against 48 us, 192 74 against 75, 256 73 against 95.  Sequences of few rows count as
+        // if they were of many, so that one prompt among many decoding ones takes the large blocks)
         if (blocks < 0.75 * cus)
             weigh_many_kernel<T, FORM, DP, 1><<<2 * cus, 64 * kWeighWaves, 0, s>>>(a);
         else
